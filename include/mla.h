@@ -330,6 +330,113 @@ mla_status mla_rope_append(const void* q_pe, const void* c_kv, const void* k_pe,
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* The serving step around the latent attention                               */
+/* ------------------------------------------------------------------------- */
+/*
+ * Block tables, positions and slots of one step's tokens, built on the GPU from request lengths.
+ * Request b holds lens[b] tokens and gains (n > 0) or drops (n < 0) n = new_tokens[b] of them
+ * (drops: rejected draft tokens; n <= -lens[b] ends the request).  With
+ *   len' = max(0, len + n), have = ceil(len / page_size), need = ceil(len' / page_size)
+ * a grown request takes need - have page ids from the pool into block_table[b][have .. need - 1], in
+ * request order; a shrunk one gives the ids in block_table[b][need .. have - 1] back (the entries
+ * stay as they are).  The pool is a ring: pool_state = {head, count}, the free ids are
+ * pool[(head + i) % num_pages], i < count; ids are taken at the head and given back behind the tail,
+ * so what a call gives back serves from the next call on.  A request that starts has lens[b] = 0.
+ * Tokens are packed by request: token i of request b is row cu_tokens[b] + i, sits at position
+ * len + i and in slot (cache row) page * page_size + position % page_size of its page.
+ *
+ * lens, new_tokens DEVICE int32 [B]; block_table DEVICE int32 [B, max_pages], in place;
+ * pool     DEVICE int32 [num_pages], in place; num_pages * page_size below 2^31.
+ * pool_state DEVICE int32 [2]; pool_state_out int32 [2] receives the new state, may be pool_state.
+ * N        capacity in tokens of positions and slots (e.g. the captured size of a padded batch).
+ * cu_tokens  int32 [B + 1]: first row of each request's tokens, then the total (both cut at N).
+ * positions, slots int32 [N]; rows behind the last token get -1 in both (mla_kv_append skips them).
+ * lens_out int32 [B]: the new lengths (the lens of mla_decode); may be lens.
+ * Every other output is a buffer of its own.  Given unchanged lens, new_tokens and pool_state a
+ * repeated call writes the same values.
+ * A request whose tokens run past N, whose pages the pool does not hold (or the ring does not take),
+ * whose length would pass max_pages * page_size or is invalid keeps its length and its pages, its
+ * tokens get -1 in positions and slots, and MLA_ERR_DEVICE_RANGE is recorded
+ * (mla_check_device_status; detail 0x2072, 0x2071, 0x2073, 0x2070); requests after one that ran out
+ * of tokens or pages and that need some too are refused with it.  A pool_state outside the ring (0x2074) refuses
+ * every page; a page id outside [0, num_pages) in the pool or the table (0x2075) gives slot -1.
+ */
+size_t mla_slot_map_workspace_size(int B);
+mla_status mla_slot_map(const int32_t* lens, const int32_t* new_tokens, int B, int32_t* block_table, int max_pages,
+                        int page_size, int64_t num_pages, int32_t* pool, const int32_t* pool_state, int N,
+                        int32_t* cu_tokens, int32_t* positions, int32_t* slots, int32_t* lens_out,
+                        int32_t* pool_state_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Root-mean-square norm of T rows of D columns, with the residual's addition and an 8-bit output.
+ *   h = x + residual (x alone without one),  y = h / sqrt(mean(h^2) + eps) * weight
+ * in fp32; residual_out = h as bf16 (the norm reads the unrounded sum).  out is y as bf16, or with
+ * out_e4m3 the e4m3 values of y / s, one fp32 scale s = max(max|y| / 448, 2^-126) for each `group`
+ * columns (0: one for the whole row), so that y is e4m3 * s; a NaN among a group's y makes its
+ * scale NaN.
+ *
+ * x, residual (nullable) bf16 rows at element strides x_stride, residual_stride; weight bf16 [D].
+ * residual_out bf16 rows (stride residual_out_stride), given if and only if residual is; it may be
+ *          the residual's or the x's buffer with the same stride (in place).
+ * out      bf16 or e4m3 rows (stride out_stride); a bf16 out may be x's buffer with the same stride.
+ * scales   fp32 [T, D / group] contiguous (group 0: [T, 1]) with out_e4m3, else NULL.
+ * group    0, or 32, 64 or 128 dividing D.  1 <= D <= 32768 (above: MLA_ERR_UNSUPPORTED); any D and
+ *          any element-aligned address or stride is taken, rows on 16-byte boundaries are faster.
+ */
+mla_status mla_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                        const void* weight, float eps, int T, int D, void* residual_out, int64_t residual_out_stride,
+                        int out_e4m3, int group, void* out, int64_t out_stride, float* scales, void* stream);
+
+/*
+ * Latent norm, RoPE and the write of cache rows by slot, for any number of tokens (one decode step,
+ * several tokens per request, a prompt), into a bf16 or an e4m3 cache.
+ *   row = [c_kv / sqrt(mean(c_kv^2) + eps) * norm_weight | k_pe turned at positions[t]]   (fp32)
+ *   cache row slots[t] = row as bf16, or e4m3(row / kv_scale), saturating at +-448 (the cache of
+ *   mla_decode_fp8);  q_out[t, h, 512..575] = q_pe[t, h] turned, as bf16;  kv_out[t] = row as bf16.
+ * Pairs and the angle table are those of mla_rope_append.
+ *
+ * c_kv, k_pe  bf16 rows of 512 and 64 at element strides c_kv_stride, k_pe_stride (views of one
+ *          down-projection's output are fine); norm_weight bf16 [512], NULL: no norm (eps unused).
+ * q_pe     bf16 rows of 64 at strides (q_pe_stride_t, q_pe_stride_h); NULL with H = 0: no query.
+ * q_out    bf16, the fused query: columns 512..575 of rows at (q_out_stride_t, q_out_stride_h) are
+ *          written, the others left as they are.  kv_out (nullable) bf16 rows of 576: the tokens'
+ *          rows for mla_prefill.
+ * positions DEVICE int32 [T]: -1 marks a row that holds no token (nothing is written for it); another
+ *          position outside [0, max_pos) records MLA_ERR_DEVICE_RANGE and is skipped likewise.
+ * slots    DEVICE int32 [T]: cache rows (mla_slot_map).  -1: no cache row is written (q_out and
+ *          kv_out are); another slot outside [0, num_pages * page_size) is recorded, too.  The slots
+ *          of a call's tokens are distinct: of two tokens in one slot either's values may stay.
+ * kv_cache bf16 or (cache_e4m3) e4m3 [num_pages, page_size, 576]; kv_scale > 0 with e4m3.
+ * Tensors are 16-byte aligned, strides multiples of 8 elements.
+ */
+size_t mla_kv_append_workspace_size(int T);
+mla_status mla_kv_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t k_pe_stride,
+                         const void* norm_weight, float eps, const void* q_pe, int64_t q_pe_stride_t,
+                         int64_t q_pe_stride_h, const int32_t* positions, const int32_t* slots, const float* cos_sin,
+                         int max_pos, int is_neox, int T, int H, void* kv_cache, int cache_e4m3, float kv_scale,
+                         int64_t num_pages, int page_size, void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+                         void* kv_out, int64_t kv_out_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Per-head products with 4-bit weights and group scales (the absorption products of a decode step
+ * with a quarter of the weights' bytes; H = 1 is an ordinary projection):
+ *   out[t, h, n] = sum_k x[t, h, k] * (code[h, n, k] - 8) * scale[h, n, k / group]
+ * with codes 0..15, fp32 sums, bf16 out.
+ *
+ * x        bf16, element (t, h, k) at x + t * x_stride_t + h * x_stride_h + k.
+ * w4       bytes [H, N, K / 2] contiguous, 16-byte aligned: byte j of a row holds the code of k = 2j in
+ *          its low half and that of k = 2j + 1 in its high half.
+ * scales   [H, N, K / group] contiguous, bf16 or (scales_f32) fp32.
+ * group    32, 64 or 128, dividing K.
+ * out      bf16, element (t, h, n) at out + t * out_stride_t + h * out_stride_h + n; only these are
+ *          written (the latent columns of a fused query: strides (H * 576, 576)).
+ * Built for few tokens (up to about 64): the weights are read once for every 64 tokens.
+ */
+mla_status mla_bmm_w4(const void* x, int64_t x_stride_t, int64_t x_stride_h, const void* w4, const void* scales,
+                      int scales_f32, int group, int T, int H, int N, int K, void* out, int64_t out_stride_t,
+                      int64_t out_stride_h, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Top-k sparse latent + RoPE attention                                       */
 /* ------------------------------------------------------------------------- */
 /*

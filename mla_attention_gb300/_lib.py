@@ -75,6 +75,17 @@ _SIGNATURES = {
     "mla_rope_append_workspace_size": ([c_int], c_size_t),
     "mla_rope_append": ([c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p, c_int64, c_int,
                          c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_size_t, c_void_p], c_int),
+    "mla_slot_map_workspace_size": ([c_int], c_size_t),
+    "mla_slot_map": ([c_void_p, c_void_p, c_int, c_void_p, c_int, c_int, c_int64, c_void_p, c_void_p, c_int, c_void_p,
+                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p], c_int),
+    "mla_rms_norm": ([c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_float, c_int, c_int, c_void_p, c_int64, c_int,
+                      c_int, c_void_p, c_int64, c_void_p, c_void_p], c_int),
+    "mla_kv_append_workspace_size": ([c_int], c_size_t),
+    "mla_kv_append": ([c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_float, c_void_p, c_int64, c_int64, c_void_p,
+                       c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_float, c_int64, c_int,
+                       c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_size_t, c_void_p], c_int),
+    "mla_bmm_w4": ([c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_void_p,
+                    c_int64, c_int64, c_void_p], c_int),
     "mla_merge_lse": ([c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p],
                       c_int),
 }

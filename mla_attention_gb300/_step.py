@@ -1,0 +1,190 @@
+"""The serving step around the latent attention: ctypes binding of mla_slot_map, mla_rms_norm,
+mla_kv_append and mla_bmm_w4 (argument marshalling only, as in _lib).
+
+These calls run many times a token, so the checks are plain attribute comparisons.  A call is issued
+on `stream` or on the current stream of the tensors' device, whichever device is current.
+"""
+from __future__ import annotations
+
+import torch
+
+from ._lib import MLAError, _check, lib, workspace
+
+_BF16, _I32, _F32, _E4M3, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn, torch.uint8
+
+
+def _tensor(t, name, dtype, dev, shape):
+    """A tensor of this type, device and shape whose last dimension is contiguous (other strides are free)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise MLAError(1, f"{name} must be a torch.Tensor of {dtype}, got {getattr(t, 'dtype', type(t).__name__)}")
+    if t.device != dev:
+        raise MLAError(1, f"{name} is on {t.device}, expected {dev}")
+    if t.shape != shape:
+        raise MLAError(1, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise MLAError(1, f"{name} needs a contiguous last dimension")
+    return t.data_ptr()
+
+
+def _dense(t, name, dtype, dev, shape):
+    p = _tensor(t, name, dtype, dev, shape)
+    if not t.is_contiguous():
+        raise MLAError(1, f"{name} must be contiguous")
+    return p
+
+
+def _device(t, name, dims):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MLAError(1, f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise MLAError(1, f"{name} must have {dims} dimensions, got {t.dim()}")
+    return t.device
+
+
+def _call(fn, dev, stream, *args):
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status:
+        _check(status)
+
+
+def mla_slot_map(lens, new_tokens, block_table, pool, pool_state, page_size: int, N: int, positions=None, slots=None,
+                 cu_tokens=None, lens_out=None, pool_state_out=None, ws=None, stream=None):
+    """Page tables, positions and slots of a step's tokens: lens, new_tokens int32 [B] (negative: tokens
+    dropped), block_table int32 [B,max_pages] and pool int32 [num_pages] in place, pool_state int32 [2]
+    (ring head, free pages).  Rows behind the last token get -1.  lens_out / pool_state_out may be
+    lens / pool_state.  Returns positions [N], slots [N], cu_tokens [B+1], lens_out, pool_state_out."""
+    dev = _device(lens, "lens", 1)
+    B, N = lens.shape[0], int(N)
+    _device(block_table, "block_table", 2)
+    _device(pool, "pool", 1)
+    if N < 0:
+        raise MLAError(1, "N must not be negative")
+    if positions is None:
+        positions = torch.empty(N, dtype=_I32, device=dev)
+    if slots is None:
+        slots = torch.empty(N, dtype=_I32, device=dev)
+    if cu_tokens is None:
+        cu_tokens = torch.empty(B + 1, dtype=_I32, device=dev)
+    if lens_out is None:
+        lens_out = torch.empty(B, dtype=_I32, device=dev)
+    if pool_state_out is None:
+        pool_state_out = torch.empty(2, dtype=_I32, device=dev)
+    ws = workspace(256, dev) if ws is None else ws
+    max_pages, num_pages = block_table.shape[1], pool.shape[0]
+    _call(lib().mla_slot_map, dev, stream, _dense(lens, "lens", _I32, dev, (B,)),
+          _dense(new_tokens, "new_tokens", _I32, dev, (B,)), B,
+          _dense(block_table, "block_table", _I32, dev, (B, max_pages)), max_pages, int(page_size), num_pages,
+          _dense(pool, "pool", _I32, dev, (num_pages,)), _dense(pool_state, "pool_state", _I32, dev, (2,)), N,
+          _dense(cu_tokens, "cu_tokens", _I32, dev, (B + 1,)), _dense(positions, "positions", _I32, dev, (N,)),
+          _dense(slots, "slots", _I32, dev, (N,)), _dense(lens_out, "lens_out", _I32, dev, (B,)),
+          _dense(pool_state_out, "pool_state_out", _I32, dev, (2,)), ws.data_ptr(), ws.numel())
+    return positions, slots, cu_tokens, lens_out, pool_state_out
+
+
+def mla_rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out=None, e4m3: bool = False,
+                 group: int = 0, scales=None, stream=None):
+    """y = h / sqrt(mean(h^2) + eps) * weight with h = x (+ residual); x, residual bf16 [T,D] rows.
+    Returns out, residual_out, scales: out bf16, or e4m3 (e4m3=True or an e4m3 `out`) with fp32 scales
+    [T, D / group] ([T, 1] with group 0); residual_out = h in bf16 (None without a residual; may be
+    the residual itself); scales None with a bf16 out."""
+    dev = _device(x, "x", 2)
+    T, D = x.shape
+    e4m3 = bool(e4m3) if out is None else out.dtype is _E4M3
+    group = int(group)
+    if group and (not e4m3 or group not in (32, 64, 128) or D % group):
+        raise MLAError(1, f"group must be 0, or with e4m3 32, 64 or 128 dividing D (got {group}, D = {D})")
+    if out is None:
+        out = torch.empty((T, D), dtype=_E4M3 if e4m3 else _BF16, device=dev)
+    px = _tensor(x, "x", _BF16, dev, (T, D))
+    pw = _dense(weight, "weight", _BF16, dev, (D,))
+    po = _tensor(out, "out", _E4M3 if e4m3 else _BF16, dev, (T, D))
+    pr = pro = ps = None
+    sr = sro = 0
+    if residual is not None:
+        if residual_out is None:
+            residual_out = torch.empty((T, D), dtype=_BF16, device=dev)
+        pr, pro = _tensor(residual, "residual", _BF16, dev, (T, D)), _tensor(residual_out, "residual_out", _BF16, dev, (T, D))
+        sr, sro = residual.stride(0), residual_out.stride(0)
+    elif residual_out is not None:
+        raise MLAError(1, "residual_out goes with a residual")
+    if e4m3:
+        shape = (T, D // group if group else 1)
+        if scales is None:
+            scales = torch.empty(shape, dtype=_F32, device=dev)
+        ps = _dense(scales, "scales", _F32, dev, shape)
+    elif scales is not None:
+        raise MLAError(1, "scales go with an e4m3 output")
+    _call(lib().mla_rms_norm, dev, stream, px, x.stride(0), pr, sr, pw, float(eps), T, D, pro, sro, int(e4m3), group, po,
+          out.stride(0), ps)
+    return out, residual_out, scales
+
+
+def mla_kv_append(c_kv, k_pe, slots, positions, cos_sin, kv_cache, kv_scale: float = 1.0, norm_weight=None,
+                  eps: float = 1e-6, q_pe=None, q_out=None, kv_out=None, is_neox: bool = False, ws=None, stream=None):
+    """Cache rows by slot: [norm(c_kv) * norm_weight | turned k_pe] of tokens [T] into kv_cache [pages,page,576]
+    (bf16, or e4m3 of row / kv_scale) in place at rows slots[t]; the turned q_pe [T,H,64] into
+    q_out[:, :, 512:576]; kv_out [T,576] (if given) the rows in bf16.  positions[t] = -1: no token;
+    slots[t] = -1: no cache row.  Returns q_out, kv_out."""
+    dev = _device(c_kv, "c_kv", 2)
+    T = c_kv.shape[0]
+    _device(kv_cache, "kv_cache", 3)
+    e4m3 = kv_cache.dtype is _E4M3
+    pages, page = kv_cache.shape[0], kv_cache.shape[1]
+    pc = _tensor(c_kv, "c_kv", _BF16, dev, (T, 512))
+    pk = _tensor(k_pe, "k_pe", _BF16, dev, (T, 64))
+    pcache = _dense(kv_cache, "kv_cache", _E4M3 if e4m3 else _BF16, dev, (pages, page, 576))
+    _device(cos_sin, "cos_sin", 2)
+    max_pos = cos_sin.shape[0]
+    pcs = _dense(cos_sin, "cos_sin", _F32, dev, (max_pos, 64))
+    pw = None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, dev, (512,))
+    pq = pqo = pkv = None
+    H = qt = qh = ot = oh = st = 0
+    if q_pe is not None:
+        _device(q_pe, "q_pe", 3)
+        H = q_pe.shape[1]
+        if H < 1:
+            raise MLAError(1, "q_pe must have at least one head")
+        if q_out is None:
+            q_out = torch.empty((T, H, 576), dtype=_BF16, device=dev)
+        pq, pqo = _tensor(q_pe, "q_pe", _BF16, dev, (T, H, 64)), _tensor(q_out, "q_out", _BF16, dev, (T, H, 576))
+        qt, qh, ot, oh = q_pe.stride(0), q_pe.stride(1), q_out.stride(0), q_out.stride(1)
+    elif q_out is not None:
+        raise MLAError(1, "q_out goes with q_pe")
+    if kv_out is not None:
+        pkv, st = _tensor(kv_out, "kv_out", _BF16, dev, (T, 576)), kv_out.stride(0)
+    ws = workspace(256, dev) if ws is None else ws
+    _call(lib().mla_kv_append, dev, stream, pc, c_kv.stride(0), pk, k_pe.stride(0), pw, float(eps), pq, qt, qh,
+          _dense(positions, "positions", _I32, dev, (T,)), _dense(slots, "slots", _I32, dev, (T,)), pcs, max_pos,
+          int(bool(is_neox)), T, H, pcache, int(e4m3), float(kv_scale), pages, page, pqo, ot, oh, pkv, st,
+          ws.data_ptr(), ws.numel())
+    return q_out, kv_out
+
+
+def mla_bmm_w4(x, w4, scales, out=None, stream=None):
+    """out[t, h, n] = sum_k x[t, h, k] (code[h, n, k] - 8) scales[h, n, k // group]: x bf16 [T,H,K], w4 uint8
+    [H,N,K/2] (byte j of a row: code 2j low, 2j+1 high), scales bf16 or fp32 [H,N,K/group], group 32, 64 or
+    128 -> bf16 [T,H,N] (a strided `out` is fine)."""
+    dev = _device(x, "x", 3)
+    T, H, K = x.shape
+    _device(w4, "w4", 3)
+    _device(scales, "scales", 3)
+    N, groups = w4.shape[1], scales.shape[2]
+    if groups < 1 or K % groups or K // groups not in (32, 64, 128):
+        raise MLAError(1, f"scales must have K / group columns, group 32, 64 or 128 (got {groups}, K = {K})")
+    f32 = scales.dtype is _F32
+    px = _tensor(x, "x", _BF16, dev, (T, H, K))
+    pw = _dense(w4, "w4", _U8, dev, (H, N, K // 2))
+    ps = _dense(scales, "scales", _F32 if f32 else _BF16, dev, (H, N, groups))
+    if out is None:
+        out = torch.empty((T, H, N), dtype=_BF16, device=dev)
+    po = _tensor(out, "out", _BF16, dev, (T, H, N))
+    _call(lib().mla_bmm_w4, dev, stream, px, x.stride(0), x.stride(1), pw, ps, int(f32), K // groups, T, H, N, K, po,
+          out.stride(0), out.stride(1))
+    return out

@@ -42,5 +42,6 @@ __device__ __forceinline__ bool guard_span(uint32_t* err, uint32_t site, const v
 enum : uint32_t {
   G_BLOCK_TABLE = 1, G_LENS, G_TOPK, G_CACHE8, G_Q, G_Q_PE, G_OUT, G_PREV_OUT, G_LSE, G_PREV_LSE, G_TILE_PREFIX,
   G_PART_O, G_PART_LSE, G_C_KV, G_K_PE, G_SINKS, G_MERGE_IN, G_MERGE_OUT, G_ROPE_IN, G_ROPE_OUT, G_POS,
+  G_STEP_IN, G_STEP_OUT,
 };
 }  // namespace mla

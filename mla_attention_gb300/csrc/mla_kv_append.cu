@@ -1,0 +1,179 @@
+// Cache rows by slot: the latent's RMS norm, RoPE and the write of [latent | rotated k_pe] into the
+// paged cache in bf16 or e4m3, and the rotated q_pe into the fused query.
+//
+//   row = [c_kv / sqrt(mean(c_kv^2) + eps) * w | turn(k_pe)]       cache[slot] = bf16(row) or e4m3(row / kv_scale)
+// A pair (a, b) of a RoPE vector turns by its angle: (a cos - b sin, a sin + b cos); pair i is
+// (x[2i], x[2i+1]) or, with is_neox, (x[i], x[i+32]).  Everything is computed in fp32 and rounded once.
+//
+// HBM-bound: per token 1152 bytes in, 576 or 1152 out and 256 per head of q.  One warp per cache row and one
+// per 32 heads of a token's q, all independent: no shared memory, no barrier.  In both pairings a
+// lane's two 16-byte vectors at columns 8u and 32 + 8u (u = 0..3) hold whole pairs, so four lanes
+// serve a RoPE vector, read its angles once and use them for all of the warp's heads.
+#include "mla_step.h"
+#include "row_vec.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kR = 64, kPairs = 32;
+constexpr int kHeadsPerWarp = 32;   // 4 steps of 8 heads, the loads of all steps in flight at once
+constexpr int kSteps = kHeadsPerWarp / 8;
+
+struct Angles {
+  float c[8], s[8];
+};
+
+// the angles of lane u's eight pairs
+__device__ __forceinline__ Angles load_angles(const float* cs, int u, bool neox) {
+  Angles a;
+  const int i0 = neox ? 8 * u : 4 * u, i1 = neox ? 8 * u + 4 : 16 + 4 * u;
+  const float4 c0 = *reinterpret_cast<const float4*>(cs + i0), c1 = *reinterpret_cast<const float4*>(cs + i1);
+  const float4 s0 = *reinterpret_cast<const float4*>(cs + kPairs + i0);
+  const float4 s1 = *reinterpret_cast<const float4*>(cs + kPairs + i1);
+  a.c[0] = c0.x, a.c[1] = c0.y, a.c[2] = c0.z, a.c[3] = c0.w, a.c[4] = c1.x, a.c[5] = c1.y, a.c[6] = c1.z, a.c[7] = c1.w;
+  a.s[0] = s0.x, a.s[1] = s0.y, a.s[2] = s0.z, a.s[3] = s0.w, a.s[4] = s1.x, a.s[5] = s1.y, a.s[6] = s1.z, a.s[7] = s1.w;
+  return a;
+}
+
+// lo: columns 8u .. 8u + 7, hi: columns 32 + 8u ..
+__device__ __forceinline__ void turn(float (&lo)[8], float (&hi)[8], const Angles& g, bool neox) {
+  if (neox) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = lo[i], b = hi[i];
+      lo[i] = a * g.c[i] - b * g.s[i];
+      hi[i] = a * g.s[i] + b * g.c[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a = lo[2 * i], b = lo[2 * i + 1];
+      lo[2 * i] = a * g.c[i] - b * g.s[i];
+      lo[2 * i + 1] = a * g.s[i] + b * g.c[i];
+      a = hi[2 * i], b = hi[2 * i + 1];
+      hi[2 * i] = a * g.c[4 + i] - b * g.s[4 + i];
+      hi[2 * i + 1] = a * g.s[4 + i] + b * g.c[4 + i];
+    }
+  }
+}
+
+// eight values of row `row` of the cache from column `col`
+__device__ __forceinline__ void store_cache8(const KvAppendParams& p, int64_t row, int col, const float (&f)[8]) {
+  const uint64_t ext = (uint64_t)p.cache_rows * kDk * (p.e4m3 ? 1 : 2);
+  if (p.e4m3) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = f[i] / p.kv_scale;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(p.cache) + row * kDk + col;
+    if (guard_span(p.err, G_STEP_OUT, dst, 8, p.cache, ext)) *reinterpret_cast<uint2*>(dst) = e4m3x8_pack(q);
+  } else {
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.cache) + row * kDk + col;
+    if (guard_span(p.err, G_STEP_OUT, dst, 16, p.cache, ext)) *reinterpret_cast<uint4*>(dst) = bf16x8_pack(f);
+  }
+}
+
+__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+  const int lane = threadIdx.x & 31;
+  const int parts = 1 + (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp;   // a token's warps: its row, its heads
+  const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+  const int64_t t = w / parts;
+  const int part = (int)(w - t * parts);
+  if (t >= p.T) return;
+  const bool neox = p.is_neox != 0;
+  const uint64_t ext_t = (uint64_t)p.T * 4;
+  const int pos = guard_span(p.err, G_STEP_IN, p.positions + t, 4, p.positions, ext_t) ? p.positions[t] : -1;
+  if (pos < 0 || pos >= p.max_pos) {
+    if (pos != -1 && part == 0 && lane == 0) record_error(p.err, DEV_RANGE_BASE | 0x78);
+    return;
+  }
+  const float* cs = p.cos_sin + (int64_t)pos * kR;
+  const int u = lane & 3;
+
+  if (part > 0) {  // ---- heads: four lanes a head, eight heads a step ----
+    const Angles g = load_angles(cs, u, neox);
+    const int h0 = (part - 1) * kHeadsPerWarp + (lane >> 2);
+    uint4 lo[kSteps], hi[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int h = h0 + 8 * k;
+      if (h < p.H) {
+        const __nv_bfloat16* src = p.q_pe + t * p.q_pe_stride_t + h * p.q_pe_stride_h + 8 * u;
+        lo[k] = *reinterpret_cast<const uint4*>(src);
+        hi[k] = *reinterpret_cast<const uint4*>(src + 32);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int h = h0 + 8 * k;
+      if (h < p.H) {
+        float a[8], b[8];
+        bf16x8_unpack(lo[k], a);
+        bf16x8_unpack(hi[k], b);
+        turn(a, b, g, neox);
+        __nv_bfloat16* dst = p.q_out + t * p.q_out_stride_t + h * p.q_out_stride_h + kLatent + 8 * u;
+        *reinterpret_cast<uint4*>(dst) = bf16x8_pack(a);
+        *reinterpret_cast<uint4*>(dst + 32) = bf16x8_pack(b);
+      }
+    }
+    return;
+  }
+
+  // ---- the row: lane l holds latent columns 8l .. and 256 + 8l .., lanes 0-3 the RoPE columns ----
+  int64_t slot = guard_span(p.err, G_STEP_IN, p.slots + t, 4, p.slots, ext_t) ? p.slots[t] : -1;
+  if (slot < 0 || slot >= p.cache_rows) {
+    if (slot != -1 && lane == 0) record_error(p.err, DEV_RANGE_BASE | 0x79);
+    slot = -1;
+  }
+  if (slot < 0 && !p.kv_out) return;
+  const __nv_bfloat16* src = p.c_kv + t * p.c_kv_stride;
+  float a[8], b[8];
+  bf16x8_unpack(*reinterpret_cast<const uint4*>(src + 8 * lane), a);
+  bf16x8_unpack(*reinterpret_cast<const uint4*>(src + 256 + 8 * lane), b);
+  if (p.weight) {
+    float wa[8], wb[8], sum = 0.f;
+    bf16x8_unpack(*reinterpret_cast<const uint4*>(p.weight + 8 * lane), wa);
+    bf16x8_unpack(*reinterpret_cast<const uint4*>(p.weight + 256 + 8 * lane), wb);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
+    const float inv = rsqrtf(warp_sum(sum) * (1.f / kLatent) + p.eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] *= inv * wa[i];
+      b[i] *= inv * wb[i];
+    }
+  }
+  if (slot >= 0) {
+    store_cache8(p, slot, 8 * lane, a);
+    store_cache8(p, slot, 256 + 8 * lane, b);
+  }
+  __nv_bfloat16* rows = p.kv_out ? p.kv_out + t * p.kv_out_stride : nullptr;
+  if (rows) {
+    *reinterpret_cast<uint4*>(rows + 8 * lane) = bf16x8_pack(a);
+    *reinterpret_cast<uint4*>(rows + 256 + 8 * lane) = bf16x8_pack(b);
+  }
+  if (lane < 4) {
+    const __nv_bfloat16* pe = p.k_pe + t * p.k_pe_stride + 8 * u;
+    const Angles g = load_angles(cs, u, neox);
+    bf16x8_unpack(*reinterpret_cast<const uint4*>(pe), a);
+    bf16x8_unpack(*reinterpret_cast<const uint4*>(pe + 32), b);
+    turn(a, b, g, neox);
+    if (slot >= 0) {
+      store_cache8(p, slot, kLatent + 8 * u, a);
+      store_cache8(p, slot, kLatent + 32 + 8 * u, b);
+    }
+    if (rows) {
+      *reinterpret_cast<uint4*>(rows + kLatent + 8 * u) = bf16x8_pack(a);
+      *reinterpret_cast<uint4*>(rows + kLatent + 32 + 8 * u) = bf16x8_pack(b);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
+  const int64_t warps = (int64_t)p.T * (1 + (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp);
+  kv_append_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -1,0 +1,68 @@
+// Eight columns of a row at a time: 16-byte loads and stores where the row allows them, single values
+// at its ragged end or where its address does not; bf16 and e4m3 packing.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "sm103_ptx.cuh"
+
+namespace mla {
+
+__device__ __forceinline__ void bf16x8_unpack(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 bf16x8_pack(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+// nearest e4m3, saturating at 448; NaN stays NaN
+__device__ __forceinline__ uint32_t e4m3x4_pack(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+__device__ __forceinline__ uint2 e4m3x8_pack(const float (&f)[8]) {
+  return make_uint2(e4m3x4_pack(f[0], f[1], f[2], f[3]), e4m3x4_pack(f[4], f[5], f[6], f[7]));
+}
+
+// n (1..8) bf16 values at src; the rest are 0.  `wide`: src is 16-byte aligned.
+__device__ __forceinline__ void load_row8(const __nv_bfloat16* src, int n, bool wide, float (&f)[8]) {
+  if (wide && n == 8) {
+    bf16x8_unpack(*reinterpret_cast<const uint4*>(src), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < n ? __bfloat162float(src[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store_row8(__nv_bfloat16* dst, int n, bool wide, const float (&f)[8]) {
+  if (wide && n == 8) {
+    *reinterpret_cast<uint4*>(dst) = bf16x8_pack(f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) dst[i] = __float2bfloat16_rn(f[i]);
+  }
+}
+// as e4m3; `wide`: dst is 8-byte aligned
+__device__ __forceinline__ void store_row8_e4m3(uint8_t* dst, int n, bool wide, const float (&f)[8]) {
+  const uint2 v = e4m3x8_pack(f);
+  if (wide && n == 8) {
+    *reinterpret_cast<uint2*>(dst) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) dst[i] = (uint8_t)((i < 4 ? v.x : v.y) >> (8 * (i & 3)));
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+  return v;
+}
+
+}  // namespace mla
