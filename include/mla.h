@@ -406,7 +406,8 @@ mla_status mla_rms_norm(const void* x, int64_t x_stride, const void* residual, i
  * slots    DEVICE int32 [T]: cache rows (mla_slot_map).  -1: no cache row is written (q_out and
  *          kv_out are); another slot outside [0, num_pages * page_size) is recorded, too.  The slots
  *          of a call's tokens are distinct: of two tokens in one slot either's values may stay.
- * kv_cache bf16 or (cache_e4m3) e4m3 [num_pages, page_size, 576]; kv_scale > 0 with e4m3.
+ * kv_cache bf16 or (cache_e4m3) e4m3 [num_pages, page_size, 576]; with e4m3
+ *          2^-126 <= kv_scale <= 2^126.
  * Tensors are 16-byte aligned, strides multiples of 8 elements.
  */
 size_t mla_kv_append_workspace_size(int T);

@@ -6,7 +6,9 @@
 // (x[2i], x[2i+1]) or, with is_neox, (x[i], x[i+32]).  Everything is computed in fp32 and rounded once.
 //
 // HBM-bound: per token 1152 bytes in, 576 or 1152 out and 256 per head of q.  One warp per cache row and one
-// per 32 heads of a token's q, all independent: no shared memory, no barrier.  In both pairings a
+// per 16 heads of a token's q, all independent: no shared memory, no barrier.  What a warp reads goes out
+// before it looks at its token's position and slot: a chain of three loads would leave most of
+// the bandwidth idle.  In both pairings a
 // lane's two 16-byte vectors at columns 8u and 32 + 8u (u = 0..3) hold whole pairs, so four lanes
 // serve a RoPE vector, read its angles once and use them for all of the warp's heads.
 #include "mla_step.h"
@@ -16,7 +18,7 @@ namespace mla {
 namespace {
 
 constexpr int kR = 64, kPairs = 32;
-constexpr int kHeadsPerWarp = 32;   // 4 steps of 8 heads, the loads of all steps in flight at once
+constexpr int kHeadsPerWarp = 16;   // 2 steps of 8 heads, the loads of both in flight at once
 constexpr int kSteps = kHeadsPerWarp / 8;
 
 struct Angles {
@@ -24,8 +26,10 @@ struct Angles {
 };
 
 // the angles of lane u's eight pairs
-__device__ __forceinline__ Angles load_angles(const float* cs, int u, bool neox) {
-  Angles a;
+__device__ __forceinline__ Angles load_angles(const KvAppendParams& p, int pos, int u, bool neox) {
+  Angles a = {};
+  const float* cs = p.cos_sin + (int64_t)pos * kR;
+  if (!guard_span(p.err, G_STEP_IN, cs, kR * 4, p.cos_sin, (uint64_t)p.max_pos * kR * 4)) return a;
   const int i0 = neox ? 8 * u : 4 * u, i1 = neox ? 8 * u + 4 : 16 + 4 * u;
   const float4 c0 = *reinterpret_cast<const float4*>(cs + i0), c1 = *reinterpret_cast<const float4*>(cs + i1);
   const float4 s0 = *reinterpret_cast<const float4*>(cs + kPairs + i0);
@@ -63,7 +67,7 @@ __device__ __forceinline__ void store_cache8(const KvAppendParams& p, int64_t ro
   if (p.e4m3) {
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = f[i] / p.kv_scale;
+    for (int i = 0; i < 8; ++i) q[i] = f[i] * p.inv_kv_scale;
     uint8_t* dst = reinterpret_cast<uint8_t*>(p.cache) + row * kDk + col;
     if (guard_span(p.err, G_STEP_OUT, dst, 8, p.cache, ext)) *reinterpret_cast<uint2*>(dst) = e4m3x8_pack(q);
   } else {
@@ -72,25 +76,33 @@ __device__ __forceinline__ void store_cache8(const KvAppendParams& p, int64_t ro
   }
 }
 
+__device__ __forceinline__ uint4 load16(const KvAppendParams& p, const __nv_bfloat16* src, const __nv_bfloat16* base, int64_t extent) {
+  return guard_span(p.err, G_STEP_IN, src, 16, base, (uint64_t)extent * 2) ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void store16(const KvAppendParams& p, __nv_bfloat16* dst, const __nv_bfloat16* base, int64_t extent, const float (&f)[8]) {
+  if (guard_span(p.err, G_STEP_OUT, dst, 16, base, (uint64_t)extent * 2)) *reinterpret_cast<uint4*>(dst) = bf16x8_pack(f);
+}
+
 __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   const int lane = threadIdx.x & 31;
   const int parts = 1 + (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp;   // a token's warps: its row, its heads
-  const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-  const int64_t t = w / parts;
-  const int part = (int)(w - t * parts);
+  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);            // T * parts is below 2^31
+  const int t = w / parts, part = w - t * parts;
   if (t >= p.T) return;
   const bool neox = p.is_neox != 0;
-  const uint64_t ext_t = (uint64_t)p.T * 4;
-  const int pos = guard_span(p.err, G_STEP_IN, p.positions + t, 4, p.positions, ext_t) ? p.positions[t] : -1;
-  if (pos < 0 || pos >= p.max_pos) {
-    if (pos != -1 && part == 0 && lane == 0) record_error(p.err, DEV_RANGE_BASE | 0x78);
-    return;
-  }
-  const float* cs = p.cos_sin + (int64_t)pos * kR;
   const int u = lane & 3;
+  const uint64_t ext_t = (uint64_t)p.T * 4;
+  auto token_int = [&](const int32_t* base) { return guard_span(p.err, G_STEP_IN, base + t, 4, base, ext_t) ? base[t] : -1; };
+  const int pos = token_int(p.positions);
+  auto valid = [&] {
+    if (pos >= 0 && pos < p.max_pos) return true;
+    if (pos != -1 && part == 0 && lane == 0) record_error(p.err, DEV_RANGE_BASE | 0x78);
+    return false;
+  };
 
   if (part > 0) {  // ---- heads: four lanes a head, eight heads a step ----
-    const Angles g = load_angles(cs, u, neox);
+    const int64_t ext_q = (p.T - 1) * p.q_pe_stride_t + (p.H - 1) * p.q_pe_stride_h + kR;
+    const int64_t ext_o = (p.T - 1) * p.q_out_stride_t + (p.H - 1) * p.q_out_stride_h + kDk;
     const int h0 = (part - 1) * kHeadsPerWarp + (lane >> 2);
     uint4 lo[kSteps], hi[kSteps];
 #pragma unroll
@@ -98,10 +110,12 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
       const int h = h0 + 8 * k;
       if (h < p.H) {
         const __nv_bfloat16* src = p.q_pe + t * p.q_pe_stride_t + h * p.q_pe_stride_h + 8 * u;
-        lo[k] = *reinterpret_cast<const uint4*>(src);
-        hi[k] = *reinterpret_cast<const uint4*>(src + 32);
+        lo[k] = load16(p, src, p.q_pe, ext_q);
+        hi[k] = load16(p, src + 32, p.q_pe, ext_q);
       }
     }
+    if (!valid()) return;
+    const Angles g = load_angles(p, pos, u, neox);
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       const int h = h0 + 8 * k;
@@ -111,59 +125,71 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
         bf16x8_unpack(hi[k], b);
         turn(a, b, g, neox);
         __nv_bfloat16* dst = p.q_out + t * p.q_out_stride_t + h * p.q_out_stride_h + kLatent + 8 * u;
-        *reinterpret_cast<uint4*>(dst) = bf16x8_pack(a);
-        *reinterpret_cast<uint4*>(dst + 32) = bf16x8_pack(b);
+        store16(p, dst, p.q_out, ext_o, a);
+        store16(p, dst + 32, p.q_out, ext_o, b);
       }
     }
     return;
   }
 
   // ---- the row: lane l holds latent columns 8l .. and 256 + 8l .., lanes 0-3 the RoPE columns ----
-  int64_t slot = guard_span(p.err, G_STEP_IN, p.slots + t, 4, p.slots, ext_t) ? p.slots[t] : -1;
+  int64_t slot = token_int(p.slots);
+  const int64_t ext_c = (p.T - 1) * p.c_kv_stride + kLatent, ext_k = (p.T - 1) * p.k_pe_stride + kR;
+  const __nv_bfloat16* src = p.c_kv + t * p.c_kv_stride + 8 * lane;
+  const uint4 va = load16(p, src, p.c_kv, ext_c), vb = load16(p, src + 256, p.c_kv, ext_c);
+  uint4 ka, kb, wa, wb;
+  if (lane < 4) {
+    const __nv_bfloat16* pe = p.k_pe + t * p.k_pe_stride + 8 * u;
+    ka = load16(p, pe, p.k_pe, ext_k);
+    kb = load16(p, pe + 32, p.k_pe, ext_k);
+  }
+  if (p.weight) {
+    wa = load16(p, p.weight + 8 * lane, p.weight, kLatent);
+    wb = load16(p, p.weight + 256 + 8 * lane, p.weight, kLatent);
+  }
+  if (!valid()) return;
   if (slot < 0 || slot >= p.cache_rows) {
     if (slot != -1 && lane == 0) record_error(p.err, DEV_RANGE_BASE | 0x79);
     slot = -1;
   }
-  if (slot < 0 && !p.kv_out) return;
-  const __nv_bfloat16* src = p.c_kv + t * p.c_kv_stride;
+  __nv_bfloat16* rows = p.kv_out ? p.kv_out + t * p.kv_out_stride : nullptr;
+  const int64_t ext_r = (p.T - 1) * p.kv_out_stride + kDk;
+  if (slot < 0 && !rows) return;
   float a[8], b[8];
-  bf16x8_unpack(*reinterpret_cast<const uint4*>(src + 8 * lane), a);
-  bf16x8_unpack(*reinterpret_cast<const uint4*>(src + 256 + 8 * lane), b);
+  bf16x8_unpack(va, a);
+  bf16x8_unpack(vb, b);
   if (p.weight) {
-    float wa[8], wb[8], sum = 0.f;
-    bf16x8_unpack(*reinterpret_cast<const uint4*>(p.weight + 8 * lane), wa);
-    bf16x8_unpack(*reinterpret_cast<const uint4*>(p.weight + 256 + 8 * lane), wb);
+    float f[8], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
     const float inv = rsqrtf(warp_sum(sum) * (1.f / kLatent) + p.eps);
+    bf16x8_unpack(wa, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      a[i] *= inv * wa[i];
-      b[i] *= inv * wb[i];
-    }
+    for (int i = 0; i < 8; ++i) a[i] *= inv * f[i];
+    bf16x8_unpack(wb, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] *= inv * f[i];
   }
   if (slot >= 0) {
     store_cache8(p, slot, 8 * lane, a);
     store_cache8(p, slot, 256 + 8 * lane, b);
   }
-  __nv_bfloat16* rows = p.kv_out ? p.kv_out + t * p.kv_out_stride : nullptr;
   if (rows) {
-    *reinterpret_cast<uint4*>(rows + 8 * lane) = bf16x8_pack(a);
-    *reinterpret_cast<uint4*>(rows + 256 + 8 * lane) = bf16x8_pack(b);
+    store16(p, rows + 8 * lane, p.kv_out, ext_r, a);
+    store16(p, rows + 256 + 8 * lane, p.kv_out, ext_r, b);
   }
   if (lane < 4) {
-    const __nv_bfloat16* pe = p.k_pe + t * p.k_pe_stride + 8 * u;
-    const Angles g = load_angles(cs, u, neox);
-    bf16x8_unpack(*reinterpret_cast<const uint4*>(pe), a);
-    bf16x8_unpack(*reinterpret_cast<const uint4*>(pe + 32), b);
+    const Angles g = load_angles(p, pos, u, neox);
+    bf16x8_unpack(ka, a);
+    bf16x8_unpack(kb, b);
     turn(a, b, g, neox);
     if (slot >= 0) {
       store_cache8(p, slot, kLatent + 8 * u, a);
       store_cache8(p, slot, kLatent + 32 + 8 * u, b);
     }
     if (rows) {
-      *reinterpret_cast<uint4*>(rows + kLatent + 8 * u) = bf16x8_pack(a);
-      *reinterpret_cast<uint4*>(rows + kLatent + 32 + 8 * u) = bf16x8_pack(b);
+      store16(p, rows + kLatent + 8 * u, p.kv_out, ext_r, a);
+      store16(p, rows + kLatent + 32 + 8 * u, p.kv_out, ext_r, b);
     }
   }
 }

@@ -142,9 +142,10 @@ mla_status mla_kv_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe
   MLA_REQUIRE(num_pages <= INT32_MAX / page_size, "mla_kv_append: num_pages * page_size must be below 2^31");
   MLA_REQUIRE((is_neox == 0 || is_neox == 1) && (cache_e4m3 == 0 || cache_e4m3 == 1),
               "mla_kv_append: is_neox and cache_e4m3 must be 0 or 1");
-  MLA_REQUIRE(!cache_e4m3 || (std::isfinite(kv_scale) && kv_scale > 0.f), "mla_kv_append: kv_scale must be positive");
+  MLA_REQUIRE(!cache_e4m3 || (kv_scale >= 0x1p-126f && kv_scale <= 0x1p126f),
+              "mla_kv_append: kv_scale must be positive and normal, as must its reciprocal");
   MLA_REQUIRE(!norm_weight || (std::isfinite(eps) && eps >= 0.f), "mla_kv_append: eps must be finite and not negative");
-  MLA_REQUIRE((int64_t)T * (1 + (H + 31) / 32) <= (int64_t)INT32_MAX, "mla_kv_append: too many (token, head) rows");
+  MLA_REQUIRE((int64_t)T * (1 + ((int64_t)H + 15) / 16) <= (int64_t)INT32_MAX - 8, "mla_kv_append: too many (token, head) rows");
   if (!workspace || workspace_bytes < mla_kv_append_workspace_size(T))
     return fail(MLA_ERR_WORKSPACE, "mla_kv_append: workspace must hold %zu bytes", mla_kv_append_workspace_size(T));
   if (T == 0) return finish(cudaSuccess, "");
@@ -186,7 +187,7 @@ mla_status mla_kv_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe
   p.kv_out_stride = kv_out_stride;
   p.cache_rows = num_pages * page_size;
   p.eps = eps;
-  p.kv_scale = kv_scale;
+  p.inv_kv_scale = 1.f / kv_scale;
   p.T = T;
   p.H = H;
   p.max_pos = max_pos;

@@ -29,14 +29,13 @@ __device__ __forceinline__ uint2 e4m3x8_pack(const float (&f)[8]) {
   return make_uint2(e4m3x4_pack(f[0], f[1], f[2], f[3]), e4m3x4_pack(f[4], f[5], f[6], f[7]));
 }
 
-// n (1..8) bf16 values at src; the rest are 0.  `wide`: src is 16-byte aligned.
-__device__ __forceinline__ void load_row8(const __nv_bfloat16* src, int n, bool wide, float (&f)[8]) {
-  if (wide && n == 8) {
-    bf16x8_unpack(*reinterpret_cast<const uint4*>(src), f);
-  } else {
+// n (1..8) bf16 values at src one by one; the rest are 0
+__device__ __forceinline__ uint4 load_row8_narrow(const __nv_bfloat16* src, int n) {
+  const uint16_t* b = reinterpret_cast<const uint16_t*>(src);
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < n ? __bfloat162float(src[i]) : 0.f;
-  }
+  for (int i = 0; i < 4; ++i) w[i] = (2 * i < n ? b[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)b[2 * i + 1] << 16 : 0u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void store_row8(__nv_bfloat16* dst, int n, bool wide, const float (&f)[8]) {
   if (wide && n == 8) {

@@ -474,6 +474,30 @@ def test_w4_infinity_stays_in_its_token():
     assert bad[3, 0].all() and bad[7, 1].all() and bad.sum() == 128
 
 
+@pytest.mark.parametrize("T", [1, 9, 33])
+def test_w4_large_and_small_values(T):
+    """Rows of x far from one: sums beyond any scaling of the products are exact to the same bound, infinities keep
+    their sign, NaN stays in its row."""
+    g = torch.Generator().manual_seed(42 + T)
+    H, N, K = 2, 40, 256
+    w4, scales = _w4(H, N, K, 64, T == 9, g)
+    w4 |= 0x11                                                # no code 8: every weight is nonzero
+    x = gen.randn_bf16((T, H, K), g)
+    x[0] *= 2.0 ** 100
+    x[T // 2, 1] *= 2.0 ** -40
+    x[T - 1, 0, 5] = 2.0 ** 120
+    if T > 8:
+        x[3, 0, 7], x[5, 1, 9], x[6, 1, 2] = float("inf"), -float("inf"), float("nan")
+    out = mla_bmm_w4(x.to(dev()), w4, scales)
+    with np.errstate(invalid="ignore"):
+        ref, mass = so.bmm_w4(to_np(x), w4.cpu().numpy(), to_np(scales))
+    finite = np.isfinite(ref)
+    o = to_np(out)
+    assert (np.isnan(o) == np.isnan(ref)).all() and (o[np.isinf(ref)] == ref[np.isinf(ref)]).all()
+    err = np.abs(np.where(finite, o - np.where(finite, ref, 0), 0))
+    assert (err <= np.where(finite, np.abs(np.where(finite, ref, 0)) * (BF16 + ARITH) + np.where(finite, mass, 0) * K * 2.0 ** -24, 0)).all()
+
+
 # ---------------------------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------------------------
