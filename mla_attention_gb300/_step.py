@@ -1,55 +1,96 @@
 """The serving step around the latent attention: ctypes binding of mla_slot_map, mla_rms_norm,
 mla_kv_append and mla_bmm_w4 (argument marshalling only, as in _lib).
 
-These calls run many times a token, so the checks are plain attribute comparisons.  A call is issued
-on `stream` or on the current stream of the tensors' device, whichever device is current.
+A decode step makes hundreds of these calls, most of them a few microseconds long on the GPU, so the
+host's part is kept short: one expression checks a tensor, and only a tensor that fails it is looked at
+for what is wrong.  A call is issued on `stream` or on the current stream of the tensors' device,
+whichever device is current.
 """
 from __future__ import annotations
 
 import torch
 
-from ._lib import MLAError, _check, lib, workspace
+from . import _lib
+from ._lib import MLAError, _check, workspace
 
 _BF16, _I32, _F32, _E4M3, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn, torch.uint8
+_current_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: torch.cuda.current_stream() builds a Stream, 2 us
 
 
-def _tensor(t, name, dtype, dev, shape):
-    """A tensor of this type, device and shape whose last dimension is contiguous (other strides are free)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
-        raise MLAError(1, f"{name} must be a torch.Tensor of {dtype}, got {getattr(t, 'dtype', type(t).__name__)}")
-    if t.device != dev:
-        raise MLAError(1, f"{name} is on {t.device}, expected {dev}")
-    if t.shape != shape:
-        raise MLAError(1, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+def _dense(t, name, dtype, dev, shape):
+    """The address of a contiguous tensor of this type, device and shape."""
+    try:
+        if t.dtype is dtype and t.is_contiguous() and t.get_device() == dev and t.shape == shape:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, dev, shape)
+    raise MLAError(1, f"{name} must be contiguous")
+
+
+def _rows(t, name, dtype, dev, shape):
+    """The same with free strides but for a contiguous last dimension."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and (t.is_contiguous() or t.stride(-1) == 1):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, dev, shape)
+    if shape[-1] > 1:
         raise MLAError(1, f"{name} needs a contiguous last dimension")
     return t.data_ptr()
 
 
-def _dense(t, name, dtype, dev, shape):
-    p = _tensor(t, name, dtype, dev, shape)
-    if not t.is_contiguous():
-        raise MLAError(1, f"{name} must be contiguous")
-    return p
+def _refuse(t, name, dtype, dev, shape):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise MLAError(1, f"{name} must be a torch.Tensor of {dtype}, got {getattr(t, 'dtype', type(t).__name__)}")
+    if t.get_device() != dev:
+        raise MLAError(1, f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.shape != shape:
+        raise MLAError(1, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _device(t, name, dims):
+    """The index of the GPU that holds t."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MLAError(1, f"{name} must be a CUDA tensor")
     if t.dim() != dims:
         raise MLAError(1, f"{name} must have {dims} dimensions, got {t.dim()}")
-    return t.device
+    return t.get_device()
 
 
-def _call(fn, dev, stream, *args):
+def _empty(shape, dtype, dev):
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+
+
+def _workspace(ws, dev):
+    """Address and size of the status word's buffer: the caller's, or the one of this device."""
+    if ws is None:
+        ws = _lib._ws_cache.get(("cuda", dev))
+        if ws is None:
+            ws = workspace(256, torch.device("cuda", dev))
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+        raise MLAError(1, f"ws must be a contiguous tensor on cuda:{dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+_several_devices = None
+
+
+def _call(name, dev, stream, *args):
+    global _several_devices
+    fn = getattr(_lib._lib or _lib.lib(), name)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, s)
-    else:
+        stream = _current_stream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if _several_devices is None:
+        _several_devices = torch.cuda.device_count() > 1
+    if _several_devices and dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            status = fn(*args, s)
+            status = fn(*args, stream)
+    else:
+        status = fn(*args, stream)
     if status:
         _check(status)
 
@@ -67,24 +108,23 @@ def mla_slot_map(lens, new_tokens, block_table, pool, pool_state, page_size: int
     if N < 0:
         raise MLAError(1, "N must not be negative")
     if positions is None:
-        positions = torch.empty(N, dtype=_I32, device=dev)
+        positions = _empty(N, _I32, dev)
     if slots is None:
-        slots = torch.empty(N, dtype=_I32, device=dev)
+        slots = _empty(N, _I32, dev)
     if cu_tokens is None:
-        cu_tokens = torch.empty(B + 1, dtype=_I32, device=dev)
+        cu_tokens = _empty(B + 1, _I32, dev)
     if lens_out is None:
-        lens_out = torch.empty(B, dtype=_I32, device=dev)
+        lens_out = _empty(B, _I32, dev)
     if pool_state_out is None:
-        pool_state_out = torch.empty(2, dtype=_I32, device=dev)
-    ws = workspace(256, dev) if ws is None else ws
+        pool_state_out = _empty(2, _I32, dev)
     max_pages, num_pages = block_table.shape[1], pool.shape[0]
-    _call(lib().mla_slot_map, dev, stream, _dense(lens, "lens", _I32, dev, (B,)),
+    _call("mla_slot_map", dev, stream, _dense(lens, "lens", _I32, dev, (B,)),
           _dense(new_tokens, "new_tokens", _I32, dev, (B,)), B,
           _dense(block_table, "block_table", _I32, dev, (B, max_pages)), max_pages, int(page_size), num_pages,
           _dense(pool, "pool", _I32, dev, (num_pages,)), _dense(pool_state, "pool_state", _I32, dev, (2,)), N,
           _dense(cu_tokens, "cu_tokens", _I32, dev, (B + 1,)), _dense(positions, "positions", _I32, dev, (N,)),
           _dense(slots, "slots", _I32, dev, (N,)), _dense(lens_out, "lens_out", _I32, dev, (B,)),
-          _dense(pool_state_out, "pool_state_out", _I32, dev, (2,)), ws.data_ptr(), ws.numel())
+          _dense(pool_state_out, "pool_state_out", _I32, dev, (2,)), *_workspace(ws, dev))
     return positions, slots, cu_tokens, lens_out, pool_state_out
 
 
@@ -96,32 +136,32 @@ def mla_rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None,
     the residual itself); scales None with a bf16 out."""
     dev = _device(x, "x", 2)
     T, D = x.shape
-    e4m3 = bool(e4m3) if out is None else out.dtype is _E4M3
+    e4m3 = bool(e4m3) if out is None else getattr(out, "dtype", None) is _E4M3
     group = int(group)
     if group and (not e4m3 or group not in (32, 64, 128) or D % group):
         raise MLAError(1, f"group must be 0, or with e4m3 32, 64 or 128 dividing D (got {group}, D = {D})")
     if out is None:
-        out = torch.empty((T, D), dtype=_E4M3 if e4m3 else _BF16, device=dev)
-    px = _tensor(x, "x", _BF16, dev, (T, D))
+        out = _empty((T, D), _E4M3 if e4m3 else _BF16, dev)
+    px = _rows(x, "x", _BF16, dev, (T, D))
     pw = _dense(weight, "weight", _BF16, dev, (D,))
-    po = _tensor(out, "out", _E4M3 if e4m3 else _BF16, dev, (T, D))
+    po = _rows(out, "out", _E4M3 if e4m3 else _BF16, dev, (T, D))
     pr = pro = ps = None
     sr = sro = 0
     if residual is not None:
         if residual_out is None:
-            residual_out = torch.empty((T, D), dtype=_BF16, device=dev)
-        pr, pro = _tensor(residual, "residual", _BF16, dev, (T, D)), _tensor(residual_out, "residual_out", _BF16, dev, (T, D))
+            residual_out = _empty((T, D), _BF16, dev)
+        pr, pro = _rows(residual, "residual", _BF16, dev, (T, D)), _rows(residual_out, "residual_out", _BF16, dev, (T, D))
         sr, sro = residual.stride(0), residual_out.stride(0)
     elif residual_out is not None:
         raise MLAError(1, "residual_out goes with a residual")
     if e4m3:
         shape = (T, D // group if group else 1)
         if scales is None:
-            scales = torch.empty(shape, dtype=_F32, device=dev)
+            scales = _empty(shape, _F32, dev)
         ps = _dense(scales, "scales", _F32, dev, shape)
     elif scales is not None:
         raise MLAError(1, "scales go with an e4m3 output")
-    _call(lib().mla_rms_norm, dev, stream, px, x.stride(0), pr, sr, pw, float(eps), T, D, pro, sro, int(e4m3), group, po,
+    _call("mla_rms_norm", dev, stream, px, x.stride(0), pr, sr, pw, float(eps), T, D, pro, sro, int(e4m3), group, po,
           out.stride(0), ps)
     return out, residual_out, scales
 
@@ -137,8 +177,8 @@ def mla_kv_append(c_kv, k_pe, slots, positions, cos_sin, kv_cache, kv_scale: flo
     _device(kv_cache, "kv_cache", 3)
     e4m3 = kv_cache.dtype is _E4M3
     pages, page = kv_cache.shape[0], kv_cache.shape[1]
-    pc = _tensor(c_kv, "c_kv", _BF16, dev, (T, 512))
-    pk = _tensor(k_pe, "k_pe", _BF16, dev, (T, 64))
+    pc = _rows(c_kv, "c_kv", _BF16, dev, (T, 512))
+    pk = _rows(k_pe, "k_pe", _BF16, dev, (T, 64))
     pcache = _dense(kv_cache, "kv_cache", _E4M3 if e4m3 else _BF16, dev, (pages, page, 576))
     _device(cos_sin, "cos_sin", 2)
     max_pos = cos_sin.shape[0]
@@ -152,18 +192,17 @@ def mla_kv_append(c_kv, k_pe, slots, positions, cos_sin, kv_cache, kv_scale: flo
         if H < 1:
             raise MLAError(1, "q_pe must have at least one head")
         if q_out is None:
-            q_out = torch.empty((T, H, 576), dtype=_BF16, device=dev)
-        pq, pqo = _tensor(q_pe, "q_pe", _BF16, dev, (T, H, 64)), _tensor(q_out, "q_out", _BF16, dev, (T, H, 576))
+            q_out = _empty((T, H, 576), _BF16, dev)
+        pq, pqo = _rows(q_pe, "q_pe", _BF16, dev, (T, H, 64)), _rows(q_out, "q_out", _BF16, dev, (T, H, 576))
         qt, qh, ot, oh = q_pe.stride(0), q_pe.stride(1), q_out.stride(0), q_out.stride(1)
     elif q_out is not None:
         raise MLAError(1, "q_out goes with q_pe")
     if kv_out is not None:
-        pkv, st = _tensor(kv_out, "kv_out", _BF16, dev, (T, 576)), kv_out.stride(0)
-    ws = workspace(256, dev) if ws is None else ws
-    _call(lib().mla_kv_append, dev, stream, pc, c_kv.stride(0), pk, k_pe.stride(0), pw, float(eps), pq, qt, qh,
+        pkv, st = _rows(kv_out, "kv_out", _BF16, dev, (T, 576)), kv_out.stride(0)
+    _call("mla_kv_append", dev, stream, pc, c_kv.stride(0), pk, k_pe.stride(0), pw, float(eps), pq, qt, qh,
           _dense(positions, "positions", _I32, dev, (T,)), _dense(slots, "slots", _I32, dev, (T,)), pcs, max_pos,
           int(bool(is_neox)), T, H, pcache, int(e4m3), float(kv_scale), pages, page, pqo, ot, oh, pkv, st,
-          ws.data_ptr(), ws.numel())
+          *_workspace(ws, dev))
     return q_out, kv_out
 
 
@@ -179,12 +218,12 @@ def mla_bmm_w4(x, w4, scales, out=None, stream=None):
     if groups < 1 or K % groups or K // groups not in (32, 64, 128):
         raise MLAError(1, f"scales must have K / group columns, group 32, 64 or 128 (got {groups}, K = {K})")
     f32 = scales.dtype is _F32
-    px = _tensor(x, "x", _BF16, dev, (T, H, K))
+    px = _rows(x, "x", _BF16, dev, (T, H, K))
     pw = _dense(w4, "w4", _U8, dev, (H, N, K // 2))
     ps = _dense(scales, "scales", _F32 if f32 else _BF16, dev, (H, N, groups))
     if out is None:
-        out = torch.empty((T, H, N), dtype=_BF16, device=dev)
-    po = _tensor(out, "out", _BF16, dev, (T, H, N))
-    _call(lib().mla_bmm_w4, dev, stream, px, x.stride(0), x.stride(1), pw, ps, int(f32), K // groups, T, H, N, K, po,
+        out = _empty((T, H, N), _BF16, dev)
+    po = _rows(out, "out", _BF16, dev, (T, H, N))
+    _call("mla_bmm_w4", dev, stream, px, x.stride(0), x.stride(1), pw, ps, int(f32), K // groups, T, H, N, K, po,
           out.stride(0), out.stride(1))
     return out

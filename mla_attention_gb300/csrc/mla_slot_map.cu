@@ -11,8 +11,10 @@
 // The call is a few KB to a few hundred KB of integers, so what bounds it is the latency of one
 // launch and of one scan.  One cluster does all of it: every CTA scans the lengths (a chunk of
 // kThreads requests at a time, 64-bit sums), and the tokens and the moved pages of the chunk are
-// dealt over all threads of the cluster, each finding its request by bisection in shared memory,
-// so that one long prompt among many single tokens costs no more than the same tokens spread evenly.
+// dealt over all threads of the cluster, so that one long prompt among many single tokens costs no
+// more than the same tokens spread evenly.  A thread takes four tokens in a row: it finds the first
+// one's request by bisection in shared memory and walks on from there, and looks a page up where the
+// position enters it.
 // lens_out and pool_state_out may be the buffers that are read: the cluster's barrier stands between
 // the last read and the first write.
 #include "mla_step.h"
@@ -21,8 +23,6 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 
 struct Sums {
   long long tok, pop, put;
@@ -34,8 +34,9 @@ __device__ __forceinline__ Sums shfl_up(const Sums& a, int d) {
   return {__shfl_up_sync(~0u, a.tok, d), __shfl_up_sync(~0u, a.pop, d), __shfl_up_sync(~0u, a.put, d)};
 }
 
+template <int kThreads>
 struct Shared {
-  Sums warp[kWarps];
+  Sums warp[32];
   long long total[3];
   // per request of the chunk: first token / popped / returned page, relative to the chunk's first
   int tok[kThreads + 1], pop[kThreads + 1], put[kThreads + 1];
@@ -55,8 +56,10 @@ __device__ __forceinline__ int owner(const int* first, int n, int v) {
   return lo;
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constant__ SlotMapParams p) {
-  __shared__ Shared s;
+  constexpr int kWarps = kThreads / 32;
+  __shared__ Shared<kThreads> s;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = blockIdx.x, step = gridDim.x * kThreads, mine = rank * kThreads + tid;
   const int64_t P = p.num_pages;
@@ -76,6 +79,7 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
     if (rank == 0 && tid == 0) record_error(p.err, DEV_RANGE_BASE | 0x74);
   }
   auto ring = [&](int64_t i) { return i >= P ? i - P : i; };  // i < 2 P
+  const bool vec = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
   if (tid == 0) s.popped = s.returned = 0;
   Sums carry = {0, 0, 0};
 
@@ -103,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
     if (lane == 31) s.warp[wid] = v;
     __syncthreads();
     if (wid == 0) {
-      Sums w = s.warp[lane];
+      Sums w = lane < kWarps ? s.warp[lane] : Sums{0, 0, 0};
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const Sums u = shfl_up(w, d);
@@ -164,20 +168,45 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
       store(p.pool, ring(ring(head + count) + put0 + j), P, good ? pg : -1);
     }
     // ---- tokens ----
-    for (int j = mine; j < ntok; j += step) {
-      const int r = owner(s.tok, nb, j);
-      int pos = -1, slot = -1;
-      if (s.ok[r]) {
-        pos = s.len[r] + (j - s.tok[r]);
-        const int e = pos / p.page_size;
-        const int32_t pg = e < s.have[r]
-                               ? load(p.block_table, (b0 + r) * p.max_pages + e, (int64_t)(ext_table / 4))
-                               : load(p.pool, ring(head + pop0 + s.pop[r] + (e - s.have[r])), P);
-        if (pg >= 0 && pg < P) slot = pg * p.page_size + pos % p.page_size;
-        else record_error(p.err, DEV_RANGE_BASE | 0x75);
+    for (int j0 = 4 * mine; j0 < ntok; j0 += 4 * step) {
+      int r = owner(s.tok, nb, j0), e = -1, left = 0;   // left: tokens until the next page
+      int32_t row = -1;                                 // the page's first slot, or -1
+      int pos[4], slot[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i;
+        pos[i] = slot[i] = -1;
+        if (j >= ntok) continue;
+        while (r + 1 < nb && s.tok[r + 1] <= j) ++r, e = -1;
+        if (!s.ok[r]) continue;
+        const int in = j - s.tok[r];
+        pos[i] = s.len[r] + in;
+        if (e < 0 || left == 0) {   // another page: of those held, or of those just taken
+          e = pos[i] / p.page_size;
+          left = (e + 1) * p.page_size - pos[i];
+          const int32_t pg = e < s.have[r]
+                                 ? load(p.block_table, (b0 + r) * p.max_pages + e, (int64_t)(ext_table / 4))
+                                 : load(p.pool, ring(head + pop0 + s.pop[r] + (e - s.have[r])), P);
+          row = pg >= 0 && pg < P ? pg * p.page_size : -1;
+          if (row < 0) record_error(p.err, DEV_RANGE_BASE | 0x75);
+        }
+        if (row >= 0) slot[i] = row + p.page_size - left;
+        --left;
       }
-      store(p.positions, tok0 + j, p.N, pos);
-      store(p.slots, tok0 + j, p.N, slot);
+      const int64_t at = tok0 + j0;
+      if (vec && j0 + 4 <= ntok && (at & 3) == 0) {
+        if (guard_span(p.err, G_STEP_OUT, p.positions + at, 16, p.positions, (uint64_t)p.N * 4))
+          *reinterpret_cast<int4*>(p.positions + at) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        if (guard_span(p.err, G_STEP_OUT, p.slots + at, 16, p.slots, (uint64_t)p.N * 4))
+          *reinterpret_cast<int4*>(p.slots + at) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j0 + i < ntok) {
+            store(p.positions, at + i, p.N, pos[i]);
+            store(p.slots, at + i, p.N, slot[i]);
+          }
+      }
     }
     carry = add(carry, chunk);
     __syncthreads();  // the chunk's tables are read
@@ -196,14 +225,10 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
   }
 }
 
-}  // namespace
-
-cudaError_t launch_slot_map(const SlotMapParams& p, cudaStream_t stream) {
-  // One CTA while its own threads cover the tokens a few times over; eight (the portable cluster
-  // size) beyond that.
+template <int kThreads>
+cudaError_t launch(const SlotMapParams& p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  const int ctas = (int64_t)p.N + p.B <= 4 * kThreads ? 1 : 8;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -211,8 +236,17 @@ cudaError_t launch_slot_map(const SlotMapParams& p, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, slot_map_kernel, p);
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, slot_map_kernel<kThreads>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_slot_map(const SlotMapParams& p, cudaStream_t stream) {
+  // A decode batch fits one small CTA, whose scan and barriers are the shorter ones; a larger one gets
+  // a full CTA, and eight (the portable cluster size) where those have four tokens a thread.
+  if (p.B <= 128 && p.N <= 512) return launch<128>(p, 1, stream);
+  return launch<1024>(p, p.N + (int64_t)p.B <= 4096 ? 1 : 8, stream);
 }
 
 }  // namespace mla
