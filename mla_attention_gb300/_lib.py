@@ -85,7 +85,7 @@ _SIGNATURES = {
                        c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_float, c_int64, c_int,
                        c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_size_t, c_void_p], c_int),
     "mla_bmm_w4": ([c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_void_p,
-                    c_int64, c_int64, c_void_p], c_int),
+                    c_int64, c_int64, c_void_p, c_size_t, c_void_p], c_int),
     "mla_merge_lse": ([c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p],
                       c_int),
 }

@@ -206,7 +206,7 @@ def mla_kv_append(c_kv, k_pe, slots, positions, cos_sin, kv_cache, kv_scale: flo
     return q_out, kv_out
 
 
-def mla_bmm_w4(x, w4, scales, out=None, stream=None):
+def mla_bmm_w4(x, w4, scales, out=None, ws=None, stream=None):
     """out[t, h, n] = sum_k x[t, h, k] (code[h, n, k] - 8) scales[h, n, k // group]: x bf16 [T,H,K], w4 uint8
     [H,N,K/2] (byte j of a row: code 2j low, 2j+1 high), scales bf16 or fp32 [H,N,K/group], group 32, 64 or
     128 -> bf16 [T,H,N] (a strided `out` is fine)."""
@@ -225,5 +225,5 @@ def mla_bmm_w4(x, w4, scales, out=None, stream=None):
         out = _empty((T, H, N), _BF16, dev)
     po = _rows(out, "out", _BF16, dev, (T, H, N))
     _call("mla_bmm_w4", dev, stream, px, x.stride(0), x.stride(1), pw, ps, int(f32), K // groups, T, H, N, K, po,
-          out.stride(0), out.stride(1))
+          out.stride(0), out.stride(1), *_workspace(ws, dev))
     return out

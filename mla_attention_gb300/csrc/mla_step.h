@@ -66,7 +66,13 @@ struct BmmW4Params {
   const void* scales;           // [H, N, K / group] bf16 or fp32
   __nv_bfloat16* out;
   int64_t x_stride_t, x_stride_h, out_stride_t, out_stride_h;  // elements
+  uint32_t* err;
+  uint32_t spin_limit;
   int T, H, N, K, group, scales_f32;
+};
+struct W4Plan {
+  int cluster;     // CTAs along k
+  int vec_x;       // x rows on 16-byte boundaries
 };
 constexpr int kW4MaxT = 1 << 19;
 cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream);

@@ -199,16 +199,17 @@ mla_status mla_kv_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe
 // ---------------------------------------------------------------------------
 mla_status mla_bmm_w4(const void* x, int64_t x_stride_t, int64_t x_stride_h, const void* w4, const void* scales,
                       int scales_f32, int group, int T, int H, int N, int K, void* out, int64_t out_stride_t,
-                      int64_t out_stride_h, void* stream) {
+                      int64_t out_stride_h, void* workspace, size_t workspace_bytes, void* stream) {
   MLA_REQUIRE(T >= 0 && H >= 1 && N >= 1 && K >= 1, "mla_bmm_w4: need T >= 0, H >= 1, N >= 1, K >= 1");
   MLA_REQUIRE(group == 32 || group == 64 || group == 128, "mla_bmm_w4: group must be 32, 64 or 128 (got %d)", group);
   MLA_REQUIRE(K % group == 0, "mla_bmm_w4: K must be a multiple of the group (got %d, %d)", K, group);
   MLA_REQUIRE(scales_f32 == 0 || scales_f32 == 1, "mla_bmm_w4: scales_f32 must be 0 or 1");
   MLA_REQUIRE((int64_t)H * N <= INT32_MAX && T <= kW4MaxT && H <= 65535, "mla_bmm_w4: H <= 65535, H * N below 2^31 and T <= %d",
               kW4MaxT);
+  if (!workspace || workspace_bytes < kWsHeader) return fail(MLA_ERR_WORKSPACE, "mla_bmm_w4: workspace must hold %zu bytes", (size_t)kWsHeader);
   if (T == 0) return finish(cudaSuccess, "");
   MLA_REQUIRE(x && w4 && scales && out, "mla_bmm_w4: every tensor is required");
-  MLA_REQUIRE(aligned(x, 2) && aligned(out, 2) && aligned(scales, scales_f32 ? 4 : 2) && aligned(w4, 16),
+  MLA_REQUIRE(aligned(x, 2) && aligned(out, 2) && aligned(scales, scales_f32 ? 4 : 2) && aligned(w4, 16) && aligned(workspace, 4),
               "mla_bmm_w4: w4 must be 16-byte aligned, the other tensors to their elements");
   MLA_REQUIRE(x_stride_t >= 0 && x_stride_h >= 0, "mla_bmm_w4: negative stride of x");
   MLA_REQUIRE(rows_apart(out_stride_t, out_stride_h, T, H, N), "mla_bmm_w4: rows of out must not overlap");
@@ -227,6 +228,8 @@ mla_status mla_bmm_w4(const void* x, int64_t x_stride_t, int64_t x_stride_h, con
   p.K = K;
   p.group = group;
   p.scales_f32 = scales_f32;
+  p.err = reinterpret_cast<uint32_t*>(workspace);
+  p.spin_limit = spin_limit();
   return finish(launch_bmm_w4(p, reinterpret_cast<cudaStream_t>(stream)), "mla_bmm_w4");
 }
 

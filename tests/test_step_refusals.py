@@ -44,8 +44,8 @@ def append(L, **kw):
 
 
 def w4(L, **kw):
-    return _run(L.mla_bmm_w4, "x xt xh w s f32 group T H N K out ot oh stream",
-                dict(x=F, xt=256, xh=128, w=F, s=F, f32=0, group=64, T=2, H=2, N=32, K=128, out=F, ot=64, oh=32, stream=None), kw)
+    return _run(L.mla_bmm_w4, "x xt xh w s f32 group T H N K out ot oh ws wsb stream",
+                dict(x=F, xt=256, xh=128, w=F, s=F, f32=0, group=64, T=2, H=2, N=32, K=128, out=F, ot=64, oh=32, ws=F, wsb=256, stream=None), kw)
 
 
 @pytest.mark.parametrize("kw", [dict(B=-1), dict(N=-1), dict(mp=-1), dict(ps=0), dict(np=-1), dict(np=1 << 27), dict(np=1 << 40), dict(lens=None),
@@ -58,6 +58,7 @@ def test_slot_map_refuses(L, kw):
 def test_workspaces_are_required(L):
     assert slot_map(L, ws=None) == 6 and slot_map(L, wsb=16) == 6
     assert append(L, ws=None) == 6 and append(L, wsb=255) == 6
+    assert w4(L, ws=None) == 6 and w4(L, wsb=255) == 6
     assert L.mla_slot_map_workspace_size(5) == L.mla_kv_append_workspace_size(5) == 256
 
 
