@@ -11,10 +11,8 @@
 // The call is a few KB to a few hundred KB of integers, so what bounds it is the latency of one
 // launch and of one scan.  One cluster does all of it: every CTA scans the lengths (a chunk of
 // kThreads requests at a time, 64-bit sums), and the tokens and the moved pages of the chunk are
-// dealt over all threads of the cluster, so that one long prompt among many single tokens costs no
-// more than the same tokens spread evenly.  A thread takes four tokens in a row: it finds the first
-// one's request by bisection in shared memory and walks on from there, and looks a page up where the
-// position enters it.
+// dealt over all threads of the cluster, so that one long prompt among many single tokens costs no more
+// than the same tokens spread evenly; a thread finds its request by bisection in shared memory.
 // lens_out and pool_state_out may be the buffers that are read: the cluster's barrier stands between
 // the last read and the first write.
 #include "mla_step.h"
@@ -22,7 +20,6 @@
 
 namespace mla {
 namespace {
-
 
 struct Sums {
   long long tok, pop, put;
@@ -45,9 +42,9 @@ struct Shared {
   long long popped, returned;  // ends of the last request whose pages were moved
 };
 
-// last index i in [0, n) with first[i] <= v
-__device__ __forceinline__ int owner(const int* first, int n, int v) {
-  int lo = 0, hi = n;
+// last index i in [lo, n) with first[i] <= v
+__device__ __forceinline__ int owner(const int* first, int n, int v, int lo = 0) {
+  int hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= v) lo = mid;
@@ -56,7 +53,8 @@ __device__ __forceinline__ int owner(const int* first, int n, int v) {
   return lo;
 }
 
-template <int kThreads>
+// kRun: neighbouring tokens of a thread
+template <int kThreads, int kRun>
 __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constant__ SlotMapParams p) {
   constexpr int kWarps = kThreads / 32;
   __shared__ Shared<kThreads> s;
@@ -71,13 +69,10 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
   auto store = [&](int32_t* base, int64_t i, int64_t n, int32_t v) {
     if (guard_span(p.err, G_STEP_OUT, base + i, 4, base, (uint64_t)n * 4)) base[i] = v;
   };
-  int64_t head = load(p.pool_state, 0, 2), count = load(p.pool_state, 1, 2);
-  const int head_in = (int)head, count_in = (int)count;
-  const bool pool_ok = head >= 0 && (head < P || (head == 0 && P == 0)) && count >= 0 && count <= P;
-  if (!pool_ok) {
-    head = count = 0;
-    if (rank == 0 && tid == 0) record_error(p.err, DEV_RANGE_BASE | 0x74);
-  }
+  const int head_in = load(p.pool_state, 0, 2), count_in = load(p.pool_state, 1, 2);
+  const bool pool_ok = head_in >= 0 && (head_in < P || (head_in == 0 && P == 0)) && count_in >= 0 && count_in <= P;
+  const int64_t head = pool_ok ? head_in : 0, count = pool_ok ? count_in : 0;
+  if (!pool_ok && rank == 0 && tid == 0) record_error(p.err, DEV_RANGE_BASE | 0x74);
   auto ring = [&](int64_t i) { return i >= P ? i - P : i; };  // i < 2 P
   const bool vec = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
   if (tid == 0) s.popped = s.returned = 0;
@@ -149,63 +144,98 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
       store(p.cu_tokens, b0 + tid, (int64_t)p.B + 1, (int32_t)min(first.tok, (long long)p.N));
       store(p.lens_out, b0 + tid, p.B, ok ? now : len);
     }
-    // ---- pages taken from the ring ----
-    for (int j = mine; j < npop; j += step) {
-      const int r = owner(s.pop, nb, j);
-      if (!s.ok[r]) continue;
-      const int32_t pg = load(p.pool, ring(head + pop0 + j), P);
-      const bool good = pg >= 0 && pg < P;
-      if (!good) record_error(p.err, DEV_RANGE_BASE | 0x75);
-      store(p.block_table, (b0 + r) * p.max_pages + s.have[r] + (j - s.pop[r]), (int64_t)(ext_table / 4), good ? pg : -1);
-    }
-    // ---- pages given back ----
-    for (int j = mine; j < nput; j += step) {
-      const int r = owner(s.put, nb, j);
-      if (!s.ok[r]) continue;
-      const int32_t pg = load(p.block_table, (b0 + r) * p.max_pages + s.need[r] + (j - s.put[r]), (int64_t)(ext_table / 4));
-      const bool good = pg >= 0 && pg < P;
-      if (!good) record_error(p.err, DEV_RANGE_BASE | 0x75);
-      store(p.pool, ring(ring(head + count) + put0 + j), P, good ? pg : -1);
-    }
-    // ---- tokens ----
-    for (int j0 = 4 * mine; j0 < ntok; j0 += 4 * step) {
-      int r = owner(s.tok, nb, j0), e = -1, left = 0;   // left: tokens until the next page
-      int32_t row = -1;                                 // the page's first slot, or -1
-      int pos[4], slot[4];
+    // ---- tokens, pages taken from the ring, pages given back behind its tail.  A pass of the loop does kRun
+    // neighbouring tokens and kPages of each kind of page, and asks for everything it reads before it
+    // waits for any.  Tokens start with the first warps, pages with the last and the middle ones: where there
+    // are few of each, no warp has the instructions of all three. ----
+    constexpr int kPages = 2;
+    const int64_t table = (int64_t)(ext_table / 4);
+    const int pop_first = step - 1 - mine, put_first = mine < step / 2 ? mine + step / 2 : mine - step / 2;
+    // (unsigned: a pass beyond 2^31 - 1 still compares as beyond)
+    for (uint32_t j0 = kRun * mine, jpop = pop_first, jput = put_first; j0 < (uint32_t)ntok || jpop < (uint32_t)npop || jput < (uint32_t)nput;
+         j0 += kRun * step, jpop += kPages * step, jput += kPages * step) {
+      auto checked = [&](int32_t pg) {
+        if (pg >= 0 && pg < P) return pg;
+        record_error(p.err, DEV_RANGE_BASE | 0x75);
+        return -1;
+      };
+      // tokens j0 .. : their requests, on from the first one's, and their pages
+      int pos[kRun], entry[kRun];
+      int32_t page[kRun];
+      if (j0 < (uint32_t)ntok) {
+        int r = owner(s.tok, nb, (int)j0), before = -1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = j0 + i;
-        pos[i] = slot[i] = -1;
-        if (j >= ntok) continue;
-        while (r + 1 < nb && s.tok[r + 1] <= j) ++r, e = -1;
-        if (!s.ok[r]) continue;
-        const int in = j - s.tok[r];
-        pos[i] = s.len[r] + in;
-        if (e < 0 || left == 0) {   // another page: of those held, or of those just taken
-          e = pos[i] / p.page_size;
-          left = (e + 1) * p.page_size - pos[i];
-          const int32_t pg = e < s.have[r]
-                                 ? load(p.block_table, (b0 + r) * p.max_pages + e, (int64_t)(ext_table / 4))
-                                 : load(p.pool, ring(head + pop0 + s.pop[r] + (e - s.have[r])), P);
-          row = pg >= 0 && pg < P ? pg * p.page_size : -1;
-          if (row < 0) record_error(p.err, DEV_RANGE_BASE | 0x75);
-        }
-        if (row >= 0) slot[i] = row + p.page_size - left;
-        --left;
-      }
-      const int64_t at = tok0 + j0;
-      if (vec && j0 + 4 <= ntok && (at & 3) == 0) {
-        if (guard_span(p.err, G_STEP_OUT, p.positions + at, 16, p.positions, (uint64_t)p.N * 4))
-          *reinterpret_cast<int4*>(p.positions + at) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-        if (guard_span(p.err, G_STEP_OUT, p.slots + at, 16, p.slots, (uint64_t)p.N * 4))
-          *reinterpret_cast<int4*>(p.slots + at) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j0 + i < ntok) {
-            store(p.positions, at + i, p.N, pos[i]);
-            store(p.slots, at + i, p.N, slot[i]);
+        for (int i = 0; i < kRun; ++i) {
+          const int jt = (int)(j0 + i);
+          pos[i] = -1;
+          entry[i] = 0;
+          page[i] = 0;
+          if (j0 + i >= (uint32_t)ntok) continue;
+          if (r + 1 < nb && s.tok[r + 1] <= jt) {   // mostly the next one; one behind requests without tokens else
+            ++r;
+            if (r + 1 < nb && s.tok[r + 1] <= jt) r = owner(s.tok, nb, jt, r);
           }
+          if (!s.ok[r]) continue;
+          pos[i] = s.len[r] + (jt - s.tok[r]);
+          const int e = pos[i] / p.page_size;
+          entry[i] = e * p.page_size;
+          if (i > 0 && before == r && entry[i] == entry[i - 1]) {   // the same page, held or just taken
+            page[i] = page[i - 1];
+          } else {
+            page[i] = e < s.have[r] ? load(p.block_table, (b0 + r) * p.max_pages + e, table)
+                                    : load(p.pool, ring(head + pop0 + s.pop[r] + (e - s.have[r])), P);
+          }
+          before = r;
+        }
+      }
+      int64_t pop_to[kPages], put_from[kPages];   // the table entries that get and hold the pages
+      int32_t pop_page[kPages], put_page[kPages];
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) {
+        pop_to[i] = put_from[i] = -1;
+        if (const uint32_t j = jpop + i * step; j < (uint32_t)npop) {
+          const int r = owner(s.pop, nb, (int)j);
+          if (s.ok[r]) {
+            pop_to[i] = (b0 + r) * p.max_pages + s.have[r] + ((int)j - s.pop[r]);
+            pop_page[i] = load(p.pool, ring(head + pop0 + j), P);
+          }
+        }
+        if (const uint32_t j = jput + i * step; j < (uint32_t)nput) {
+          const int r = owner(s.put, nb, (int)j);
+          if (s.ok[r]) {
+            put_from[i] = (b0 + r) * p.max_pages + s.need[r] + ((int)j - s.put[r]);
+            put_page[i] = load(p.block_table, put_from[i], table);
+          }
+        }
+      }
+      if (j0 < (uint32_t)ntok) {
+        int slot[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+          slot[i] = -1;
+          if (pos[i] < 0) continue;
+          const int32_t pg = checked(page[i]);
+          if (pg >= 0) slot[i] = pg * p.page_size + (pos[i] - entry[i]);
+        }
+        const int64_t at = tok0 + j0;
+        if (kRun == 4 && vec && j0 + 4 <= (uint32_t)ntok && (at & 3) == 0) {
+          if (guard_span(p.err, G_STEP_OUT, p.positions + at, 16, p.positions, (uint64_t)p.N * 4))
+            *reinterpret_cast<int4*>(p.positions + at) = make_int4(pos[0], pos[1 % kRun], pos[2 % kRun], pos[3 % kRun]);
+          if (guard_span(p.err, G_STEP_OUT, p.slots + at, 16, p.slots, (uint64_t)p.N * 4))
+            *reinterpret_cast<int4*>(p.slots + at) = make_int4(slot[0], slot[1 % kRun], slot[2 % kRun], slot[3 % kRun]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kRun; ++i)
+            if (j0 + i < (uint32_t)ntok) {
+              store(p.positions, at + i, p.N, pos[i]);
+              store(p.slots, at + i, p.N, slot[i]);
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) {
+        if (pop_to[i] >= 0) store(p.block_table, pop_to[i], table, checked(pop_page[i]));
+        if (put_from[i] >= 0) store(p.pool, ring(ring(head + count) + put0 + jput + i * step), P, checked(put_page[i]));
       }
     }
     carry = add(carry, chunk);
@@ -225,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
   }
 }
 
-template <int kThreads>
+template <int kThreads, int kRun>
 cudaError_t launch(const SlotMapParams& p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -237,16 +267,21 @@ cudaError_t launch(const SlotMapParams& p, int ctas, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, slot_map_kernel<kThreads>, p);
+  return cudaLaunchKernelEx(&cfg, slot_map_kernel<kThreads, kRun>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_slot_map(const SlotMapParams& p, cudaStream_t stream) {
-  // A decode batch fits one small CTA, whose scan and barriers are the shorter ones; a larger one gets
-  // a full CTA, and eight (the portable cluster size) where those have four tokens a thread.
-  if (p.B <= 128 && p.N <= 512) return launch<128>(p, 1, stream);
-  return launch<1024>(p, p.N + (int64_t)p.B <= 4096 ? 1 : 8, stream);
+  // What a small step takes is the length of one thread's instructions, so tokens go one to a thread while two
+  // passes of a cluster's threads (eight CTAs, the portable size) cover them, and a decode batch runs in one
+  // small CTA, whose scan and barriers are the shorter ones.  Measured, one small CTA / eight of 512 /
+  // eight of 1024 with four tokens a thread: 1 request 3.2 / 4.6 / 5.6 us; 64 requests of 0-4 tokens 4.1 /
+  // 5.0 / 7.8; 512 requests of one token in 16-token pages 23 / 6.5 / 9.3; 16384 tokens of 64 requests
+  // 59 / 8.1 / 8.1; 65536 of 512 252 / 22.6 / 12.2.
+  if (p.B <= 64 && p.N <= 256) return launch<256, 1>(p, 1, stream);
+  if (p.N <= 2 * 8 * 512) return launch<512, 1>(p, 8, stream);
+  return launch<1024, 4>(p, 8, stream);
 }
 
 }  // namespace mla
