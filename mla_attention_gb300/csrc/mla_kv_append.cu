@@ -5,12 +5,13 @@
 // A pair (a, b) of a RoPE vector turns by its angle: (a cos - b sin, a sin + b cos); pair i is
 // (x[2i], x[2i+1]) or, with is_neox, (x[i], x[i+32]).  Everything is computed in fp32 and rounded once.
 //
-// HBM-bound: per token 1152 bytes in, 576 or 1152 out and 256 per head of q.  One warp per cache row and one
-// per 16 heads of a token's q, all independent: no shared memory, no barrier.  What a warp reads goes out
-// before it looks at its token's position and slot: a chain of three loads would leave most of
-// the bandwidth idle.  In both pairings a
-// lane's two 16-byte vectors at columns 8u and 32 + 8u (u = 0..3) hold whole pairs, so four lanes
-// serve a RoPE vector, read its angles once and use them for all of the warp's heads.
+// HBM-bound: per token 1152 bytes in, 576 or 1152 out and 256 per head of q.  Half a warp per cache row and a
+// warp per 16 heads of a token's q, all independent: no shared memory, no barrier.  What a warp reads goes
+// out before it looks at its token's position and slot: a chain of three loads would leave most of the
+// bandwidth idle; and two rows a warp, each lane with four 16-byte vectors, keep twice as many bytes on
+// the way as one.  In both pairings a lane's two 16-byte vectors at columns 8u and 32 + 8u (u = 0..3)
+// hold whole pairs, so four lanes serve a RoPE vector, read its angles once and use them for all of
+// the warp's heads.
 #include "mla_step.h"
 #include "row_vec.cuh"
 
@@ -83,121 +84,138 @@ __device__ __forceinline__ void store16(const KvAppendParams& p, __nv_bfloat16* 
   if (guard_span(p.err, G_STEP_OUT, dst, 16, base, (uint64_t)extent * 2)) *reinterpret_cast<uint4*>(dst) = bf16x8_pack(f);
 }
 
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
-  const int lane = threadIdx.x & 31;
-  const int parts = 1 + (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp;   // a token's warps: its row, its heads
-  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);            // T * parts is below 2^31
-  const int t = w / parts, part = w - t * parts;
-  if (t >= p.T) return;
+__device__ __forceinline__ int token_int(const KvAppendParams& p, const int32_t* base, int t) {
+  return guard_span(p.err, G_STEP_IN, base + t, 4, base, (uint64_t)p.T * 4) ? base[t] : -1;
+}
+
+// ---- 16 heads of a token: four lanes a head, eight heads a step ----
+__device__ __forceinline__ void turn_heads(const KvAppendParams& p, int t, int first, int lane) {
   const bool neox = p.is_neox != 0;
-  const int u = lane & 3;
-  const uint64_t ext_t = (uint64_t)p.T * 4;
-  auto token_int = [&](const int32_t* base) { return guard_span(p.err, G_STEP_IN, base + t, 4, base, ext_t) ? base[t] : -1; };
-  const int pos = token_int(p.positions);
-  auto valid = [&] {
-    if (pos >= 0 && pos < p.max_pos) return true;
-    if (pos != -1 && part == 0 && lane == 0) record_error(p.err, DEV_RANGE_BASE | 0x78);
-    return false;
-  };
-
-  if (part > 0) {  // ---- heads: four lanes a head, eight heads a step ----
-    const int64_t ext_q = (p.T - 1) * p.q_pe_stride_t + (p.H - 1) * p.q_pe_stride_h + kR;
-    const int64_t ext_o = (p.T - 1) * p.q_out_stride_t + (p.H - 1) * p.q_out_stride_h + kDk;
-    const int h0 = (part - 1) * kHeadsPerWarp + (lane >> 2);
-    uint4 lo[kSteps], hi[kSteps];
+  const int u = lane & 3, h0 = first + (lane >> 2), pos = token_int(p, p.positions, t);
+  const int64_t ext_q = (p.T - 1) * p.q_pe_stride_t + (p.H - 1) * p.q_pe_stride_h + kR;
+  const int64_t ext_o = (p.T - 1) * p.q_out_stride_t + (p.H - 1) * p.q_out_stride_h + kDk;
+  uint4 lo[kSteps], hi[kSteps];
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int h = h0 + 8 * k;
-      if (h < p.H) {
-        const __nv_bfloat16* src = p.q_pe + t * p.q_pe_stride_t + h * p.q_pe_stride_h + 8 * u;
-        lo[k] = load16(p, src, p.q_pe, ext_q);
-        hi[k] = load16(p, src + 32, p.q_pe, ext_q);
-      }
+  for (int k = 0; k < kSteps; ++k) {
+    const int h = h0 + 8 * k;
+    if (h < p.H) {
+      const __nv_bfloat16* src = p.q_pe + t * p.q_pe_stride_t + h * p.q_pe_stride_h + 8 * u;
+      lo[k] = load16(p, src, p.q_pe, ext_q);
+      hi[k] = load16(p, src + 32, p.q_pe, ext_q);
     }
-    if (!valid()) return;
-    const Angles g = load_angles(p, pos, u, neox);
+  }
+  if (pos < 0 || pos >= p.max_pos) return;   // the token's row reports it
+  const Angles g = load_angles(p, pos, u, neox);
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int h = h0 + 8 * k;
-      if (h < p.H) {
-        float a[8], b[8];
-        bf16x8_unpack(lo[k], a);
-        bf16x8_unpack(hi[k], b);
-        turn(a, b, g, neox);
-        __nv_bfloat16* dst = p.q_out + t * p.q_out_stride_t + h * p.q_out_stride_h + kLatent + 8 * u;
-        store16(p, dst, p.q_out, ext_o, a);
-        store16(p, dst + 32, p.q_out, ext_o, b);
-      }
+  for (int k = 0; k < kSteps; ++k) {
+    const int h = h0 + 8 * k;
+    if (h < p.H) {
+      float a[8], b[8];
+      bf16x8_unpack(lo[k], a);
+      bf16x8_unpack(hi[k], b);
+      turn(a, b, g, neox);
+      __nv_bfloat16* dst = p.q_out + t * p.q_out_stride_t + h * p.q_out_stride_h + kLatent + 8 * u;
+      store16(p, dst, p.q_out, ext_o, a);
+      store16(p, dst + 32, p.q_out, ext_o, b);
     }
-    return;
   }
+}
 
-  // ---- the row: lane l holds latent columns 8l .. and 256 + 8l .., lanes 0-3 the RoPE columns ----
-  int64_t slot = token_int(p.slots);
-  const int64_t ext_c = (p.T - 1) * p.c_kv_stride + kLatent, ext_k = (p.T - 1) * p.k_pe_stride + kR;
-  const __nv_bfloat16* src = p.c_kv + t * p.c_kv_stride + 8 * lane;
-  const uint4 va = load16(p, src, p.c_kv, ext_c), vb = load16(p, src + 256, p.c_kv, ext_c);
-  uint4 ka, kb, wa, wb;
-  if (lane < 4) {
-    const __nv_bfloat16* pe = p.k_pe + t * p.k_pe_stride + 8 * u;
-    ka = load16(p, pe, p.k_pe, ext_k);
-    kb = load16(p, pe + 32, p.k_pe, ext_k);
+// ---- two rows: of each, lane l of its 16 holds latent columns 128 k + 8 l .. (k = 0..3), lanes 0-3 the
+// RoPE columns as well.  t is past the last token for the half that has none. ----
+__device__ __forceinline__ void append_rows(const KvAppendParams& p, int t, int lane) {
+  const bool neox = p.is_neox != 0, real = t < p.T;
+  const int l = lane & 15, u = lane & 3;
+  int pos = -1;
+  int64_t slot = -1;
+  uint4 v[4], w[4], ka, kb;
+  if (real) {
+    pos = token_int(p, p.positions, t);
+    slot = token_int(p, p.slots, t);
+    const __nv_bfloat16* src = p.c_kv + t * p.c_kv_stride + 8 * l;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = load16(p, src + 128 * k, p.c_kv, (p.T - 1) * p.c_kv_stride + kLatent);
+    if (l < 4) {
+      const __nv_bfloat16* pe = p.k_pe + t * p.k_pe_stride + 8 * u;
+      ka = load16(p, pe, p.k_pe, (p.T - 1) * p.k_pe_stride + kR);
+      kb = load16(p, pe + 32, p.k_pe, (p.T - 1) * p.k_pe_stride + kR);
+    }
+    if (pos < 0 || pos >= p.max_pos) {
+      if (pos != -1 && l == 0) record_error(p.err, DEV_RANGE_BASE | 0x78);
+      pos = -1;
+    }
+    if (slot < 0 || slot >= p.cache_rows) {
+      if (slot != -1 && pos >= 0 && l == 0) record_error(p.err, DEV_RANGE_BASE | 0x79);
+      slot = -1;
+    }
   }
+  const bool row = pos >= 0 && (slot >= 0 || p.kv_out);   // something to write
+  Angles ang;
+  if (row && l < 4) ang = load_angles(p, pos, u, neox);
+  float inv = 1.f;
   if (p.weight) {
-    wa = load16(p, p.weight + 8 * lane, p.weight, kLatent);
-    wb = load16(p, p.weight + 256 + 8 * lane, p.weight, kLatent);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent);
+    float sum = 0.f;
+    if (row) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f[8];
+        bf16x8_unpack(v[k], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += f[i] * f[i];
+      }
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    inv = rsqrtf(sum * (1.f / kLatent) + p.eps);
   }
-  if (!valid()) return;
-  if (slot < 0 || slot >= p.cache_rows) {
-    if (slot != -1 && lane == 0) record_error(p.err, DEV_RANGE_BASE | 0x79);
-    slot = -1;
-  }
+  if (!row) return;
   __nv_bfloat16* rows = p.kv_out ? p.kv_out + t * p.kv_out_stride : nullptr;
   const int64_t ext_r = (p.T - 1) * p.kv_out_stride + kDk;
-  if (slot < 0 && !rows) return;
-  float a[8], b[8];
-  bf16x8_unpack(va, a);
-  bf16x8_unpack(vb, b);
-  if (p.weight) {
-    float f[8], sum = 0.f;
+  auto put = [&](int col, const float(&f)[8]) {
+    if (slot >= 0) store_cache8(p, slot, col, f);
+    if (rows) store16(p, rows + col, p.kv_out, ext_r, f);
+  };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
-    const float inv = rsqrtf(warp_sum(sum) * (1.f / kLatent) + p.eps);
-    bf16x8_unpack(wa, f);
+  for (int k = 0; k < 4; ++k) {
+    float f[8];
+    bf16x8_unpack(v[k], f);
+    if (p.weight) {
+      float wf[8];
+      bf16x8_unpack(w[k], wf);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] *= inv * f[i];
-    bf16x8_unpack(wb, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] *= inv * f[i];
+      for (int i = 0; i < 8; ++i) f[i] *= inv * wf[i];
+    }
+    put(128 * k + 8 * l, f);
   }
-  if (slot >= 0) {
-    store_cache8(p, slot, 8 * lane, a);
-    store_cache8(p, slot, 256 + 8 * lane, b);
-  }
-  if (rows) {
-    store16(p, rows + 8 * lane, p.kv_out, ext_r, a);
-    store16(p, rows + 256 + 8 * lane, p.kv_out, ext_r, b);
-  }
-  if (lane < 4) {
-    const Angles g = load_angles(p, pos, u, neox);
+  if (l < 4) {
+    float a[8], b[8];
     bf16x8_unpack(ka, a);
     bf16x8_unpack(kb, b);
-    turn(a, b, g, neox);
-    if (slot >= 0) {
-      store_cache8(p, slot, kLatent + 8 * u, a);
-      store_cache8(p, slot, kLatent + 32 + 8 * u, b);
-    }
-    if (rows) {
-      store16(p, rows + kLatent + 8 * u, p.kv_out, ext_r, a);
-      store16(p, rows + kLatent + 32 + 8 * u, p.kv_out, ext_r, b);
-    }
+    turn(a, b, ang, neox);
+    put(kLatent + 8 * u, a);
+    put(kLatent + 32 + 8 * u, b);
+  }
+}
+
+// The first warps bring the rows, two each, the others the heads.
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5), row_warps = ((uint32_t)p.T + 1) / 2;
+  if (w < row_warps) {
+    append_rows(p, 2 * w + (lane >> 4), lane);
+  } else {
+    const uint32_t parts = (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp, i = w - row_warps;
+    const uint32_t t = parts ? i / parts : p.T;
+    if (t < (uint32_t)p.T) turn_heads(p, t, (i - t * parts) * kHeadsPerWarp, lane);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
-  const int64_t warps = (int64_t)p.T * (1 + (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp);
+  const int64_t warps = ((int64_t)p.T + 1) / 2 + (int64_t)p.T * ((p.H + kHeadsPerWarp - 1) / kHeadsPerWarp);
   kv_append_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
