@@ -360,6 +360,8 @@ mla_status mla_rope_append(const void* q_pe, const void* c_kv, const void* k_pe,
  * (mla_check_device_status; detail 0x2072, 0x2071, 0x2073, 0x2070); requests after one that ran out
  * of tokens or pages and that need some too are refused with it.  A pool_state outside the ring (0x2074) refuses
  * every page; a page id outside [0, num_pages) in the pool or the table (0x2075) gives slot -1.
+ * workspace: >= 256 bytes (the status word).  The attention calls give up waiting while their own
+ * workspace's word is set, so let it be another one than theirs.
  */
 size_t mla_slot_map_workspace_size(int B);
 mla_status mla_slot_map(const int32_t* lens, const int32_t* new_tokens, int B, int32_t* block_table, int max_pages,

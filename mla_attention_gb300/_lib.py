@@ -150,26 +150,42 @@ def _need(t: torch.Tensor, name: str, dtype, device=None, contiguous: bool = Tru
 # workspace: caller-owned scratch, cached per device; first bytes = status word
 # ---------------------------------------------------------------------------
 _ws_cache = {}
+_ws_outgrown = []      # replaced by larger ones; a captured graph may still hold their addresses
+_status_cache = {}     # status words of the calls around the attention (see _step), one buffer per device
 
 
 def workspace(nbytes: int, device: torch.device) -> torch.Tensor:
     key = (device.type, device.index)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
+        if ws is not None:
+            _ws_outgrown.append(ws)
         ws = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
         _ws_cache[key] = ws
     return ws
 
 
 def check_device_status(ws: Optional[torch.Tensor] = None, device=None, stream=None) -> int:
-    """Read and clear the device status word; raise MLAError if a kernel reported a fault."""
+    """Read and clear the device status word; raise MLAError if a kernel reported a fault.  Without a
+    workspace: the device's own and the one of the calls around the attention."""
+    words = [ws]
     if ws is None:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        ws = workspace(256, device)
-    detail = c_uint32(0)
-    s = lib().mla_check_device_status(_ptr(ws), _stream(stream), ctypes.byref(detail))
-    _check(s)
-    return detail.value
+        words = [workspace(256, device)]
+        if device.index in _status_cache:
+            words.append(_status_cache[device.index])
+    failed, found = None, 0
+    for w in words:
+        detail = c_uint32(0)
+        s = lib().mla_check_device_status(_ptr(w), _stream(stream), ctypes.byref(detail))
+        try:
+            _check(s)
+        except MLAError as e:
+            failed = failed or e
+        found = found or detail.value
+    if failed:
+        raise failed
+    return found
 
 
 def set_spin_limit(limit: int):

@@ -4,14 +4,15 @@ mla_kv_append and mla_bmm_w4 (argument marshalling only, as in _lib).
 A decode step makes hundreds of these calls, most of them a few microseconds long on the GPU, so the
 host's part is kept short: one expression checks a tensor, and only a tensor that fails it is looked at
 for what is wrong.  A call is issued on `stream` or on the current stream of the tensors' device,
-whichever device is current.
+whichever device is current.  The first call on a device that takes a workspace allocates the status word's
+buffer: make it before any stream capture.
 """
 from __future__ import annotations
 
 import torch
 
 from . import _lib
-from ._lib import MLAError, _check, workspace
+from ._lib import MLAError, _check
 
 _BF16, _I32, _F32, _E4M3, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn, torch.uint8
 _current_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: torch.cuda.current_stream() builds a Stream, 2 us
@@ -64,11 +65,13 @@ def _empty(shape, dtype, dev):
 
 
 def _workspace(ws, dev):
-    """Address and size of the status word's buffer: the caller's, or the one of this device."""
+    """Address and size of the status word's buffer: the caller's, or the device's own for these calls.  It is not
+    the attention's, whose kernels give up their waits while their word is set: a refused request of
+    mla_slot_map is an everyday answer."""
     if ws is None:
-        ws = _lib._ws_cache.get(("cuda", dev))
+        ws = _lib._status_cache.get(dev)
         if ws is None:
-            ws = workspace(256, torch.device("cuda", dev))
+            ws = _lib._status_cache[dev] = torch.zeros(256, dtype=_U8, device=torch.device("cuda", dev))
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise MLAError(1, f"ws must be a contiguous tensor on cuda:{dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size()

@@ -84,6 +84,9 @@ __device__ __noinline__ float plain_value(const BmmW4Params& p, int tok, int h, 
   const uint8_t* w = p.w4 + row * (p.K / 2);
   const __nv_bfloat16* x = p.x + tok * p.x_stride_t + h * p.x_stride_h;
   const int groups = p.K / p.group;
+  if (!guard_span(p.err, G_STEP_IN, w, p.K / 2, p.w4, (uint64_t)p.H * p.N * (p.K / 2)) ||
+      !guard_span(p.err, G_STEP_IN, x, p.K * 2, p.x, ((uint64_t)(p.T - 1) * p.x_stride_t + (uint64_t)(p.H - 1) * p.x_stride_h + p.K) * 2))
+    return 0.f;
   float v = 0.f;
   for (int q = 0; q < groups && v == v; ++q) {   // a NaN stays one
     const float s = scale_at(p, reinterpret_cast<const uint8_t*>(p.scales) + (row * groups + q) * (p.scales_f32 ? 4 : 2));
@@ -130,8 +133,12 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
     fence_mbar_init();
   }
   __syncthreads();
-  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {   // warp-uniform; bounded
-    return __all_sync(~0u, mbar_wait(bar, parity, p.err, site, p.spin_limit)) != 0;
+  // Warp-uniform and bounded.  The status word is written where a wait runs out, but not heeded: another
+  // call's report in the same workspace is no reason to stop.
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    const bool there = __all_sync(~0u, mbar_wait(bar, parity, nullptr, site, p.spin_limit)) != 0;
+    if (!there && lane == 0) record_error(p.err, DEV_TIMEOUT_BASE | site);
+    return there;
   };
 
   if (warp >= kWarps) {

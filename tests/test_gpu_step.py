@@ -615,6 +615,56 @@ def test_serving_steps_on_another_stream():
             assert torch.equal(a[name], b[name]), name
 
 
+def test_a_refused_request_stops_no_other_call():
+    """A pool that runs out is reported when the status is read, and until then nothing else gives up its waits."""
+    d, g = dev(), torch.Generator().manual_seed(70)
+    D = gen.decode_inputs([300, 17, 129], H=16, seed=71, page_size=16)
+    w4, sc = _w4(16, 128, 512, 64, False, g)
+    x = gen.randn_bf16((5, 16, 512), g).to(d)
+    args = (D.q.to(d), D.cache.to(d), D.block_table.to(d), D.lens.to(d), D.scale)
+    out, lse = mla_decode(*args)
+    y = mla_bmm_w4(x, w4, sc)
+    _done()
+    z = torch.zeros(2, dtype=torch.int32, device=d)
+    mla_slot_map(z, z + 50, torch.full((2, 9), -1, dtype=torch.int32, device=d), _i32([0, 1, 2, 3]).to(d), _i32([0, 4]).to(d), 16, 100)
+    for _ in range(3):
+        out2, lse2 = mla_decode(*args)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2) and torch.equal(y, mla_bmm_w4(x, w4, sc))
+    with pytest.raises(MLAError) as e:
+        check_device_status()
+    assert e.value.status == 5 and "0x71" in str(e.value)
+    check_device_status()
+
+
+def test_a_graph_outlives_a_larger_workspace():
+    """A captured step keeps the status word that it was captured with, whatever later calls need."""
+    from mla_attention_gb300 import workspace
+    d, g = dev(), torch.Generator().manual_seed(72)
+    D = gen.decode_inputs([40, 17], H=16, seed=73, page_size=16)
+    args = (D.q.to(d), D.cache.to(d), D.block_table.to(d), D.lens.to(d), D.scale)
+    w4, sc = _w4(16, 128, 512, 64, False, g)
+    mla_bmm_w4(mla_decode(*args)[0], w4, sc)
+    torch.cuda.synchronize()
+    G = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(G):
+        o, lse = mla_decode(*args)
+        y = mla_bmm_w4(o, w4, sc)
+    G.replay()
+    torch.cuda.synchronize()
+    first = y.clone()
+    ws = workspace(256, d)
+    bigger = workspace(2 * ws.numel(), d)
+    assert bigger.data_ptr() != ws.data_ptr()
+    size = ws.numel()
+    del ws
+    junk = [torch.full((size,), 255, dtype=torch.uint8, device=d) for _ in range(4)]
+    y.zero_()
+    G.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, first) and all((j == 255).all() for j in junk)
+    check_device_status()
+
+
 def test_explicit_stream_argument():
     """The call runs on the stream it is given, after that stream's own work."""
     d, s = dev(), torch.cuda.Stream()
