@@ -401,8 +401,9 @@ mla_status mla_rms_norm(const void* x, int64_t x_stride, const void* residual, i
  *          down-projection's output are fine); norm_weight bf16 [512], NULL: no norm (eps unused).
  * q_pe     bf16 rows of 64 at strides (q_pe_stride_t, q_pe_stride_h); NULL with H = 0: no query.
  * q_out    bf16, the fused query: columns 512..575 of rows at (q_out_stride_t, q_out_stride_h) are
- *          written, the others left as they are.  kv_out (nullable) bf16 rows of 576: the tokens'
- *          rows for mla_prefill.
+ *          written, the others left as they are (q_pe may be those columns: turned in place).
+ * kv_out   (nullable) bf16 rows of 576: the tokens' rows for mla_prefill; c_kv and k_pe may be views of the
+ *          same rows (in place).
  * positions DEVICE int32 [T]: -1 marks a row that holds no token (nothing is written for it); another
  *          position outside [0, max_pos) records MLA_ERR_DEVICE_RANGE and is skipped likewise.
  * slots    DEVICE int32 [T]: cache rows (mla_slot_map).  -1: no cache row is written (q_out and

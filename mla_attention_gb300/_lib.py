@@ -172,8 +172,9 @@ def check_device_status(ws: Optional[torch.Tensor] = None, device=None, stream=N
     if ws is None:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         words = [workspace(256, device)]
-        if device.index in _status_cache:
-            words.append(_status_cache[device.index])
+        step = _status_cache.get(torch.cuda.current_device() if device.index is None else device.index)
+        if step is not None:
+            words.append(step)
     failed, found = None, 0
     for w in words:
         detail = c_uint32(0)

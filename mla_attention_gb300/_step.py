@@ -15,6 +15,7 @@ from . import _lib
 from ._lib import MLAError, _check
 
 _BF16, _I32, _F32, _E4M3, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn, torch.uint8
+_INT_MAX = 2 ** 31 - 1
 _current_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: torch.cuda.current_stream() builds a Stream, 2 us
 
 
@@ -52,12 +53,28 @@ def _refuse(t, name, dtype, dev, shape):
 
 
 def _device(t, name, dims):
-    """The index of the GPU that holds t."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    """The index of the GPU that holds t, and t's shape."""
+    try:
+        dev, shape = t.get_device(), t.shape
+    except AttributeError:
+        raise MLAError(1, f"{name} must be a CUDA tensor, got {type(t).__name__}") from None
+    if dev < 0:
         raise MLAError(1, f"{name} must be a CUDA tensor")
-    if t.dim() != dims:
-        raise MLAError(1, f"{name} must have {dims} dimensions, got {t.dim()}")
-    return t.get_device()
+    if len(shape) != dims:
+        raise MLAError(1, f"{name} must have {dims} dimensions, got {len(shape)}")
+    if shape[0] > _INT_MAX:
+        raise MLAError(1, f"{name} has too many rows ({shape[0]})")
+    return dev, shape
+
+
+def _shape(t, name, dims):
+    try:
+        shape = t.shape
+    except AttributeError:
+        raise MLAError(1, f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
+    if len(shape) != dims:
+        raise MLAError(1, f"{name} must have {dims} dimensions, got {len(shape)}")
+    return shape
 
 
 def _empty(shape, dtype, dev):
@@ -77,18 +94,20 @@ def _workspace(ws, dev):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+_functions = {}
 _several_devices = None
 
 
 def _call(name, dev, stream, *args):
     global _several_devices
-    fn = getattr(_lib._lib or _lib.lib(), name)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.lib(), name)
+        _several_devices = torch.cuda.device_count() > 1
     if stream is None:
         stream = _current_stream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if _several_devices is None:
-        _several_devices = torch.cuda.device_count() > 1
     if _several_devices and dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             status = fn(*args, stream)
@@ -104,12 +123,10 @@ def mla_slot_map(lens, new_tokens, block_table, pool, pool_state, page_size: int
     dropped), block_table int32 [B,max_pages] and pool int32 [num_pages] in place, pool_state int32 [2]
     (ring head, free pages).  Rows behind the last token get -1.  lens_out / pool_state_out may be
     lens / pool_state.  Returns positions [N], slots [N], cu_tokens [B+1], lens_out, pool_state_out."""
-    dev = _device(lens, "lens", 1)
-    B, N = lens.shape[0], int(N)
-    _device(block_table, "block_table", 2)
-    _device(pool, "pool", 1)
-    if N < 0:
-        raise MLAError(1, "N must not be negative")
+    dev, (B,) = _device(lens, "lens", 1)
+    max_pages, num_pages, N = _shape(block_table, "block_table", 2)[1], _shape(pool, "pool", 1)[0], int(N)
+    if not 0 <= N <= _INT_MAX:
+        raise MLAError(1, f"N must be between 0 and 2^31 - 1, got {N}")
     if positions is None:
         positions = _empty(N, _I32, dev)
     if slots is None:
@@ -120,7 +137,6 @@ def mla_slot_map(lens, new_tokens, block_table, pool, pool_state, page_size: int
         lens_out = _empty(B, _I32, dev)
     if pool_state_out is None:
         pool_state_out = _empty(2, _I32, dev)
-    max_pages, num_pages = block_table.shape[1], pool.shape[0]
     _call("mla_slot_map", dev, stream, _dense(lens, "lens", _I32, dev, (B,)),
           _dense(new_tokens, "new_tokens", _I32, dev, (B,)), B,
           _dense(block_table, "block_table", _I32, dev, (B, max_pages)), max_pages, int(page_size), num_pages,
@@ -137,8 +153,7 @@ def mla_rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None,
     Returns out, residual_out, scales: out bf16, or e4m3 (e4m3=True or an e4m3 `out`) with fp32 scales
     [T, D / group] ([T, 1] with group 0); residual_out = h in bf16 (None without a residual; may be
     the residual itself); scales None with a bf16 out."""
-    dev = _device(x, "x", 2)
-    T, D = x.shape
+    dev, (T, D) = _device(x, "x", 2)
     e4m3 = bool(e4m3) if out is None else getattr(out, "dtype", None) is _E4M3
     group = int(group)
     if group and (not e4m3 or group not in (32, 64, 128) or D % group):
@@ -175,29 +190,25 @@ def mla_kv_append(c_kv, k_pe, slots, positions, cos_sin, kv_cache, kv_scale: flo
     (bf16, or e4m3 of row / kv_scale) in place at rows slots[t]; the turned q_pe [T,H,64] into
     q_out[:, :, 512:576]; kv_out [T,576] (if given) the rows in bf16.  positions[t] = -1: no token;
     slots[t] = -1: no cache row.  Returns q_out, kv_out."""
-    dev = _device(c_kv, "c_kv", 2)
-    T = c_kv.shape[0]
-    _device(kv_cache, "kv_cache", 3)
+    dev, (T, _) = _device(c_kv, "c_kv", 2)
+    pages, page, _ = _shape(kv_cache, "kv_cache", 3)
     e4m3 = kv_cache.dtype is _E4M3
-    pages, page = kv_cache.shape[0], kv_cache.shape[1]
     pc = _rows(c_kv, "c_kv", _BF16, dev, (T, 512))
     pk = _rows(k_pe, "k_pe", _BF16, dev, (T, 64))
     pcache = _dense(kv_cache, "kv_cache", _E4M3 if e4m3 else _BF16, dev, (pages, page, 576))
-    _device(cos_sin, "cos_sin", 2)
-    max_pos = cos_sin.shape[0]
+    max_pos = _shape(cos_sin, "cos_sin", 2)[0]
     pcs = _dense(cos_sin, "cos_sin", _F32, dev, (max_pos, 64))
     pw = None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, dev, (512,))
     pq = pqo = pkv = None
     H = qt = qh = ot = oh = st = 0
     if q_pe is not None:
-        _device(q_pe, "q_pe", 3)
-        H = q_pe.shape[1]
+        H = _shape(q_pe, "q_pe", 3)[1]
         if H < 1:
             raise MLAError(1, "q_pe must have at least one head")
         if q_out is None:
             q_out = _empty((T, H, 576), _BF16, dev)
         pq, pqo = _rows(q_pe, "q_pe", _BF16, dev, (T, H, 64)), _rows(q_out, "q_out", _BF16, dev, (T, H, 576))
-        qt, qh, ot, oh = q_pe.stride(0), q_pe.stride(1), q_out.stride(0), q_out.stride(1)
+        (qt, qh, _), (ot, oh, _) = q_pe.stride(), q_out.stride()
     elif q_out is not None:
         raise MLAError(1, "q_out goes with q_pe")
     if kv_out is not None:
@@ -213,11 +224,8 @@ def mla_bmm_w4(x, w4, scales, out=None, ws=None, stream=None):
     """out[t, h, n] = sum_k x[t, h, k] (code[h, n, k] - 8) scales[h, n, k // group]: x bf16 [T,H,K], w4 uint8
     [H,N,K/2] (byte j of a row: code 2j low, 2j+1 high), scales bf16 or fp32 [H,N,K/group], group 32, 64 or
     128 -> bf16 [T,H,N] (a strided `out` is fine)."""
-    dev = _device(x, "x", 3)
-    T, H, K = x.shape
-    _device(w4, "w4", 3)
-    _device(scales, "scales", 3)
-    N, groups = w4.shape[1], scales.shape[2]
+    dev, (T, H, K) = _device(x, "x", 3)
+    N, groups = _shape(w4, "w4", 3)[1], _shape(scales, "scales", 3)[2]
     if groups < 1 or K % groups or K // groups not in (32, 64, 128):
         raise MLAError(1, f"scales must have K / group columns, group 32, 64 or 128 (got {groups}, K = {K})")
     f32 = scales.dtype is _F32
@@ -227,6 +235,7 @@ def mla_bmm_w4(x, w4, scales, out=None, ws=None, stream=None):
     if out is None:
         out = _empty((T, H, N), _BF16, dev)
     po = _rows(out, "out", _BF16, dev, (T, H, N))
-    _call("mla_bmm_w4", dev, stream, px, x.stride(0), x.stride(1), pw, ps, int(f32), K // groups, T, H, N, K, po,
-          out.stride(0), out.stride(1), *_workspace(ws, dev))
+    (xt, xh, _), (ot, oh, _) = x.stride(), out.stride()
+    _call("mla_bmm_w4", dev, stream, px, xt, xh, pw, ps, int(f32), K // groups, T, H, N, K, po,
+          ot, oh, *_workspace(ws, dev))
     return out

@@ -68,9 +68,15 @@ __device__ __forceinline__ void store_cache8(const KvAppendParams& p, int64_t ro
   if (p.e4m3) {
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = f[i] * p.inv_kv_scale;
+    for (int i = 0; i < 8; ++i) q[i] = quotient(f[i], p.kv_scale, p.inv_kv_scale);
+    uint2 v = e4m3x8_pack(q);
+    if ((((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) {   // a NaN code
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = f[i] * p.inv_kv_scale;   // of an infinite value saturates, of a NaN stays
+      v = e4m3x8_pack(q);
+    }
     uint8_t* dst = reinterpret_cast<uint8_t*>(p.cache) + row * kDk + col;
-    if (guard_span(p.err, G_STEP_OUT, dst, 8, p.cache, ext)) *reinterpret_cast<uint2*>(dst) = e4m3x8_pack(q);
+    if (guard_span(p.err, G_STEP_OUT, dst, 8, p.cache, ext)) *reinterpret_cast<uint2*>(dst) = v;
   } else {
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.cache) + row * kDk + col;
     if (guard_span(p.err, G_STEP_OUT, dst, 16, p.cache, ext)) *reinterpret_cast<uint4*>(dst) = bf16x8_pack(f);
@@ -128,7 +134,7 @@ __device__ __forceinline__ void append_rows(const KvAppendParams& p, int t, int 
   const int l = lane & 15, u = lane & 3;
   int pos = -1;
   int64_t slot = -1;
-  uint4 v[4], w[4], ka, kb;
+  uint4 v[4], ka, kb;
   if (real) {
     pos = token_int(p, p.positions, t);
     slot = token_int(p, p.slots, t);
@@ -154,21 +160,20 @@ __device__ __forceinline__ void append_rows(const KvAppendParams& p, int t, int 
   if (row && l < 4) ang = load_angles(p, pos, u, neox);
   float inv = 1.f;
   if (p.weight) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent);
     float sum = 0.f;
     if (row) {
+      float part[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float f[8];
         bf16x8_unpack(v[k], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += f[i] * f[i];
+        part[k] = square_sum8(f);
       }
+      sum = (part[0] + part[1]) + (part[2] + part[3]);
     }
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-    inv = rsqrtf(sum * (1.f / kLatent) + p.eps);
+    inv = rsqrt_newton(sum * (1.f / kLatent) + p.eps);
   }
   if (!row) return;
   __nv_bfloat16* rows = p.kv_out ? p.kv_out + t * p.kv_out_stride : nullptr;
@@ -183,9 +188,9 @@ __device__ __forceinline__ void append_rows(const KvAppendParams& p, int t, int 
     bf16x8_unpack(v[k], f);
     if (p.weight) {
       float wf[8];
-      bf16x8_unpack(w[k], wf);
+      bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), wf);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= inv * wf[i];
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * wf[i];
     }
     put(128 * k + 8 * l, f);
   }

@@ -10,16 +10,14 @@
 // reduction is another's load.  The weight's vectors are asked for together with the row's; x and
 // the residual pass by L1, which keeps the weight.
 //
-// max|y| and the sum keep a NaN (a row that holds one is NaN throughout).  s is max|y| times the
-// reciprocal of 448, and y / s is y times the approximate reciprocal of s: 2^-22 off at most before it is
-// rounded to four bits.
+// max|y| and the sum keep a NaN (a row that holds one is NaN throughout).
 #include "mla_step.h"
 #include "row_vec.cuh"
 
 namespace mla {
 namespace {
 
-constexpr float kMinScale = 0x1p-126f, kInvE4m3Max = 1.f / 448.f;
+constexpr float kMinScale = 0x1p-126f, kE4m3Max = 448.f;
 
 __device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
   uint4 v;
@@ -111,9 +109,7 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
   auto sum_squares = [&] {
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += h[k][i] * h[k][i];
+    for (int k = 0; k < NV; ++k) sum += square_sum8(h[k]);
     return row_reduce<kBlock, false>(sum, red);
   };
   float sum = sum_squares(), eps = p.eps;
@@ -128,7 +124,7 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
       for (int i = 0; i < 8; ++i) h[k][i] *= 0x1p-96f;
     sum = sum_squares();
   }
-  const float inv = rsqrtf(sum / (float)p.D + eps);
+  const float inv = rsqrt_newton(sum / (float)p.D + eps);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     if constexpr (!kWeightFirst) wv[k] = load(p.weight, 0, 0, wide & kWideW, k);
@@ -173,11 +169,13 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = sub + k * per_row, c = 8 * v, n = min(8, p.D - c);
-      const float s = nan_max(kMinScale, m[k] * kInvE4m3Max);
+      // (max / 448; an infinite one is kept, leaves 0 of finite values and NaN of infinite ones)
+      const bool fin = m[k] < __int_as_float(0x7f800000);
+      const float s = nan_max(kMinScale, fin ? quotient(m[k], kE4m3Max, 1.f / kE4m3Max) : m[k]), s_or_0 = fin ? s : 0.f;
       float inv_s;
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv_s) : "f"(s));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[k][i] *= inv_s;
+      for (int i = 0; i < 8; ++i) h[k][i] = quotient(h[k][i], s_or_0, inv_s);
       if (n > 0) {
         if (guard_span(nullptr, G_STEP_OUT, out + c, n, p.out, (uint64_t)(p.T - 1) * p.out_stride + p.D))
           store_row8_e4m3(out + c, n, wide & kWideOut, h[k]);

@@ -54,7 +54,7 @@ struct KvAppendParams {
   uint32_t* err;
   int64_t c_kv_stride, k_pe_stride, q_pe_stride_t, q_pe_stride_h, q_out_stride_t, q_out_stride_h, kv_out_stride;
   int64_t cache_rows;
-  float eps, inv_kv_scale;         // 1 / kv_scale: the quotient is 2^-23 off at most before it is rounded to 4 bits
+  float eps, kv_scale, inv_kv_scale;
   int T, H, max_pos, is_neox, e4m3;
 };
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);

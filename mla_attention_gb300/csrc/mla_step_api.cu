@@ -187,6 +187,7 @@ mla_status mla_kv_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe
   p.kv_out_stride = kv_out_stride;
   p.cache_rows = num_pages * page_size;
   p.eps = eps;
+  p.kv_scale = kv_scale;
   p.inv_kv_scale = 1.f / kv_scale;
   p.T = T;
   p.H = H;

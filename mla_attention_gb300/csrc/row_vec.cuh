@@ -29,6 +29,22 @@ __device__ __forceinline__ uint2 e4m3x8_pack(const float (&f)[8]) {
   return make_uint2(e4m3x4_pack(f[0], f[1], f[2], f[3]), e4m3x4_pack(f[4], f[5], f[6], f[7]));
 }
 
+// a / b from r, 1 / b to an ulp or two: the product's remainder is exact in one fma and puts it right
+// (Markstein's correction step), so that a value next to a border between two e4m3 values falls on its own side
+// of it.  Finite a and b; an infinite quotient becomes NaN.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+// 1 / sqrt(x), the approximation after one Newton step
+__device__ __forceinline__ float rsqrt_newton(float x) {
+  const float y = rsqrtf(x), z = fmaf(0.5f * y, fmaf(-(x * y), y, 1.f), y);
+  return x > 0.f && x < __int_as_float(0x7f800000) ? z : y;
+}
+__device__ __forceinline__ float square_sum8(const float (&f)[8]) {   // pairwise: a row's error is that of a few roundings
+  return ((f[0] * f[0] + f[1] * f[1]) + (f[2] * f[2] + f[3] * f[3])) + ((f[4] * f[4] + f[5] * f[5]) + (f[6] * f[6] + f[7] * f[7]));
+}
+
 // n (1..8) bf16 values at src one by one; the rest are 0
 __device__ __forceinline__ uint4 load_row8_narrow(const __nv_bfloat16* src, int n) {
   const uint16_t* b = reinterpret_cast<const uint16_t*>(src);

@@ -282,6 +282,26 @@ def test_norm_nan_and_infinity():
     assert np.isnan(y[1]).all() and np.isnan(y[2, 3]).all() and (y[2, :3] == 0).all() and np.isfinite(y[[0, 3]]).all()
 
 
+def test_norm_infinite_weight_and_codes_at_borders():
+    """An infinite weight makes its group's scale infinite and its finite values 0; with power-of-two rows the
+    quotients are exact and every code is the nearest one, ties to even."""
+    x = torch.ones((1, 128), dtype=torch.bfloat16, device=dev())
+    w = torch.ones(128, dtype=torch.bfloat16)
+    w[5] = float("inf")
+    out, _, scales = mla_rms_norm(x, w.to(dev()), eps=0.0, e4m3=True, group=64)
+    y, s = to_np(out)[0], to_np(scales)[0]
+    assert np.isinf(s[0]) and np.isnan(y[5]) and (np.delete(y[:64], 5) == 0).all() and s[1] == np.float32(1 / 448) and (y[64:] == 448).all()
+    # |x| = 1 everywhere: y = w; the first weight fixes the scale at 1, the others are e4m3 values and their midpoints
+    steps = torch.arange(0, 448 * 2 + 1, dtype=torch.float32) / 2
+    mids = steps[(steps == steps.to(torch.bfloat16).float())]
+    w = torch.cat([torch.tensor([448.0]), mids]).to(torch.bfloat16).to(dev())
+    x = torch.ones((1, w.numel()), dtype=torch.bfloat16, device=dev())
+    x[:, ::2] = -1
+    out, _, scales = mla_rms_norm(x, w, eps=0.0, e4m3=True)
+    assert to_np(scales)[0, 0] == 1
+    np.testing.assert_array_equal(to_np(out)[0], so.round_e4m3(to_np(x)[0] * to_np(w)))
+
+
 def test_norm_rows_past_2_31_elements():
     T, D = 70000, 32768
     x = torch.zeros((T, D), dtype=torch.bfloat16, device=dev())
@@ -372,6 +392,22 @@ def test_append_pages_and_dense_rows(page):
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 def test_append_reports_and_skips_bad_rows(e4m3):
     _check_append(40, 16, e4m3, rows_out=True, bad=True)
+
+
+@pytest.mark.parametrize("neox", [False, True], ids=["interleaved", "halves"])
+def test_append_in_place(neox):
+    """kv_out over c_kv and k_pe themselves and q_out over q_pe: the same bits as into buffers of their own."""
+    d, g, T, H = dev(), torch.Generator().manual_seed(9), 21, 5
+    kv, q = gen.randn_bf16((T, 576), g).to(d), gen.randn_bf16((T, H, 576), g).to(d)
+    w = (1 + 0.3 * torch.randn(512, generator=g)).bfloat16().to(d)
+    slots, pos, cs = torch.randperm(32, generator=g)[:T].to(torch.int32).to(d), _i32(list(range(T))).to(d), gen.rope_cos_sin(64).to(d)
+    one, two = torch.zeros((2, 16, 576), dtype=torch.bfloat16, device=d), torch.zeros((2, 16, 576), dtype=torch.bfloat16, device=d)
+    rows, q2 = torch.empty_like(kv), q.clone()
+    mla_kv_append(kv[:, :512], kv[:, 512:], slots, pos, cs, one, norm_weight=w, q_pe=q[:, :, 512:], q_out=q2, kv_out=rows, is_neox=neox)
+    mla_kv_append(kv[:, :512], kv[:, 512:], slots, pos, cs, two, norm_weight=w, q_pe=q[:, :, 512:], q_out=q, kv_out=kv, is_neox=neox)
+    _done()
+    assert torch.equal(one, two) and torch.equal(rows, kv) and torch.equal(q2, q)
+    assert torch.equal(one.view(-1, 576)[slots.long()], kv)
 
 
 def test_append_saturates_and_keeps_nan():
