@@ -73,6 +73,9 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
   const bool pool_ok = head_in >= 0 && (head_in < P || (head_in == 0 && P == 0)) && count_in >= 0 && count_in <= P;
   const int64_t head = pool_ok ? head_in : 0, count = pool_ok ? count_in : 0;
   if (!pool_ok && rank == 0 && tid == 0) record_error(p.err, DEV_RANGE_BASE | 0x74);
+  // (32-bit quotients, a shift where the page size allows: the divisions are most of a thread's instructions)
+  auto page_of = [&](int pos) { return p.page_log2 >= 0 ? pos >> p.page_log2 : pos / p.page_size; };
+  auto pages_of = [&](int tokens) { return tokens > 0 ? page_of(tokens - 1) + 1 : 0; };
   auto ring = [&](int64_t i) { return i >= P ? i - P : i; };  // i < 2 P
   const bool vec = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
   if (tid == 0) s.popped = s.returned = 0;
@@ -90,8 +93,7 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
     bool ok = len >= 0 && len <= cap && grown <= cap;
     uint32_t why = ok ? 0 : 0x70;
     const int now = ok ? (int)grown : len;
-    const int have = ok ? (int)(((int64_t)len + p.page_size - 1) / p.page_size) : 0;
-    const int need = ok ? (int)(((int64_t)now + p.page_size - 1) / p.page_size) : 0;
+    const int have = ok ? pages_of(len) : 0, need = ok ? pages_of(now) : 0;
     Sums v = {max(n, 0), max(need - have, 0), max(have - need, 0)};
     const Sums own = v;
 #pragma unroll
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
           }
           if (!s.ok[r]) continue;
           pos[i] = s.len[r] + (jt - s.tok[r]);
-          const int e = pos[i] / p.page_size;
+          const int e = page_of(pos[i]);
           entry[i] = e * p.page_size;
           if (i > 0 && before == r && entry[i] == entry[i - 1]) {   // the same page, held or just taken
             page[i] = page[i - 1];

@@ -20,6 +20,7 @@ struct SlotMapParams {
   uint32_t* err;
   int64_t num_pages;
   int B, max_pages, page_size, N;
+  int page_log2;              // of page_size, -1 if it is not a power of two
 };
 cudaError_t launch_slot_map(const SlotMapParams& p, cudaStream_t stream);
 

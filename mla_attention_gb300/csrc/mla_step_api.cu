@@ -84,6 +84,9 @@ mla_status mla_slot_map(const int32_t* lens, const int32_t* new_tokens, int B, i
   p.max_pages = max_pages;
   p.page_size = page_size;
   p.N = N;
+  p.page_log2 = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page_size == 1 << i) p.page_log2 = i;
   return finish(launch_slot_map(p, reinterpret_cast<cudaStream_t>(stream)), "mla_slot_map");
 }
 
