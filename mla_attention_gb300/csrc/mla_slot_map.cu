@@ -259,6 +259,11 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const __grid_constan
 
 template <int kThreads, int kRun>
 cudaError_t launch(const SlotMapParams& p, int ctas, cudaStream_t stream) {
+  if (ctas > 8) {   // more than the portable size has to be asked for
+    static PerDeviceOnce once;
+    cudaError_t e = once.run([] { return cudaFuncSetAttribute(slot_map_kernel<kThreads, kRun>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -276,14 +281,14 @@ cudaError_t launch(const SlotMapParams& p, int ctas, cudaStream_t stream) {
 
 cudaError_t launch_slot_map(const SlotMapParams& p, cudaStream_t stream) {
   // What a small step takes is the length of one thread's instructions, so tokens go one to a thread while two
-  // passes of a cluster's threads (eight CTAs, the portable size) cover them, and a decode batch runs in one
-  // small CTA, whose scan and barriers are the shorter ones.  Measured, one small CTA / eight of 512 /
-  // eight of 1024 with four tokens a thread: 1 request 3.2 / 4.6 / 5.6 us; 64 requests of 0-4 tokens 4.1 /
-  // 5.0 / 7.8; 512 requests of one token in 16-token pages 23 / 6.5 / 9.3; 16384 tokens of 64 requests
-  // 59 / 8.1 / 8.1; 65536 of 512 252 / 22.6 / 12.2.
+  // passes of a cluster's threads cover them, and a decode batch runs in one small CTA, whose scan and
+  // barriers are the shorter ones.  Measured, one CTA of 256 / eight of 512 / sixteen of 1024 with four
+  // tokens a thread: 1 request 3.1 / 4.5 / 5.6 us; 64 requests of 0-4 tokens 3.8 / 4.9 / 7; 512 requests of one
+  // token in 16-token pages 23 / 6.4 / 8.5; 8192 tokens of 32 requests 29 / 5.6 / 7.0; 16384 of 64
+  // 59 / 7.5 / 7.3; 65536 of 512 252 / 21 / 8.5 (eight of 1024: 10.9).
   if (p.B <= 64 && p.N <= 256) return launch<256, 1>(p, 1, stream);
   if (p.N <= 2 * 8 * 512) return launch<512, 1>(p, 8, stream);
-  return launch<1024, 4>(p, 8, stream);
+  return launch<1024, 4>(p, 16, stream);
 }
 
 }  // namespace mla
