@@ -5,10 +5,11 @@
 //
 // HBM-bound: 2 bytes a column in, 2 more for the residual and 2 for its sum, 1 or 2 out.  A row is read
 // once and kept in registers as h in fp32, eight columns (16 bytes) a vector: one warp a row up to 1024
-// columns (no barrier), one CTA a row above, as many threads as give each two vectors (four above 16384
-// columns).  Short CTAs beat long ones here: six rows of 5120 columns share an SM, so that one's
-// reduction is another's load.  The weight's vectors are asked for together with the row's; x and
-// the residual pass by L1, which keeps the weight.
+// columns (no barrier), one CTA a row above.  The weight's vectors are asked for together with the row's
+// where registers allow; x and the residual pass by L1, which keeps the weight.  bf16 rows written off the
+// vector boundaries (an odd width) go value by value instead, neighbouring columns in neighbouring lanes.
+// 16384 x 5120 with residual to e4m3: 99 us, 88 % of the copy's bandwidth; 8000 x 8192 to bf16 80 us, 96 %;
+// one row of 8192 2.5 us.
 //
 // max|y| and the sum keep a NaN (a row that holds one is NaN throughout).
 #include "mla_step.h"
@@ -29,6 +30,13 @@ __device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
 __device__ __forceinline__ float nan_max(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// the larger magnitude, with some sign; NaN if either is
+__device__ __forceinline__ float nan_max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -58,20 +66,45 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 
 enum : int { kWideX = 1, kWideR = 2, kWideRo = 4, kWideW = 8, kWideOut = 16 };  // rows on vector boundaries
 
-template <int NV, bool kBlock, bool kE4m3>
+template <int NV, bool kBlock, bool kE4m3, bool kStrided>
 __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __grid_constant__ RmsNormParams p, int wide) {
   __shared__ float red[32];
   const int per_row = kBlock ? blockDim.x : 32, sub = kBlock ? threadIdx.x : threadIdx.x & 31;
   const int64_t t = kBlock ? blockIdx.x : (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
   if (!kBlock && t >= p.T) return;
-  // vector k of this thread: columns c .. c + n - 1
+  // Vector k of this thread: columns c .. c + n - 1, or with kStrided every per_row-th from sub + 8 k per_row on.
   auto load = [&](const __nv_bfloat16* base, int64_t stride, int64_t row, bool on_vec, int k) {
+    const uint64_t ext = ((uint64_t)(row ? p.T - 1 : 0) * stride + p.D) * 2;
+    if constexpr (kStrided) {
+      uint32_t b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (8 * k + i) * per_row + sub;
+        const __nv_bfloat16* src = base + row * stride + sub + (8 * k + i) * per_row;
+        b[i] = c < p.D && guard_span(nullptr, G_STEP_IN, src, 2, base, ext) ? *reinterpret_cast<const uint16_t*>(src) : 0u;
+      }
+      return make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
+    }
     const int c = 8 * (sub + k * per_row), n = min(8, p.D - c);
     const __nv_bfloat16* src = base + row * stride + c;
-    if (n <= 0 || !guard_span(nullptr, G_STEP_IN, src, 2 * n, base, ((uint64_t)(row ? p.T - 1 : 0) * stride + p.D) * 2))
-      return make_uint4(0, 0, 0, 0);
+    if (n <= 0 || !guard_span(nullptr, G_STEP_IN, src, 2 * n, base, ext)) return make_uint4(0, 0, 0, 0);
     if (!on_vec || n < 8) return load_row8_narrow(src, n);
     return base == p.weight ? *reinterpret_cast<const uint4*>(src) : load_once(src);
+  };
+  auto store = [&](__nv_bfloat16* base, int64_t stride, bool on_vec, int k, const float(&f)[8]) {
+    const uint64_t ext = ((uint64_t)(p.T - 1) * stride + p.D) * 2;
+    if constexpr (kStrided) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (8 * k + i) * per_row + sub;
+        __nv_bfloat16* dst = base + t * stride + c;
+        if (c < p.D && guard_span(nullptr, G_STEP_OUT, dst, 2, base, ext)) *dst = __float2bfloat16_rn(f[i]);
+      }
+    } else {
+      const int c = 8 * (sub + k * per_row), n = min(8, p.D - c);
+      __nv_bfloat16* dst = base + t * stride + c;
+      if (n > 0 && guard_span(nullptr, G_STEP_OUT, dst, 2 * n, base, ext)) store_row8(dst, n, on_vec, f);
+    }
   };
   constexpr bool kWeightFirst = NV <= 2;   // more vectors leave no registers for it
   uint4 xv[NV], wv[NV];
@@ -86,17 +119,14 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
 #pragma unroll
       for (int k = 0; k < NV; ++k) wv[k] = load(p.weight, 0, 0, wide & kWideW, k);
     // the sum goes out before the norm: residual_out may be the residual or x, read by this thread alone
-    __nv_bfloat16* ro = p.residual_out + t * p.residual_out_stride;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = 8 * (sub + k * per_row), n = min(8, p.D - c);
       float f[8];
       bf16x8_unpack(xv[k], h[k]);
       bf16x8_unpack(rv[k], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[k][i] += f[i];
-      if (n > 0 && guard_span(nullptr, G_STEP_OUT, ro + c, 2 * n, p.residual_out, ((uint64_t)(p.T - 1) * p.residual_out_stride + p.D) * 2))
-        store_row8(ro + c, n, wide & kWideRo, h[k]);
+      store(p.residual_out, p.residual_out_stride, wide & kWideRo, k, h[k]);
     }
   } else {
     if constexpr (kWeightFirst)
@@ -135,13 +165,8 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
   }
 
   if constexpr (!kE4m3) {
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + t * p.out_stride;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = 8 * (sub + k * per_row), n = min(8, p.D - c);
-      if (n > 0 && guard_span(nullptr, G_STEP_OUT, out + c, 2 * n, p.out, ((uint64_t)(p.T - 1) * p.out_stride + p.D) * 2))
-        store_row8(out + c, n, wide & kWideOut, h[k]);
-    }
+    for (int k = 0; k < NV; ++k) store(reinterpret_cast<__nv_bfloat16*>(p.out), p.out_stride, wide & kWideOut, k, h[k]);
   } else {
     uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + t * p.out_stride;
     float m[NV], all = 0.f;
@@ -149,7 +174,8 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
     for (int k = 0; k < NV; ++k) {
       m[k] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m[k] = nan_max(m[k], fabsf(h[k][i]));
+      for (int i = 0; i < 8; ++i) m[k] = nan_max_abs(m[k], h[k][i]);
+      m[k] = fabsf(m[k]);
       all = nan_max(all, m[k]);
     }
     const bool whole = p.group == p.D;
@@ -168,7 +194,7 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = sub + k * per_row, c = 8 * v, n = min(8, p.D - c);
+      const int c = 8 * (sub + k * per_row), n = min(8, p.D - c);
       // (max / 448; an infinite one is kept, leaves 0 of finite values and NaN of infinite ones)
       const bool fin = m[k] < __int_as_float(0x7f800000);
       const float s = nan_max(kMinScale, fin ? quotient(m[k], kE4m3Max, 1.f / kE4m3Max) : m[k]), s_or_0 = fin ? s : 0.f;
@@ -176,21 +202,29 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv_s) : "f"(s));
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[k][i] = quotient(h[k][i], s_or_0, inv_s);
-      if (n > 0) {
-        if (guard_span(nullptr, G_STEP_OUT, out + c, n, p.out, (uint64_t)(p.T - 1) * p.out_stride + p.D))
-          store_row8_e4m3(out + c, n, wide & kWideOut, h[k]);
-        float* sc = p.scales + t * groups + (whole ? 0 : c >> group_log2);
-        if ((whole ? v == 0 : (c & (p.group - 1)) == 0) && guard_span(nullptr, G_STEP_OUT, sc, 4, p.scales, (uint64_t)p.T * groups * 4)) *sc = s;
+      float* sc = p.scales + t * groups + (whole ? 0 : c >> group_log2);
+      const bool writes = whole ? sub == 0 && k == 0 : n > 0 && (c & (p.group - 1)) == 0;
+      if (writes && guard_span(nullptr, G_STEP_OUT, sc, 4, p.scales, (uint64_t)p.T * groups * 4)) *sc = s;
+      const uint64_t ext = (uint64_t)(p.T - 1) * p.out_stride + p.D;
+      if constexpr (kStrided) {
+        const uint2 q = e4m3x8_pack(h[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int ci = (8 * k + i) * per_row + sub;
+          if (ci < p.D && guard_span(nullptr, G_STEP_OUT, out + ci, 1, p.out, ext)) out[ci] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+        }
+      } else if (n > 0 && guard_span(nullptr, G_STEP_OUT, out + c, n, p.out, ext)) {
+        store_row8_e4m3(out + c, n, wide & kWideOut, h[k]);
       }
     }
   }
 }
 
-template <int NV, bool kBlock>
+template <int NV, bool kBlock, bool kStrided = false>
 cudaError_t launch(const RmsNormParams& p, int wide, int threads, cudaStream_t stream) {
   const unsigned grid = kBlock ? (unsigned)p.T : (unsigned)(((int64_t)p.T * 32 + threads - 1) / threads);
-  if (p.scales) rms_norm_kernel<NV, kBlock, true><<<grid, threads, 0, stream>>>(p, wide);
-  else rms_norm_kernel<NV, kBlock, false><<<grid, threads, 0, stream>>>(p, wide);
+  if (p.scales) rms_norm_kernel<NV, kBlock, true, kStrided><<<grid, threads, 0, stream>>>(p, wide);
+  else rms_norm_kernel<NV, kBlock, false, kStrided><<<grid, threads, 0, stream>>>(p, wide);
   return cudaGetLastError();
 }
 
@@ -209,11 +243,28 @@ cudaError_t launch_rms_norm(const RmsNormParams& p, cudaStream_t stream) {
   if (p.scales ? on(p.out, p.out_stride, p.T, 8, 1) : on(p.out, p.out_stride, p.T, 16, 2)) wide |= kWideOut;
   const int vecs = (p.D + 7) / 8;
   auto threads = [&](int nv) { return (vecs + 32 * nv - 1) / (32 * nv) * 32; };
+  // bf16 rows that are written off the vector boundaries: every eight values of a lane would be eight writes
+  // with 16 bytes between the lanes, so neighbouring columns go to neighbouring lanes (30000 x 1279: 97 us and
+  // 52; 3 x 8191 with residual: 6.9 and 3.6).  Rows that are only read off them, and bytes written so, stay with
+  // vectors (10000 x 2047 to e4m3: 28.6 us, so 41; 32000 x 1024 with x alone off: 48 and 70).  Not with scales of
+  // groups, whose columns lie in one warp only with eight to a lane, nor above 8192 columns, where eight
+  // values a thread are too few.
+  const bool narrow_out = (p.residual && !(wide & kWideRo)) || (!p.scales && !(wide & kWideOut));
+  if (narrow_out && (!p.scales || p.group == p.D) && vecs <= 1024) {
+    if (vecs <= 32) return launch<1, false, true>(p, wide, 128, stream);
+    if (vecs <= 64) return launch<2, false, true>(p, wide, 128, stream);
+    return launch<1, true, true>(p, wide, threads(1), stream);
+  }
   if (vecs <= 32) return launch<1, false>(p, wide, 128, stream);
   if (vecs <= 64) return launch<2, false>(p, wide, 128, stream);
   if (vecs <= 128) return launch<4, false>(p, wide, 128, stream);
-  if (vecs <= 2048) return launch<2, true>(p, wide, threads(2), stream);
-  return launch<4, true>(p, wide, threads(4), stream);
+  // A CTA a row.  Two vectors a thread are the shorter way through one row (8192 columns: 2.6 us, four 3.4);
+  // four put more rows on an SM, which pays for wide ones once the SMs are full (8000 x 8192 with residual:
+  // 84.6 us and 80.2; 16384 x 5120 to e4m3: 100.4 and 98.2; 4000 x 16384 to e4m3: 78.8 and 61.4; but
+  // 2048 x 4096: 12.9 and 13.9).
+  const int sms = device_sm_count();
+  if (vecs > (p.T >= 32 * sms ? 319 : p.T >= 2 * sms ? 1023 : 2048)) return launch<4, true>(p, wide, threads(4), stream);
+  return launch<2, true>(p, wide, threads(2), stream);
 }
 
 }  // namespace mla

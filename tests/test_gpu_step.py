@@ -239,6 +239,18 @@ def test_norm_strides_and_groups(pad, off, D, e4m3, group):
     _check_norm(5, D, pad, off, residual=pad != 64, e4m3=e4m3, group=group)
 
 
+@pytest.mark.parametrize("D", [1, 9, 255, 333, 511, 1023, 2047, 8191, 8193])
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_norm_odd_widths(D, e4m3):
+    _check_norm(40, D, e4m3=e4m3, in_place=D % 3 == 0)
+    _check_norm(3, D, pad=1, off=1, residual=e4m3, e4m3=e4m3)
+
+
+@pytest.mark.parametrize("T,D,e4m3,group", [(4900, 2568, False, 0), (4900, 2560, True, 128), (310, 8200, False, 0)])
+def test_norm_many_rows(T, D, e4m3, group):
+    _check_norm(T, D, e4m3=e4m3, group=group)
+
+
 def test_norm_in_place():
     for D, e4m3 in ((1536, False), (8192, False), (1535, False), (5120, True)):
         _check_norm(9, D, e4m3=e4m3, in_place=True)
