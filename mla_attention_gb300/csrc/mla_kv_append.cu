@@ -68,7 +68,8 @@ __device__ __forceinline__ void store_cache8(const KvAppendParams& p, int64_t ro
   if (p.e4m3) {
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = quotient(f[i], p.kv_scale, p.inv_kv_scale);
+    for (int i = 0; i < 8; ++i) q[i] = f[i];
+    quotient8(q, p.kv_scale, p.inv_kv_scale);
     uint2 v = e4m3x8_pack(q);
     if ((((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) {   // a NaN code
 #pragma unroll
@@ -189,8 +190,7 @@ __device__ __forceinline__ void append_rows(const KvAppendParams& p, int t, int 
     if (p.weight) {
       float wf[8];
       bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), wf);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * wf[i];
+      norm8(f, inv, wf);
     }
     put(128 * k + 8 * l, f);
   }

@@ -8,8 +8,8 @@
 // columns (no barrier), one CTA a row above.  The weight's vectors are asked for together with the row's
 // where registers allow; x and the residual pass by L1, which keeps the weight.  bf16 rows written off the
 // vector boundaries (an odd width) go value by value instead, neighbouring columns in neighbouring lanes.
-// 16384 x 5120 with residual to e4m3: 99 us, 88 % of the copy's bandwidth; 8000 x 8192 to bf16 80 us, 96 %;
-// one row of 8192 2.5 us.
+// 16384 x 5120 with residual to e4m3: 94 us, 92 % of the copy's bandwidth; 8000 x 8192 to bf16 80 us, 97 %;
+// one row of 8192 2.4 us.
 //
 // max|y| and the sum keep a NaN (a row that holds one is NaN throughout).
 #include "mla_step.h"
@@ -124,8 +124,7 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
       float f[8];
       bf16x8_unpack(xv[k], h[k]);
       bf16x8_unpack(rv[k], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[k][i] += f[i];
+      add8(h[k], f);
       store(p.residual_out, p.residual_out_stride, wide & kWideRo, k, h[k]);
     }
   } else {
@@ -160,8 +159,7 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
     if constexpr (!kWeightFirst) wv[k] = load(p.weight, 0, 0, wide & kWideW, k);
     float w[8];
     bf16x8_unpack(wv[k], w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * inv * w[i];   // y; behind the row's end 0
+    norm8(h[k], inv, w);   // y; behind the row's end 0
   }
 
   if constexpr (!kE4m3) {
@@ -200,8 +198,7 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
       const float s = nan_max(kMinScale, fin ? quotient(m[k], kE4m3Max, 1.f / kE4m3Max) : m[k]), s_or_0 = fin ? s : 0.f;
       float inv_s;
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv_s) : "f"(s));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[k][i] = quotient(h[k][i], s_or_0, inv_s);
+      quotient8(h[k], s_or_0, inv_s);
       float* sc = p.scales + t * groups + (whole ? 0 : c >> group_log2);
       const bool writes = whole ? sub == 0 && k == 0 : n > 0 && (c & (p.group - 1)) == 0;
       if (writes && guard_span(nullptr, G_STEP_OUT, sc, 4, p.scales, (uint64_t)p.T * groups * 4)) *sc = s;

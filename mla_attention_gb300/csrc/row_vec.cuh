@@ -41,8 +41,31 @@ __device__ __forceinline__ float rsqrt_newton(float x) {
   const float y = rsqrtf(x), z = fmaf(0.5f * y, fmaf(-(x * y), y, 1.f), y);
   return x > 0.f && x < __int_as_float(0x7f800000) ? z : y;
 }
+
+// Eight columns, two to an instruction.
+__device__ __forceinline__ void quotient8(float (&f)[8], float b, float r) {
+  const uint64_t rr = f32x2(r, r), nb = f32x2(-b, -b);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t a = f32x2(f[i], f[i + 1]), q = mul_f32x2(a, rr);
+    f32x2_split(fma_f32x2(fma_f32x2(q, nb, a), rr, q), f[i], f[i + 1]);
+  }
+}
+__device__ __forceinline__ void add8(float (&f)[8], const float (&g)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) f32x2_split(add_f32x2(f32x2(f[i], f[i + 1]), f32x2(g[i], g[i + 1])), f[i], f[i + 1]);
+}
+__device__ __forceinline__ void norm8(float (&f)[8], float inv, const float (&w)[8]) {   // (f * inv) * w
+  const uint64_t ii = f32x2(inv, inv);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    f32x2_split(mul_f32x2(mul_f32x2(f32x2(f[i], f[i + 1]), ii), f32x2(w[i], w[i + 1])), f[i], f[i + 1]);
+}
 __device__ __forceinline__ float square_sum8(const float (&f)[8]) {   // pairwise: a row's error is that of a few roundings
-  return ((f[0] * f[0] + f[1] * f[1]) + (f[2] * f[2] + f[3] * f[3])) + ((f[4] * f[4] + f[5] * f[5]) + (f[6] * f[6] + f[7] * f[7]));
+  const uint64_t a = f32x2(f[0], f[1]), b = f32x2(f[2], f[3]), c = f32x2(f[4], f[5]), d = f32x2(f[6], f[7]);
+  float lo, hi;
+  f32x2_split(add_f32x2(fma_f32x2(a, a, mul_f32x2(b, b)), fma_f32x2(c, c, mul_f32x2(d, d))), lo, hi);
+  return lo + hi;
 }
 
 // n (1..8) bf16 values at src one by one; the rest are 0
