@@ -33,10 +33,10 @@ __device__ __forceinline__ float nan_max(float a, float b) {
   return r;
 }
 
-// the larger magnitude, with some sign; NaN if either is
-__device__ __forceinline__ float nan_max_abs(float a, float b) {
+// the largest magnitude of three; NaN if any is
+__device__ __forceinline__ float nan_max_abs(float a, float b, float c) {
   float r;
-  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -50,13 +50,12 @@ __device__ __forceinline__ float warp_reduce(float v) {
   return v;
 }
 
-// over the row's threads: its warp, or with kBlock its CTA
+// over the row's threads: its warp, or with kBlock its CTA, which gives each reduction a buffer of its own
 template <bool kBlock, bool kMax>
-__device__ __forceinline__ float row_reduce(float v, float* red) {
+__device__ __forceinline__ float row_reduce(float v, float (&red)[32]) {
   v = warp_reduce<kMax>(v);
   if constexpr (kBlock) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    __syncthreads();
     if (lane == 0) red[wid] = v;
     __syncthreads();
     v = warp_reduce<kMax>(lane < warps ? red[lane] : 0.f);
@@ -68,7 +67,7 @@ enum : int { kWideX = 1, kWideR = 2, kWideRo = 4, kWideW = 8, kWideOut = 16 };  
 
 template <int NV, bool kBlock, bool kE4m3, bool kStrided>
 __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __grid_constant__ RmsNormParams p, int wide) {
-  __shared__ float red[32];
+  __shared__ float red[3][32];
   const int per_row = kBlock ? blockDim.x : 32, sub = kBlock ? threadIdx.x : threadIdx.x & 31;
   const int64_t t = kBlock ? blockIdx.x : (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
   if (!kBlock && t >= p.T) return;
@@ -135,13 +134,13 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
     for (int k = 0; k < NV; ++k) bf16x8_unpack(xv[k], h[k]);
   }
 
-  auto sum_squares = [&] {
+  auto sum_squares = [&](float (&buf)[32]) {
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) sum += square_sum8(h[k]);
-    return row_reduce<kBlock, false>(sum, red);
+    return row_reduce<kBlock, false>(sum, buf);
   };
-  float sum = sum_squares(), eps = p.eps;
+  float sum = sum_squares(red[0]), eps = p.eps;
   if (sum > 3e38f) {
     // The squares leave fp32's range: the row once more at 2^-96 of its size, where the largest
     // values' squares still add up and the smallest that count still have one.
@@ -151,7 +150,7 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[k][i] *= 0x1p-96f;
-    sum = sum_squares();
+    sum = sum_squares(red[1]);
   }
   const float inv = rsqrt_newton(sum / (float)p.D + eps);
 #pragma unroll
@@ -172,15 +171,14 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
     for (int k = 0; k < NV; ++k) {
       m[k] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m[k] = nan_max_abs(m[k], h[k][i]);
-      m[k] = fabsf(m[k]);
+      for (int i = 0; i < 8; i += 2) m[k] = nan_max_abs(m[k], h[k][i], h[k][i + 1]);
       all = nan_max(all, m[k]);
     }
     const bool whole = p.group == p.D;
     const int group_log2 = 31 - __clz(p.group);   // used where p.group is a power of two
     const int64_t groups = whole ? 1 : p.D >> group_log2;
     if (whole) {
-      all = row_reduce<kBlock, true>(all, red);
+      all = row_reduce<kBlock, true>(all, red[2]);
 #pragma unroll
       for (int k = 0; k < NV; ++k) m[k] = all;
     } else {   // a group is 4, 8 or 16 vectors, held by as many lanes of one warp
