@@ -128,41 +128,66 @@ __device__ __forceinline__ void turn_heads(const KvAppendParams& p, int t, int f
   }
 }
 
-// ---- two rows: of each, lane l of its 16 holds latent columns 128 k + 8 l .. (k = 0..3), lanes 0-3 the
-// RoPE columns as well.  t is past the last token for the half that has none. ----
-__device__ __forceinline__ void append_rows(const KvAppendParams& p, int t, int lane) {
-  const bool neox = p.is_neox != 0, real = t < p.T;
-  const int l = lane & 15, u = lane & 3;
-  int pos = -1;
-  int64_t slot = -1;
-  uint4 v[4], ka, kb;
-  if (real) {
-    pos = token_int(p, p.positions, t);
-    slot = token_int(p, p.slots, t);
+// Where token t's row goes.  A position or slot outside its range but -1 is reported by the caller that
+// asks for it.
+struct Target {
+  int pos;            // -1: nothing is written
+  int64_t slot;       // -1: no cache row
+};
+__device__ __forceinline__ Target row_target(const KvAppendParams& p, int pos, int64_t slot, bool report) {
+  if (pos < 0 || pos >= p.max_pos) {
+    if (pos != -1 && report) record_error(p.err, DEV_RANGE_BASE | 0x78);
+    return {-1, -1};
+  }
+  if (slot < 0 || slot >= p.cache_rows) {
+    if (slot != -1 && report) record_error(p.err, DEV_RANGE_BASE | 0x79);
+    slot = -1;
+  }
+  return {slot >= 0 || p.kv_out ? pos : -1, slot};
+}
+// columns col .. col + 7 of token t's row
+__device__ __forceinline__ void put_row8(const KvAppendParams& p, int t, int64_t slot, int col, const float (&f)[8]) {
+  if (slot >= 0) store_cache8(p, slot, col, f);
+  if (p.kv_out) store16(p, p.kv_out + t * p.kv_out_stride + col, p.kv_out, (p.T - 1) * p.kv_out_stride + kDk, f);
+}
+
+// ---- the RoPE columns of eight rows, four lanes a row ----
+__device__ __forceinline__ void append_pe(const KvAppendParams& p, int t, int lane) {
+  if (t >= p.T) return;
+  const bool neox = p.is_neox != 0;
+  const int u = lane & 3, pos = token_int(p, p.positions, t);
+  const int64_t slot = token_int(p, p.slots, t), ext = (p.T - 1) * p.k_pe_stride + kR;
+  const __nv_bfloat16* src = p.k_pe + t * p.k_pe_stride + 8 * u;
+  const uint4 lo = load16(p, src, p.k_pe, ext), hi = load16(p, src + 32, p.k_pe, ext);
+  const Target to = row_target(p, pos, slot, false);
+  if (to.pos < 0) return;
+  const Angles g = load_angles(p, to.pos, u, neox);
+  float a[8], b[8];
+  bf16x8_unpack(lo, a);
+  bf16x8_unpack(hi, b);
+  turn(a, b, g, neox);
+  put_row8(p, t, to.slot, kLatent + 8 * u, a);
+  put_row8(p, t, to.slot, kLatent + 32 + 8 * u, b);
+}
+
+// ---- the latents of two rows: lane l of a row's 16 holds columns 128 k + 8 l .. (k = 0..3).  t is past the
+// last token for the half that has none. ----
+__device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, int lane) {
+  const int l = lane & 15;
+  Target to = {-1, -1};
+  uint4 v[4];
+  if (t < p.T) {
+    const int pos = token_int(p, p.positions, t);
+    const int64_t slot = token_int(p, p.slots, t);
     const __nv_bfloat16* src = p.c_kv + t * p.c_kv_stride + 8 * l;
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = load16(p, src + 128 * k, p.c_kv, (p.T - 1) * p.c_kv_stride + kLatent);
-    if (l < 4) {
-      const __nv_bfloat16* pe = p.k_pe + t * p.k_pe_stride + 8 * u;
-      ka = load16(p, pe, p.k_pe, (p.T - 1) * p.k_pe_stride + kR);
-      kb = load16(p, pe + 32, p.k_pe, (p.T - 1) * p.k_pe_stride + kR);
-    }
-    if (pos < 0 || pos >= p.max_pos) {
-      if (pos != -1 && l == 0) record_error(p.err, DEV_RANGE_BASE | 0x78);
-      pos = -1;
-    }
-    if (slot < 0 || slot >= p.cache_rows) {
-      if (slot != -1 && pos >= 0 && l == 0) record_error(p.err, DEV_RANGE_BASE | 0x79);
-      slot = -1;
-    }
+    to = row_target(p, pos, slot, l == 0);
   }
-  const bool row = pos >= 0 && (slot >= 0 || p.kv_out);   // something to write
-  Angles ang;
-  if (row && l < 4) ang = load_angles(p, pos, u, neox);
   float inv = 1.f;
   if (p.weight) {
     float sum = 0.f;
-    if (row) {
+    if (to.pos >= 0) {
       float part[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -176,13 +201,7 @@ __device__ __forceinline__ void append_rows(const KvAppendParams& p, int t, int 
     for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
     inv = rsqrt_newton(sum * (1.f / kLatent) + p.eps);
   }
-  if (!row) return;
-  __nv_bfloat16* rows = p.kv_out ? p.kv_out + t * p.kv_out_stride : nullptr;
-  const int64_t ext_r = (p.T - 1) * p.kv_out_stride + kDk;
-  auto put = [&](int col, const float(&f)[8]) {
-    if (slot >= 0) store_cache8(p, slot, col, f);
-    if (rows) store16(p, rows + col, p.kv_out, ext_r, f);
-  };
+  if (to.pos < 0) return;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float f[8];
@@ -192,35 +211,27 @@ __device__ __forceinline__ void append_rows(const KvAppendParams& p, int t, int 
       bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), wf);
       norm8(f, inv, wf);
     }
-    put(128 * k + 8 * l, f);
-  }
-  if (l < 4) {
-    float a[8], b[8];
-    bf16x8_unpack(ka, a);
-    bf16x8_unpack(kb, b);
-    turn(a, b, ang, neox);
-    put(kLatent + 8 * u, a);
-    put(kLatent + 32 + 8 * u, b);
+    put_row8(p, t, to.slot, 128 * k + 8 * l, f);
   }
 }
 
-// The first warps bring the rows, two each, the others the heads.
+// The first warps bring two latents each, the next the RoPE columns of eight rows, the others the heads.
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   const int lane = threadIdx.x & 31;
-  const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5), row_warps = ((uint32_t)p.T + 1) / 2;
-  if (w < row_warps) {
-    append_rows(p, 2 * w + (lane >> 4), lane);
-  } else {
-    const uint32_t parts = (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp, i = w - row_warps;
-    const uint32_t t = parts ? i / parts : p.T;
-    if (t < (uint32_t)p.T) turn_heads(p, t, (i - t * parts) * kHeadsPerWarp, lane);
-  }
+  uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t latents = ((uint32_t)p.T + 1) / 2, pes = ((uint32_t)p.T + 7) / 8;
+  if (w < latents) return append_latents(p, 2 * w + (lane >> 4), lane);
+  w -= latents;
+  if (w < pes) return append_pe(p, 8 * w + (lane >> 2), lane);
+  w -= pes;
+  const uint32_t parts = (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp, t = parts ? w / parts : p.T;
+  if (t < (uint32_t)p.T) turn_heads(p, t, (w - t * parts) * kHeadsPerWarp, lane);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
-  const int64_t warps = ((int64_t)p.T + 1) / 2 + (int64_t)p.T * ((p.H + kHeadsPerWarp - 1) / kHeadsPerWarp);
+  const int64_t warps = ((int64_t)p.T + 1) / 2 + ((int64_t)p.T + 7) / 8 + (int64_t)p.T * ((p.H + kHeadsPerWarp - 1) / kHeadsPerWarp);
   kv_append_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
