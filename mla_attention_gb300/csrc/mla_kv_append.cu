@@ -5,13 +5,17 @@
 // A pair (a, b) of a RoPE vector turns by its angle: (a cos - b sin, a sin + b cos); pair i is
 // (x[2i], x[2i+1]) or, with is_neox, (x[i], x[i+32]).  Everything is computed in fp32 and rounded once.
 //
-// HBM-bound: per token 1152 bytes in, 576 or 1152 out and 256 per head of q.  Half a warp per cache row and a
-// warp per 16 heads of a token's q, all independent: no shared memory, no barrier.  What a warp reads goes
+// HBM-bound: per token 1152 bytes in, 576 or 1152 out and 256 per head of q.  Half a warp per latent, four
+// lanes per row's RoPE columns and a warp per 16 heads of a token's q (eight: 55 us for the prefill below),
+// all independent: no shared memory, no barrier.  What a warp reads goes
 // out before it looks at its token's position and slot: a chain of three loads would leave most of the
-// bandwidth idle; and two rows a warp, each lane with four 16-byte vectors, keep twice as many bytes on
+// bandwidth idle; and two latents a warp, each lane with four 16-byte vectors, keep twice as many bytes on
 // the way as one.  In both pairings a lane's two 16-byte vectors at columns 8u and 32 + 8u (u = 0..3)
 // hold whole pairs, so four lanes serve a RoPE vector, read its angles once and use them for all of
 // the warp's heads.
+// Prefill of 8192 tokens with 128 heads and the rows written too 47.9 us, 92 % of the copy's bandwidth (the cache
+// stays partly in L2); 32768 rows to e4m3 without heads 14.0 us, 69 %, bound by issue; a decode step of
+// 64 tokens with 128 heads 2.5 us.
 #include "mla_step.h"
 #include "row_vec.cuh"
 
@@ -215,10 +219,11 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
   }
 }
 
+// CTAs of four warps: of eight, 15.0 us for the 32768 rows above and 2.7 for the decode step.
 // The first warps bring two latents each, the next the RoPE columns of eight rows, the others the heads.
-__global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(128, 8) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   const int lane = threadIdx.x & 31;
-  uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
   const uint32_t latents = ((uint32_t)p.T + 1) / 2, pes = ((uint32_t)p.T + 7) / 8;
   if (w < latents) return append_latents(p, 2 * w + (lane >> 4), lane);
   w -= latents;
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
   const int64_t warps = ((int64_t)p.T + 1) / 2 + ((int64_t)p.T + 7) / 8 + (int64_t)p.T * ((p.H + kHeadsPerWarp - 1) / kHeadsPerWarp);
-  kv_append_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
+  kv_append_kernel<<<(unsigned)((warps + 3) / 4), 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
