@@ -24,6 +24,9 @@
 // every warp waiting for loads and for the slowest.
 // Few columns with a long k are cut over a cluster's CTAs, whose sums are joined in shared memory in
 // a fixed order.
+// 8192 columns, k of 16384, groups of 128, 4 tokens: 19.3 us, 53 % of the copy's bandwidth, at half of the
+// issue slots.  128 heads of 512 columns, k of 128, one token 5.2 us, of 128 columns, k of 512, 17 tokens
+// 6.0: a launch, one chunk brought in and one joined.
 #include <type_traits>
 
 #include "mla_step.h"
@@ -96,6 +99,27 @@ __device__ __noinline__ float plain_value(const BmmW4Params& p, int tok, int h, 
   return v;
 }
 
+// kVec scales: fp32 to a word each, bf16 two to a word (the first kVec / 2 words)
+template <int kVec>
+__device__ __forceinline__ void load_scales(uint32_t* w, const uint8_t* f, bool f32) {
+  if constexpr (kVec == 4) {
+    if (f32) {
+      const uint4 v = *reinterpret_cast<const uint4*>(f);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(f);
+      w[0] = v.x, w[1] = v.y;
+    }
+  } else if constexpr (kVec == 2) {
+    if (f32) {
+      const uint2 v = *reinterpret_cast<const uint2*>(f);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(f);
+    }
+  }
+}
+
 // GL: 2^GL pieces of 32 k are a group
 template <int NT, int GL>
 struct W4Smem {
@@ -147,6 +171,10 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
     constexpr int kUnits = (KC * NT + kHelpers - 1) / kHelpers;     // (step, eight tokens) of a helper
     constexpr int kRow = KC * kPer, kScales = kCols * kRow / 32;    // a lane has kScales neighbours of one column
     constexpr int kTiles = kWarps / kHelpers;                       // warps whose scales a helper brings
+    // Scales come one by one, or kVec in a load (8192 columns, k of 16384: groups of 32 28.4 -> 24.8 us, of 128 20.1 ->
+    // 19.4; groups of 64 would spill: 128 heads, k of 128, 8 tokens 5.8 -> 6.4).
+    constexpr int kVec = NT > 1 || GL == 1 ? 1 : GL == 0 ? 4 : 2;
+    const bool vec_s = kVec > 1 && plan.vec_s && groups % kVec == 0 && u0 * kPer % kVec == 0, pairs = vec_s && !p.scales_f32;
     const uint64_t ext_x = ((uint64_t)(p.T - 1) * p.x_stride_t + (uint64_t)(p.H - 1) * p.x_stride_h + p.K) * 2;
     const uint64_t ext_s = (uint64_t)p.H * p.N * groups * scale_bytes;
     const __nv_bfloat16* xh = p.x + h * p.x_stride_h + tok0 * p.x_stride_t + 8 * t;   // lane (g, t): token g, k 8t ..
@@ -171,6 +199,20 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
             xv[n][i] = plan.vec_x ? *reinterpret_cast<const uint4*>(from + k) : load_row8_narrow(from + k, 8);
         }
       }
+      if constexpr (kVec > 1)
+        if (vec_s) {
+          if (chunk * KC < count)
+#pragma unroll
+            for (int w = 0; w < kTiles; ++w)
+#pragma unroll
+              for (int r = 0; r < kScales; r += kVec) {
+                const int q = chunk * kRow + r;
+                const uint8_t* f = scale[w] + q * scale_bytes;
+                if (u0 * kPer + q0 + q < groups && guard_span(p.err, G_STEP_IN, f, kVec * scale_bytes, p.scales, ext_s))
+                  load_scales<kVec>(&sv[w][r], f, p.scales_f32);
+              }
+          return;
+        }
 #pragma unroll
       for (int w = 0; w < kTiles; ++w)
 #pragma unroll
@@ -212,9 +254,14 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
 #pragma unroll
       for (int w = 0; w < kTiles; ++w)
 #pragma unroll
-        for (int r = 0; r < kScales; ++r)
-          s.scale[b * KC + (q0 + r) / kPer][(q0 + r) % kPer][helper + w * kHelpers][col & 7][col >> 3] =
-              __uint_as_float(sv[w][r] << to_f32) * kDown;
+        for (int r = 0; r < kScales; ++r) {
+          uint32_t v = sv[w][r] << to_f32;
+          if (kVec > 1 && pairs) {   // two to a word, in the first words of a load's
+            v = sv[w][r / kVec * kVec + r % kVec / 2];
+            v = r & 1 ? v & 0xffff0000u : v << 16;
+          }
+          s.scale[b * KC + (q0 + r) / kPer][(q0 + r) % kPer][helper + w * kHelpers][col & 7][col >> 3] = __uint_as_float(v) * kDown;
+        }
       warp_arrive(&s.full[b]);
       load(chunk + 1);
     }
@@ -367,8 +414,9 @@ cudaError_t launch(const BmmW4Params& p, const W4Plan& plan, cudaStream_t stream
 cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream) {
   W4Plan plan;
   plan.vec_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.x_stride_t % 8 == 0 && p.x_stride_h % 8 == 0;
+  plan.vec_s = reinterpret_cast<uintptr_t>(p.scales) % (p.scales_f32 ? 16 : 8) == 0;
   // k is cut over a cluster's CTAs, two ways at a time, while all of them still run at once: two on an SM, or one where
-  // more tokens take its registers.  (8192 columns, k of 16384, 4 tokens, cut 1, 2, 4, 8 ways: 40, 24, 19.5,
+  // more tokens take its registers.  (8192 columns, k of 16384, 4 tokens, cut 1, 2, 4, 8 ways: 40, 24, 19.3,
   // 24.5 us; 2102 columns, k of 6400: 8 ways 7.9 us, 2 ways 11.4.)
   const int steps = (p.K + kStep - 1) / kStep;
   const int64_t blocks = (int64_t)p.H * ((p.N + kWarps * kCols - 1) / (kWarps * kCols)) * ((p.T + 63) / 64);

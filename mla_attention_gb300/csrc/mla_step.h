@@ -74,6 +74,7 @@ struct BmmW4Params {
 struct W4Plan {
   int cluster;     // CTAs along k
   int vec_x;       // x rows on 16-byte boundaries
+  int vec_s;       // scales likewise (bf16 ones on 8-byte boundaries)
 };
 constexpr int kW4MaxT = 1 << 19;
 cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream);

@@ -499,6 +499,21 @@ def test_w4_widths(T, H, N, K, group):
     _check_w4(T, H, N, K, group, f32=N % 2 == 1, strided=T == 5)
 
 
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("off", [0, 1, 2, 4])
+@pytest.mark.parametrize("H,N,K,group", [(3, 40, 256, 32), (1, 64, 1792, 64), (1, 64, 1792, 128), (2, 20, 1664, 128)])
+def test_w4_scales_off_their_boundaries(H, N, K, group, off, f32):
+    g = torch.Generator().manual_seed(N + K + off)
+    w4, scales = _w4(H, N, K, group, f32, g)
+    buf = torch.full((scales.numel() + off,), float("nan"), dtype=scales.dtype, device=dev())
+    at = buf[off:].view(scales.shape)
+    at.copy_(scales)
+    x = gen.randn_bf16((3, H, K), g).to(dev())
+    out = mla_bmm_w4(x, w4, at)
+    ref, mass = so.bmm_w4(to_np(x), w4.cpu().numpy(), to_np(scales))
+    _bf16(out, ref, "out", mass * K * 2.0 ** -24)
+
+
 def test_w4_codes_are_exact():
     """One-hot rows read single weights back: every code of every k, times its own group's scale, in its own place."""
     H, N, K = 2, 24, 256
