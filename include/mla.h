@@ -402,8 +402,8 @@ mla_status mla_rms_norm(const void* x, int64_t x_stride, const void* residual, i
  * q_pe     bf16 rows of 64 at strides (q_pe_stride_t, q_pe_stride_h); NULL with H = 0: no query.
  * q_out    bf16, the fused query: columns 512..575 of rows at (q_out_stride_t, q_out_stride_h) are
  *          written, the others left as they are (q_pe may be those columns: turned in place).
- * kv_out   (nullable) bf16 rows of 576: the tokens' rows for mla_prefill; c_kv and k_pe may be views of the
- *          same rows (in place).
+ * kv_out   (nullable) bf16 rows of 576: the tokens' rows for mla_prefill; c_kv and k_pe may be their columns
+ *          0..511 and 512..575 (in place), and overlap them in no other way.
  * positions DEVICE int32 [T]: -1 marks a row that holds no token (nothing is written for it); another
  *          position outside [0, max_pos) records MLA_ERR_DEVICE_RANGE and is skipped likewise.
  * slots    DEVICE int32 [T]: cache rows (mla_slot_map).  -1: no cache row is written (q_out and
@@ -431,7 +431,7 @@ mla_status mla_kv_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe
  * w4       bytes [H, N, K / 2] contiguous, 16-byte aligned: byte j of a row holds the code of k = 2j in
  *          its low half and that of k = 2j + 1 in its high half.
  * scales   [H, N, K / group] contiguous, bf16 or (scales_f32) fp32.
- * group    32, 64 or 128, dividing K.
+ * group    32, 64 or 128, dividing K; K <= 2^30.
  * out      bf16, element (t, h, n) at out + t * out_stride_t + h * out_stride_h + n; only these are
  *          written (the latent columns of a fused query: strides (H * 576, 576)).
  * workspace: >= 256 bytes (the status word).

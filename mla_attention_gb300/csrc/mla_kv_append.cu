@@ -188,22 +188,33 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
     for (int k = 0; k < 4; ++k) v[k] = load16(p, src + 128 * k, p.c_kv, (p.T - 1) * p.c_kv_stride + kLatent);
     to = row_target(p, pos, slot, l == 0);
   }
-  float inv = 1.f;
+  float inv = 1.f, down = 1.f;
   if (p.weight) {
-    float sum = 0.f;
-    if (to.pos >= 0) {
-      float part[4];
+    auto mean_square = [&] {
+      float sum = 0.f;
+      if (to.pos >= 0) {
+        float part[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float f[8];
-        bf16x8_unpack(v[k], f);
-        part[k] = square_sum8(f);
+        for (int k = 0; k < 4; ++k) {
+          float f[8];
+          bf16x8_unpack(v[k], f);
+          if (down != 1.f) scale8(f, down);
+          part[k] = square_sum8(f);
+        }
+        sum = (part[0] + part[1]) + (part[2] + part[3]);
       }
-      sum = (part[0] + part[1]) + (part[2] + part[3]);
-    }
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-    inv = rsqrt_newton(sum * (1.f / kLatent) + p.eps);
+      for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      return sum * (1.f / kLatent);
+    };
+    float mean = mean_square(), eps = p.eps;
+    const bool huge = mean > 5e35f;
+    if (__any_sync(~0u, huge)) {   // the squares leave fp32's range: these rows once more at 2^-96 of their size
+      down = huge ? 0x1p-96f : 1.f;
+      const float again = mean_square();
+      if (huge) mean = again, eps = eps * down * down;
+    }
+    inv = rsqrt_newton(mean + eps);
   }
   if (to.pos < 0) return;
 #pragma unroll
@@ -213,6 +224,7 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
     if (p.weight) {
       float wf[8];
       bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), wf);
+      if (down != 1.f) scale8(f, down);
       norm8(f, inv, wf);
     }
     put_row8(p, t, to.slot, 128 * k + 8 * l, f);

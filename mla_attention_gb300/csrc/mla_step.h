@@ -76,7 +76,7 @@ struct W4Plan {
   int vec_x;       // x rows on 16-byte boundaries
   int vec_s;       // scales likewise (bf16 ones on 8-byte boundaries)
 };
-constexpr int kW4MaxT = 1 << 19;
+constexpr int kW4MaxT = 1 << 19, kW4MaxK = 1 << 30;
 cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream);
 
 }  // namespace mla

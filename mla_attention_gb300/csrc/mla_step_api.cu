@@ -208,8 +208,8 @@ mla_status mla_bmm_w4(const void* x, int64_t x_stride_t, int64_t x_stride_h, con
   MLA_REQUIRE(group == 32 || group == 64 || group == 128, "mla_bmm_w4: group must be 32, 64 or 128 (got %d)", group);
   MLA_REQUIRE(K % group == 0, "mla_bmm_w4: K must be a multiple of the group (got %d, %d)", K, group);
   MLA_REQUIRE(scales_f32 == 0 || scales_f32 == 1, "mla_bmm_w4: scales_f32 must be 0 or 1");
-  MLA_REQUIRE((int64_t)H * N <= INT32_MAX && T <= kW4MaxT && H <= 65535, "mla_bmm_w4: H <= 65535, H * N below 2^31 and T <= %d",
-              kW4MaxT);
+  MLA_REQUIRE((int64_t)H * N <= INT32_MAX && T <= kW4MaxT && H <= 65535 && K <= kW4MaxK,
+              "mla_bmm_w4: H <= 65535, H * N below 2^31, T <= %d and K <= %d", kW4MaxT, kW4MaxK);
   if (!workspace || workspace_bytes < kWsHeader) return fail(MLA_ERR_WORKSPACE, "mla_bmm_w4: workspace must hold %zu bytes", (size_t)kWsHeader);
   if (T == 0) return finish(cudaSuccess, "");
   MLA_REQUIRE(x && w4 && scales && out, "mla_bmm_w4: every tensor is required");

@@ -55,6 +55,11 @@ __device__ __forceinline__ void add8(float (&f)[8], const float (&g)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; i += 2) f32x2_split(add_f32x2(f32x2(f[i], f[i + 1]), f32x2(g[i], g[i + 1])), f[i], f[i + 1]);
 }
+__device__ __forceinline__ void scale8(float (&f)[8], float s) {
+  const uint64_t ss = f32x2(s, s);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) f32x2_split(mul_f32x2(f32x2(f[i], f[i + 1]), ss), f[i], f[i + 1]);
+}
 __device__ __forceinline__ void norm8(float (&f)[8], float inv, const float (&w)[8]) {   // (f * inv) * w
   const uint64_t ii = f32x2(inv, inv);
 #pragma unroll

@@ -84,7 +84,8 @@ def test_append_refuses(L, kw):
 
 @pytest.mark.parametrize("kw", [dict(T=-1), dict(H=0), dict(N=0), dict(K=0), dict(group=16), dict(group=48), dict(K=96), dict(f32=2), dict(x=None),
                                 dict(w=None), dict(s=None), dict(out=None), dict(x=BYTE), dict(out=BYTE), dict(s=BYTE), dict(s=ODD, f32=1), dict(w=ODD),
-                                dict(xt=-1), dict(xh=-1), dict(ot=32), dict(oh=31), dict(H=70000), dict(H=60000, N=60000), dict(T=(1 << 19) + 1)])
+                                dict(xt=-1), dict(xh=-1), dict(ot=32), dict(oh=31), dict(H=70000), dict(H=60000, N=60000), dict(T=(1 << 19) + 1),
+                                dict(K=(1 << 30) + 64)])
 def test_w4_refuses(L, kw):
     assert w4(L, **kw) == 1 and b"mla_bmm_w4" in L.mla_last_error_string()
 
