@@ -77,8 +77,16 @@ def _shape(t, name, dims):
     return shape
 
 
-def _empty(shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+def _empty(shape, dtype, dev, stream):
+    """An output in the memory of the stream that writes it, as under torch.cuda.stream(stream)."""
+    device = torch.device("cuda", dev)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _workspace(ws, dev):
@@ -88,7 +96,11 @@ def _workspace(ws, dev):
     if ws is None:
         ws = _lib._status_cache.get(dev)
         if ws is None:
-            ws = _lib._status_cache[dev] = torch.zeros(256, dtype=_U8, device=torch.device("cuda", dev))
+            if torch.cuda.is_current_stream_capturing():
+                raise MLAError(1, "the first call on a device without a ws allocates the status word: make it before a capture")
+            ws = torch.zeros(256, dtype=_U8, device=torch.device("cuda", dev))
+            torch.cuda.current_stream(dev).synchronize()   # the call may be issued on another stream
+            _lib._status_cache[dev] = ws
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise MLAError(1, f"ws must be a contiguous tensor on cuda:{dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
@@ -128,15 +140,15 @@ def mla_slot_map(lens, new_tokens, block_table, pool, pool_state, page_size: int
     if not 0 <= N <= _INT_MAX:
         raise MLAError(1, f"N must be between 0 and 2^31 - 1, got {N}")
     if positions is None:
-        positions = _empty(N, _I32, dev)
+        positions = _empty(N, _I32, dev, stream)
     if slots is None:
-        slots = _empty(N, _I32, dev)
+        slots = _empty(N, _I32, dev, stream)
     if cu_tokens is None:
-        cu_tokens = _empty(B + 1, _I32, dev)
+        cu_tokens = _empty(B + 1, _I32, dev, stream)
     if lens_out is None:
-        lens_out = _empty(B, _I32, dev)
+        lens_out = _empty(B, _I32, dev, stream)
     if pool_state_out is None:
-        pool_state_out = _empty(2, _I32, dev)
+        pool_state_out = _empty(2, _I32, dev, stream)
     _call("mla_slot_map", dev, stream, _dense(lens, "lens", _I32, dev, (B,)),
           _dense(new_tokens, "new_tokens", _I32, dev, (B,)), B,
           _dense(block_table, "block_table", _I32, dev, (B, max_pages)), max_pages, int(page_size), num_pages,
@@ -154,12 +166,17 @@ def mla_rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None,
     [T, D / group] ([T, 1] with group 0); residual_out = h in bf16 (None without a residual; may be
     the residual itself); scales None with a bf16 out."""
     dev, (T, D) = _device(x, "x", 2)
-    e4m3 = bool(e4m3) if out is None else getattr(out, "dtype", None) is _E4M3
+    if out is None:
+        e4m3 = bool(e4m3)
+    elif e4m3 and getattr(out, "dtype", None) is not _E4M3:
+        raise MLAError(1, f"out must be a torch.Tensor of {_E4M3} with e4m3")
+    else:
+        e4m3 = getattr(out, "dtype", None) is _E4M3
     group = int(group)
     if group and (not e4m3 or group not in (32, 64, 128) or D % group):
         raise MLAError(1, f"group must be 0, or with e4m3 32, 64 or 128 dividing D (got {group}, D = {D})")
     if out is None:
-        out = _empty((T, D), _E4M3 if e4m3 else _BF16, dev)
+        out = _empty((T, D), _E4M3 if e4m3 else _BF16, dev, stream)
     px = _rows(x, "x", _BF16, dev, (T, D))
     pw = _dense(weight, "weight", _BF16, dev, (D,))
     po = _rows(out, "out", _E4M3 if e4m3 else _BF16, dev, (T, D))
@@ -167,7 +184,7 @@ def mla_rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None,
     sr = sro = 0
     if residual is not None:
         if residual_out is None:
-            residual_out = _empty((T, D), _BF16, dev)
+            residual_out = _empty((T, D), _BF16, dev, stream)
         pr, pro = _rows(residual, "residual", _BF16, dev, (T, D)), _rows(residual_out, "residual_out", _BF16, dev, (T, D))
         sr, sro = residual.stride(0), residual_out.stride(0)
     elif residual_out is not None:
@@ -175,7 +192,7 @@ def mla_rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None,
     if e4m3:
         shape = (T, D // group if group else 1)
         if scales is None:
-            scales = _empty(shape, _F32, dev)
+            scales = _empty(shape, _F32, dev, stream)
         ps = _dense(scales, "scales", _F32, dev, shape)
     elif scales is not None:
         raise MLAError(1, "scales go with an e4m3 output")
@@ -206,7 +223,7 @@ def mla_kv_append(c_kv, k_pe, slots, positions, cos_sin, kv_cache, kv_scale: flo
         if H < 1:
             raise MLAError(1, "q_pe must have at least one head")
         if q_out is None:
-            q_out = _empty((T, H, 576), _BF16, dev)
+            q_out = _empty((T, H, 576), _BF16, dev, stream)
         pq, pqo = _rows(q_pe, "q_pe", _BF16, dev, (T, H, 64)), _rows(q_out, "q_out", _BF16, dev, (T, H, 576))
         (qt, qh, _), (ot, oh, _) = q_pe.stride(), q_out.stride()
     elif q_out is not None:
@@ -233,7 +250,7 @@ def mla_bmm_w4(x, w4, scales, out=None, ws=None, stream=None):
     pw = _dense(w4, "w4", _U8, dev, (H, N, K // 2))
     ps = _dense(scales, "scales", _F32 if f32 else _BF16, dev, (H, N, groups))
     if out is None:
-        out = _empty((T, H, N), _BF16, dev)
+        out = _empty((T, H, N), _BF16, dev, stream)
     po = _rows(out, "out", _BF16, dev, (T, H, N))
     (xt, xh, _), (ot, oh, _) = x.stride(), out.stride()
     _call("mla_bmm_w4", dev, stream, px, xt, xh, pw, ps, int(f32), K // groups, T, H, N, K, po,

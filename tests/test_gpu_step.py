@@ -422,6 +422,22 @@ def test_append_in_place(neox):
     assert torch.equal(one.view(-1, 576)[slots.long()], kv)
 
 
+def test_append_norms_rows_whose_squares_overflow():
+    g, d = torch.Generator().manual_seed(12), dev()
+    c = torch.randn((4, 512), generator=g)
+    c[0] *= 2.0 ** 80
+    c[2, 7] = 2.0 ** 100
+    c[3] *= 2.0 ** -30
+    c = c.to(torch.bfloat16).to(d)
+    pe = gen.randn_bf16((4, 64), g).to(d)
+    w = (1 + 0.3 * torch.randn(512, generator=g)).to(torch.bfloat16).to(d)
+    cs, pos = gen.rope_cos_sin(8), _i32([0, 3, 5, 7])
+    cache = torch.zeros((1, 4, 576), dtype=torch.bfloat16, device=d)
+    mla_kv_append(c, pe, _i32([0, 1, 2, 3]).to(d), pos.to(d), cs.to(d), cache, norm_weight=w, eps=0.0)
+    ref, _ = so.kv_append(to_np(c), to_np(pe), pos.numpy(), cs.numpy(), to_np(w), 0.0, None, False)
+    _bf16(cache[0, :, :512], ref[:, :512], "latents")
+
+
 def test_append_saturates_and_keeps_nan():
     d = dev()
     c_kv, k_pe = torch.full((2, 512), 1000.0).bfloat16().to(d), torch.zeros((2, 64)).bfloat16().to(d)
@@ -740,6 +756,45 @@ def test_explicit_stream_argument():
     out, _, _ = mla_rms_norm(x, w, stream=s)
     s.synchronize()
     assert (out == 1).all()
+
+
+def test_outputs_lie_in_the_memory_of_the_stream_that_writes_them():
+    """An output made for a call on another stream is not handed, when dropped, to the current stream's next
+    tensor while the call may still write it."""
+    d, s = dev(), torch.cuda.Stream()
+    x = torch.ones((64, 8192), dtype=torch.bfloat16, device=d)
+    w = torch.ones(8192, dtype=torch.bfloat16, device=d)
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        out, _, _ = mla_rms_norm(x, w, stream=stream)
+        at = out.data_ptr()
+        del out
+        assert torch.empty_like(x).data_ptr() != at
+    torch.cuda.synchronize()
+    assert (mla_rms_norm(x, w, stream=0)[0] == 1).all()
+
+
+def test_a_first_call_inside_a_capture_is_refused():
+    """It would put the status word into the graph's memory."""
+    from mla_attention_gb300 import _lib
+    d = dev()
+    x, w4, scales = (torch.zeros(1, 1, 32, dtype=torch.bfloat16, device=d), torch.zeros(1, 1, 16, dtype=torch.uint8, device=d),
+                     torch.zeros(1, 1, 1, dtype=torch.bfloat16, device=d))
+    out = mla_bmm_w4(x, w4, scales)
+    word = _lib._status_cache.pop(d.index or 0)
+    try:
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            with pytest.raises(MLAError, match="capture"):
+                mla_bmm_w4(x, w4, scales, out=out)
+    finally:
+        _lib._status_cache[d.index or 0] = word
+
+
+def test_norm_refuses_an_output_of_another_type():
+    x = torch.ones((2, 512), dtype=torch.bfloat16, device=dev())
+    with pytest.raises(MLAError) as e:
+        mla_rms_norm(x, x[0], out=torch.empty_like(x), e4m3=True)
+    assert e.value.status == 1
 
 
 def test_w4_stands_in_for_the_absorption_products():
