@@ -14,7 +14,7 @@
 // hold whole pairs, so four lanes serve a RoPE vector, read its angles once and use them for all of
 // the warp's heads.
 // Prefill of 8192 tokens with 128 heads and the rows written too 47.9 us, 92 % of the copy's bandwidth (the cache
-// stays partly in L2); 32768 rows to e4m3 without heads 14.0 us, 69 %, bound by issue; a decode step of
+// stays partly in L2); 32768 rows to e4m3 without heads 14.1 us, 68 %, bound by issue and load latency; a decode step of
 // 64 tokens with 128 heads 2.5 us.
 #include "mla_step.h"
 #include "row_vec.cuh"
@@ -188,7 +188,7 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
     for (int k = 0; k < 4; ++k) v[k] = load16(p, src + 128 * k, p.c_kv, (p.T - 1) * p.c_kv_stride + kLatent);
     to = row_target(p, pos, slot, l == 0);
   }
-  float inv = 1.f, down = 1.f;
+  float inv = 1.f;
   if (p.weight) {
     auto mean_square = [&] {
       float sum = 0.f;
@@ -198,7 +198,6 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
         for (int k = 0; k < 4; ++k) {
           float f[8];
           bf16x8_unpack(v[k], f);
-          if (down != 1.f) scale8(f, down);
           part[k] = square_sum8(f);
         }
         sum = (part[0] + part[1]) + (part[2] + part[3]);
@@ -209,10 +208,22 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
     };
     float mean = mean_square(), eps = p.eps;
     const bool huge = mean > 5e35f;
-    if (__any_sync(~0u, huge)) {   // the squares leave fp32's range: these rows once more at 2^-96 of their size
-      down = huge ? 0x1p-96f : 1.f;
+    if (__any_sync(~0u, huge)) {
+      // The squares leave fp32's range: these rows go on at 2^-70 of their size, exact in bf16 but for values
+      // 2^114 times smaller than the row's largest.
+      if (huge) {
+        eps *= 0x1p-70f;
+        eps *= 0x1p-70f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float f[8];
+          bf16x8_unpack(v[k], f);
+          scale8(f, 0x1p-70f);
+          v[k] = bf16x8_pack(f);
+        }
+      }
       const float again = mean_square();
-      if (huge) mean = again, eps = eps * down * down;
+      if (huge) mean = again;
     }
     inv = rsqrt_newton(mean + eps);
   }
@@ -224,7 +235,6 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
     if (p.weight) {
       float wf[8];
       bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), wf);
-      if (down != 1.f) scale8(f, down);
       norm8(f, inv, wf);
     }
     put_row8(p, t, to.slot, 128 * k + 8 * l, f);
