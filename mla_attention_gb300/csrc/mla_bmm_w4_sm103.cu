@@ -24,9 +24,10 @@
 // every warp waiting for loads and for the slowest.
 // Few columns with a long k are cut over a cluster's CTAs, whose sums are joined in shared memory in
 // a fixed order.
-// 8192 columns, k of 16384, groups of 128, 4 tokens: 19.3 us, 53 % of the copy's bandwidth, at half of the
-// issue slots.  128 heads of 512 columns, k of 128, one token 5.2 us, of 128 columns, k of 512, 17 tokens
-// 6.0: a launch, one chunk brought in and one joined.
+// 8192 columns, k of 16384, groups of 128, 4 tokens: 19.2 us, 53 % of the copy's bandwidth, at half of the
+// issue slots.  128 heads of 512 columns, k of 128, one token 4.6 us, of 128 columns, k of 512, 17 tokens
+// 5.5: a launch, the first chunk's way in and the sums' way out.  Instructions are kept few as well: each is
+// fetched once a launch (the helpers' loads in three places instead of one cost 0.2 us).
 #include <type_traits>
 
 #include "mla_step.h"
@@ -40,6 +41,7 @@ constexpr int kStages = 4;
 constexpr int kStep = 128;          // k per step
 constexpr int kCols = 16;           // columns n of a warp
 constexpr int kTileBytes = kCols * kStep / 2;
+constexpr int kPitch = kCols + 4;   // a token's sums: 16-byte reads, and the writes of a warp hit 32 banks
 constexpr uint32_t kUp = 0x67806780u, kUp4 = 0x65806580u;   // 2^80 and 2^76, twice
 constexpr float kDown = 0x1p53f, kOff = -0x1p-50f;          // 2^(133 - 80), -8 / kDown
 
@@ -127,19 +129,21 @@ struct W4Smem {
   uint4 x[2 * kChunk<NT>][4][NT][32];         // [step][32 k][8 tokens][lane], two chunks
   float off[2 * kChunk<NT>][4 >> GL][NT][8];  // -8 sum x of a step's groups
   float scale[2 * kChunk<NT>][4 >> GL][kWarps][8][2];   // times 2^53, of columns (g, g + 8)
+  float sums[kWarps][8 * NT][kPitch];         // of a warp's columns, [token][column]
   uint64_t full[2], free[2];                  // a chunk's x, sums and scales are in place / read
 };
 
 template <int NT, int GL>
-__global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant__ BmmW4Params p, const W4Plan plan) {
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) bmm_w4_kernel(const __grid_constant__ BmmW4Params p, const W4Plan plan) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTok = 8 * NT, KC = kChunk<NT>;
   W4Smem<NT, GL>& s = *reinterpret_cast<W4Smem<NT, GL>*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int rank = plan.cluster > 1 ? (int)cluster_ctarank() : 0;
-  const int blocks_h = (p.N + kWarps * kCols - 1) / (kWarps * kCols);
+  const int wide = plan.rounds * kWarps * kCols, blocks_h = plan.blocks_h;   // columns of a CTA, CTAs of a head
   const int block = plan.cluster > 1 ? blockIdx.x / plan.cluster : blockIdx.x;
-  const int h = block / blocks_h, n00 = (block - h * blocks_h) * kWarps * kCols, n0 = n00 + warp * kCols;
+  const int h = block / blocks_h, first = (block - h * blocks_h) * wide;
+  const int rounds = min(plan.rounds, (p.N - first + kWarps * kCols - 1) / (kWarps * kCols));
   const int tok0 = blockIdx.y * kTok;
   const int steps = (p.K + kStep - 1) / kStep;
   const int u0 = plan.cluster > 1 ? (int)((int64_t)steps * rank / plan.cluster) : 0;
@@ -180,13 +184,16 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
     const __nv_bfloat16* xh = p.x + h * p.x_stride_h + tok0 * p.x_stride_t + 8 * t;   // lane (g, t): token g, k 8t ..
     const int col = lane % kCols, q0 = lane / kCols * kScales, to_f32 = p.scales_f32 ? 0 : 16;
     const uint8_t* scale[kTiles];
+    auto to_round = [&](int r) {
 #pragma unroll
-    for (int w = 0; w < kTiles; ++w)
-      scale[w] = reinterpret_cast<const uint8_t*>(p.scales) +
-                 (((int64_t)h * p.N + min(n00 + (helper + w * kHelpers) * kCols + col, p.N - 1)) * groups + u0 * kPer + q0) * scale_bytes;
+      for (int w = 0; w < kTiles; ++w)
+        scale[w] = reinterpret_cast<const uint8_t*>(p.scales) +
+                   (((int64_t)h * p.N + min(first + (r * kWarps + helper + w * kHelpers) * kCols + col, p.N - 1)) * groups + u0 * kPer + q0) *
+                       scale_bytes;
+    };
     uint4 xv[kUnits][4];
     uint32_t sv[kTiles][kScales] = {};
-    auto load = [&](int chunk) {   // past T and past K: zeros; scales past K: what was there before, for weights that are not
+    auto load_x = [&](int chunk) {   // past T and past K: zeros
 #pragma unroll
       for (int n = 0; n < kUnits; ++n) {
         const int unit = helper + n * kHelpers, st = unit / NT, tok = tok0 + unit % NT * 8 + g;
@@ -199,6 +206,8 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
             xv[n][i] = plan.vec_x ? *reinterpret_cast<const uint4*>(from + k) : load_row8_narrow(from + k, 8);
         }
       }
+    };
+    auto load_s = [&](int chunk) {   // past K: what was there before, for weights that are not
       if constexpr (kVec > 1)
         if (vec_s) {
           if (chunk * KC < count)
@@ -225,10 +234,7 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
           }
         }
     };
-    load(0);
-    for (int chunk = 0; chunk * KC < count; ++chunk) {
-      const int b = chunk & 1;
-      if (chunk >= 2 && !wait(&s.free[b], ((chunk >> 1) - 1) & 1, W_CHUNK_FREE)) break;
+    auto place_x = [&](int b) {
 #pragma unroll
       for (int n = 0; n < kUnits; ++n) {
         const int unit = helper + n * kHelpers, st = unit / NT, nt = unit % NT;
@@ -251,6 +257,8 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
           }
         }
       }
+    };
+    auto place_s = [&](int b) {
 #pragma unroll
       for (int w = 0; w < kTiles; ++w)
 #pragma unroll
@@ -262,8 +270,23 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
           }
           s.scale[b * KC + (q0 + r) / kPer][(q0 + r) % kPer][helper + w * kHelpers][col & 7][col >> 3] = __uint_as_float(v) * kDown;
         }
-      warp_arrive(&s.full[b]);
-      load(chunk + 1);
+    };
+    // one place in the code for each: a launch waits for its instructions
+    for (int r = 0, chunk = 0, turn = 0;; ++turn) {
+      if (turn > 0) {
+        const int b = chunk & 1, use = r + (chunk >> 1);   // of the chunk's buffer
+        if (use > 0 && !wait(&s.free[b], (use - 1) & 1, W_CHUNK_FREE)) break;
+        if (r == 0) place_x(b);
+        place_s(b);
+        warp_arrive(&s.full[b]);
+        if (++chunk * KC >= count) {
+          chunk = 0;
+          if (++r == rounds) break;
+        }
+      }
+      if (chunk == 0) to_round(r);
+      if (r == 0) load_x(chunk);
+      load_s(chunk);
     }
     if (plan.cluster > 1) {
       cluster_sync();
@@ -275,9 +298,13 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
   // ---- weights: this lane copies piece t of a step of columns g and g + 8 of each 16 (columns past N: any
   // column of the head, nothing of theirs is stored) ----
   const uint8_t* src[2];
+  int n0 = 0;
+  auto to_round = [&](int r) {
+    n0 = first + (r * kWarps + warp) * kCols;
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    src[e] = p.w4 + ((int64_t)h * p.N + min(n0 + 8 * e + g, p.N - 1)) * row_bytes + u0 * (kStep / 2) + 16 * t;
+    for (int e = 0; e < 2; ++e)
+      src[e] = p.w4 + ((int64_t)h * p.N + min(n0 + 8 * e + g, p.N - 1)) * row_bytes + u0 * (kStep / 2) + 16 * t;
+  };
   const int swz = (g >> 1) & 3;
   const uint32_t put = smem_u32(s.w[warp]) + g * 64 + ((t ^ swz) << 4);
   const int left = min(row_bytes, u1 * (kStep / 2)) - u0 * (kStep / 2) - 16 * t;   // > 64 s: step u0 + s has this piece
@@ -293,20 +320,24 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
     if (ok(src[1])) cp_async16_below<kTo + 512, kFrom>(put, src[1], k, left);
     cp_commit();
   };
-  float acc[NT][4] = {}, part[NT][4];
-  fetch(std::integral_constant<int, 0>{}, 0);
-  fetch(std::integral_constant<int, 1>{}, 0);
-  fetch(std::integral_constant<int, 2>{}, 0);
+  auto fetch_first = [&] {
+    fetch(std::integral_constant<int, 0>{}, 0);
+    fetch(std::integral_constant<int, 1>{}, 0);
+    fetch(std::integral_constant<int, 2>{}, 0);
+  };
+  to_round(0);
+  fetch_first();
+  float acc[NT][4], part[NT][4];
   const uint8_t* take[4];   // word t of piece i of column g
 #pragma unroll
   for (int i = 0; i < 4; ++i) take[i] = s.w[warp][0] + g * 64 + ((i ^ swz) << 4) + 4 * t;
   bool live = true;
 
-  auto step = [&](auto at, int base) {
+  auto step = [&](auto at, int base, int r) {
     constexpr int kAt = decltype(at)::value;
     const int j = base + kAt;
     const int chunk = j / KC;
-    if (kAt % KC == 0 && live) live = wait(&s.full[chunk & 1], (chunk >> 1) & 1, W_CHUNK_FULL);
+    if (kAt % KC == 0 && live) live = wait(&s.full[chunk & 1], (r + (chunk >> 1)) & 1, W_CHUNK_FULL);
     cp_wait<kStages - 2>();
     __syncwarp();          // every lane's copies of step j have landed, and step j - 1 is read
     fetch(std::integral_constant<int, kAt + kStages - 1>{}, base);
@@ -340,42 +371,78 @@ __global__ void __launch_bounds__(kThreads) bmm_w4_kernel(const __grid_constant_
     }
     if (kAt % KC == KC - 1) warp_arrive(&s.free[chunk & 1]);
   };
-  for (int base = 0; base < u1 - u0; base += kStages) {
-    const int n = u1 - u0 - base;
-    step(std::integral_constant<int, 0>{}, base);
-    if (n > 1) step(std::integral_constant<int, 1>{}, base);
-    if (n > 2) step(std::integral_constant<int, 2>{}, base);
-    if (n > 3) step(std::integral_constant<int, 3>{}, base);
-    src[0] += kStages * (kStep / 2), src[1] += kStages * (kStep / 2);
+  const uint64_t ext_out = ((uint64_t)(p.T - 1) * p.out_stride_t + (uint64_t)(p.H - 1) * p.out_stride_h + p.N) * 2;
+  const int tokens = min(kTok, p.T - tok0);
+  // ---- a warp's sums in shared memory, out along n, dealt over the cluster's CTAs ----
+  auto total = [&](int tok, int c) {
+    if (plan.cluster == 1) return s.sums[warp][tok][c];
+    float v = 0.f;
+    for (int q = 0; q < plan.cluster; ++q) v += ld_cluster_f32(map_to_rank(smem_u32(&s.sums[warp][tok][c]), q));
+    return v;
+  };
+  auto put_value = [&](int tok, int c, int at) {   // one value, of column `at`
+    float v = total(tok, c);
+    if (!(fabsf(v) < __int_as_float(0x7f800000))) v = plain_value(p, tok0 + tok, h, at);
+    __nv_bfloat16* o = p.out + (tok0 + tok) * p.out_stride_t + h * p.out_stride_h + at;
+    if (guard_span(p.err, G_STEP_OUT, o, 2, p.out, ext_out)) *o = __float2bfloat16_rn(v);
+  };
+  auto epilogue = [&](int at) {   // columns from `at` on
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s.sums[warp][8 * nt + 2 * t + (j & 1)][8 * (j >> 1) + g] = acc[nt][j];
+    if (plan.cluster > 1) cluster_sync();
+    else __syncwarp();
+    if (NT > 1 && plan.cluster == 1) {
+      // Eight columns a lane.  Where a cluster deals the tokens out, single columns keep more lanes at its
+      // loads (2746 columns, k of 4608, 20 tokens: 10.4 us, eight at a time 14.7).
+      for (int i = lane; i < 2 * tokens; i += 32) {
+        const int c = 8 * (i & 1), tok = i >> 1, n = at + c;
+        if (n >= p.N) continue;
+        float f[8];
+        *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&s.sums[warp][tok][c]);
+        *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&s.sums[warp][tok][c + 4]);
+        bool plain = plan.vec_out && n + 8 <= p.N;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) plain = plain && fabsf(f[j]) < __int_as_float(0x7f800000);
+        __nv_bfloat16* o = p.out + (tok0 + tok) * p.out_stride_t + h * p.out_stride_h + n;
+        if (plain) {
+          if (guard_span(p.err, G_STEP_OUT, o, 16, p.out, ext_out)) *reinterpret_cast<uint4*>(o) = bf16x8_pack(f);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < min(8, p.N - n); ++j) put_value(tok, c + j, n + j);
+        }
+      }
+    } else {
+      for (int i = rank * 32 + lane; i < tokens * kCols; i += plan.cluster * 32)
+        if (at + i % kCols < p.N) put_value(i / kCols, i % kCols, at + i % kCols);
+    }
+    __syncwarp();
+  };
+
+  for (int r = 0; r < rounds; ++r) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[nt][j] = 0.f;
+    for (int base = 0; base < count; base += kStages) {
+      const int n = count - base;
+      step(std::integral_constant<int, 0>{}, base, r);
+      if (n > 1) step(std::integral_constant<int, 1>{}, base, r);
+      if (n > 2) step(std::integral_constant<int, 2>{}, base, r);
+      if (n > 3) step(std::integral_constant<int, 3>{}, base, r);
+      src[0] += kStages * (kStep / 2), src[1] += kStages * (kStep / 2);
+    }
+    const int at = n0;
+    if (r + 1 < rounds) {   // the next round's weights come while this one's sums go out
+      __syncwarp();
+      if (count % KC) warp_arrive(&s.free[count / KC & 1]);
+      to_round(r + 1);
+      fetch_first();
+    }
+    epilogue(at);
   }
   cp_wait<0>();
-
-  // ---- a warp's sums, [token][column] in its own ring, out along n ----
-  constexpr int kPitch = kTok * (kCols + 1) * 4 <= (int)sizeof(s.w[0]) ? kCols + 1 : kCols;   // odd where it fits
-  float* sums = reinterpret_cast<float*>(s.w[warp]);
-  static_assert(kTok * kPitch * 4 <= (int)sizeof(s.w[0]), "a warp's sums lie in its ring");
-  __syncwarp();
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sums[(8 * nt + 2 * t + (j & 1)) * kPitch + 8 * (j >> 1) + g] = acc[nt][j];
-  if (plan.cluster > 1) cluster_sync();
-  else __syncwarp();
-  const uint64_t ext_out = ((uint64_t)(p.T - 1) * p.out_stride_t + (uint64_t)(p.H - 1) * p.out_stride_h + p.N) * 2;
-  const int items = min(kTok, p.T - tok0) * kCols;
-  for (int i = rank * 32 + lane; i < items; i += plan.cluster * 32) {   // dealt over the cluster's CTAs
-    const int c = i % kCols, tok = i / kCols, n = n0 + c;
-    if (n >= p.N) continue;
-    float v = 0.f;
-    if (plan.cluster == 1) {
-      v = sums[tok * kPitch + c];
-    } else {
-      for (int r = 0; r < plan.cluster; ++r) v += ld_cluster_f32(map_to_rank(smem_u32(sums + tok * kPitch + c), r));
-    }
-    if (!(fabsf(v) < __int_as_float(0x7f800000))) v = plain_value(p, tok0 + tok, h, n);
-    __nv_bfloat16* o = p.out + (tok0 + tok) * p.out_stride_t + h * p.out_stride_h + n;
-    if (guard_span(p.err, G_STEP_OUT, o, 2, p.out, ext_out)) *o = __float2bfloat16_rn(v);
-  }
   if (plan.cluster > 1) cluster_sync();   // the others may still read this CTA's sums
 }
 
@@ -388,7 +455,7 @@ cudaError_t launch(const BmmW4Params& p, const W4Plan& plan, cudaStream_t stream
     return r != cudaSuccess ? r : cudaFuncSetAttribute(bmm_w4_kernel<NT, GL>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   });
   if (e != cudaSuccess) return e;
-  const int blocks = p.H * ((p.N + kWarps * kCols - 1) / (kWarps * kCols));
+  const int blocks = p.H * plan.blocks_h;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -414,6 +481,7 @@ cudaError_t launch(const BmmW4Params& p, const W4Plan& plan, cudaStream_t stream
 cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream) {
   W4Plan plan;
   plan.vec_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.x_stride_t % 8 == 0 && p.x_stride_h % 8 == 0;
+  plan.vec_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.out_stride_t % 8 == 0 && p.out_stride_h % 8 == 0;
   plan.vec_s = reinterpret_cast<uintptr_t>(p.scales) % (p.scales_f32 ? 16 : 8) == 0;
   // k is cut over a cluster's CTAs, two ways at a time, while all of them still run at once: two on an SM, or one where
   // more tokens take its registers.  (8192 columns, k of 16384, 4 tokens, cut 1, 2, 4, 8 ways: 40, 24, 19.3,
@@ -423,6 +491,14 @@ cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream) {
   const int64_t room = (int64_t)device_sm_count() * (p.T <= 16 ? 2 : 1);
   plan.cluster = 1;
   while (plan.cluster < 8 && 2 * plan.cluster <= steps && blocks * 2 * plan.cluster <= room) plan.cluster *= 2;
+  // Where two chunks hold all of k, a CTA keeps x and goes on to the next columns of its head, so that all CTAs
+  // run at once (128 heads of 512 columns, k of 128, 1, 32, 64 tokens: 5.4, 16.7, 28.4 us with a CTA for every
+  // 128 columns and single columns a lane, 4.6, 7.4, 11.4 so).
+  const int blocks_h = (p.N + kWarps * kCols - 1) / (kWarps * kCols);
+  plan.rounds = 1;
+  if (plan.cluster == 1 && steps <= 2 * (p.T <= 8 ? kChunk<1> : kChunk<8>))
+    while (plan.rounds < blocks_h && blocks / blocks_h * ((blocks_h + plan.rounds - 1) / plan.rounds) > room) ++plan.rounds;
+  plan.blocks_h = (blocks_h + plan.rounds - 1) / plan.rounds;
   if (p.T <= 8) return launch<1>(p, plan, stream);
   if (p.T <= 16) return launch<2>(p, plan, stream);
   if (p.T <= 32) return launch<4>(p, plan, stream);

@@ -73,7 +73,10 @@ struct BmmW4Params {
 };
 struct W4Plan {
   int cluster;     // CTAs along k
+  int rounds;      // of 128 columns a CTA does one after another
+  int blocks_h;    // CTAs of a head's columns
   int vec_x;       // x rows on 16-byte boundaries
+  int vec_out;     // out rows on 16-byte boundaries
   int vec_s;       // scales likewise (bf16 ones on 8-byte boundaries)
 };
 constexpr int kW4MaxT = 1 << 19, kW4MaxK = 1 << 30;

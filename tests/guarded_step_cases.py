@@ -42,6 +42,8 @@ def w4_cases():
     for args in ((1, 3, 512, 128, 32), (17, 2, 128, 512, 64), (65, 1, 100, 1024, 128), (5, 5, 33, 160, 32), (9, 1, 7, 4096, 128)):
         cases._check_w4(*args, f32=args[0] == 5, strided=args[0] == 9)
     cases.test_w4_large_and_small_values(9)
+    for args in ((1, 128, 512, 128, 32), (17, 60, 700, 512, 64)):
+        cases._check_w4(*args)
 
 
 if __name__ == "__main__":

@@ -515,6 +515,28 @@ def test_w4_widths(T, H, N, K, group):
     _check_w4(T, H, N, K, group, f32=N % 2 == 1, strided=T == 5)
 
 
+@pytest.mark.parametrize("T,H,N,K,group", [(1, 128, 512, 128, 32), (3, 90, 700, 1024, 128), (5, 90, 700, 640, 64), (17, 60, 700, 512, 64),
+                                           (64, 40, 700, 384, 32), (130, 24, 513, 256, 128)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_w4_several_rounds_of_columns(T, H, N, K, group, strided):
+    _check_w4(T, H, N, K, group, f32=strided, strided=strided)
+
+
+def test_w4_infinity_in_several_rounds():
+    g = torch.Generator().manual_seed(3)
+    w4, scales = _w4(60, 700, 512, 64, False, g)
+    x = gen.randn_bf16((20, 60, 512), g)
+    x[3, 59, 500] = float("inf")
+    out, clean = to_np(mla_bmm_w4(x.to(dev()), w4, scales)), x.clone()
+    clean[3, 59, 500] = 0
+    ref, mass = so.bmm_w4(to_np(clean), w4.cpu().numpy(), to_np(scales))
+    code = so.unpack_w4(w4.cpu().numpy(), to_np(scales))[59, :, 500]
+    assert (~np.isfinite(out[3, 59])).all() and (np.sign(out[3, 59])[code != 0] == np.sign(code)[code != 0]).all()
+    rest = np.ones((20, 60), bool)
+    rest[3, 59] = False
+    _bf16(torch.from_numpy(out[rest]), ref[rest], "out", mass[rest] * 512 * 2.0 ** -24)
+
+
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("off", [0, 1, 2, 4])
 @pytest.mark.parametrize("H,N,K,group", [(3, 40, 256, 32), (1, 64, 1792, 64), (1, 64, 1792, 128), (2, 20, 1664, 128)])
@@ -774,6 +796,7 @@ def test_outputs_lie_in_the_memory_of_the_stream_that_writes_them():
     assert (mla_rms_norm(x, w, stream=0)[0] == 1).all()
 
 
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
 def test_a_first_call_inside_a_capture_is_refused():
     """It would put the status word into the graph's memory."""
     from mla_attention_gb300 import _lib
