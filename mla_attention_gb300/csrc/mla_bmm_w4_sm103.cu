@@ -26,7 +26,7 @@
 // a fixed order.
 // 8192 columns, k of 16384, groups of 128, 4 tokens: 19.2 us, 53 % of the copy's bandwidth, at half of the
 // issue slots.  128 heads of 512 columns, k of 128, one token 4.6 us, of 128 columns, k of 512, 17 tokens
-// 5.5: a launch, the first chunk's way in and the sums' way out.  Instructions are kept few as well: each is
+// 5.05: a launch, the first chunk's way in and the sums' way out.  Instructions are kept few as well: each is
 // fetched once a launch (the helpers' loads in three places instead of one cost 0.2 us).
 #include <type_traits>
 
@@ -133,8 +133,10 @@ struct W4Smem {
   uint64_t full[2], free[2];                  // a chunk's x, sums and scales are in place / read
 };
 
+// NT: tokens by the eight.  (Two CTAs an SM up to 16 tokens; for 9 to 16 the compiler's own choice does that without the spills
+// that asking for it brings: 4.6 us against 4.9 for 128 heads of 512 columns, k of 128, and 6.4 with one.)
 template <int NT, int GL>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) bmm_w4_kernel(const __grid_constant__ BmmW4Params p, const W4Plan plan) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : NT == 2 ? 0 : 1) bmm_w4_kernel(const __grid_constant__ BmmW4Params p, const W4Plan plan) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTok = 8 * NT, KC = kChunk<NT>;
   W4Smem<NT, GL>& s = *reinterpret_cast<W4Smem<NT, GL>*>(smem);
@@ -501,7 +503,10 @@ cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream) {
   plan.blocks_h = (blocks_h + plan.rounds - 1) / plan.rounds;
   if (p.T <= 8) return launch<1>(p, plan, stream);
   if (p.T <= 16) return launch<2>(p, plan, stream);
+  // (24 and 48 as well as 32 and 64: 17 tokens of 128 heads, k of 512, 5.5 -> 5.05 us, 48 with k of 128 12.9 -> 9.6)
+  if (p.T <= 24) return launch<3>(p, plan, stream);
   if (p.T <= 32) return launch<4>(p, plan, stream);
+  if (p.T <= 48) return launch<6>(p, plan, stream);
   return launch<8>(p, plan, stream);
 }
 

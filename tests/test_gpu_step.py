@@ -502,7 +502,7 @@ def _check_w4(T, H, N, K, group, f32=False, strided=False, seed=0):
     assert (buf[:, :, N:] == 3).all()
 
 
-@pytest.mark.parametrize("T", [0, 1, 2, 7, 8, 9, 16, 17, 31, 33, 64, 65, 130])
+@pytest.mark.parametrize("T", [0, 1, 2, 7, 8, 9, 16, 17, 24, 25, 31, 33, 48, 49, 64, 65, 130])
 @pytest.mark.parametrize("H,N,K,group", [(3, 512, 128, 32), (2, 128, 512, 64), (1, 100, 1024, 128)])
 def test_w4_tokens(T, H, N, K, group):
     _check_w4(T, H, N, K, group, f32=T % 2 == 0)
