@@ -28,6 +28,7 @@
 // issue slots.  128 heads of 512 columns, k of 128, one token 4.6 us, of 128 columns, k of 512, 17 tokens
 // 5.05: a launch, the first chunk's way in and the sums' way out.  Instructions are kept few as well: each is
 // fetched once a launch (the helpers' loads in three places instead of one cost 0.2 us).
+#include <algorithm>
 #include <type_traits>
 
 #include "mla_step.h"
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : NT == 2 ? 0 : 1) bmm_w
   const int wide = plan.rounds * kWarps * kCols, blocks_h = plan.blocks_h;   // columns of a CTA, CTAs of a head
   const int block = plan.cluster > 1 ? blockIdx.x / plan.cluster : blockIdx.x;
   const int h = block / blocks_h, first = (block - h * blocks_h) * wide;
-  const int rounds = min(plan.rounds, (p.N - first + kWarps * kCols - 1) / (kWarps * kCols));
+  const int rounds = min(plan.rounds, (p.N - 1 - first) / (kWarps * kCols) + 1);
   const int tok0 = blockIdx.y * kTok;
   const int steps = (p.K + kStep - 1) / kStep;
   const int u0 = plan.cluster > 1 ? (int)((int64_t)steps * rank / plan.cluster) : 0;
@@ -489,18 +490,20 @@ cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream) {
   // more tokens take its registers.  (8192 columns, k of 16384, 4 tokens, cut 1, 2, 4, 8 ways: 40, 24, 19.3,
   // 24.5 us; 2102 columns, k of 6400: 8 ways 7.9 us, 2 ways 11.4.)
   const int steps = (p.K + kStep - 1) / kStep;
-  const int64_t blocks = (int64_t)p.H * ((p.N + kWarps * kCols - 1) / (kWarps * kCols)) * ((p.T + 63) / 64);
+  const int blocks_h = (p.N - 1) / (kWarps * kCols) + 1;
+  const int64_t rows = (int64_t)p.H * ((p.T + 63) / 64), blocks = rows * blocks_h;
   const int64_t room = (int64_t)device_sm_count() * (p.T <= 16 ? 2 : 1);
   plan.cluster = 1;
   while (plan.cluster < 8 && 2 * plan.cluster <= steps && blocks * 2 * plan.cluster <= room) plan.cluster *= 2;
   // Where two chunks hold all of k, a CTA keeps x and goes on to the next columns of its head, so that all CTAs
   // run at once (128 heads of 512 columns, k of 128, 1, 32, 64 tokens: 5.4, 16.7, 28.4 us with a CTA for every
   // 128 columns and single columns a lane, 4.6, 7.4, 11.4 so).
-  const int blocks_h = (p.N + kWarps * kCols - 1) / (kWarps * kCols);
   plan.rounds = 1;
-  if (plan.cluster == 1 && steps <= 2 * (p.T <= 8 ? kChunk<1> : kChunk<8>))
-    while (plan.rounds < blocks_h && blocks / blocks_h * ((blocks_h + plan.rounds - 1) / plan.rounds) > room) ++plan.rounds;
-  plan.blocks_h = (blocks_h + plan.rounds - 1) / plan.rounds;
+  if (plan.cluster == 1 && steps <= 2 * (p.T <= 8 ? kChunk<1> : kChunk<8>)) {
+    const int at_once = (int)std::min<int64_t>(blocks_h, std::max<int64_t>(1, room / rows));   // CTAs of a head
+    plan.rounds = (blocks_h - 1) / at_once + 1;
+  }
+  plan.blocks_h = (blocks_h - 1) / plan.rounds + 1;
   if (p.T <= 8) return launch<1>(p, plan, stream);
   if (p.T <= 16) return launch<2>(p, plan, stream);
   // (24 and 48 as well as 32 and 64: 17 tokens of 128 heads, k of 512, 5.5 -> 5.05 us, 48 with k of 128 12.9 -> 9.6)

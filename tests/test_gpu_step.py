@@ -522,6 +522,21 @@ def test_w4_several_rounds_of_columns(T, H, N, K, group, strided):
     _check_w4(T, H, N, K, group, f32=strided, strided=strided)
 
 
+def test_w4_most_columns():
+    """34 GB of weights; the column numbers reach 2^31 - 2."""
+    g, d, N = torch.Generator().manual_seed(8), dev(), 2 ** 31 - 1
+    w4 = torch.empty((1, N, 16), dtype=torch.uint8, device=d).random_()
+    scales = torch.empty((1, N, 1), dtype=torch.bfloat16, device=d).uniform_(0.5, 1.5)
+    x = gen.randn_bf16((2, 1, 32), g).to(d)
+    out = mla_bmm_w4(x, w4, scales)
+    _done()
+    at = torch.cat([torch.arange(300), torch.randint(0, N, (2000,), generator=g), torch.arange(N - 300, N)]).to(d)
+    ref, mass = so.bmm_w4(to_np(x), w4[:, at].cpu().numpy(), to_np(scales[:, at]))
+    _bf16(out[:, :, at], ref, "out", mass * 32 * 2.0 ** -24)
+    del w4, scales, out
+    torch.cuda.empty_cache()
+
+
 def test_w4_infinity_in_several_rounds():
     g = torch.Generator().manual_seed(3)
     w4, scales = _w4(60, 700, 512, 64, False, g)
