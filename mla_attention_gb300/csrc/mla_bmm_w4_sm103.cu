@@ -449,27 +449,67 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : NT == 2 ? 0 : 1) bmm_w
   if (plan.cluster > 1) cluster_sync();   // the others may still read this CTA's sums
 }
 
+// What one launch of a kernel has running at once.
+struct AtOnce {
+  int clusters[4];   // of 1, 2, 4 and 8 CTAs
+};
 template <int NT, int GL>
-cudaError_t launch(const BmmW4Params& p, const W4Plan& plan, cudaStream_t stream) {
-  constexpr int kSmem = (int)sizeof(W4Smem<NT, GL>);
-  static PerDeviceOnce once;
-  cudaError_t e = once.run([] {
-    cudaError_t r = cudaFuncSetAttribute(bmm_w4_kernel<NT, GL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    return r != cudaSuccess ? r : cudaFuncSetAttribute(bmm_w4_kernel<NT, GL>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  });
-  if (e != cudaSuccess) return e;
-  const int blocks = p.H * plan.blocks_h;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = plan.cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)blocks * plan.cluster, (unsigned)((p.T + 8 * NT - 1) / (8 * NT)));
+void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int cluster, unsigned ctas, unsigned rows) {
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas, rows);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = sizeof(W4Smem<NT, GL>);
+  cfg.attrs = &attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+}
+template <int NT, int GL>
+cudaError_t prepare(AtOnce& n) {
+  const auto kernel = bmm_w4_kernel<NT, GL>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(W4Smem<NT, GL>));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n.clusters[0], kernel, kThreads, sizeof(W4Smem<NT, GL>));
+  n.clusters[0] *= device_sm_count();
+  for (int i = 1; i < 4 && e == cudaSuccess; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    configure<NT, GL>(cfg, attr, 1 << i, n.clusters[0] << i, 1);
+    e = cudaOccupancyMaxActiveClusters(&n.clusters[i], kernel, &cfg);
+  }
+  return e;
+}
+
+template <int NT, int GL>
+cudaError_t launch(const BmmW4Params& p, W4Plan plan, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  static AtOnce cached[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = once.run([dev] { return prepare<NT, GL>(cached[dev]); });
+  if (e != cudaSuccess) return e;
+  const AtOnce& at_once = cached[dev];
+  // k is cut over a cluster's CTAs, two ways at a time, while all of them still run at once (8192 columns, k of
+  // 16384, 4 tokens, cut 1, 2, 4, 8 ways: 40, 24, 19.3, 24.5 us; 2102 columns, k of 6400: 8 ways 7.9 us, 2 ways 11.4).
+  // How many do depends on how clusters fit a part of the GPU: 4 tokens, k of 4096, 36 clusters of eight 5.8 us, 37 9.1.
+  const int steps = (p.K - 1) / kStep + 1, blocks_h = (p.N - 1) / (kWarps * kCols) + 1;
+  const int64_t rows = (int64_t)p.H * ((p.T + 8 * NT - 1) / (8 * NT));
+  int log2 = 0;
+  while (log2 < 3 && 2 << log2 <= steps && rows * blocks_h <= at_once.clusters[log2 + 1]) ++log2;
+  plan.cluster = 1 << log2;
+  // Where two chunks hold all of k, a CTA keeps x and goes on to the next columns of its head, so that all CTAs
+  // run at once (128 heads of 512 columns, k of 128, 1, 32, 64 tokens: 5.4, 16.7, 28.4 us with a CTA for every
+  // 128 columns and single columns a lane, 4.6, 7.4, 11.4 so).
+  plan.rounds = 1;
+  if (plan.cluster == 1 && steps <= 2 * kChunk<NT>) {
+    const int of_a_head = (int)std::min<int64_t>(blocks_h, std::max<int64_t>(1, at_once.clusters[0] / rows));
+    plan.rounds = (blocks_h - 1) / of_a_head + 1;
+  }
+  plan.blocks_h = (blocks_h - 1) / plan.rounds + 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  configure<NT, GL>(cfg, attr, plan.cluster, (unsigned)p.H * plan.blocks_h * plan.cluster, (unsigned)((p.T + 8 * NT - 1) / (8 * NT)));
   cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = plan.cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, bmm_w4_kernel<NT, GL>, p, plan);
 }
 template <int NT>
@@ -486,24 +526,6 @@ cudaError_t launch_bmm_w4(const BmmW4Params& p, cudaStream_t stream) {
   plan.vec_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.x_stride_t % 8 == 0 && p.x_stride_h % 8 == 0;
   plan.vec_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.out_stride_t % 8 == 0 && p.out_stride_h % 8 == 0;
   plan.vec_s = reinterpret_cast<uintptr_t>(p.scales) % (p.scales_f32 ? 16 : 8) == 0;
-  // k is cut over a cluster's CTAs, two ways at a time, while all of them still run at once: two on an SM, or one where
-  // more tokens take its registers.  (8192 columns, k of 16384, 4 tokens, cut 1, 2, 4, 8 ways: 40, 24, 19.3,
-  // 24.5 us; 2102 columns, k of 6400: 8 ways 7.9 us, 2 ways 11.4.)
-  const int steps = (p.K + kStep - 1) / kStep;
-  const int blocks_h = (p.N - 1) / (kWarps * kCols) + 1;
-  const int64_t rows = (int64_t)p.H * ((p.T + 63) / 64), blocks = rows * blocks_h;
-  const int64_t room = (int64_t)device_sm_count() * (p.T <= 16 ? 2 : 1);
-  plan.cluster = 1;
-  while (plan.cluster < 8 && 2 * plan.cluster <= steps && blocks * 2 * plan.cluster <= room) plan.cluster *= 2;
-  // Where two chunks hold all of k, a CTA keeps x and goes on to the next columns of its head, so that all CTAs
-  // run at once (128 heads of 512 columns, k of 128, 1, 32, 64 tokens: 5.4, 16.7, 28.4 us with a CTA for every
-  // 128 columns and single columns a lane, 4.6, 7.4, 11.4 so).
-  plan.rounds = 1;
-  if (plan.cluster == 1 && steps <= 2 * (p.T <= 8 ? kChunk<1> : kChunk<8>)) {
-    const int at_once = (int)std::min<int64_t>(blocks_h, std::max<int64_t>(1, room / rows));   // CTAs of a head
-    plan.rounds = (blocks_h - 1) / at_once + 1;
-  }
-  plan.blocks_h = (blocks_h - 1) / plan.rounds + 1;
   if (p.T <= 8) return launch<1>(p, plan, stream);
   if (p.T <= 16) return launch<2>(p, plan, stream);
   // (24 and 48 as well as 32 and 64: 17 tokens of 128 heads, k of 512, 5.5 -> 5.05 us, 48 with k of 128 12.9 -> 9.6)
