@@ -435,9 +435,9 @@ mla_status mla_kv_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe
  * out      bf16, element (t, h, n) at out + t * out_stride_t + h * out_stride_h + n; only these are
  *          written (the latent columns of a fused query: strides (H * 576, 576)).
  * workspace: >= 256 bytes (the status word).
- * Built for few tokens (up to about 64): the weights are read once for every 64 tokens.  |x| from 2^-73 to
- * 2^48 runs on the tensor cores; values of x below 2^-73 may count as 0, and a token with larger, infinite or
- * NaN values in x is computed in plain fp32, far slower.
+ * Built for few tokens (up to about 64): the weights are read once for every 64 tokens.  A value of out whose
+ * sum on the tensor cores is not finite is computed over in plain fp32, far slower: all values of a token with an infinity or
+ * a NaN in x, others where a sum passes fp32's range.
  */
 mla_status mla_bmm_w4(const void* x, int64_t x_stride_t, int64_t x_stride_h, const void* w4, const void* scales,
                       int scales_f32, int group, int T, int H, int N, int K, void* out, int64_t out_stride_t,

@@ -7,19 +7,20 @@
 // the scale multiplies a group's sum where it lies, in the thread's accumulators.
 //
 // A code c in the low bits of a bf16 word is the subnormal number c 2^-133, and one four bits higher
-// is 16 c 2^-133: numbers that the products take exactly.  So w & 0x000f000f, w & 0x00f000f0 and the same
-// of w >> 8 are the bf16 pairs (k0, k4), (k1, k5), (k2, k6), (k3, k7) of a word, five
-// instructions for eight weights and no conversion.  x is put in the same order of k, times 2^80, or 2^76
-// where the code stands four bits higher; a group's sum starts at -8 sum x, and the scale brings 2^53
-// back.  The scaling is exact for |x| from 2^-73 to 2^48; larger and infinite values make the sum infinite
-// or NaN, and a sum that is not finite is done over in plain fp32 by the thread that stores it.
+// is 16 c 2^-133.  So w & 0x000f000f, w & 0x00f000f0 and the same of w >> 8 hold the codes of (k0, k4),
+// (k1, k5), (k2, k6), (k3, k7) of a word, and one exact fma a pair, times 2^127 or 2^123 and less 2^-3, makes them the
+// weights (c - 8) 2^-6: nine instructions for eight weights.  x is put in the same order of k as it is, and
+// the scale brings 2^6 back.  The weights have their sign before they meet x: a sum of c x less 8 sum x would
+// be five instructions, but it rounds at the size of 8 x also where the weight is 0, so that one large x under a
+// code of 8 takes the other terms with it.
+// A sum that is not finite is done over in plain fp32, scale by scale, by the thread that stores it.
 //
 // A CTA's eight warps hold 16 columns each of one head and walk the CTA's slice of k together, 128
 // k a step.  Every warp brings its own weights through a ring of kStages cp.async stages (no barrier for
 // them): 1 KB per 16 columns and step, the 16-byte pieces of a row swizzled by its number so that the
 // word reads hit 32 banks; lane (g, t) holds columns g and g + 8 and takes word t of each 32 k, so that
 // the four words of a product lie in one group whatever the group's size.  Four more warps put the tokens'
-// k (in the order in which a lane reads them, scaled), their sums and the weights' scales down in shared
+// k (in the order in which a lane reads them) and the weights' scales down in shared
 // memory, a chunk of kChunk steps ahead of the others: the same work between the products kept
 // every warp waiting for loads and for the slowest.
 // Few columns with a long k are cut over a cluster's CTAs, whose sums are joined in shared memory in
@@ -43,8 +44,9 @@ constexpr int kStep = 128;          // k per step
 constexpr int kCols = 16;           // columns n of a warp
 constexpr int kTileBytes = kCols * kStep / 2;
 constexpr int kPitch = kCols + 4;   // a token's sums: 16-byte reads, and the writes of a warp hit 32 banks
-constexpr uint32_t kUp = 0x67806780u, kUp4 = 0x65806580u;   // 2^80 and 2^76, twice
-constexpr float kDown = 0x1p53f, kOff = -0x1p-50f;          // 2^(133 - 80), -8 / kDown
+constexpr uint32_t kCode = 0x7f007f00u, kCode4 = 0x7d007d00u;   // bf16 2^127 and 2^123, twice: a code and one four bits higher to c 2^-6
+constexpr uint32_t kEight = 0xbe00be00u;                        // -8 2^-6, twice
+constexpr float kWeight = 64.f;                                 // what the scales take back
 
 enum : uint32_t { W_CHUNK_FULL = 0x90, W_CHUNK_FREE };
 
@@ -67,9 +69,10 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+// (volatile: made where they are used, the weights keep fewer registers: 9 tokens of 128 heads, k of 128, groups of 32 5.8 -> 5.5 us)
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm volatile("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -84,7 +87,7 @@ __device__ __forceinline__ float scale_at(const BmmW4Params& p, const uint8_t* s
   return p.scales_f32 ? *reinterpret_cast<const float*>(s) : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(s));
 }
 
-// One value in plain fp32: where the products' range does not reach.
+// One value in plain fp32: where a partial sum left fp32's range (its scale may bring it back).
 __device__ __noinline__ float plain_value(const BmmW4Params& p, int tok, int h, int n) {
   const int64_t row = (int64_t)h * p.N + n;
   const uint8_t* w = p.w4 + row * (p.K / 2);
@@ -128,16 +131,14 @@ template <int NT, int GL>
 struct W4Smem {
   uint8_t w[kWarps][kStages][kTileBytes];
   uint4 x[2 * kChunk<NT>][4][NT][32];         // [step][32 k][8 tokens][lane], two chunks
-  float off[2 * kChunk<NT>][4 >> GL][NT][8];  // -8 sum x of a step's groups
-  float scale[2 * kChunk<NT>][4 >> GL][kWarps][8][2];   // times 2^53, of columns (g, g + 8)
+  float scale[2 * kChunk<NT>][4 >> GL][kWarps][8][2];   // times kWeight, of columns (g, g + 8)
   float sums[kWarps][8 * NT][kPitch];         // of a warp's columns, [token][column]
-  uint64_t full[2], free[2];                  // a chunk's x, sums and scales are in place / read
+  uint64_t full[2], free[2];                  // a chunk's x and scales are in place / read
 };
 
-// NT: tokens by the eight.  (Two CTAs an SM up to 16 tokens; for 9 to 16 the compiler's own choice does that without the spills
-// that asking for it brings: 4.6 us against 4.9 for 128 heads of 512 columns, k of 128, and 6.4 with one.)
+// NT: tokens by the eight.  (Two CTAs an SM up to 16 tokens.)
 template <int NT, int GL>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : NT == 2 ? 0 : 1) bmm_w4_kernel(const __grid_constant__ BmmW4Params p, const W4Plan plan) {
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) bmm_w4_kernel(const __grid_constant__ BmmW4Params p, const W4Plan plan) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTok = 8 * NT, KC = kChunk<NT>;
   W4Smem<NT, GL>& s = *reinterpret_cast<W4Smem<NT, GL>*>(smem);
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : NT == 2 ? 0 : 1) bmm_w
   };
 
   if (warp >= kWarps) {
-    // ---- the helpers put a chunk's x, sums and scales in place while the others compute on the one before ----
+    // ---- the helpers put a chunk's x and scales in place while the others compute on the one before ----
     const int helper = warp - kWarps;
     constexpr int kUnits = (KC * NT + kHelpers - 1) / kHelpers;     // (step, eight tokens) of a helper
     constexpr int kRow = KC * kPer, kScales = kCols * kRow / 32;    // a lane has kScales neighbours of one column
@@ -242,22 +243,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : NT == 2 ? 0 : 1) bmm_w
       for (int n = 0; n < kUnits; ++n) {
         const int unit = helper + n * kHelpers, st = unit / NT, nt = unit % NT;
         if (unit >= KC * NT) break;
-        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint4 v = xv[n][i];
-          float f[8];
-          bf16x8_unpack(v, f);
-          sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-          s.x[b * KC + st][i][nt][lane] =
-              make_uint4(mul_bf16x2(__byte_perm(v.x, v.z, 0x5410), kUp), mul_bf16x2(__byte_perm(v.x, v.z, 0x7632), kUp4),
-                         mul_bf16x2(__byte_perm(v.y, v.w, 0x5410), kUp), mul_bf16x2(__byte_perm(v.y, v.w, 0x7632), kUp4));
-          if ((i & kLast) == kLast) {   // the end of a group
-            sum += __shfl_xor_sync(~0u, sum, 1);
-            sum += __shfl_xor_sync(~0u, sum, 2);
-            if (t == 0) s.off[b * KC + st][i >> GL][nt][g] = sum * kOff;
-            sum = 0.f;
-          }
+          s.x[b * KC + st][i][nt][lane] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                                     __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
         }
       }
     };
@@ -271,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : NT == 2 ? 0 : 1) bmm_w
             v = sv[w][r / kVec * kVec + r % kVec / 2];
             v = r & 1 ? v & 0xffff0000u : v << 16;
           }
-          s.scale[b * KC + (q0 + r) / kPer][(q0 + r) % kPer][helper + w * kHelpers][col & 7][col >> 3] = __uint_as_float(v) * kDown;
+          s.scale[b * KC + (q0 + r) / kPer][(q0 + r) % kPer][helper + w * kHelpers][col & 7][col >> 3] = __uint_as_float(v) * kWeight;
         }
     };
     // one place in the code for each: a launch waits for its instructions
@@ -347,20 +337,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : NT == 2 ? 0 : 1) bmm_w
     const int slot = (base & (2 * KC - 1)) + kAt % (2 * KC);   // of the two chunks
 #pragma unroll
     for (int i = 0; i < 4; ++i) {   // 32 k each
-      if ((i & kLast) == 0) {       // a group's sums start at -8 sum x
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float2 o = *reinterpret_cast<const float2*>(&s.off[slot][i >> GL][nt][2 * t]);
-          part[nt][0] = part[nt][2] = o.x, part[nt][1] = part[nt][3] = o.y;
-        }
-      }
       const uint32_t* from = reinterpret_cast<const uint32_t*>(take[i] + kAt * kTileBytes);
       const uint32_t w0 = from[0], w1 = from[128], v0 = w0 >> 8, v1 = w1 >> 8;
-      const uint32_t lo[4] = {w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u};
-      const uint32_t hi[4] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u};
+      const uint32_t lo[4] = {fma_bf16x2(w0 & 0x000f000fu, kCode, kEight), fma_bf16x2(w1 & 0x000f000fu, kCode, kEight),
+                              fma_bf16x2(w0 & 0x00f000f0u, kCode4, kEight), fma_bf16x2(w1 & 0x00f000f0u, kCode4, kEight)};
+      const uint32_t hi[4] = {fma_bf16x2(v0 & 0x000f000fu, kCode, kEight), fma_bf16x2(v1 & 0x000f000fu, kCode, kEight),
+                              fma_bf16x2(v0 & 0x00f000f0u, kCode4, kEight), fma_bf16x2(v1 & 0x00f000f0u, kCode4, kEight)};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 b = s.x[slot][i][nt][lane];
+        if ((i & kLast) == 0) part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.f;   // a group's sums start
         mma16816(part[nt], lo, b.x, b.y);
         mma16816(part[nt], hi, b.z, b.w);
       }

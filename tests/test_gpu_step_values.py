@@ -1,0 +1,83 @@
+"""The serving step's operators on values far from one, against the fp64 oracle.
+
+Tolerances as in test_gpu_step.py: half a step of the output's type, the fp32 arithmetic, and for sums their
+error bound over the sum of the terms' magnitudes."""
+import pytest
+import torch
+
+import oracle.step_oracle as so
+from mla_attention_gb300 import inputs as gen, mla_bmm_w4
+from tests.helpers import dev, to_np
+from tests.test_gpu_step import _bf16, _done, _w4
+
+pytestmark = pytest.mark.gpu
+
+TOKENS = [1, 9, 17, 25, 33, 49]          # one for each width of the token tiles
+
+
+# ---------------------------------------------------------------------------------------------
+# products with 4-bit weights
+# ---------------------------------------------------------------------------------------------
+def _set_code(w4, k, code):
+    """Every column's code of this k."""
+    keep, put = (0xF0, code) if k % 2 == 0 else (0x0F, code << 4)
+    w4[:, :, k // 2] = (w4[:, :, k // 2] & keep) | put
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T", TOKENS)
+def test_w4_a_large_value_under_a_weight_of_zero_adds_nothing(T, group):
+    """Code 8 is the weight 0: what x holds there is not part of any sum, however large."""
+    g = torch.Generator().manual_seed(T + group)
+    H, N, K = 2, 70, 384
+    w4, scales = _w4(H, N, K, group, T % 2 == 1, g)
+    x = gen.randn_bf16((T, H, K), g)
+    for k, size in ((5, 2.0 ** 16), (100, -2.0 ** 20), (170, 2.0 ** 24), (255, 2.0 ** 30), (383, -2.0 ** 40)):
+        _set_code(w4, k, 8)
+        x[:, :, k] = size
+    out = mla_bmm_w4(x.to(dev()), w4, scales)
+    _done()
+    ref, mass = so.bmm_w4(to_np(x), w4.cpu().numpy(), to_np(scales))
+    _bf16(out, ref, "out", mass * K * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("T", [1, 17, 64])
+def test_w4_weights_of_zero_give_zero(T):
+    w4 = torch.full((1, 33, 256), 0x88, dtype=torch.uint8, device=dev())
+    scales = torch.ones((1, 33, 4), dtype=torch.bfloat16, device=dev())
+    x = gen.randn_bf16((T, 1, 512), torch.Generator().manual_seed(2)).to(dev())
+    assert not mla_bmm_w4(x, w4, scales).any()
+
+
+@pytest.mark.parametrize("T", TOKENS)
+def test_w4_rows_of_any_size(T):
+    """Tokens of 2^-110 to 2^100: each to the bound of its own terms."""
+    g = torch.Generator().manual_seed(T)
+    H, N, K = 2, 40, 256
+    w4, scales = _w4(H, N, K, 64, True, g)
+    x = gen.randn_bf16((T, H, K), g)
+    size = torch.tensor([2.0 ** -110, 2.0 ** -90, 2.0 ** -74, 1.0, 2.0 ** 50, 2.0 ** 100])
+    x = (x.float() * size[torch.arange(T * H).view(T, H, 1) % 6]).to(torch.bfloat16)
+    scales[:, :, 0] *= 2.0 ** 10         # out of the smallest rows stays a normal number
+    out = mla_bmm_w4(x.to(dev()), w4, scales)
+    _done()
+    ref, mass = so.bmm_w4(to_np(x), w4.cpu().numpy(), to_np(scales))
+    _bf16(out, ref, "out", mass * K * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("N", [200, 4500, 4700])       # k cut eight, four and two ways
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T", TOKENS)
+def test_w4_whole_numbers_are_exact(T, group, N):
+    """Whole numbers in x and powers of two as scales: every sum is a multiple of 1/4 below 2^22, exact in fp32 in any order,
+    so out is the exact value rounded once."""
+    g = torch.Generator(device=dev()).manual_seed(N + T + group)
+    K = 16384
+    w4 = torch.randint(0, 256, (1, N, K // 2), generator=g, device=dev(), dtype=torch.uint8)
+    scales = torch.exp2(torch.randint(-2, 2, (1, N, K // group), generator=g, device=dev()).float()).to(torch.bfloat16)
+    x = torch.randint(-8, 9, (T, 1, K), generator=g, device=dev()).to(torch.bfloat16)
+    out = mla_bmm_w4(x, w4, scales)
+    w = torch.stack([w4[0] & 15, w4[0] >> 4], -1).view(N, K).double() - 8
+    w *= scales[0].double().repeat_interleave(group, 1)
+    ref = x[:, 0].double() @ w.T
+    assert torch.equal(out[:, 0].double(), ref.to(torch.float32).to(torch.bfloat16).double())
