@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) bmm_w4_kernel(const
         float f[8];
         *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&s.sums[warp][tok][c]);
         *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&s.sums[warp][tok][c + 4]);
-        bool plain = plan.vec_out && n + 8 <= p.N;
+        bool plain = plan.vec_out && p.N - n >= 8;   // (n + 8 can pass 2^31 - 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) plain = plain && fabsf(f[j]) < __int_as_float(0x7f800000);
         __nv_bfloat16* o = p.out + (tok0 + tok) * p.out_stride_t + h * p.out_stride_h + n;

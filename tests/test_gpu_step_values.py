@@ -81,3 +81,20 @@ def test_w4_whole_numbers_are_exact(T, group, N):
     w *= scales[0].double().repeat_interleave(group, 1)
     ref = x[:, 0].double() @ w.T
     assert torch.equal(out[:, 0].double(), ref.to(torch.float32).to(torch.bfloat16).double())
+
+
+def test_w4_most_columns_of_several_tokens_in_wider_rows():
+    """2^31 - 1 columns, eight a store, in rows of 2^31: the last group is cut at its seventh column."""
+    g, d, T, N = torch.Generator().manual_seed(8), dev(), 9, 2 ** 31 - 1
+    w4 = torch.empty((1, N, 16), dtype=torch.uint8, device=d).random_()
+    scales = torch.empty((1, N, 1), dtype=torch.bfloat16, device=d).uniform_(0.5, 1.5)
+    x = gen.randn_bf16((T, 1, 32), g).to(d)
+    rows = torch.full((T, 1, N + 1), 3.0, dtype=torch.bfloat16, device=d)
+    out = mla_bmm_w4(x, w4, scales, out=rows[:, :, :N])
+    _done()
+    assert (rows[:, :, N] == 3).all()
+    at = torch.cat([torch.arange(300), torch.randint(0, N, (1000,), generator=g), torch.arange(N - 300, N)]).to(d)
+    ref, mass = so.bmm_w4(to_np(x), w4[:, at].cpu().numpy(), to_np(scales[:, at]))
+    _bf16(out[:, :, at], ref, "out", mass * 32 * 2.0 ** -24)
+    del w4, scales, rows, out
+    torch.cuda.empty_cache()
