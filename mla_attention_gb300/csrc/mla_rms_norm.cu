@@ -145,32 +145,39 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
     for (int k = 0; k < NV; ++k) bf16x8_unpack(xv[k], h[k]);
   }
 
-  auto sum_squares = [&](float (&buf)[32]) {
+  // of the row times `up`, a power of two
+  auto sum_squares = [&](float up, float (&buf)[32]) {
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) sum += square_sum8(h[k]);
+    for (int k = 0; k < NV; ++k) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = h[k][i];
+      if (up != 1.f) scale8(f, up);
+      sum += square_sum8(f);
+    }
     return row_reduce<kBlock, false>(sum, buf);
   };
-  float sum = sum_squares(red[0]), eps = p.eps;
+  float sum = sum_squares(1.f, red[0]), eps = p.eps, back = 1.f;
   if (sum > 3e38f) {
-    // The squares leave fp32's range: the row once more at 2^-96 of its size, where the largest
+    // The squares leave fp32's range: once more at 2^-96 of the row's size, where the largest
     // values' squares still add up and the smallest that count still have one.
-    eps *= 0x1p-96f;
-    eps *= 0x1p-96f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[k][i] *= 0x1p-96f;
-    sum = sum_squares(red[1]);
+    back = 0x1p-96f;
+    eps = eps * back * back;
+    sum = sum_squares(back, red[1]);
   }
   const float inv = rsqrt_newton(sum / (float)p.D + eps);
+  auto weigh = [&](auto&& norm) {   // y; behind the row's end 0
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    if constexpr (!kWeightFirst) wv[k] = load(p.weight, 0, 0, wide & kWideW, k);
-    float w[8];
-    bf16x8_unpack(wv[k], w);
-    norm8(h[k], inv, w);   // y; behind the row's end 0
-  }
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (!kWeightFirst) wv[k] = load(p.weight, 0, 0, wide & kWideW, k);
+      float w[8];
+      bf16x8_unpack(wv[k], w);
+      norm(h[k], w);
+    }
+  };
+  if (__builtin_expect(back == 1.f, 1)) weigh([&](float(&f)[8], const float(&w)[8]) { norm8(f, inv, w); });
+  else weigh([&](float(&f)[8], const float(&w)[8]) { norm8_back(f, inv, w, back); });
 
   if constexpr (!kE4m3) {
 #pragma unroll

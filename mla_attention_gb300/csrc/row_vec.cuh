@@ -66,6 +66,15 @@ __device__ __forceinline__ void norm8(float (&f)[8], float inv, const float (&w)
   for (int i = 0; i < 8; i += 2)
     f32x2_split(mul_f32x2(mul_f32x2(f32x2(f[i], f[i + 1]), ii), f32x2(w[i], w[i + 1])), f[i], f[i + 1]);
 }
+// The same times `back`, of a row whose inv was found at `back` of its size: last, so that what is small next to the row
+// but not to its weight stays, or before the weight where the product passes fp32 without it.
+__device__ __forceinline__ void norm8_back(float (&f)[8], float inv, const float (&w)[8], float back) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = f[i] * inv, t = y * w[i];
+    f[i] = fabsf(t) < __int_as_float(0x7f800000) ? t * back : y * back * w[i];
+  }
+}
 __device__ __forceinline__ float square_sum8(const float (&f)[8]) {   // pairwise: a row's error is that of a few roundings
   const uint64_t a = f32x2(f[0], f[1]), b = f32x2(f[2], f[3]), c = f32x2(f[4], f[5]), d = f32x2(f[6], f[7]);
   float lo, hi;

@@ -8,7 +8,7 @@ import torch
 import oracle.step_oracle as so
 from mla_attention_gb300 import inputs as gen, mla_bmm_w4
 from tests.helpers import dev, to_np
-from tests.test_gpu_step import _bf16, _done, _w4
+from tests.test_gpu_step import _bf16, _check_norm, _done, _w4
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,19 @@ def test_w4_most_columns_of_several_tokens_in_wider_rows():
     _bf16(out[:, :, at], ref, "out", mass * 32 * 2.0 ** -24)
     del w4, scales, rows, out
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------------------------
+# RMS norm
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("D", [64, 1535, 8192, 20000])
+def test_norm_keeps_the_small_values_of_huge_rows(D):
+    """2^-50 next to 2^70 is a normal number of the output, to the output's precision."""
+    g = torch.Generator().manual_seed(D)
+    x = torch.randn((3, D), generator=g)
+    x[0] *= 2.0 ** 70
+    x[1] *= 2.0 ** 100
+    x[2] *= 2.0 ** 120
+    x[:, ::2] = torch.randn((3, (D + 1) // 2), generator=g) * 2.0 ** -50
+    w = torch.full((D,), 2.0 ** 60, dtype=torch.bfloat16, device=dev())
+    _check_norm(3, D, residual=False, x=x.to(torch.bfloat16).to(dev()), w=w)
