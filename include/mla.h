@@ -372,7 +372,8 @@ mla_status mla_slot_map(const int32_t* lens, const int32_t* new_tokens, int B, i
 /*
  * Root-mean-square norm of T rows of D columns, with the residual's addition and an 8-bit output.
  *   h = x + residual (x alone without one),  y = h / sqrt(mean(h^2) + eps) * weight
- * in fp32; residual_out = h as bf16 (the norm reads the unrounded sum).  out is y as bf16, or with
+ * in fp32, rows of any size, with any eps (a row of zeros without one is NaN); residual_out = h as
+ * bf16 (the norm reads the unrounded sum).  out is y as bf16, or with
  * out_e4m3 the e4m3 values of y / s, one fp32 scale s = max(max|y| / 448, 2^-126) for each `group`
  * columns (0: one for the whole row), so that y is e4m3 * s; a NaN among a group's y makes its
  * scale NaN.

@@ -145,28 +145,29 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
     for (int k = 0; k < NV; ++k) bf16x8_unpack(xv[k], h[k]);
   }
 
-  // of the row times `up`, a power of two
-  auto sum_squares = [&](float up, float (&buf)[32]) {
-    float sum = 0.f;
+  float sum = 0.f, back = 1.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float f[8];
+  for (int k = 0; k < NV; ++k) sum += square_sum8(h[k]);
+  float mean = row_reduce<kBlock, false>(sum, red[0]) / (float)p.D + p.eps;
+  if (__builtin_expect(!(mean >= 0x1p-100f && mean <= 3e38f), 0)) {
+    // The squares leave fp32's range (or the row holds a NaN): once more at 2^-96 of the row's size, where the largest values'
+    // squares still add up and the smallest that count still have one, or at 2^96 of it, where every value's square
+    // is a normal number.  A small row goes on at that size, a huge one as it is: 2^-96 of it would lose its small values.
+    const bool tiny = mean < 0x1p-100f;
+    const float up = tiny ? 0x1p96f : 0x1p-96f;
+    sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = h[k][i];
-      if (up != 1.f) scale8(f, up);
-      sum += square_sum8(f);
-    }
-    return row_reduce<kBlock, false>(sum, buf);
-  };
-  float sum = sum_squares(1.f, red[0]), eps = p.eps, back = 1.f;
-  if (sum > 3e38f) {
-    // The squares leave fp32's range: once more at 2^-96 of the row's size, where the largest
-    // values' squares still add up and the smallest that count still have one.
-    back = 0x1p-96f;
-    eps = eps * back * back;
-    sum = sum_squares(back, red[1]);
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = h[k][i] * up;
+        sum = fmaf(f, f, sum);
+        if (tiny) h[k][i] = f;
+      }
+    mean = row_reduce<kBlock, false>(sum, red[1]) / (float)p.D + p.eps * up * up;
+    if (!tiny) back = up;
   }
-  const float inv = rsqrt_newton(sum / (float)p.D + eps);
+  const float inv = rsqrt_newton(mean);
   auto weigh = [&](auto&& norm) {   // y; behind the row's end 0
 #pragma unroll
     for (int k = 0; k < NV; ++k) {

@@ -2,6 +2,7 @@
 
 Tolerances as in test_gpu_step.py: half a step of the output's type, the fp32 arithmetic, and for sums their
 error bound over the sum of the terms' magnitudes."""
+import numpy as np
 import pytest
 import torch
 
@@ -114,3 +115,18 @@ def test_norm_keeps_the_small_values_of_huge_rows(D):
     x[:, ::2] = torch.randn((3, (D + 1) // 2), generator=g) * 2.0 ** -50
     w = torch.full((D,), 2.0 ** 60, dtype=torch.bfloat16, device=dev())
     _check_norm(3, D, residual=False, x=x.to(torch.bfloat16).to(dev()), w=w)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 500, 1535, 8192, 20000])
+def test_norm_rows_far_below_one(D, e4m3):
+    """Without an eps, or with one as small as the rows' squares, a row of any size is normed."""
+    g = torch.Generator().manual_seed(D)
+    sizes = [2.0 ** -62, 2.0 ** -72, 2.0 ** -76, 2.0 ** -100, 2.0 ** -122, 2.0 ** -126]
+    x = torch.randn((len(sizes), D), generator=g) * torch.tensor(sizes)[:, None]
+    x[4, : D // 2] = 0
+    x[5] = 2.0 ** -130                   # below the smallest normal number
+    x = x.to(torch.bfloat16).to(dev())
+    w = (1 + 0.3 * torch.randn(D, generator=g)).to(torch.bfloat16).to(dev())
+    for eps in (0.0, float(np.float32(2.0 ** -140)), float(np.float32(2.0 ** -125))):
+        _check_norm(len(sizes), D, residual=False, e4m3=e4m3, eps=eps, x=x, w=w)
