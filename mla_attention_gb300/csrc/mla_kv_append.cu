@@ -174,6 +174,40 @@ __device__ __forceinline__ void append_pe(const KvAppendParams& p, int t, int la
   put_row8(p, t, to.slot, kLatent + 32 + 8 * u, b);
 }
 
+__device__ __forceinline__ float row_sum16(float v) {   // over a row's 16 lanes
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+  return v;
+}
+
+// Two rows one or both of whose squares leave fp32's range: the sum of squares at `up` of the row's size, a power of
+// two that goes back behind the weight.  Out of line: between the other instructions it cost 0.1 us a launch.
+__device__ __noinline__ void append_far_latents(const KvAppendParams& p, int t, Target to, int lane, float up) {
+  const int l = lane & 15;
+  auto load = [&](int k, float(&f)[8]) {
+    bf16x8_unpack(load16(p, p.c_kv + t * p.c_kv_stride + 128 * k + 8 * l, p.c_kv, (p.T - 1) * p.c_kv_stride + kLatent), f);
+  };
+  float sum = 0.f;
+  if (to.pos >= 0)
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      load(k, f);
+      scale8(f, up);
+      sum += square_sum8(f);
+    }
+  const float inv = rsqrt_newton(row_sum16(sum) * (1.f / kLatent) + p.eps * up * up);
+  if (to.pos < 0) return;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    float f[8], w[8];
+    load(k, f);
+    bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), w);
+    norm8_back(f, inv, w, up);
+    put_row8(p, t, to.slot, 128 * k + 8 * l, f);
+  }
+}
+
 // ---- the latents of two rows: lane l of a row's 16 holds columns 128 k + 8 l .. (k = 0..3).  t is past the
 // last token for the half that has none. ----
 __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, int lane) {
@@ -190,42 +224,21 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
   }
   float inv = 1.f;
   if (p.weight) {
-    auto mean_square = [&] {
-      float sum = 0.f;
-      if (to.pos >= 0) {
-        float part[4];
+    float sum = 0.f;
+    if (to.pos >= 0) {
+      float part[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float f[8];
-          bf16x8_unpack(v[k], f);
-          part[k] = square_sum8(f);
-        }
-        sum = (part[0] + part[1]) + (part[2] + part[3]);
+      for (int k = 0; k < 4; ++k) {
+        float f[8];
+        bf16x8_unpack(v[k], f);
+        part[k] = square_sum8(f);
       }
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-      return sum * (1.f / kLatent);
-    };
-    float mean = mean_square(), eps = p.eps;
-    const bool huge = mean > 5e35f;
-    if (__any_sync(~0u, huge)) {
-      // The squares leave fp32's range: these rows go on at 2^-70 of their size, exact in bf16 but for values
-      // 2^114 times smaller than the row's largest.
-      if (huge) {
-        eps *= 0x1p-70f;
-        eps *= 0x1p-70f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float f[8];
-          bf16x8_unpack(v[k], f);
-          scale8(f, 0x1p-70f);
-          v[k] = bf16x8_pack(f);
-        }
-      }
-      const float again = mean_square();
-      if (huge) mean = again;
+      sum = (part[0] + part[1]) + (part[2] + part[3]);
     }
-    inv = rsqrt_newton(mean + eps);
+    const float mean = row_sum16(sum) * (1.f / kLatent) + p.eps;
+    const bool huge = mean > 5e35f;
+    if (__any_sync(~0u, huge)) return append_far_latents(p, t, to, lane, huge ? 0x1p-96f : 1.f);
+    inv = rsqrt_newton(mean);
   }
   if (to.pos < 0) return;
 #pragma unroll

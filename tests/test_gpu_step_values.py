@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import oracle.step_oracle as so
-from mla_attention_gb300 import inputs as gen, mla_bmm_w4
+from mla_attention_gb300 import inputs as gen, mla_bmm_w4, mla_kv_append
 from tests.helpers import dev, to_np
 from tests.test_gpu_step import _bf16, _check_norm, _done, _w4
 
@@ -130,3 +130,25 @@ def test_norm_rows_far_below_one(D, e4m3):
     w = (1 + 0.3 * torch.randn(D, generator=g)).to(torch.bfloat16).to(dev())
     for eps in (0.0, float(np.float32(2.0 ** -140)), float(np.float32(2.0 ** -125))):
         _check_norm(len(sizes), D, residual=False, e4m3=e4m3, eps=eps, x=x, w=w)
+
+
+# ---------------------------------------------------------------------------------------------
+# cache append
+# ---------------------------------------------------------------------------------------------
+def _append(c, w, eps, e4m3, scale=1.0):
+    d, T = dev(), c.shape[0]
+    pe = torch.zeros((T, 64), dtype=torch.bfloat16, device=d)
+    cache = torch.zeros((1, T, 576), device=d).to(torch.float8_e4m3fn if e4m3 else torch.bfloat16)
+    at = torch.arange(T, dtype=torch.int32, device=d)
+    mla_kv_append(c.to(d), pe, at, at, gen.rope_cos_sin(T).to(d), cache, scale, norm_weight=None if w is None else w.to(d), eps=eps)
+    _done()
+    return cache[0, :, :512]
+
+
+def test_append_keeps_the_small_values_of_huge_latents():
+    g = torch.Generator().manual_seed(32)
+    c = torch.randn((3, 512), generator=g) * torch.tensor([2.0 ** 62, 2.0 ** 70, 2.0 ** 120])[:, None]
+    c[:, ::2] = torch.randn((3, 256), generator=g) * 2.0 ** -64
+    c = c.to(torch.bfloat16)
+    w = torch.full((512,), 2.0 ** 70, dtype=torch.bfloat16)
+    _bf16(_append(c, w, 1e-6, False), so.rms_norm(to_np(c), to_np(w), 1e-6)[0], "latents")
