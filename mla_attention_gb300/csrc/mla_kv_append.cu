@@ -180,8 +180,9 @@ __device__ __forceinline__ float row_sum16(float v) {   // over a row's 16 lanes
   return v;
 }
 
-// Two rows one or both of whose squares leave fp32's range: the sum of squares at `up` of the row's size, a power of
-// two that goes back behind the weight.  Out of line: between the other instructions it cost 0.1 us a launch.
+// Two rows one or both of whose squares leave fp32's range at either end: the sum of squares at `up` of the row's size, a
+// power of two.  A small row goes on at that size; of a huge one, whose small values that would lose, it goes back behind
+// the weight.  Out of line: between the other instructions it cost 0.1 us a launch.
 __device__ __noinline__ void append_far_latents(const KvAppendParams& p, int t, Target to, int lane, float up) {
   const int l = lane & 15;
   auto load = [&](int k, float(&f)[8]) {
@@ -196,14 +197,15 @@ __device__ __noinline__ void append_far_latents(const KvAppendParams& p, int t, 
       scale8(f, up);
       sum += square_sum8(f);
     }
-  const float inv = rsqrt_newton(row_sum16(sum) * (1.f / kLatent) + p.eps * up * up);
+  const float inv = rsqrt_newton(row_sum16(sum) * (1.f / kLatent) + p.eps * up * up), grow = fmaxf(up, 1.f), back = fminf(up, 1.f);
   if (to.pos < 0) return;
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     float f[8], w[8];
     load(k, f);
     bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), w);
-    norm8_back(f, inv, w, up);
+    scale8(f, grow);
+    norm8_back(f, inv, w, back);
     put_row8(p, t, to.slot, 128 * k + 8 * l, f);
   }
 }
@@ -236,8 +238,8 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
       sum = (part[0] + part[1]) + (part[2] + part[3]);
     }
     const float mean = row_sum16(sum) * (1.f / kLatent) + p.eps;
-    const bool huge = mean > 5e35f;
-    if (__any_sync(~0u, huge)) return append_far_latents(p, t, to, lane, huge ? 0x1p-96f : 1.f);
+    const bool huge = mean > 5e35f, tiny = mean < 0x1p-100f && to.pos >= 0;
+    if (__any_sync(~0u, huge || tiny)) return append_far_latents(p, t, to, lane, huge ? 0x1p-96f : tiny ? 0x1p96f : 1.f);
     inv = rsqrt_newton(mean);
   }
   if (to.pos < 0) return;

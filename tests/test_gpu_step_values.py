@@ -9,7 +9,7 @@ import torch
 import oracle.step_oracle as so
 from mla_attention_gb300 import inputs as gen, mla_bmm_w4, mla_kv_append
 from tests.helpers import dev, to_np
-from tests.test_gpu_step import _bf16, _check_norm, _done, _w4
+from tests.test_gpu_step import ARITH, E4M3, _bf16, _check_norm, _done, _w4, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +152,22 @@ def test_append_keeps_the_small_values_of_huge_latents():
     c = c.to(torch.bfloat16)
     w = torch.full((512,), 2.0 ** 70, dtype=torch.bfloat16)
     _bf16(_append(c, w, 1e-6, False), so.rms_norm(to_np(c), to_np(w), 1e-6)[0], "latents")
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_append_norms_latents_far_below_one(e4m3):
+    g = torch.Generator().manual_seed(31)
+    sizes = [2.0 ** -62, 2.0 ** -72, 2.0 ** -76, 2.0 ** -100, 1.0, 2.0 ** -126, 2.0 ** 80]
+    c = torch.randn((len(sizes), 512), generator=g) * torch.tensor(sizes)[:, None]
+    c[5] = 2.0 ** -130
+    c = c.to(torch.bfloat16)
+    w = (1 + 0.3 * torch.randn(512, generator=g)).to(torch.bfloat16)
+    scale = 0.021 if e4m3 else 1.0
+    s = float(np.float32(scale))
+    for eps in (0.0, float(np.float32(2.0 ** -140))):
+        ref = so.rms_norm(to_np(c), to_np(w), eps)[0]
+        got = _append(c, w, eps, e4m3, scale)
+        if e4m3:
+            _within(torch.from_numpy(to_np(got) * s), ref, np.abs(ref) * (E4M3 + ARITH) + s * 2.0 ** -10, "latents")
+        else:
+            _bf16(got, ref, "latents")
