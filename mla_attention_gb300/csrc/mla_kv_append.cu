@@ -77,7 +77,8 @@ __device__ __forceinline__ void store_cache8(const KvAppendParams& p, int64_t ro
     uint2 v = e4m3x8_pack(q);
     if ((((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) {   // a NaN code
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = f[i] * p.inv_kv_scale;   // of an infinite value saturates, of a NaN stays
+      for (int i = 0; i < 8; ++i)
+        if (q[i] != q[i]) q[i] = f[i] * p.inv_kv_scale;   // of an infinite value or quotient saturates, of a NaN stays
       v = e4m3x8_pack(q);
     }
     uint8_t* dst = reinterpret_cast<uint8_t*>(p.cache) + row * kDk + col;

@@ -171,3 +171,13 @@ def test_append_norms_latents_far_below_one(e4m3):
             _within(torch.from_numpy(to_np(got) * s), ref, np.abs(ref) * (E4M3 + ARITH) + s * 2.0 ** -10, "latents")
         else:
             _bf16(got, ref, "latents")
+
+
+def test_append_next_to_a_nan_or_an_infinity_rounds_to_nearest():
+    """1.3671875 / 0.109375 is 12.5, between the codes of 12 and 13: to even, whatever else the row holds."""
+    c = torch.full((4, 512), 1.3671875)
+    c[1, 3::8], c[2, 6::8], c[3, 1::8] = float("nan"), float("inf"), -3e38
+    got = to_np(_append(c.to(torch.bfloat16), None, 0.0, True, 0.109375))
+    want = np.full((4, 512), 12.0)
+    want[1, 3::8], want[2, 6::8], want[3, 1::8] = np.nan, 448, -448
+    np.testing.assert_array_equal(got, want)
