@@ -136,9 +136,11 @@ def mla_slot_map(lens, new_tokens, block_table, pool, pool_state, page_size: int
     (ring head, free pages).  Rows behind the last token get -1.  lens_out / pool_state_out may be
     lens / pool_state.  Returns positions [N], slots [N], cu_tokens [B+1], lens_out, pool_state_out."""
     dev, (B,) = _device(lens, "lens", 1)
-    max_pages, num_pages, N = _shape(block_table, "block_table", 2)[1], _shape(pool, "pool", 1)[0], int(N)
+    max_pages, num_pages, N, page_size = _shape(block_table, "block_table", 2)[1], _shape(pool, "pool", 1)[0], int(N), int(page_size)
     if not 0 <= N <= _INT_MAX:
         raise MLAError(1, f"N must be between 0 and 2^31 - 1, got {N}")
+    if not 1 <= page_size <= _INT_MAX or max_pages > _INT_MAX:
+        raise MLAError(1, f"page_size must be between 1 and 2^31 - 1 and max_pages at most that, got {page_size} and {max_pages}")
     if positions is None:
         positions = _empty(N, _I32, dev, stream)
     if slots is None:
@@ -151,7 +153,7 @@ def mla_slot_map(lens, new_tokens, block_table, pool, pool_state, page_size: int
         pool_state_out = _empty(2, _I32, dev, stream)
     _call("mla_slot_map", dev, stream, _dense(lens, "lens", _I32, dev, (B,)),
           _dense(new_tokens, "new_tokens", _I32, dev, (B,)), B,
-          _dense(block_table, "block_table", _I32, dev, (B, max_pages)), max_pages, int(page_size), num_pages,
+          _dense(block_table, "block_table", _I32, dev, (B, max_pages)), max_pages, page_size, num_pages,
           _dense(pool, "pool", _I32, dev, (num_pages,)), _dense(pool_state, "pool_state", _I32, dev, (2,)), N,
           _dense(cu_tokens, "cu_tokens", _I32, dev, (B + 1,)), _dense(positions, "positions", _I32, dev, (N,)),
           _dense(slots, "slots", _I32, dev, (N,)), _dense(lens_out, "lens_out", _I32, dev, (B,)),
@@ -166,6 +168,8 @@ def mla_rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None,
     [T, D / group] ([T, 1] with group 0); residual_out = h in bf16 (None without a residual; may be
     the residual itself); scales None with a bf16 out."""
     dev, (T, D) = _device(x, "x", 2)
+    if D > _INT_MAX:
+        raise MLAError(2, f"D is far above the 32768 that a row may have (got {D})")
     if out is None:
         e4m3 = bool(e4m3)
     elif e4m3 and getattr(out, "dtype", None) is not _E4M3:
@@ -214,14 +218,16 @@ def mla_kv_append(c_kv, k_pe, slots, positions, cos_sin, kv_cache, kv_scale: flo
     pk = _rows(k_pe, "k_pe", _BF16, dev, (T, 64))
     pcache = _dense(kv_cache, "kv_cache", _E4M3 if e4m3 else _BF16, dev, (pages, page, 576))
     max_pos = _shape(cos_sin, "cos_sin", 2)[0]
+    if page > _INT_MAX or max_pos > _INT_MAX:
+        raise MLAError(1, f"page size and max_pos must be below 2^31, got {page} and {max_pos}")
     pcs = _dense(cos_sin, "cos_sin", _F32, dev, (max_pos, 64))
     pw = None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, dev, (512,))
     pq = pqo = pkv = None
     H = qt = qh = ot = oh = st = 0
     if q_pe is not None:
         H = _shape(q_pe, "q_pe", 3)[1]
-        if H < 1:
-            raise MLAError(1, "q_pe must have at least one head")
+        if not 1 <= H <= _INT_MAX:
+            raise MLAError(1, f"q_pe must have between 1 and 2^31 - 1 heads (H), got {H}")
         if q_out is None:
             q_out = _empty((T, H, 576), _BF16, dev, stream)
         pq, pqo = _rows(q_pe, "q_pe", _BF16, dev, (T, H, 64)), _rows(q_out, "q_out", _BF16, dev, (T, H, 576))
@@ -243,6 +249,8 @@ def mla_bmm_w4(x, w4, scales, out=None, ws=None, stream=None):
     128 -> bf16 [T,H,N] (a strided `out` is fine)."""
     dev, (T, H, K) = _device(x, "x", 3)
     N, groups = _shape(w4, "w4", 3)[1], _shape(scales, "scales", 3)[2]
+    if H > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        raise MLAError(1, f"H, N and K must be below 2^31, got {H}, {N}, {K}")
     if groups < 1 or K % groups or K // groups not in (32, 64, 128):
         raise MLAError(1, f"scales must have K / group columns, group 32, 64 or 128 (got {groups}, K = {K})")
     f32 = scales.dtype is _F32
