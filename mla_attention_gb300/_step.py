@@ -100,7 +100,7 @@ def _workspace(ws, dev):
                 raise MLAError(1, "the first call on a device without a ws allocates the status word: make it before a capture")
             ws = torch.zeros(256, dtype=_U8, device=torch.device("cuda", dev))
             torch.cuda.current_stream(dev).synchronize()   # the call may be issued on another stream
-            _lib._status_cache[dev] = ws
+            ws = _lib._status_cache.setdefault(dev, ws)    # of two threads' first calls one buffer stays, and both use it
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise MLAError(1, f"ws must be a contiguous tensor on cuda:{dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size()

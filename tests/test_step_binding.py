@@ -1,9 +1,12 @@
-"""The serving step's binding on the host: sizes beyond the C ABI's 32-bit arguments (CPU only: nothing is launched)."""
+"""The serving step's binding on the host: sizes beyond the C ABI's 32-bit arguments, two threads' first calls (CPU
+only: nothing is launched)."""
+import threading
+
 import pytest
 import torch
 
 import mla_attention_gb300 as m
-from mla_attention_gb300 import _lib
+from mla_attention_gb300 import _lib, _step
 
 
 class Shaped:
@@ -78,3 +81,29 @@ def test_sizes_beyond_32_bits_are_refused(word, call, kw, status, what):
     with pytest.raises(m.MLAError) as e:
         call(**kw)
     assert e.value.status == status and what in str(e.value), e.value
+
+
+def test_two_threads_first_calls_share_one_status_word(monkeypatch):
+    """Both threads find no buffer and wait for their own; the address that each goes on with must be the one that is kept."""
+    meet = threading.Barrier(2)
+
+    class Stream:
+        def synchronize(self):   # lets the other thread run up to here
+            try:
+                meet.wait(timeout=2)
+            except threading.BrokenBarrierError:
+                pass             # the other one waits for a lock, or has found the buffer
+
+    zeros = torch.zeros
+    monkeypatch.setattr(_lib, "_status_cache", {})
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream())
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(_step._workspace(None, 0))) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    kept = _lib._status_cache[0]
+    assert got == [(kept.data_ptr(), 256)] * 2
