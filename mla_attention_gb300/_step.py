@@ -114,8 +114,8 @@ def _call(name, dev, stream, *args):
     global _several_devices
     fn = _functions.get(name)
     if fn is None:
+        _several_devices = torch.cuda.device_count() > 1    # before the function: a thread that finds that goes by it
         fn = _functions[name] = getattr(_lib.lib(), name)
-        _several_devices = torch.cuda.device_count() > 1
     if stream is None:
         stream = _current_stream(dev)
     elif hasattr(stream, "cuda_stream"):

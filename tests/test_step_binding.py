@@ -107,3 +107,36 @@ def test_two_threads_first_calls_share_one_status_word(monkeypatch):
         t.join()
     kept = _lib._status_cache[0]
     assert got == [(kept.data_ptr(), 256)] * 2
+
+
+def test_a_thread_that_finds_the_function_knows_the_number_of_devices(monkeypatch):
+    """A second thread's call on GPU 1, made as soon as the first thread's call has looked the function up, runs on GPU 1."""
+    on, current = [], [0]
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.dev
+
+        def __exit__(self, *_):
+            current[0] = self.was
+
+    def second(*_):
+        on.append(current[0])
+        return 0
+
+    class Functions(dict):
+        def __setitem__(self, name, fn):        # the first thread stops here, just behind the store
+            super().__setitem__(name, second)
+            _step._call(name, 1, 0)
+
+    monkeypatch.setattr(_step, "_functions", Functions())
+    monkeypatch.setattr(_step, "_several_devices", None)
+    monkeypatch.setattr(_lib, "lib", lambda: type("L", (), {"mla_rms_norm": second}))
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    _step._call("mla_rms_norm", 0, 0)
+    assert on == [1, 0]
