@@ -16,7 +16,8 @@ from ._lib import MLAError, _check
 
 _BF16, _I32, _F32, _E4M3, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn, torch.uint8
 _INT_MAX = 2 ** 31 - 1
-_current_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: torch.cuda.current_stream() builds a Stream, 2 us
+# the handle alone: torch.cuda.current_stream() builds a Stream, 2 us (a torch without CUDA has none, and no tensor that asks for it)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _dense(t, name, dtype, dev, shape):

@@ -1,5 +1,8 @@
 """The serving step's binding on the host: sizes beyond the C ABI's 32-bit arguments, two threads' first calls (CPU
 only: nothing is launched)."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -140,3 +143,11 @@ def test_a_thread_that_finds_the_function_knows_the_number_of_devices(monkeypatc
     monkeypatch.setattr(torch.cuda, "device", Device)
     _step._call("mla_rms_norm", 0, 0)
     assert on == [1, 0]
+
+
+def test_the_package_imports_with_a_torch_without_cuda():
+    """Such a build has no _cuda_* functions; the oracle's and the inputs' users need none."""
+    code = ("import torch\nfor n in dir(torch._C):\n    if n.startswith('_cuda_'): delattr(torch._C, n)\n"
+            "import mla_attention_gb300 as m\nprint(len(m.__all__))")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and int(r.stdout) == len(m.__all__), r.stderr[-2000:]
