@@ -155,13 +155,22 @@ _status_cache = {}     # status words of the calls around the attention (see _st
 
 
 def workspace(nbytes: int, device: torch.device) -> torch.Tensor:
+    """The device's scratch buffer of at least this size.  It grows by doubling, so that the outgrown ones together stay
+    below the present one; where memory does not hold twice the size, by what the call needs."""
     key = (device.type, device.index)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
-        if ws is not None:
-            _ws_outgrown.append(ws)
-        ws = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+        with _lock:
+            ws = _ws_cache.get(key)
+            if ws is None or ws.numel() < nbytes:
+                need = max(int(nbytes), 256)
+                try:
+                    new = torch.zeros(max(need, 0 if ws is None else 2 * ws.numel()), dtype=torch.uint8, device=device)
+                except torch.cuda.OutOfMemoryError:
+                    new = torch.zeros(need, dtype=torch.uint8, device=device)
+                if ws is not None:
+                    _ws_outgrown.append(ws)
+                ws = _ws_cache[key] = new
     return ws
 
 
