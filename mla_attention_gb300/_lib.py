@@ -26,6 +26,7 @@ class MLAError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
         self.status = status
+        self.message = message
 
 
 _lib = None
@@ -176,7 +177,7 @@ def workspace(nbytes: int, device: torch.device) -> torch.Tensor:
 
 def check_device_status(ws: Optional[torch.Tensor] = None, device=None, stream=None) -> int:
     """Read and clear the device status word; raise MLAError if a kernel reported a fault.  Without a
-    workspace: the device's own and the one of the calls around the attention."""
+    workspace: the device's own and the one of the calls around the attention (both faults in one error, with the first's status)."""
     words = [ws]
     if ws is None:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
@@ -184,17 +185,19 @@ def check_device_status(ws: Optional[torch.Tensor] = None, device=None, stream=N
         step = _status_cache.get(torch.cuda.current_device() if device.index is None else device.index)
         if step is not None:
             words.append(step)
-    failed, found = None, 0
+    faults, found = [], 0
     for w in words:
         detail = c_uint32(0)
         s = lib().mla_check_device_status(_ptr(w), _stream(stream), ctypes.byref(detail))
         try:
             _check(s)
         except MLAError as e:
-            failed = failed or e
+            faults.append(e)
         found = found or detail.value
-    if failed:
-        raise failed
+    if len(faults) > 1:   # both words are cleared: one error tells of both
+        raise MLAError(faults[0].status, f"{faults[0].message}; and {faults[1]}")
+    if faults:
+        raise faults[0]
     return found
 
 

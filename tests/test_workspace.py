@@ -1,4 +1,4 @@
-"""The binding's cached workspaces, on host memory (CPU only)."""
+"""The binding's cached workspaces and status words, on host memory (CPU only)."""
 import pytest
 import torch
 
@@ -40,3 +40,36 @@ def test_where_twice_the_size_does_not_fit_the_need_is_enough(monkeypatch):
 
     monkeypatch.setattr(torch, "zeros", small)
     assert workspace(1200, CPU).numel() == 1200 and first.numel() == 1000
+
+
+class Words:
+    """The C calls that read a status word, over words on the host."""
+
+    def __init__(self, codes):
+        self.codes, self.last = codes, b""       # by address
+
+    def mla_check_device_status(self, ptr, stream, detail):
+        code, self.codes[ptr.value] = self.codes.get(ptr.value, 0), 0
+        detail._obj.value = code
+        self.last = b"" if code == 0 else b"site 0x%x" % code
+        return 0 if code == 0 else 4 if code < 0x2000 else 5
+
+    def mla_last_error_string(self):
+        return self.last
+
+
+@pytest.mark.parametrize("own,step,status,told", [(0, 0, 0, []), (0x1011, 0, 4, ["0x1011"]), (0, 0x2071, 5, ["0x2071"]),
+                                                  (0x1011, 0x2071, 4, ["0x1011", "0x2071"])])
+def test_a_status_check_tells_of_every_fault_that_it_clears(monkeypatch, own, step, status, told):
+    a, b = torch.zeros(256, dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8)
+    words = Words({a.data_ptr(): own, b.data_ptr(): step})
+    monkeypatch.setattr(_lib, "lib", lambda: words)
+    monkeypatch.setattr(_lib, "workspace", lambda n, device: a)
+    monkeypatch.setattr(_lib, "_status_cache", {0: b})
+    if not status:
+        assert _lib.check_device_status(device="cuda:0", stream=0) == 0
+        return
+    with pytest.raises(_lib.MLAError) as e:
+        _lib.check_device_status(device="cuda:0", stream=0)
+    assert e.value.status == status and all(t in str(e.value) for t in told)
+    assert _lib.check_device_status(device="cuda:0", stream=0) == 0 and not any(words.codes.values())
