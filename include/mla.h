@@ -69,7 +69,8 @@ const char* mla_status_string(mla_status s);
  * receives the raw word (wait or check site id): 0x1000 | wait site for a timeout,
  * 0x2000 | check site for an out-of-range page id or length, and, in the guarded build
  * (libmla_guard.so, compiled with MLA_GUARD), 0x3000 | site for a plain load or store of a
- * kernel that would have left its buffer (the access was skipped).
+ * kernel that would have left its buffer (the access was skipped; those of calls without a workspace
+ * are reported through any).
  */
 mla_status mla_check_device_status(void* workspace, void* stream, uint32_t* detail);
 

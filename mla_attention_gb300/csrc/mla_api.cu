@@ -384,10 +384,15 @@ mla_status mla_check_device_status(void* workspace, void* stream, uint32_t* deta
   if (!workspace) return fail(MLA_ERR_INVALID_ARG, "mla_check_device_status: workspace is NULL");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t word = 0;
-  cudaError_t e = cudaMemcpyAsync(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, sizeof(word), st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  auto take = [&](void* from) {
+    cudaError_t e = cudaMemcpyAsync(&word, from, sizeof(word), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(from, 0, sizeof(word), st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    return e;
+  };
+  cudaError_t e = take(workspace);
+  if (uint32_t* guard = e == cudaSuccess && word == 0 ? guard_word() : nullptr) e = take(guard);
   if (e != cudaSuccess) return cuda_fail(e, "mla_check_device_status");
   if (detail) *detail = word;
   if (word == 0) return ok();

@@ -240,6 +240,9 @@ CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank
 
 int device_sm_count();
 
+// Guarded build: the status word on the current device of calls without a workspace (null in the default build).
+uint32_t* guard_word();
+
 // Record `msg` as the calling thread's last error and return `s`.
 mla_status set_last_error(mla_status s, const char* msg);
 

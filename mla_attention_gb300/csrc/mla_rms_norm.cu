@@ -21,6 +21,10 @@ namespace {
 
 constexpr float kMinScale = 0x1p-126f, kE4m3Max = 448.f;
 
+#ifdef MLA_GUARD
+__device__ uint32_t guard_status;   // the call has no workspace
+#endif
+
 __device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
@@ -91,13 +95,13 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
       for (int i = 0; i < 8; ++i) {
         const int c = (8 * k + i) * per_row + sub;
         const __nv_bfloat16* src = base + row * stride + sub + (8 * k + i) * per_row;
-        b[i] = c < p.D && guard_span(nullptr, G_STEP_IN, src, 2, base, ext) ? *reinterpret_cast<const uint16_t*>(src) : 0u;
+        b[i] = c < p.D && guard_span(p.err, G_STEP_IN, src, 2, base, ext) ? *reinterpret_cast<const uint16_t*>(src) : 0u;
       }
       return make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
     }
     const int c = 8 * (sub + k * per_row), n = min(8, p.D - c);
     const __nv_bfloat16* src = base + row * stride + c;
-    if (n <= 0 || !guard_span(nullptr, G_STEP_IN, src, 2 * n, base, ext)) return make_uint4(0, 0, 0, 0);
+    if (n <= 0 || !guard_span(p.err, G_STEP_IN, src, 2 * n, base, ext)) return make_uint4(0, 0, 0, 0);
     if (!on_vec || n < 8) return load_row8_narrow(src, n);
     return base == p.weight ? *reinterpret_cast<const uint4*>(src) : load_once(src);
   };
@@ -108,12 +112,12 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
       for (int i = 0; i < 8; ++i) {
         const int c = (8 * k + i) * per_row + sub;
         __nv_bfloat16* dst = base + t * stride + c;
-        if (c < p.D && guard_span(nullptr, G_STEP_OUT, dst, 2, base, ext)) *dst = __float2bfloat16_rn(f[i]);
+        if (c < p.D && guard_span(p.err, G_STEP_OUT, dst, 2, base, ext)) *dst = __float2bfloat16_rn(f[i]);
       }
     } else {
       const int c = 8 * (sub + k * per_row), n = min(8, p.D - c);
       __nv_bfloat16* dst = base + t * stride + c;
-      if (n > 0 && guard_span(nullptr, G_STEP_OUT, dst, 2 * n, base, ext)) store_row8(dst, n, on_vec, f);
+      if (n > 0 && guard_span(p.err, G_STEP_OUT, dst, 2 * n, base, ext)) store_row8(dst, n, on_vec, f);
     }
   };
   constexpr bool kWeightFirst = NV <= 2;   // more vectors leave no registers for it
@@ -218,16 +222,16 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) rms_norm_kernel(const __g
       quotient8(h[k], s_or_0, inv_s);
       float* sc = p.scales + t * groups + (whole ? 0 : c >> group_log2);
       const bool writes = whole ? sub == 0 && k == 0 : n > 0 && (c & (p.group - 1)) == 0;
-      if (writes && guard_span(nullptr, G_STEP_OUT, sc, 4, p.scales, (uint64_t)p.T * groups * 4)) *sc = s;
+      if (writes && guard_span(p.err, G_STEP_OUT, sc, 4, p.scales, (uint64_t)p.T * groups * 4)) *sc = s;
       const uint64_t ext = (uint64_t)(p.T - 1) * p.out_stride + p.D;
       if constexpr (kStrided) {
         const uint2 q = e4m3x8_pack(h[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int ci = (8 * k + i) * per_row + sub;
-          if (ci < p.D && guard_span(nullptr, G_STEP_OUT, out + ci, 1, p.out, ext)) out[ci] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+          if (ci < p.D && guard_span(p.err, G_STEP_OUT, out + ci, 1, p.out, ext)) out[ci] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
         }
-      } else if (n > 0 && guard_span(nullptr, G_STEP_OUT, out + c, n, p.out, ext)) {
+      } else if (n > 0 && guard_span(p.err, G_STEP_OUT, out + c, n, p.out, ext)) {
         store_row8_e4m3(out + c, n, wide & kWideOut, h[k]);
       }
     }
@@ -250,6 +254,14 @@ bool on(const void* p, int64_t stride, int T, int bytes, int elem) {
 }
 
 }  // namespace
+
+uint32_t* guard_word() {
+  void* at = nullptr;
+#ifdef MLA_GUARD
+  if (cudaGetSymbolAddress(&at, guard_status) != cudaSuccess) return nullptr;
+#endif
+  return reinterpret_cast<uint32_t*>(at);
+}
 
 cudaError_t launch_rms_norm(const RmsNormParams& p, cudaStream_t stream) {
   int wide = 0;

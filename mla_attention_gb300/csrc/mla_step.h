@@ -32,6 +32,7 @@ struct RmsNormParams {
   __nv_bfloat16* residual_out;        // with residual
   void* out;                          // bf16, or e4m3 with scales
   float* scales;                      // [T, groups] or null (bf16 out)
+  uint32_t* err;                      // guarded build: guard_word(), else null
   int64_t x_stride, residual_stride, residual_out_stride, out_stride;  // elements
   float eps;
   int T, D;

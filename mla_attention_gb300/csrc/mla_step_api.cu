@@ -125,6 +125,7 @@ mla_status mla_rms_norm(const void* x, int64_t x_stride, const void* residual, i
   p.T = T;
   p.D = D;
   p.group = group ? group : D;
+  p.err = guard_word();
   return finish(launch_rms_norm(p, reinterpret_cast<cudaStream_t>(stream)), "mla_rms_norm");
 }
 
