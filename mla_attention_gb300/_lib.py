@@ -177,11 +177,13 @@ def workspace(nbytes: int, device: torch.device) -> torch.Tensor:
 
 def check_device_status(ws: Optional[torch.Tensor] = None, device=None, stream=None) -> int:
     """Read and clear the device status word; raise MLAError if a kernel reported a fault.  Without a
-    workspace: the device's own and the one of the calls around the attention (both faults in one error, with the first's status)."""
+    workspace: the device's own, those that it outgrew and the one of the calls around the attention (several faults in one
+    error, with the first's status)."""
     words = [ws]
     if ws is None:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         words = [workspace(256, device)]
+        words += [w for w in _ws_outgrown if w.device == words[0].device]    # a captured graph reports in the one that it holds
         step = _status_cache.get(torch.cuda.current_device() if device.index is None else device.index)
         if step is not None:
             words.append(step)
@@ -194,8 +196,8 @@ def check_device_status(ws: Optional[torch.Tensor] = None, device=None, stream=N
         except MLAError as e:
             faults.append(e)
         found = found or detail.value
-    if len(faults) > 1:   # both words are cleared: one error tells of both
-        raise MLAError(faults[0].status, f"{faults[0].message}; and {faults[1]}")
+    if len(faults) > 1:   # all words are cleared: one error tells of all
+        raise MLAError(faults[0].status, "; and ".join([faults[0].message, *map(str, faults[1:])]))
     if faults:
         raise faults[0]
     return found

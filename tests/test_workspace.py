@@ -73,3 +73,15 @@ def test_a_status_check_tells_of_every_fault_that_it_clears(monkeypatch, own, st
         _lib.check_device_status(device="cuda:0", stream=0)
     assert e.value.status == status and all(t in str(e.value) for t in told)
     assert _lib.check_device_status(device="cuda:0", stream=0) == 0 and not any(words.codes.values())
+
+
+def test_a_fault_in_an_outgrown_workspace_is_reported(monkeypatch):
+    """A graph captured before the workspace grew reports in the old one, and its kernels give up their waits until it is cleared."""
+    old, new = workspace(256, CPU), workspace(9000, CPU)
+    words = Words({old.data_ptr(): 0x1011, new.data_ptr(): 0})
+    monkeypatch.setattr(_lib, "lib", lambda: words)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(_lib.MLAError) as e:
+        _lib.check_device_status(device=CPU, stream=0)
+    assert e.value.status == 4
+    assert _lib.check_device_status(device=CPU, stream=0) == 0 and not any(words.codes.values())
