@@ -336,7 +336,8 @@ mla_status mla_rope_append(const void* q_pe, const void* c_kv, const void* k_pe,
 /*
  * Block tables, positions and slots of one step's tokens, built on the GPU from request lengths.
  * Request b holds lens[b] tokens and gains (n > 0) or drops (n < 0) n = new_tokens[b] of them
- * (drops: rejected draft tokens; n <= -lens[b] ends the request).  With
+ * (drops: rejected draft tokens; n <= -lens[b] ends the request; a step that drops and gains tokens of
+ * one request takes two calls).  With
  *   len' = max(0, len + n), have = ceil(len / page_size), need = ceil(len' / page_size)
  * a grown request takes need - have page ids from the pool into block_table[b][have .. need - 1], in
  * request order; a shrunk one gives the ids in block_table[b][need .. have - 1] back (the entries
@@ -410,7 +411,7 @@ mla_status mla_rms_norm(const void* x, int64_t x_stride, const void* residual, i
  *          position outside [0, max_pos) records MLA_ERR_DEVICE_RANGE and is skipped likewise.
  * slots    DEVICE int32 [T]: cache rows (mla_slot_map).  -1: no cache row is written (q_out and
  *          kv_out are); another slot outside [0, num_pages * page_size) is recorded, too.  The slots
- *          of a call's tokens are distinct: of two tokens in one slot either's values may stay.
+ *          of a call's tokens are distinct: of two tokens in one slot the row may hold parts of both.
  * kv_cache bf16 or (cache_e4m3) e4m3 [num_pages, page_size, 576]; with e4m3
  *          2^-126 <= kv_scale <= 2^126.
  * Tensors are 16-byte aligned, strides multiples of 8 elements.

@@ -34,7 +34,6 @@ __device__ __forceinline__ Sums shfl_up(const Sums& a, int d) {
 template <int kThreads>
 struct Shared {
   Sums warp[32];
-  long long total[3];
   // per request of the chunk: first token / popped / returned page, relative to the chunk's first
   int tok[kThreads + 1], pop[kThreads + 1], put[kThreads + 1];
   int len[kThreads], have[kThreads], need[kThreads];

@@ -111,10 +111,4 @@ __device__ __forceinline__ void store_row8_e4m3(uint8_t* dst, int n, bool wide, 
   }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-  return v;
-}
-
 }  // namespace mla
