@@ -25,10 +25,11 @@
 // every warp waiting for loads and for the slowest.
 // Few columns with a long k are cut over a cluster's CTAs, whose sums are joined in shared memory in
 // a fixed order.
-// 8192 columns, k of 16384, groups of 128, 4 tokens: 19.2 us, 53 % of the copy's bandwidth, at half of the
-// issue slots.  128 heads of 512 columns, k of 128, one token 4.6 us, of 128 columns, k of 512, 17 tokens
-// 5.05: a launch, the first chunk's way in and the sums' way out.  Instructions are kept few as well: each is
-// fetched once a launch (the helpers' loads in three places instead of one cost 0.2 us).
+// 8192 columns, k of 16384, groups of 128, 4 tokens: 19.6 us, 52 % of the copy's bandwidth, at half of the
+// issue slots.  128 heads of 512 columns, k of 128, one token 5.3 us, of 128 columns, k of 512, 17 tokens
+// 5.8 (inputs from HBM): a launch, the first chunk's way in and the sums' way out.  Instructions are kept few as well: each is
+// fetched once a launch (the helpers' loads in three places instead of one cost 0.2 us).  Two times side by side below are
+// of two forms of one build, some of them before the weights had their sign.
 #include <algorithm>
 #include <type_traits>
 

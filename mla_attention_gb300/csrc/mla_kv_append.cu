@@ -13,9 +13,9 @@
 // the way as one.  In both pairings a lane's two 16-byte vectors at columns 8u and 32 + 8u (u = 0..3)
 // hold whole pairs, so four lanes serve a RoPE vector, read its angles once and use them for all of
 // the warp's heads.
-// Prefill of 8192 tokens with 128 heads and the rows written too 47.9 us, 92 % of the copy's bandwidth (the cache
-// stays partly in L2); 32768 rows to e4m3 without heads 14.1 us, 68 %, bound by issue and load latency; a decode step of
-// 64 tokens with 128 heads 2.5 us.
+// Prefill of 8192 tokens with 128 heads and the rows written too 47.4 us, 93 % of the copy's bandwidth (the cache
+// stays partly in L2); 32768 rows to e4m3 without heads 14.1 to 14.8 us, 65 to 68 %, bound by issue and load latency; a decode
+// step of 64 tokens with 128 heads 2.4 to 2.6 us.
 #include "mla_step.h"
 #include "row_vec.cuh"
 

@@ -9,8 +9,8 @@
 // where registers allow; x and the residual pass by L1, which keeps the weight, and are asked for in L2 a
 // little before their CTA starts: what is on its way between HBM and L2 takes no registers.  bf16 rows written off the
 // vector boundaries (an odd width) go value by value instead, neighbouring columns in neighbouring lanes.
-// 16384 x 5120 with residual to e4m3: 89 us, 97 % of the copy's bandwidth; 8000 x 8192 to bf16 78 us, 98 %;
-// one row of 8192 2.4 us.
+// 16384 x 5120 with residual to e4m3: 90 us, 97 % of the copy's bandwidth; 8000 x 8192 with residual to bf16 78.8 us, 98 %;
+// one row of 8192 2.3 to 2.5 us.  To e4m3 without a residual the arithmetic bounds it: 4000 x 16384 54.6 us, 53 %.
 //
 // max|y| and the sum keep a NaN (a row that holds one is NaN throughout).
 #include "mla_step.h"
@@ -287,7 +287,7 @@ cudaError_t launch_rms_norm(const RmsNormParams& p, cudaStream_t stream) {
   if (vecs <= 32) return launch<1, false>(p, wide, 128, stream);
   if (vecs <= 64) return launch<2, false>(p, wide, 128, stream);
   if (vecs <= 128) return launch<4, false>(p, wide, 128, stream);
-  // A CTA a row.  Two vectors a thread are the shorter way through one row (8192 columns: 2.6 us, four 3.4);
+  // A CTA a row.  Two vectors a thread are the shorter way through one row (8192 columns when it was chosen: 2.6 us, four 3.4);
   // four put more rows on an SM, which pays for wide ones once the SMs are full (8000 x 8192 with residual:
   // 84.6 us and 80.2; 16384 x 5120 to e4m3: 100.4 and 98.2; 4000 x 16384 to e4m3: 78.8 and 61.4; but
   // 2048 x 4096: 12.9 and 13.9).
