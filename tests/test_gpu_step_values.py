@@ -181,3 +181,30 @@ def test_append_next_to_a_nan_or_an_infinity_rounds_to_nearest():
     want = np.full((4, 512), 12.0)
     want[1, 3::8], want[2, 6::8], want[3, 1::8] = np.nan, 448, -448
     np.testing.assert_array_equal(got, want)
+
+
+def test_append_norms_far_latents_in_place():
+    """Rows that are read twice, written over themselves: the same bits as into a buffer of their own."""
+    g, d, T = torch.Generator().manual_seed(33), dev(), 5
+    kv = torch.randn((T, 576), generator=g)
+    kv[0] *= 2.0 ** 80
+    kv[3] *= 2.0 ** -90
+    kv, w = kv.to(torch.bfloat16).to(d), (1 + 0.3 * torch.randn(512, generator=g)).to(torch.bfloat16).to(d)
+    at, cs, rows = torch.arange(T, dtype=torch.int32, device=d), gen.rope_cos_sin(T).to(d), torch.empty_like(kv)
+    one, two = torch.zeros((1, T, 576), dtype=torch.bfloat16, device=d), torch.zeros((1, T, 576), dtype=torch.bfloat16, device=d)
+    mla_kv_append(kv[:, :512], kv[:, 512:], at, at, cs, one, norm_weight=w, eps=0.0, kv_out=rows)
+    mla_kv_append(kv[:, :512], kv[:, 512:], at, at, cs, two, norm_weight=w, eps=0.0, kv_out=kv)
+    _done()
+    assert torch.equal(one, two) and torch.equal(rows, kv) and torch.equal(one[0], kv)
+
+
+@pytest.mark.parametrize("T", [1, 9, 64])
+def test_w4_smallest_numbers_in_x(T):
+    """x below the smallest normal number, scales that bring out back up."""
+    g = torch.Generator().manual_seed(50 + T)
+    w4, scales = _w4(1, 64, 512, 64, True, g)
+    x = (torch.randn((T, 1, 512), generator=g) * 2.0 ** -128).to(torch.bfloat16)
+    out = mla_bmm_w4(x.to(dev()), w4, scales * 2.0 ** 60)
+    _done()
+    ref, mass = so.bmm_w4(to_np(x), w4.cpu().numpy(), to_np(scales * 2.0 ** 60))
+    _bf16(out, ref, "out", mass * 512 * 2.0 ** -24)
