@@ -447,6 +447,109 @@ mla_status mla_bmm_w4(const void* x, int64_t x_stride_t, int64_t x_stride_h, con
                       int64_t out_stride_h, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* A smaller cache: 4-bit rows, and rows kept by the attention they got       */
+/* ------------------------------------------------------------------------- */
+/*
+ * A row of the 4-bit latent cache has 416 bytes (the cache is [num_pages, page_size, 416] bytes, contiguous,
+ * 16-byte aligned):
+ *   bytes   0..255  codes of the 512 latent columns in e2m1 (0 .5 1 1.5 2 3 4 6 and their negatives): column
+ *                   2j in the low half of byte j, column 2j + 1 in its high half
+ *   bytes 256..287  32 e4m3 scales, one for 16 columns
+ *   bytes 288..415  the 64 rotated RoPE columns in bf16
+ * Latent column c stands for code[c] * scale[c / 16] * kv_scale, a RoPE column for its value * kv_scale.  The rows move
+ * through page tables as those of the other caches: mla_slot_map gives the slots.
+ *
+ * mla_kv_append_fp4: mla_kv_append with such rows.  From the unrounded row of mla_kv_append, v = row / kv_scale:
+ *   scale of 16 columns = e4m3(min(max(max|v| / 6, 2^-9), 448)),  code = e2m1(v / scale), both to the nearest value,
+ *   ties to even, codes saturating at +-6; a NaN among 16 columns makes their scale NaN.
+ * The codes and scales are those of the exact quotients: a value next to a border is decided in 64 bits.
+ * Arguments as mla_kv_append; 2^-100 <= kv_scale <= 2^100.  q_out and kv_out are as there (kv_out: the rows in
+ * bf16, before the 4 bits).  workspace: >= 256 bytes (the status word).
+ */
+size_t mla_kv_append_fp4_workspace_size(int T);
+mla_status mla_kv_append_fp4(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t k_pe_stride,
+                             const void* norm_weight, float eps, const void* q_pe, int64_t q_pe_stride_t,
+                             int64_t q_pe_stride_h, const int32_t* positions, const int32_t* slots,
+                             const float* cos_sin, int max_pos, int is_neox, int T, int H, void* kv_cache_fp4,
+                             float kv_scale, int64_t num_pages, int page_size, void* q_out, int64_t q_out_stride_t,
+                             int64_t q_out_stride_h, void* kv_out, int64_t kv_out_stride, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Decode over a 4-bit latent cache.  Arguments, masks, sinks and results as mla_decode_fp8 (q bf16
+ * [B, q_per_req, H, 576]; out bf16 [B, q_per_req, H, 512]; lse fp32 [B, q_per_req, H] or NULL), with any
+ * page_size >= 1, num_pages * page_size below 2^31 and 2^-100 <= kv_scale <= 2^100.  The products of the latent part run on f16
+ * operands (a code times its scale is exact there; q is rounded to f16: |q| must stay below 65504, values below
+ * 2^-14 keep an absolute error of 2^-25) and those of the RoPE part on bf16 ones; sums are fp32.  A page id outside
+ * [0, num_pages) reads as keys of zeros, a length outside [0, max_pages * page_size] is cut to it; both
+ * record MLA_ERR_DEVICE_RANGE (details 0x207a, 0x207b).  Rows of the block table behind a request's last page
+ * are not read.
+ * workspace_bytes >= mla_decode_fp4_workspace_size(B, q_per_req, H, num_splits).
+ */
+size_t mla_decode_fp4_workspace_size(int B, int q_per_req, int H, int num_splits);
+mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4, float kv_scale, int64_t num_pages,
+                          int page_size, const int32_t* block_table, int max_pages, const int32_t* lens, int B, int H,
+                          float scale, const float* sinks, int num_splits, void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * How much attention each cached key got from a request's last query tokens, added up over tokens and heads:
+ *   weights[b, j] = decay * weights[b, j] + sum_{i, h: key j visible to token i} exp(scale * q[b, i, h] . key_j - lse[b, i, h])
+ * for j < lens[b]; the others are left as they are.  Token i of request b sees the keys j <= lens[b] - q_per_req + i, as
+ * in mla_decode_ex; lse is what the decode (or prefill) over the same keys gave, in its layout.  With decay = 0 the old
+ * weights are not read.  A token whose lse is -inf saw no key and adds nothing; one whose lse is +inf adds nothing.
+ *
+ * q        bf16 [B, q_per_req, H, 576]; lse fp32 [B, q_per_req, H]; both contiguous, q 16-byte aligned.
+ * kv_cache 16-byte aligned: cache_format 0 bf16 [.., 576], 1 e4m3 [.., 576], 2 the 4-bit rows [.., 416]; every
+ *          value stands for value * kv_scale (2^-100 <= kv_scale <= 2^100; 1 for a bf16 cache of plain values).
+ * weights  fp32 [B, width] at row stride weights_stride >= width.  A length outside [0, min(width, max_pages *
+ *          page_size)] is cut to it and recorded (0x207b), as is a page id outside [0, num_pages) (0x207a; keys of zeros).
+ * decay    finite, >= 0.  H >= 1, q_per_req * H <= 2^20, B <= 65535.
+ * Formats 1 and 2 round q to f16 for the latent (1: all) columns, as mla_decode_fp8 and mla_decode_fp4 do.
+ * No atomics: the same inputs give the same weights.
+ */
+size_t mla_key_weights_workspace_size(int B, int q_per_req, int H);
+mla_status mla_key_weights(const void* q, int q_per_req, const float* lse, const void* kv_cache, int cache_format,
+                           float kv_scale, int64_t num_pages, int page_size, const int32_t* block_table, int max_pages,
+                           const int32_t* lens, int B, int H, float scale, float decay, float* weights,
+                           int64_t weights_stride, int width, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Which rows of each request stay in a cache of at most keep[b] rows: n = min(lens[b], keep[b]) of them, namely
+ * the last min(recent, n), the first min(first, n - those), and of the others those with the largest weights (of equal
+ * weights the lowest index; a NaN counts as the largest).
+ *   idx[b, 0 .. n-1] = their indices, ascending; idx[b, n .. K-1] = -1; count[b] = n; dropped[b] = n - lens[b]
+ * dropped is the new_tokens that gives the pages behind the kept rows back (mla_slot_map, after mla_compact_rows).
+ *
+ * weights  fp32 [B, width] at row stride weights_stride >= width; lens, keep DEVICE int32 [B]; idx int32 [B, K]
+ *          contiguous; count, dropped int32 [B].  first, recent, K >= 0; K, width < 2^31 - 2^16.
+ * A request with lens[b] outside [0, width], keep[b] < 0 or n > K is refused: count = dropped = 0, idx -1, and
+ * MLA_ERR_DEVICE_RANGE recorded (0x207c).  workspace: >= 256 bytes (the status word).
+ */
+size_t mla_select_keys_workspace_size(int B);
+mla_status mla_select_keys(const float* weights, int64_t weights_stride, int width, const int32_t* lens,
+                           const int32_t* keep, int first, int recent, int B, int K, int32_t* idx, int32_t* count,
+                           int32_t* dropped, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The kept rows moved to the front of their request, in place: row i of request b becomes its row idx[b, i], for
+ * i < count[b]; with weights also weights[b, i] = weights[b, idx[b, i]].  The rows behind are left as they are.  RoPE is in
+ * the rows already: later tokens keep their positions and go on behind row count[b].
+ *
+ * kv_cache [num_pages, page_size, row_bytes] contiguous, 16-byte aligned, row_bytes a multiple of 16 up to
+ *          65536 (1152 bf16, 576 e4m3, 416 4-bit rows); a page belongs to one request.
+ * idx      int32 [B, K] contiguous, ascending as mla_select_keys writes them; count DEVICE int32 [B]; B <= 65535.
+ * weights  (nullable) fp32 [B, width] at row stride weights_stride >= width.
+ * An entry that is not above the one before it, lies below its own place i or outside the table (or the weights' width), or
+ * whose pages are not in [0, num_pages), is skipped and recorded (MLA_ERR_DEVICE_RANGE, 0x207d), as is a request whose
+ * count is not in [0, K].  workspace: >= 256 bytes (the status word).
+ */
+size_t mla_compact_rows_workspace_size(int B);
+mla_status mla_compact_rows(void* kv_cache, int row_bytes, int64_t num_pages, int page_size, const int32_t* block_table,
+                            int max_pages, const int32_t* idx, int K, const int32_t* count, int B, float* weights,
+                            int64_t weights_stride, int width, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Top-k sparse latent + RoPE attention                                       */
 /* ------------------------------------------------------------------------- */
 /*

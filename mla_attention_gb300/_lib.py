@@ -87,6 +87,22 @@ _SIGNATURES = {
                        c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_size_t, c_void_p], c_int),
     "mla_bmm_w4": ([c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_void_p,
                     c_int64, c_int64, c_void_p, c_size_t, c_void_p], c_int),
+    "mla_kv_append_fp4_workspace_size": ([c_int], c_size_t),
+    "mla_kv_append_fp4": ([c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_float, c_void_p, c_int64, c_int64, c_void_p,
+                           c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_float, c_int64, c_int, c_void_p,
+                           c_int64, c_int64, c_void_p, c_int64, c_void_p, c_size_t, c_void_p], c_int),
+    "mla_decode_fp4_workspace_size": ([c_int, c_int, c_int, c_int], c_size_t),
+    "mla_decode_fp4": ([c_void_p, c_int, c_void_p, c_float, c_int64, c_int, c_void_p, c_int, c_void_p, c_int, c_int,
+                        c_float, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p], c_int),
+    "mla_key_weights_workspace_size": ([c_int, c_int, c_int], c_size_t),
+    "mla_key_weights": ([c_void_p, c_int, c_void_p, c_void_p, c_int, c_float, c_int64, c_int, c_void_p, c_int, c_void_p,
+                         c_int, c_int, c_float, c_float, c_void_p, c_int64, c_int, c_void_p, c_size_t, c_void_p], c_int),
+    "mla_select_keys_workspace_size": ([c_int], c_size_t),
+    "mla_select_keys": ([c_void_p, c_int64, c_int, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
+                         c_void_p, c_void_p, c_size_t, c_void_p], c_int),
+    "mla_compact_rows_workspace_size": ([c_int], c_size_t),
+    "mla_compact_rows": ([c_void_p, c_int, c_int64, c_int, c_void_p, c_int, c_void_p, c_int, c_void_p, c_int, c_void_p,
+                          c_int64, c_int, c_void_p, c_size_t, c_void_p], c_int),
     "mla_merge_lse": ([c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p],
                       c_int),
 }

@@ -1,0 +1,49 @@
+// Rows of a paged cache and the values of 4-bit ones.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "mla_cache.h"
+#include "row_vec.cuh"
+
+namespace mla {
+
+// an int32 of a table or list (guarded build: 0 outside it)
+__device__ __forceinline__ int32_t guarded_int(uint32_t* err, const int32_t* base, int64_t i, int64_t n) {
+  return guard_span(err, G_STEP_IN, base + i, 4, base, (uint64_t)n * 4) ? base[i] : 0;
+}
+
+// length of request b, cut to `cap`; `report`: one thread of the call records a length outside it
+__device__ __forceinline__ int paged_len(const PagedRows& kv, uint32_t* err, int b, int64_t cap, bool report) {
+  int64_t n = guarded_int(err, kv.lens, b, kv.B);
+  if (n < 0 || n > cap) {
+    if (report) record_error(err, DEV_RANGE_BASE | Y_LEN);
+    n = n < 0 ? 0 : cap;
+  }
+  return (int)n;
+}
+
+// row of key j of request b, null (and recorded) where its page is none
+__device__ __forceinline__ const uint8_t* paged_row(const PagedRows& kv, uint32_t* err, int b, int j) {
+  const int pg = j / kv.page_size;
+  const int page = guarded_int(err, kv.block_table, (int64_t)b * kv.max_pages + pg, (int64_t)kv.B * kv.max_pages);
+  if (page < 0 || page >= kv.num_pages) {
+    record_error(err, DEV_RANGE_BASE | Y_PAGE);
+    return nullptr;
+  }
+  const uint8_t* row = kv.cache + ((int64_t)page * kv.page_size + (j - pg * kv.page_size)) * kv.row_bytes;
+  const bool in = guard_span(err, G_STEP_IN, row, kv.row_bytes, kv.cache, (uint64_t)kv.num_pages * kv.page_size * kv.row_bytes);
+  return in ? row : nullptr;
+}
+
+// two codes (low half first) as f16
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
+  return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+__device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
+}
+
+}  // namespace mla

@@ -1,0 +1,78 @@
+// A smaller latent cache: parameters and launchers of the decode over 4-bit rows, the keys' attention weights, the
+// choice of the rows that stay and their move to the front of their request.
+#pragma once
+#include "mla_internal.h"
+
+namespace mla {
+
+// a 4-bit cache row: [codes of 512 latent columns | 32 scales | 64 RoPE columns in bf16]
+constexpr int kFp4Codes = kLatent / 2;                     // bytes
+constexpr int kFp4Scales = kLatent / 16;
+constexpr int kFp4Pe = kFp4Codes + kFp4Scales;             // offset of the RoPE columns
+constexpr int kFp4Row = kFp4Pe + 2 * kRope;                // 416
+
+// device range codes (below DEV_RANGE_BASE)
+enum : uint32_t { Y_PAGE = 0x7A, Y_LEN = 0x7B, Y_SELECT = 0x7C, Y_COMPACT = 0x7D };
+
+// the rows of a request's keys, through its block table
+struct PagedRows {
+  const uint8_t* cache;          // [num_pages * page_size] rows
+  const int32_t* block_table;    // [B, max_pages]
+  const int32_t* lens;           // [B] (null where the call has none)
+  int64_t num_pages;
+  int max_pages, page_size, B;
+  int row_bytes;
+};
+
+struct DecodeFp4Params {
+  PagedRows kv;
+  const __nv_bfloat16* q;        // [B, s, H, 576]
+  const float* sinks;            // [H] or null
+  __nv_bfloat16* out;            // [B, s, H, 512]
+  float* lse;                    // [B, s, H] or null
+  uint32_t* err;
+  float scale;                   // scale * kv_scale
+  float kv_scale;
+  int s, H;
+};
+cudaError_t launch_decode_fp4(const DecodeFp4Params& p, cudaStream_t stream);
+
+struct KeyWeightsParams {
+  PagedRows kv;
+  const __nv_bfloat16* q;        // [B, s, H, 576]
+  const float* lse;              // [B, s, H]
+  float* weights;                // [B, width] rows at stride
+  int64_t stride;
+  uint32_t* err;
+  float scale;                   // scale * kv_scale
+  float decay;
+  int format;                    // 0 bf16, 1 e4m3, 2 4-bit rows
+  int s, H, width;
+};
+cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
+
+struct SelectParams {
+  const float* weights;          // [B, width] rows at stride
+  const int32_t* lens;           // [B]
+  const int32_t* keep;           // [B]
+  int32_t* idx;                  // [B, K]
+  int32_t* count;                // [B]
+  int32_t* dropped;              // [B]
+  uint32_t* err;
+  int64_t stride;
+  int width, first, recent, B, K;
+};
+cudaError_t launch_select_keys(const SelectParams& p, cudaStream_t stream);
+
+struct CompactParams {
+  PagedRows kv;                  // lens null
+  const int32_t* idx;            // [B, K]
+  const int32_t* count;          // [B]
+  float* weights;                // [B, width] rows at stride, or null
+  uint32_t* err;
+  int64_t stride;
+  int K, width;
+};
+cudaError_t launch_compact_rows(const CompactParams& p, cudaStream_t stream);
+
+}  // namespace mla

@@ -1,9 +1,13 @@
 // Cache rows by slot: the latent's RMS norm, RoPE and the write of [latent | rotated k_pe] into the
-// paged cache in bf16 or e4m3, and the rotated q_pe into the fused query.
+// paged cache in bf16, e4m3 or 4 bits, and the rotated q_pe into the fused query.
 //
 //   row = [c_kv / sqrt(mean(c_kv^2) + eps) * w | turn(k_pe)]       cache[slot] = bf16(row) or e4m3(row / kv_scale)
 // A pair (a, b) of a RoPE vector turns by its angle: (a cos - b sin, a sin + b cos); pair i is
 // (x[2i], x[2i+1]) or, with is_neox, (x[i], x[i+32]).  Everything is computed in fp32 and rounded once.
+// 4-bit rows (append_latents_fp4): two lanes hold the 16 columns of a scale.  Scale and codes are those of the exact
+// quotients: each is rounded from its fp32 value a little below and a little above (2^-20, over the 13 roundings behind it); where
+// the two differ, once or twice in 512 rows, the row is done again with its norm in fp64 and each such value is compared
+// with the border itself.
 //
 // HBM-bound: per token 1152 bytes in, 576 or 1152 out and 256 per head of q.  Half a warp per latent, four
 // lanes per row's RoPE columns and a warp per 16 heads of a token's q (eight: 55 us for the prefill below),
@@ -16,6 +20,7 @@
 // Prefill of 8192 tokens with 128 heads and the rows written too 47.4 us, 93 % of the copy's bandwidth (the cache
 // stays partly in L2); 32768 rows to e4m3 without heads 14.1 to 14.8 us, 65 to 68 %, bound by issue and load latency; a decode
 // step of 64 tokens with 128 heads 2.4 to 2.6 us.
+#include "fp4_rows.cuh"
 #include "mla_step.h"
 #include "row_vec.cuh"
 
@@ -89,6 +94,19 @@ __device__ __forceinline__ void store_cache8(const KvAppendParams& p, int64_t ro
   }
 }
 
+// eight RoPE columns of row `row` of a 4-bit cache
+__device__ __forceinline__ void store_pe8_fp4(const KvAppendParams& p, int64_t row, int col, const float (&f)[8]) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = f[i];
+  if (p.kv_scale != 1.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = f[i] / p.kv_scale;
+  }
+  uint8_t* dst = reinterpret_cast<uint8_t*>(p.cache) + row * kFp4Row + kFp4Pe + 2 * col;
+  if (guard_span(p.err, G_STEP_OUT, dst, 16, p.cache, (uint64_t)p.cache_rows * kFp4Row)) *reinterpret_cast<uint4*>(dst) = bf16x8_pack(q);
+}
+
 __device__ __forceinline__ uint4 load16(const KvAppendParams& p, const __nv_bfloat16* src, const __nv_bfloat16* base, int64_t extent) {
   return guard_span(p.err, G_STEP_IN, src, 16, base, (uint64_t)extent * 2) ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
 }
@@ -150,13 +168,18 @@ __device__ __forceinline__ Target row_target(const KvAppendParams& p, int pos, i
   }
   return {slot >= 0 || p.kv_out ? pos : -1, slot};
 }
-// columns col .. col + 7 of token t's row
+// columns col .. col + 7 of token t's row (kFp4: RoPE columns, kept in bf16)
+template <bool kFp4 = false>
 __device__ __forceinline__ void put_row8(const KvAppendParams& p, int t, int64_t slot, int col, const float (&f)[8]) {
-  if (slot >= 0) store_cache8(p, slot, col, f);
+  if (slot >= 0) {
+    if constexpr (kFp4) store_pe8_fp4(p, slot, col - kLatent, f);
+    else store_cache8(p, slot, col, f);
+  }
   if (p.kv_out) store16(p, p.kv_out + t * p.kv_out_stride + col, p.kv_out, (p.T - 1) * p.kv_out_stride + kDk, f);
 }
 
 // ---- the RoPE columns of eight rows, four lanes a row ----
+template <bool kFp4>
 __device__ __forceinline__ void append_pe(const KvAppendParams& p, int t, int lane) {
   if (t >= p.T) return;
   const bool neox = p.is_neox != 0;
@@ -171,8 +194,8 @@ __device__ __forceinline__ void append_pe(const KvAppendParams& p, int t, int la
   bf16x8_unpack(lo, a);
   bf16x8_unpack(hi, b);
   turn(a, b, g, neox);
-  put_row8(p, t, to.slot, kLatent + 8 * u, a);
-  put_row8(p, t, to.slot, kLatent + 32 + 8 * u, b);
+  put_row8<kFp4>(p, t, to.slot, kLatent + 8 * u, a);
+  put_row8<kFp4>(p, t, to.slot, kLatent + 32 + 8 * u, b);
 }
 
 __device__ __forceinline__ float row_sum16(float v) {   // over a row's 16 lanes
@@ -257,15 +280,206 @@ __device__ __forceinline__ void append_latents(const KvAppendParams& p, int t, i
   }
 }
 
+// ---- 4-bit rows ----
+// Sixteen columns, eight in each of two lanes: their scale and codes.
+struct Fp4Part {
+  uint32_t scale;    // e4m3
+  uint32_t codes;    // this lane's eight, first in the lowest four bits
+  bool unsure;       // a value near a border
+};
+constexpr float kBelow = 1.f - 0x1p-20f, kAbove = 1.f + 0x1p-20f;
+
+__device__ __forceinline__ uint32_t e4m3_byte(float v) { return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
+__device__ __forceinline__ uint32_t e2m1_byte(float lo, float hi) {
+  return (uint8_t)__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+}
+// the largest of sixteen columns' sizes: as bits a NaN is above all
+__device__ __forceinline__ float largest16(const float (&y)[8], uint32_t pair) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(y[i]) & 0x7fffffffu);
+  return __uint_as_float(max(a, __shfl_xor_sync(pair, a, 1)));
+}
+// max(a / 6, 2^-9) and a NaN where a is one
+__device__ __forceinline__ float scale_of(float v) { return v < 0x1p-9f ? 0x1p-9f : v; }
+
+// from values y of fp32 precision; inv6: 1 / (6 kv_scale)
+__device__ __forceinline__ Fp4Part fp4_part(const float (&y)[8], float kv_scale, float inv6, uint32_t pair) {
+  Fp4Part r;
+  const float u = largest16(y, pair) * inv6;
+  r.scale = e4m3_byte(scale_of(u * kBelow));
+  r.unsure = r.scale != e4m3_byte(scale_of(u * kAbove));
+  const float inv = 1.f / (e4m3_to_f32(r.scale) * kv_scale);
+  uint32_t above = 0;
+  r.codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float a = y[i] * inv, b = y[i + 1] * inv;
+    r.codes |= e2m1_byte(a * kBelow, b * kBelow) << (4 * i);
+    above |= e2m1_byte(a * kAbove, b * kAbove) << (4 * i);
+  }
+  r.unsure |= r.codes != above;
+  return r;
+}
+
+// the size of a code in halves
+__device__ __forceinline__ int e2m1_halves(uint32_t c) {
+  c &= 7u;
+  return c < 4 ? (int)c : (int)((2u + (c & 1u)) << ((c >> 1) - 1u));
+}
+// The same decided in fp64: y[i] = c[i] w[i] inv, and near a border the value against the border times scale and kv_scale.
+__device__ __forceinline__ Fp4Part fp4_part_exact(const double (&y)[8], float kv_scale, uint32_t pair) {
+  Fp4Part r;
+  r.unsure = false;
+  double top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (!(fabs(y[i]) <= top)) top = fabs(y[i]);     // a NaN takes the place of any
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (y[i] != y[i]) top = y[i];                   // and keeps it
+  const double other = __shfl_xor_sync(pair, top, 1);
+  if (other != other || other > top) top = other;
+  const float u = (float)(top / (6.0 * kv_scale));
+  uint32_t lo = e4m3_byte(scale_of(u * kBelow));
+  const uint32_t hi = e4m3_byte(scale_of(u * kAbove));
+  if (lo != hi) {    // their midpoint has five bits
+    const double mid = 3.0 * ((double)e4m3_to_f32(lo) + (double)e4m3_to_f32(hi)) * kv_scale;   // 6 times it
+    if (top > mid || (top == mid && (hi & 1u) == 0)) lo = hi;
+  }
+  r.scale = lo;
+  const double unit = (double)e4m3_to_f32(lo) * kv_scale;
+  const float inv = (float)(1.0 / unit);
+  r.codes = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const float t = (float)fmin(fmax(y[i], -0x1p126), 0x1p126) * inv;
+    uint32_t a = e2m1_byte(t * kBelow, 0.f) & 15u;
+    const uint32_t b = e2m1_byte(t * kAbove, 0.f) & 15u;
+    if (a != b) {
+      const double border = (e2m1_halves(a) + e2m1_halves(b)) * 0.25 * unit, v = fabs(y[i]);
+      if (v > border || (v == border && (b & 1u) == 0)) a = b;
+    }
+    r.codes |= a << (4 * i);
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store_part(const KvAppendParams& p, int64_t row, int k, int l, const Fp4Part& part) {
+  uint8_t* dst = reinterpret_cast<uint8_t*>(p.cache) + row * kFp4Row;
+  const uint64_t ext = (uint64_t)p.cache_rows * kFp4Row;
+  if (guard_span(p.err, G_STEP_OUT, dst + 64 * k + 4 * l, 4, p.cache, ext)) *reinterpret_cast<uint32_t*>(dst + 64 * k + 4 * l) = part.codes;
+  if ((l & 1) == 0 && guard_span(p.err, G_STEP_OUT, dst + kFp4Codes + 8 * k + l / 2, 1, p.cache, ext))
+    dst[kFp4Codes + 8 * k + l / 2] = (uint8_t)part.scale;
+}
+__device__ __forceinline__ void put_latent8_fp4(const KvAppendParams& p, int t, int col, const float (&f)[8]) {
+  if (p.kv_out) store16(p, p.kv_out + t * p.kv_out_stride + col, p.kv_out, (p.T - 1) * p.kv_out_stride + kDk, f);
+}
+
+// A row done again in fp64, by its sixteen lanes; rows of any size.  v: the row as it was read (kv_out may be c_kv's place).
+__device__ __noinline__ void append_exact_latent_fp4(const KvAppendParams& p, int t, int64_t slot, int lane, const uint4 (&v)[4]) {
+  const int l = lane & 15;
+  const uint32_t row = 0xffffu << (lane & 16), pair = 3u << (lane & 30);
+  double inv = 1;
+  if (p.weight) {
+    double sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      bf16x8_unpack(v[k], f);
+      double s[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i & 1] = fma((double)f[i], (double)f[i], s[i & 1]);
+      sum += s[0] + s[1];
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(row, sum, d);
+    inv = 1.0 / sqrt(sum * (1.0 / kLatent) + (double)p.eps);
+  }
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    float f[8], w[8];
+    double y[8];
+    bf16x8_unpack(k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3], f);
+    if (p.weight) bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = p.weight ? (double)f[i] * inv * (double)w[i] : (double)f[i];
+      f[i] = (float)y[i];
+    }
+    if (slot >= 0) store_part(p, slot, k, l, fp4_part_exact(y, p.kv_scale, pair));
+    put_latent8_fp4(p, t, 128 * k + 8 * l, f);
+  }
+}
+
+// as append_latents; t is past the last token for the half that has none
+__device__ __forceinline__ void append_latents_fp4(const KvAppendParams& p, int t, int lane) {
+  const int l = lane & 15;
+  const uint32_t pair = 3u << (lane & 30), row = 0xffffu << (lane & 16);
+  Target to = {-1, -1};
+  uint4 v[4];
+  if (t < p.T) {
+    const int pos = token_int(p, p.positions, t);
+    const int64_t slot = token_int(p, p.slots, t);
+    const __nv_bfloat16* src = p.c_kv + t * p.c_kv_stride + 8 * l;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = load16(p, src + 128 * k, p.c_kv, (p.T - 1) * p.c_kv_stride + kLatent);
+    to = row_target(p, pos, slot, l == 0);
+  }
+  if (to.pos < 0) return;
+  float inv = 1.f;
+  bool unsure = false;
+  if (p.weight) {
+    float part[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      bf16x8_unpack(v[k], f);
+      part[k] = square_sum8(f);
+    }
+    float sum = (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(row, sum, d);
+    const float mean = sum * (1.f / kLatent) + p.eps;
+    unsure = mean > 5e35f || mean < 0x1p-100f;        // squares that leave fp32
+    inv = rsqrt_newton(mean);
+  }
+  const float inv6 = 1.f / (6.f * p.kv_scale);
+  if (!unsure) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      bf16x8_unpack(v[k], f);
+      if (p.weight) {
+        float wf[8];
+        bf16x8_unpack(load16(p, p.weight + 128 * k + 8 * l, p.weight, kLatent), wf);
+        norm8(f, inv, wf);
+      }
+      if (to.slot >= 0) {
+        const Fp4Part part = fp4_part(f, p.kv_scale, inv6, pair);
+        unsure |= part.unsure;
+        store_part(p, to.slot, k, l, part);
+      }
+      put_latent8_fp4(p, t, 128 * k + 8 * l, f);
+    }
+  }
+  if (__any_sync(row, unsure)) append_exact_latent_fp4(p, t, to.slot, lane, v);
+}
+
 // CTAs of four warps: of eight, 15.0 us for the 32768 rows above and 2.7 for the decode step.
 // The first warps bring two latents each, the next the RoPE columns of eight rows, the others the heads.
+template <bool kFp4>
 __global__ void __launch_bounds__(128, 8) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   const int lane = threadIdx.x & 31;
   uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
   const uint32_t latents = ((uint32_t)p.T + 1) / 2, pes = ((uint32_t)p.T + 7) / 8;
-  if (w < latents) return append_latents(p, 2 * w + (lane >> 4), lane);
+  if (w < latents) {
+    if constexpr (kFp4) append_latents_fp4(p, 2 * w + (lane >> 4), lane);
+    else append_latents(p, 2 * w + (lane >> 4), lane);
+    return;
+  }
   w -= latents;
-  if (w < pes) return append_pe(p, 8 * w + (lane >> 2), lane);
+  if (w < pes) return append_pe<kFp4>(p, 8 * w + (lane >> 2), lane);
   w -= pes;
   const uint32_t parts = (p.H + kHeadsPerWarp - 1) / kHeadsPerWarp, t = parts ? w / parts : p.T;
   if (t < (uint32_t)p.T) turn_heads(p, t, (w - t * parts) * kHeadsPerWarp, lane);
@@ -275,7 +489,9 @@ __global__ void __launch_bounds__(128, 8) kv_append_kernel(const __grid_constant
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
   const int64_t warps = ((int64_t)p.T + 1) / 2 + ((int64_t)p.T + 7) / 8 + (int64_t)p.T * ((p.H + kHeadsPerWarp - 1) / kHeadsPerWarp);
-  kv_append_kernel<<<(unsigned)((warps + 3) / 4), 128, 0, stream>>>(p);
+  const unsigned blocks = (unsigned)((warps + 3) / 4);
+  if (p.e4m3 == kCacheFp4) kv_append_kernel<true><<<blocks, 128, 0, stream>>>(p);
+  else kv_append_kernel<false><<<blocks, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

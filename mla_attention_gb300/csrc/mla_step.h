@@ -42,6 +42,7 @@ constexpr int kNormMaxD = 32768;    // a row's values stay in one CTA's register
 cudaError_t launch_rms_norm(const RmsNormParams& p, cudaStream_t stream);
 
 // cache rows [norm(c_kv) w | rotated k_pe] by slot, rotated q_pe into the fused query
+enum CacheFormat : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheFp4 = 2 };
 struct KvAppendParams {
   const __nv_bfloat16* c_kv;       // [T, 512] rows
   const __nv_bfloat16* k_pe;       // [T, 64] rows
@@ -49,7 +50,7 @@ struct KvAppendParams {
   const __nv_bfloat16* q_pe;       // [T, H, 64] or null
   __nv_bfloat16* q_out;            // [T, H, >= 576], columns 512..575 written
   __nv_bfloat16* kv_out;           // [T, 576] rows or null
-  void* cache;                     // [num_pages * page_size, 576] bf16 or e4m3
+  void* cache;                     // [num_pages * page_size, 576] bf16 or e4m3, or 4-bit rows of 416 bytes
   const int32_t* positions;        // [T]
   const int32_t* slots;            // [T]
   const float* cos_sin;            // [max_pos, 64]
@@ -57,7 +58,8 @@ struct KvAppendParams {
   int64_t c_kv_stride, k_pe_stride, q_pe_stride_t, q_pe_stride_h, q_out_stride_t, q_out_stride_h, kv_out_stride;
   int64_t cache_rows;
   float eps, kv_scale, inv_kv_scale;
-  int T, H, max_pos, is_neox, e4m3;
+  int T, H, max_pos, is_neox;
+  int e4m3;                        // a CacheFormat
 };
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
 

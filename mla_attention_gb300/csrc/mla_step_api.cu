@@ -39,6 +39,72 @@ bool rows_apart(int64_t st, int64_t sh, int T, int H, int width) {
     if (!(cond)) return fail(MLA_ERR_INVALID_ARG, __VA_ARGS__); \
   } while (0)
 
+mla_status append_impl(const char* name, int format, const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t k_pe_stride,
+                       const void* norm_weight, float eps, const void* q_pe, int64_t q_pe_stride_t, int64_t q_pe_stride_h,
+                       const int32_t* positions, const int32_t* slots, const float* cos_sin, int max_pos, int is_neox, int T, int H,
+                       void* kv_cache, float kv_scale, int64_t num_pages, int page_size, void* q_out, int64_t q_out_stride_t,
+                       int64_t q_out_stride_h, void* kv_out, int64_t kv_out_stride, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  MLA_REQUIRE(T >= 0 && H >= 0 && max_pos >= 1 && num_pages >= 0 && page_size >= 1,
+              "%s: need T >= 0, H >= 0, max_pos >= 1, num_pages >= 0, page_size >= 1", name);
+  MLA_REQUIRE(num_pages <= INT32_MAX / page_size, "%s: num_pages * page_size must be below 2^31", name);
+  MLA_REQUIRE(is_neox == 0 || is_neox == 1, "%s: is_neox must be 0 or 1", name);
+  MLA_REQUIRE(format != kCacheE4m3 || (kv_scale >= 0x1p-126f && kv_scale <= 0x1p126f),
+              "%s: kv_scale must be positive and normal, as must its reciprocal", name);
+  MLA_REQUIRE(format != kCacheFp4 || (kv_scale >= 0x1p-100f && kv_scale <= 0x1p100f), "%s: kv_scale must be between 2^-100 and 2^100", name);
+  MLA_REQUIRE(!norm_weight || (std::isfinite(eps) && eps >= 0.f), "%s: eps must be finite and not negative", name);
+  MLA_REQUIRE((int64_t)T * (1 + ((int64_t)H + 15) / 16) <= (int64_t)INT32_MAX - 8, "%s: too many (token, head) rows", name);
+  if (!workspace || workspace_bytes < mla_kv_append_workspace_size(T))
+    return fail(MLA_ERR_WORKSPACE, "%s: workspace must hold %zu bytes", name, mla_kv_append_workspace_size(T));
+  if (T == 0) return finish(cudaSuccess, "");
+  MLA_REQUIRE(c_kv && k_pe && positions && slots && cos_sin, "%s: c_kv, k_pe, positions, slots, cos_sin required", name);
+  MLA_REQUIRE(num_pages == 0 || kv_cache, "%s: kv_cache required", name);
+  MLA_REQUIRE(H == 0 || (q_pe && q_out), "%s: q_pe and q_out required where H > 0", name);
+  MLA_REQUIRE(aligned(c_kv, 16) && aligned(k_pe, 16) && aligned(norm_weight, 16) && aligned(kv_cache, 16) &&
+                  aligned(cos_sin, 16) && aligned(kv_out, 16) && aligned(positions, 4) && aligned(slots, 4) &&
+                  aligned(workspace, 4) && (H == 0 || (aligned(q_pe, 16) && aligned(q_out, 16))),
+              "%s: tensors must be 16-byte aligned (int32 ones 4-byte)", name);
+  MLA_REQUIRE(c_kv_stride >= 0 && k_pe_stride >= 0 && c_kv_stride % 8 == 0 && k_pe_stride % 8 == 0,
+              "%s: row strides of c_kv and k_pe must be multiples of 8 elements", name);
+  MLA_REQUIRE(!kv_out || T == 1 || (kv_out_stride >= kDk && kv_out_stride % 8 == 0),
+              "%s: kv_out rows need a stride of at least 576, a multiple of 8", name);
+  if (H > 0) {
+    MLA_REQUIRE(q_pe_stride_t >= 0 && q_pe_stride_h >= 0 && q_pe_stride_t % 8 == 0 && q_pe_stride_h % 8 == 0 &&
+                    q_out_stride_t % 8 == 0 && q_out_stride_h % 8 == 0,
+                "%s: strides of q_pe and q_out must be multiples of 8 elements", name);
+    MLA_REQUIRE(rows_apart(q_out_stride_t, q_out_stride_h, T, H, kDk), "%s: q_out rows of 576 must not overlap", name);
+  }
+  KvAppendParams p;
+  p.c_kv = reinterpret_cast<const __nv_bfloat16*>(c_kv);
+  p.k_pe = reinterpret_cast<const __nv_bfloat16*>(k_pe);
+  p.weight = reinterpret_cast<const __nv_bfloat16*>(norm_weight);
+  p.q_pe = reinterpret_cast<const __nv_bfloat16*>(q_pe);
+  p.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  p.kv_out = reinterpret_cast<__nv_bfloat16*>(kv_out);
+  p.cache = kv_cache;
+  p.positions = positions;
+  p.slots = slots;
+  p.cos_sin = cos_sin;
+  p.err = reinterpret_cast<uint32_t*>(workspace);
+  p.c_kv_stride = c_kv_stride;
+  p.k_pe_stride = k_pe_stride;
+  p.q_pe_stride_t = q_pe_stride_t;
+  p.q_pe_stride_h = q_pe_stride_h;
+  p.q_out_stride_t = q_out_stride_t;
+  p.q_out_stride_h = q_out_stride_h;
+  p.kv_out_stride = kv_out_stride;
+  p.cache_rows = num_pages * page_size;
+  p.eps = eps;
+  p.kv_scale = kv_scale;
+  p.inv_kv_scale = 1.f / kv_scale;
+  p.T = T;
+  p.H = H;
+  p.max_pos = max_pos;
+  p.is_neox = is_neox;
+  p.e4m3 = format;
+  return finish(launch_kv_append(p, reinterpret_cast<cudaStream_t>(stream)), name);
+}
+
 }  // namespace
 
 extern "C" {
@@ -141,64 +207,25 @@ mla_status mla_kv_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe
                          int max_pos, int is_neox, int T, int H, void* kv_cache, int cache_e4m3, float kv_scale,
                          int64_t num_pages, int page_size, void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
                          void* kv_out, int64_t kv_out_stride, void* workspace, size_t workspace_bytes, void* stream) {
-  MLA_REQUIRE(T >= 0 && H >= 0 && max_pos >= 1 && num_pages >= 0 && page_size >= 1,
-              "mla_kv_append: need T >= 0, H >= 0, max_pos >= 1, num_pages >= 0, page_size >= 1");
-  MLA_REQUIRE(num_pages <= INT32_MAX / page_size, "mla_kv_append: num_pages * page_size must be below 2^31");
-  MLA_REQUIRE((is_neox == 0 || is_neox == 1) && (cache_e4m3 == 0 || cache_e4m3 == 1),
-              "mla_kv_append: is_neox and cache_e4m3 must be 0 or 1");
-  MLA_REQUIRE(!cache_e4m3 || (kv_scale >= 0x1p-126f && kv_scale <= 0x1p126f),
-              "mla_kv_append: kv_scale must be positive and normal, as must its reciprocal");
-  MLA_REQUIRE(!norm_weight || (std::isfinite(eps) && eps >= 0.f), "mla_kv_append: eps must be finite and not negative");
-  MLA_REQUIRE((int64_t)T * (1 + ((int64_t)H + 15) / 16) <= (int64_t)INT32_MAX - 8, "mla_kv_append: too many (token, head) rows");
-  if (!workspace || workspace_bytes < mla_kv_append_workspace_size(T))
-    return fail(MLA_ERR_WORKSPACE, "mla_kv_append: workspace must hold %zu bytes", mla_kv_append_workspace_size(T));
-  if (T == 0) return finish(cudaSuccess, "");
-  MLA_REQUIRE(c_kv && k_pe && positions && slots && cos_sin, "mla_kv_append: c_kv, k_pe, positions, slots, cos_sin required");
-  MLA_REQUIRE(num_pages == 0 || kv_cache, "mla_kv_append: kv_cache required");
-  MLA_REQUIRE(H == 0 || (q_pe && q_out), "mla_kv_append: q_pe and q_out required where H > 0");
-  MLA_REQUIRE(aligned(c_kv, 16) && aligned(k_pe, 16) && aligned(norm_weight, 16) && aligned(kv_cache, 16) &&
-                  aligned(cos_sin, 16) && aligned(kv_out, 16) && aligned(positions, 4) && aligned(slots, 4) &&
-                  aligned(workspace, 4) && (H == 0 || (aligned(q_pe, 16) && aligned(q_out, 16))),
-              "mla_kv_append: tensors must be 16-byte aligned (int32 ones 4-byte)");
-  MLA_REQUIRE(c_kv_stride >= 0 && k_pe_stride >= 0 && c_kv_stride % 8 == 0 && k_pe_stride % 8 == 0,
-              "mla_kv_append: row strides of c_kv and k_pe must be multiples of 8 elements");
-  MLA_REQUIRE(!kv_out || T == 1 || (kv_out_stride >= kDk && kv_out_stride % 8 == 0),
-              "mla_kv_append: kv_out rows need a stride of at least 576, a multiple of 8");
-  if (H > 0) {
-    MLA_REQUIRE(q_pe_stride_t >= 0 && q_pe_stride_h >= 0 && q_pe_stride_t % 8 == 0 && q_pe_stride_h % 8 == 0 &&
-                    q_out_stride_t % 8 == 0 && q_out_stride_h % 8 == 0,
-                "mla_kv_append: strides of q_pe and q_out must be multiples of 8 elements");
-    MLA_REQUIRE(rows_apart(q_out_stride_t, q_out_stride_h, T, H, kDk), "mla_kv_append: q_out rows of 576 must not overlap");
-  }
-  KvAppendParams p;
-  p.c_kv = reinterpret_cast<const __nv_bfloat16*>(c_kv);
-  p.k_pe = reinterpret_cast<const __nv_bfloat16*>(k_pe);
-  p.weight = reinterpret_cast<const __nv_bfloat16*>(norm_weight);
-  p.q_pe = reinterpret_cast<const __nv_bfloat16*>(q_pe);
-  p.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
-  p.kv_out = reinterpret_cast<__nv_bfloat16*>(kv_out);
-  p.cache = kv_cache;
-  p.positions = positions;
-  p.slots = slots;
-  p.cos_sin = cos_sin;
-  p.err = reinterpret_cast<uint32_t*>(workspace);
-  p.c_kv_stride = c_kv_stride;
-  p.k_pe_stride = k_pe_stride;
-  p.q_pe_stride_t = q_pe_stride_t;
-  p.q_pe_stride_h = q_pe_stride_h;
-  p.q_out_stride_t = q_out_stride_t;
-  p.q_out_stride_h = q_out_stride_h;
-  p.kv_out_stride = kv_out_stride;
-  p.cache_rows = num_pages * page_size;
-  p.eps = eps;
-  p.kv_scale = kv_scale;
-  p.inv_kv_scale = 1.f / kv_scale;
-  p.T = T;
-  p.H = H;
-  p.max_pos = max_pos;
-  p.is_neox = is_neox;
-  p.e4m3 = cache_e4m3;
-  return finish(launch_kv_append(p, reinterpret_cast<cudaStream_t>(stream)), "mla_kv_append");
+  MLA_REQUIRE(cache_e4m3 == 0 || cache_e4m3 == 1, "mla_kv_append: cache_e4m3 must be 0 or 1");
+  return append_impl("mla_kv_append", cache_e4m3, c_kv, c_kv_stride, k_pe, k_pe_stride, norm_weight, eps, q_pe, q_pe_stride_t,
+                     q_pe_stride_h, positions, slots, cos_sin, max_pos, is_neox, T, H, kv_cache, kv_scale, num_pages, page_size,
+                     q_out, q_out_stride_t, q_out_stride_h, kv_out, kv_out_stride, workspace, workspace_bytes, stream);
+}
+
+// its 4-bit rows (the cache's other calls are in mla_cache_api.cu)
+size_t mla_kv_append_fp4_workspace_size(int T) { return mla_kv_append_workspace_size(T); }
+
+mla_status mla_kv_append_fp4(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t k_pe_stride,
+                             const void* norm_weight, float eps, const void* q_pe, int64_t q_pe_stride_t,
+                             int64_t q_pe_stride_h, const int32_t* positions, const int32_t* slots,
+                             const float* cos_sin, int max_pos, int is_neox, int T, int H, void* kv_cache_fp4,
+                             float kv_scale, int64_t num_pages, int page_size, void* q_out, int64_t q_out_stride_t,
+                             int64_t q_out_stride_h, void* kv_out, int64_t kv_out_stride, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return append_impl("mla_kv_append_fp4", kCacheFp4, c_kv, c_kv_stride, k_pe, k_pe_stride, norm_weight, eps, q_pe, q_pe_stride_t,
+                     q_pe_stride_h, positions, slots, cos_sin, max_pos, is_neox, T, H, kv_cache_fp4, kv_scale, num_pages, page_size,
+                     q_out, q_out_stride_t, q_out_stride_h, kv_out, kv_out_stride, workspace, workspace_bytes, stream);
 }
 
 // ---------------------------------------------------------------------------
