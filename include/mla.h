@@ -507,8 +507,10 @@ mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4
  * decay    finite, >= 0.  H >= 1, q_per_req * H <= 2^20, B <= 65535.
  * Formats 1 and 2 round q to f16 for the latent (1: all) columns, as mla_decode_fp8 and mla_decode_fp4 do.
  * No atomics: the same inputs give the same weights.
+ * workspace_bytes >= mla_key_weights_workspace_size(B, q_per_req, H, width): 256 for up to 128 query rows (tokens times
+ * heads) a request.
  */
-size_t mla_key_weights_workspace_size(int B, int q_per_req, int H);
+size_t mla_key_weights_workspace_size(int B, int q_per_req, int H, int width);
 mla_status mla_key_weights(const void* q, int q_per_req, const float* lse, const void* kv_cache, int cache_format,
                            float kv_scale, int64_t num_pages, int page_size, const int32_t* block_table, int max_pages,
                            const int32_t* lens, int B, int H, float scale, float decay, float* weights,

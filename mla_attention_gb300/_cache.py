@@ -124,6 +124,8 @@ def mla_key_weights(q, lse, kv_cache, block_table, lens, scale: float, weights, 
     if width > _INT_MAX:
         raise MLAError(1, f"weights has too many columns ({width})")
     pw = _rows(weights, "weights", _F32, dev, (B, width))
+    if ws is None and s * H > 128:
+        ws = _lib.workspace(_lib.lib().mla_key_weights_workspace_size(B, s, H, width), torch.device("cuda", dev))
     _call("mla_key_weights", dev, stream, pq, s, pe, pc, fmt, float(kv_scale), pages, page, pt, max_pages,
           _dense(lens, "lens", _I32, dev, (B,)), B, H, float(scale), float(decay), pw, weights.stride(0), width,
           *_workspace(ws, dev))

@@ -94,7 +94,7 @@ _SIGNATURES = {
     "mla_decode_fp4_workspace_size": ([c_int, c_int, c_int, c_int], c_size_t),
     "mla_decode_fp4": ([c_void_p, c_int, c_void_p, c_float, c_int64, c_int, c_void_p, c_int, c_void_p, c_int, c_int,
                         c_float, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p], c_int),
-    "mla_key_weights_workspace_size": ([c_int, c_int, c_int], c_size_t),
+    "mla_key_weights_workspace_size": ([c_int, c_int, c_int, c_int], c_size_t),
     "mla_key_weights": ([c_void_p, c_int, c_void_p, c_void_p, c_int, c_float, c_int64, c_int, c_void_p, c_int, c_void_p,
                          c_int, c_int, c_float, c_float, c_void_p, c_int64, c_int, c_void_p, c_size_t, c_void_p], c_int),
     "mla_select_keys_workspace_size": ([c_int], c_size_t),

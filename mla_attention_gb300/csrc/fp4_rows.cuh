@@ -37,6 +37,32 @@ __device__ __forceinline__ const uint8_t* paged_row(const PagedRows& kv, uint32_
   return in ? row : nullptr;
 }
 
+// eight codes (a word, lowest four bits first) times a scale, in f16: exact, a product has at most six bits
+__device__ __forceinline__ uint4 fp4x8_to_f16(uint32_t w, uint32_t scale2) {
+  uint32_t r[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 c0, c1, c2, c3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 c0, b0;\n\tcvt.rn.f16x2.e2m1x2 c1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 c2, b2;\n\tcvt.rn.f16x2.e2m1x2 c3, b3;\n\t"
+      "mul.rn.f16x2 %0, c0, %5;\n\tmul.rn.f16x2 %1, c1, %5;\n\tmul.rn.f16x2 %2, c2, %5;\n\tmul.rn.f16x2 %3, c3, %5;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w), "r"(scale2));
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// two scales (e4m3, low byte first) as f16, each in both halves of a word
+__device__ __forceinline__ uint2 fp4_scales2(uint32_t two) {
+  const uint32_t h = e4m3x2_to_f16x2((uint16_t)two);
+  return make_uint2(__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232));
+}
+// eight e4m3 values as f16
+__device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t a, uint32_t b) {
+  return make_uint4(e4m3x2_to_f16x2((uint16_t)a), e4m3x2_to_f16x2((uint16_t)(a >> 16)), e4m3x2_to_f16x2((uint16_t)b),
+                    e4m3x2_to_f16x2((uint16_t)(b >> 16)));
+}
+__device__ __forceinline__ uint4 bf16x8_to_f16(const uint4& v) {
+  return make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+}
+
 // two codes (low half first) as f16
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
   const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);

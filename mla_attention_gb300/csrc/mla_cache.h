@@ -24,6 +24,8 @@ struct PagedRows {
   int row_bytes;
 };
 
+enum CacheFormat : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheFp4 = 2 };
+
 struct DecodeFp4Params {
   PagedRows kv;
   const __nv_bfloat16* q;        // [B, s, H, 576]
@@ -46,9 +48,15 @@ struct KeyWeightsParams {
   uint32_t* err;
   float scale;                   // scale * kv_scale
   float decay;
-  int format;                    // 0 bf16, 1 e4m3, 2 4-bit rows
+  uint32_t spin_limit, debug_stall;
+  int format;                    // a CacheFormat
   int s, H, width;
+  int32_t* before;               // ws, with more than 128 query rows: [B + 1][2] tiles and ranges before each request
+  float* part;                   // ws: sums of ranges of tiles
+  uint64_t part_bytes;
 };
+// bytes of `part`, and of `before`
+size_t key_weights_scratch(int B, int64_t rows, int64_t width, size_t* before);
 cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
 
 struct SelectParams {

@@ -86,9 +86,10 @@ mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4
 }
 
 // ---------------------------------------------------------------------------
-size_t mla_key_weights_workspace_size(int B, int q_per_req, int H) {
-  (void)B, (void)q_per_req, (void)H;
-  return kWsHeader;
+size_t mla_key_weights_workspace_size(int B, int q_per_req, int H, int width) {
+  size_t before;
+  const size_t part = key_weights_scratch(B, (int64_t)q_per_req * H, width, &before);
+  return kWsHeader + (before + 255) / 256 * 256 + part;
 }
 
 mla_status mla_key_weights(const void* q, int q_per_req, const float* lse, const void* kv_cache, int cache_format,
@@ -105,7 +106,8 @@ mla_status mla_key_weights(const void* q, int q_per_req, const float* lse, const
   MLA_REQUIRE(std::isfinite(decay) && decay >= 0.f, "mla_key_weights: decay must be finite and not negative");
   MLA_REQUIRE(width >= 0 && weights_stride >= 0, "mla_key_weights: need width >= 0 and weights_stride >= 0");
   MLA_REQUIRE(B <= 65535, "mla_key_weights: B <= 65535 (got %d)", B);
-  if (!workspace || workspace_bytes < kWsHeader) return fail(MLA_ERR_WORKSPACE, "mla_key_weights: workspace must hold %zu bytes", (size_t)kWsHeader);
+  const size_t need = mla_key_weights_workspace_size(B, q_per_req, H, width);
+  if (!workspace || workspace_bytes < need) return fail(MLA_ERR_WORKSPACE, "mla_key_weights: workspace must hold %zu bytes", need);
   if (B == 0) return finish(cudaSuccess, "");
   MLA_REQUIRE(q && lse && lens && (weights || width == 0), "mla_key_weights: q, lse, lens and weights required");
   MLA_REQUIRE(aligned(q, 16) && aligned(lse, 4) && aligned(weights, 4) && aligned(workspace, 4),
@@ -120,10 +122,16 @@ mla_status mla_key_weights(const void* q, int q_per_req, const float* lse, const
   p.err = reinterpret_cast<uint32_t*>(workspace);
   p.scale = scale * kv_scale;
   p.decay = decay;
+  p.spin_limit = spin_limit();
+  p.debug_stall = debug_stall();
   p.format = cache_format;
   p.s = q_per_req;
   p.H = H;
   p.width = width;
+  size_t before;
+  p.part_bytes = key_weights_scratch(B, (int64_t)q_per_req * H, width, &before);
+  p.before = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(workspace) + kWsHeader);
+  p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kWsHeader + (before + 255) / 256 * 256);
   return finish(launch_key_weights(p, reinterpret_cast<cudaStream_t>(stream)), "mla_key_weights");
 }
 

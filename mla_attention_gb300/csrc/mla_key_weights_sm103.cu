@@ -1,0 +1,519 @@
+// The attention that each cached key got, added up over query tokens and heads.
+//   weights[b, j] = decay weights[b, j] + sum_{i, h} exp(scale q_{b,i,h} . k_j - lse_{b,i,h})
+//
+// Scores are taken the other way round, S^T = K Q^T with 128 keys as the rows of a tile and up to 128 query rows (token, head) as
+// its columns: a key is then a lane of tensor memory and its sum over the query rows stays in one thread, with neither
+// shuffles nor atomics.  The query rows of a request stay in shared memory while its keys stream past.  More than 128 of
+// them are taken a chunk after the other over a few tiles at a time (kSub), so that the keys come from L2 again; a CTA's
+// part of such a range's sums goes to the workspace, and key_weights_sum_kernel adds the parts up in their order.
+//
+// A CTA per SM takes an equal share of all tiles.  16 warps:
+//   0-3   a key a thread: S from tensor memory, exponentials, the weight's update
+//   4     MMAs (one thread): nine 64-column boxes of K against those of Q
+//   5     rows of the next tiles through the block table, their lines asked for in L2, and the chunk's log-sum-exps
+//   6-15  producers, two for each stage of the ring, 64 rows each: bf16 rows by cp.async; e4m3 and 4-bit rows through
+//         registers into f16 (exact), with q in f16 too, the next box's loads out before the last one's are converted; the RoPE
+//         columns of 4-bit rows stay bf16.  A stage has producers of its own, as a parity tells no more than the last phase.
+#include <math_constants.h>
+
+#include "fp4_rows.cuh"
+#include "tile_waits.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kTile = 128;                       // keys a tile, query rows a chunk
+constexpr int kBoxes = kDk / 64;
+constexpr int kBoxBytes = kTile * 128;
+constexpr int kStages = 5;                       // K boxes on their way
+constexpr int kRowSlots = 3;                     // tiles whose rows are known
+constexpr int kSub = 8;                          // tiles before the next chunk of query rows
+constexpr int kThreads = 512, kProducers = 2 * kStages, kFirstProducer = 6;
+constexpr uint32_t kTmemCols = 256;
+
+constexpr int kOffQ = 0;
+constexpr int kOffK = kBoxes * kBoxBytes;
+constexpr int kOffRows = kOffK + kStages * kBoxBytes;
+constexpr int kOffLse = kOffRows + kRowSlots * kTile * 4;
+constexpr int kOffBars = kOffLse + 2 * kTile * 4;
+
+struct Bars {
+  uint64_t kfull[kStages], kempty[kStages];
+  uint64_t qfull[kBoxes], qempty[kBoxes];
+  uint64_t sfull[2], sfree[2];
+  uint64_t rfull[kRowSlots], rfree[kRowSlots];
+  uint64_t lfull[2], lfree[2];
+  uint64_t drain, stall;
+  uint32_t tmem_base, abort;
+  int32_t start_b, start_t, start_o;
+  int64_t share, start_range;
+};
+constexpr int kSmem = kOffBars + 512;
+static_assert(sizeof(Bars) <= 512, "barrier block too large");
+static_assert(kSmem <= 232448, "shared memory over the sm_103a limit");
+
+enum : uint32_t { W_KFULL = 0x180, W_KEMPTY, W_QFULL, W_QEMPTY, W_SFULL, W_SFREE, W_RFULL, W_RFREE, W_LFULL, W_LFREE, W_STALL, W_ALIGN };
+
+// Work of one load of query rows: chunk c of request b against tiles t0 + i0 .. t0 + i1 - 1.
+struct Segment {
+  int b, len, t0, nt, c, i0, i1;
+  int64_t range;           // with several chunks: the index of the range of nt tiles at t0
+  int from;                // and the first unit (c * nt + tile) of it that this CTA has
+};
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// This CTA's share of the units (tile, chunk): request by request, kSub tiles at a time, a chunk of query rows after the other
+// over them.  With one chunk a segment is all of a request that the share has.
+struct Shares {
+  const KeyWeightsParams* p;
+  int64_t cap, left, range;
+  int b, t0, o, from, chunks;
+  __device__ Shares(const KeyWeightsParams& prm, int64_t cap_, const Bars& bars, int chunks_)
+      : p(&prm), cap(cap_), left(bars.share), range(bars.start_range), b(bars.start_b), t0(bars.start_t), o(bars.start_o), from(bars.start_o),
+        chunks(chunks_) {}
+  __device__ bool next(Segment& s) {
+    while (left > 0 && b < p->kv.B) {
+      const int len = paged_len(p->kv, p->err, b, cap, false), all = tiles_of(len) - t0;
+      if (all <= 0) {
+        ++b, t0 = 0;
+        continue;
+      }
+      const int nt = chunks > 1 ? min(all, kSub) : all;
+      s.b = b, s.len = len, s.t0 = t0, s.nt = nt, s.range = range, s.from = from;
+      s.c = o / nt, s.i0 = o - s.c * nt;
+      s.i1 = (int)min((int64_t)nt, s.i0 + left);
+      o += s.i1 - s.i0, left -= s.i1 - s.i0;
+      if (o == nt * chunks) t0 += nt, o = 0, from = 0, ++range;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Where this CTA's share starts; by all threads.  With several chunks the first CTA puts down the tiles and ranges before each
+// request.
+__device__ __forceinline__ void find_share(const KeyWeightsParams& p, int64_t cap, int chunks, Bars& bars, int32_t* sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.kv.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.kv.B), b1 = min(b0 + per, p.kv.B);
+  int64_t tiles = 0, ranges = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = tiles_of(paged_len(p.kv, p.err, b, cap, blockIdx.x == 0));
+    tiles += n, ranges += (n + kSub - 1) / kSub;
+  }
+  int64_t t_upto = tiles, r_upto = ranges;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t v = __shfl_up_sync(~0u, t_upto, d), r = __shfl_up_sync(~0u, r_upto, d);
+    if (lane >= d) t_upto += v, r_upto += r;
+  }
+  if (lane == 31) sums[2 * warp] = (int32_t)t_upto, sums[2 * warp + 1] = (int32_t)r_upto;   // below 2^31 / 128 rows
+  __syncthreads();
+  int64_t t_at = t_upto - tiles, r_at = r_upto - ranges, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) t_at += sums[2 * w], r_at += sums[2 * w + 1];
+    total += sums[2 * w];
+  }
+  total *= chunks;
+  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  if (tid == 0) bars.share = hi - lo;
+  const bool tell = chunks > 1 && blockIdx.x == 0, here = lo < hi && t_at * chunks <= lo && lo < (t_at + tiles) * chunks;
+  if (tell || here) {
+    for (int b = b0; b < b1; ++b) {
+      const int n = tiles_of(paged_len(p.kv, p.err, b, cap, false));
+      if (tell) {
+        p.before[2 * b] = (int32_t)t_at, p.before[2 * b + 1] = (int32_t)r_at;
+        if (b == p.kv.B - 1) p.before[2 * b + 2] = (int32_t)(t_at + n);
+      }
+      if (lo < hi && t_at * chunks <= lo && lo < (t_at + n) * chunks) {
+        const int64_t off = lo - t_at * chunks;           // in units
+        bars.start_b = b;
+        if (chunks == 1) {
+          bars.start_t = (int)off, bars.start_o = 0, bars.start_range = r_at;
+        } else {
+          const int64_t k = off / (kSub * chunks);
+          bars.start_t = (int)(k * kSub), bars.start_o = (int)(off - k * kSub * chunks), bars.start_range = r_at + k;
+        }
+      }
+      t_at += n, r_at += (n + kSub - 1) / kSub;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t box_unit(uint32_t box, int row, int unit) {   // 16 bytes of a swizzled 128-byte row
+  return box + row * 128 + ((unit ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+constexpr int kNoRow = -1, kZeroRow = -2;
+
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + kOffBars);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t table = (int64_t)p.kv.max_pages * p.kv.page_size, cap = table < p.width ? table : p.width;
+  const int rows = p.s * p.H, chunks = (rows + kTile - 1) / kTile;
+  const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * p.kv.row_bytes;
+  // bf16: every lane of both producers arrives when its copies have landed
+  constexpr uint32_t kArrivals = kFmt == kCacheBf16 ? 64 : 2;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars.kfull[i], kArrivals), mbar_init(&bars.kempty[i], 1);
+    for (int i = 0; i < kBoxes; ++i) mbar_init(&bars.qfull[i], kArrivals), mbar_init(&bars.qempty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 4);
+    for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], kProducers);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.lfull[i], 1), mbar_init(&bars.lfree[i], 4);
+    mbar_init(&bars.drain, 1);
+    mbar_init(&bars.stall, 1);
+    bars.abort = 0;
+    if (smem_u32(smem) & 1023u) bars.abort = DEV_TIMEOUT_BASE | W_ALIGN, record_error(p.err, bars.abort);
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(&bars.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  find_share(p, cap, chunks, bars, reinterpret_cast<int32_t*>(smem + kOffRows));   // no row is there yet
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = bars.tmem_base;
+  const TileWaits wait{&bars.abort, p.err, p.spin_limit};
+  int32_t* row_slots = reinterpret_cast<int32_t*>(smem + kOffRows);
+  float* lse_slots = reinterpret_cast<float*>(smem + kOffLse);
+  Shares shares(p, cap, bars, chunks);
+  Segment it;
+  uint32_t u = 0, c_all = 0;                     // units and segments gone through
+  bool live = bars.abort == 0;
+
+  if (warp < 4) {
+    // ---------------- a key a thread ----------------
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const float c2 = p.scale * 1.4426950408889634f;
+    const uint64_t c22 = f32x2(c2, c2);
+    while (live && shares.next(it)) {
+      const float* minus_lse = lse_slots + (c_all & 1) * kTile;
+      if (!wait.warp(&bars.lfull[c_all & 1], (c_all >> 1) & 1, W_LFULL)) break;
+      const int n = min(rows - it.c * kTile, kTile);
+      for (int i = it.i0; i < it.i1; ++i, ++u) {
+        const int j = (it.t0 + i) * kTile + tid, buf = u & 1;
+        bool mine = j < it.len, first;
+        float* w;
+        if (chunks == 1) {
+          w = p.weights + it.b * p.stride + j, first = p.decay == 0.f;
+          mine = mine && guard_span(p.err, G_STEP_OUT, w, 4, p.weights, ((uint64_t)(p.kv.B - 1) * p.stride + p.width) * 4);
+        } else {       // this CTA's part of the range's sums
+          w = p.part + ((it.range + blockIdx.x) * kSub + i) * kTile + tid, first = it.c * it.nt + i - it.nt < it.from;
+          mine = mine && guard_span(p.err, G_PART_O, w, 4, p.part, p.part_bytes);
+        }
+        const float old = mine && !first ? *w : 0.f;
+        // query rows below `hidden` do not see the key
+        const int hidden = (int)max((int64_t)0, (int64_t)(j - (it.len - p.s)) * p.H - it.c * kTile);
+        const bool any_hidden = __any_sync(~0u, j < it.len && hidden > 0);
+        if (!wait.warp(&bars.sfull[buf], (u >> 1) & 1, W_SFULL)) { live = false; break; }
+        tc_fence_after();
+        uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+        for (int n0 = 0; n0 < n; n0 += 32) {
+          uint32_t s[32];
+          tmem_ld32(tbase + lanes + buf * kTile + n0, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i4 = 0; i4 < 32; i4 += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(minus_lse + n0 + i4);
+            float x0, x1, x2, x3;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i4]), __uint_as_float(s[i4 + 1])), c22, f32x2(l.x, l.y)), x0, x1);
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i4 + 2]), __uint_as_float(s[i4 + 3])), c22, f32x2(l.z, l.w)), x2, x3);
+            x0 = ex2_approx(x0), x1 = ex2_approx(x1), x2 = ex2_approx(x2), x3 = ex2_approx(x3);
+            if (any_hidden) {
+              x0 = n0 + i4 < hidden ? 0.f : x0, x1 = n0 + i4 + 1 < hidden ? 0.f : x1;
+              x2 = n0 + i4 + 2 < hidden ? 0.f : x2, x3 = n0 + i4 + 3 < hidden ? 0.f : x3;
+            }
+            sum2[0] = add_f32x2(sum2[0], f32x2(x0, x1));
+            sum2[1] = add_f32x2(sum2[1], f32x2(x2, x3));
+          }
+        }
+        tc_fence_before();
+        warp_arrive(&bars.sfree[buf]);
+        float a, b;
+        f32x2_split(add_f32x2(sum2[0], sum2[1]), a, b);
+        if (mine) *w = first ? a + b : chunks == 1 ? fmaf(p.decay, old, a + b) : old + (a + b);
+      }
+      if (live) warp_arrive(&bars.lfree[c_all & 1]);
+      ++c_all;
+    }
+  } else if (warp == 4) {
+    // ---------------- MMAs ----------------
+    if (lane == 0) {
+      if (p.debug_stall) live = live && wait.one(&bars.stall, 0, W_STALL);
+      uint32_t kbox = 0;
+      for (; live && shares.next(it); ++c_all) {
+        const uint32_t n = (uint32_t)(min(rows - it.c * kTile, kTile) + 31) & ~31u;
+        const uint32_t id_f16 = idesc_f16_f32(kTile, n, false, false), id_bf16 = idesc_bf16_f32(kTile, n, false, false);
+        for (int i = it.i0; i < it.i1 && live; ++i, ++u) {
+          const int buf = u & 1;
+          if (!wait.one(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, W_SFREE)) { live = false; break; }
+          for (int k = 0; k < kBoxes; ++k, ++kbox) {
+            const uint32_t slot = kbox % kStages;
+            if (i == it.i0 && !wait.one(&bars.qfull[k], c_all & 1, W_QFULL)) { live = false; break; }
+            if (!wait.one(&bars.kfull[slot], (kbox / kStages) & 1, W_KFULL)) { live = false; break; }
+            tc_fence_after();
+            if constexpr (kFmt == kCacheBf16) fence_proxy_async_smem();    // copies that other threads issued
+            const bool bf = kFmt == kCacheBf16 || (kFmt == kCacheFp4 && k == kBoxes - 1);
+            mma_box64(tbase + buf * kTile, sdesc_sw128(smem_u32(smem + kOffK + slot * kBoxBytes), 16, 1024),
+                      sdesc_sw128(smem_u32(smem + kOffQ + k * kBoxBytes), 16, 1024), bf ? id_bf16 : id_f16, k > 0 ? 1u : 0u);
+            mma_commit(&bars.kempty[slot]);
+            if (i == it.i1 - 1) mma_commit(&bars.qempty[k]);
+          }
+          if (live) mma_commit(&bars.sfull[buf]);
+        }
+      }
+      mma_commit(&bars.drain);                   // what was issued is done before tensor memory is given back
+      mbar_drain(&bars.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ---------------- rows of the tiles to come ----------------
+    for (; live && shares.next(it); ++c_all) {
+      if (!wait.warp(&bars.lfree[c_all & 1], ((c_all >> 1) & 1) ^ 1, W_LFREE)) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = it.c * kTile + 32 * i + lane;
+        const float* src = p.lse + (int64_t)it.b * rows + r;
+        float l = -CUDART_INF_F;
+        if (r < rows && guard_span(p.err, G_STEP_IN, src, 4, p.lse, (uint64_t)p.kv.B * rows * 4)) l = *src;
+        lse_slots[(c_all & 1) * kTile + 32 * i + lane] = l == -CUDART_INF_F ? -CUDART_INF_F : -l * 1.4426950408889634f;
+      }
+      warp_arrive(&bars.lfull[c_all & 1]);
+      for (int i = it.i0; i < it.i1; ++i, ++u) {
+        const int slot = u % kRowSlots;
+        int32_t at[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = (it.t0 + i) * kTile + 32 * r + lane;
+          at[r] = kNoRow;
+          if (j < it.len) {
+            const int pg = j / p.kv.page_size;
+            const int page = guarded_int(p.err, p.kv.block_table, (int64_t)it.b * p.kv.max_pages + pg, (int64_t)p.kv.B * p.kv.max_pages);
+            at[r] = kZeroRow;
+            if (page >= 0 && page < p.kv.num_pages) at[r] = page * p.kv.page_size + (j - pg * p.kv.page_size);
+            else record_error(p.err, DEV_RANGE_BASE | Y_PAGE);
+            if (at[r] >= 0) bulk_prefetch_l2(p.kv.cache + (int64_t)at[r] * p.kv.row_bytes, p.kv.row_bytes);
+          }
+        }
+        if (!wait.warp(&bars.rfree[slot], ((u / kRowSlots) & 1) ^ 1, W_RFREE)) { live = false; break; }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) row_slots[slot * kTile + 32 * r + lane] = at[r];
+        warp_arrive(&bars.rfull[slot]);
+      }
+    }
+  } else {
+    // ---------------- producers ----------------
+    const uint32_t me = (warp - kFirstProducer) % kStages;
+    const int r0 = (warp - kFirstProducer) / kStages * 64;     // this warp's rows of a box
+    uint32_t kbox = 0, due = 0;
+    // a box whose loads are out: 4-bit rows two lanes a row, 32 columns each; e4m3 four lanes a row, 16 columns each
+    constexpr int kVec = kFmt == kCacheFp4 ? 4 : 8;
+    uint4 v[kVec], ready[kVec];
+    uint32_t sc[4], ready_sc[4];
+    bool pending = false;
+    auto flush = [&]() -> bool {                  // converts the box `due`
+      if (!pending) return true;
+      pending = false;
+      const uint32_t slot = due % kStages, box = smem_u32(smem + kOffK + slot * kBoxBytes);
+      if (!wait.warp(&bars.kempty[slot], ((due / kStages) & 1) ^ 1, W_KEMPTY)) return false;
+      if constexpr (kFmt == kCacheFp4) {
+        const int half = lane & 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 16 * i + (lane >> 1);
+          const uint2 s = fp4_scales2(ready_sc[i]);
+          st_shared16(box_unit(box, r, 4 * half), fp4x8_to_f16(ready[i].x, s.x));
+          st_shared16(box_unit(box, r, 4 * half + 1), fp4x8_to_f16(ready[i].y, s.x));
+          st_shared16(box_unit(box, r, 4 * half + 2), fp4x8_to_f16(ready[i].z, s.y));
+          st_shared16(box_unit(box, r, 4 * half + 3), fp4x8_to_f16(ready[i].w, s.y));
+        }
+      } else {
+        const int quarter = lane & 3;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const int r = r0 + 8 * i + (lane >> 2);
+          st_shared16(box_unit(box, r, 2 * quarter), e4m3x8_to_f16(ready[i].x, ready[i].y));
+          st_shared16(box_unit(box, r, 2 * quarter + 1), e4m3x8_to_f16(ready[i].z, ready[i].w));
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&bars.kfull[slot]);
+      return true;
+    };
+    for (; live && shares.next(it); ++c_all) {
+      {
+        const int n = min(rows - it.c * kTile, kTile), n32 = (n + 31) & ~31;
+        const __nv_bfloat16* qsrc = p.q + ((int64_t)it.b * rows + it.c * kTile) * kDk;
+        const uint64_t q_bytes = (uint64_t)p.kv.B * rows * kDk * 2;
+        for (int t = it.i0; t < it.i1 && live; ++t, ++u) {
+          const int rslot = u % kRowSlots;
+          bool have_rows = false;
+          for (int k = 0; k < kBoxes; ++k, ++kbox) {
+            if (t == it.i0 && k % kStages == me) {
+              // ---- a box of query rows ----
+              const uint32_t box = smem_u32(smem + kOffQ + k * kBoxBytes);
+              if (!flush() || !wait.warp(&bars.qempty[k], (c_all & 1) ^ 1, W_QEMPTY)) { live = false; break; }
+              const int unit = lane & 7, rend = min(n32, r0 + 64);
+              for (int r = r0 + (lane >> 3); r < rend; r += 4) {
+                const __nv_bfloat16* src = qsrc + (int64_t)r * kDk + 64 * k + 8 * unit;
+                const bool in = r < n && guard_span(p.err, G_STEP_IN, src, 16, p.q, q_bytes);
+                cp_async16_zfill(box_unit(box, r, unit), in ? src : p.q, in ? 16u : 0u);
+              }
+              if constexpr (kFmt == kCacheBf16) {
+                cp_async_arrive_noinc(&bars.qfull[k]);
+              } else {                                   // each lane puts its own copies into f16 where they lie
+                cp_async_wait_all();
+                if (kFmt == kCacheE4m3 || k < kBoxes - 1)
+                  for (int r = r0 + (lane >> 3); r < rend; r += 4) {
+                    const uint32_t at = box_unit(box, r, unit);
+                    st_shared16(at, bf16x8_to_f16(ld_shared16(at)));
+                  }
+                fence_proxy_async_smem();
+                warp_arrive(&bars.qfull[k]);
+              }
+            }
+            if (kbox % kStages != me) continue;
+            // ---- a box of keys ----
+            if (!have_rows && !wait.warp(&bars.rfull[rslot], (u / kRowSlots) & 1, W_RFULL)) { live = false; break; }
+            have_rows = true;
+            const int32_t* at = row_slots + rslot * kTile;
+            if (kFmt == kCacheBf16 || (kFmt == kCacheFp4 && k == kBoxes - 1)) {
+              const uint32_t slot = kbox % kStages, box = smem_u32(smem + kOffK + slot * kBoxBytes);
+              if (!flush() || !wait.warp(&bars.kempty[slot], ((kbox / kStages) & 1) ^ 1, W_KEMPTY)) { live = false; break; }
+              const int unit = lane & 7;
+              const uint32_t off = (kFmt == kCacheBf16 ? 128 * k : kFp4Pe) + 16 * unit;
+#pragma unroll 8
+              for (int r = r0 + (lane >> 3); r < r0 + 64; r += 4) {
+                const int a = at[r];
+                if (a == kNoRow) continue;               // the row's lane is not looked at
+                const uint8_t* src = p.kv.cache + (int64_t)a * p.kv.row_bytes + off;
+                const bool in = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes);
+                cp_async16_zfill(box_unit(box, r, unit), in ? src : (const uint8_t*)p.q, in ? 16u : 0u);
+              }
+              if constexpr (kFmt == kCacheBf16) {
+                cp_async_arrive_noinc(&bars.kfull[slot]);
+              } else {
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                warp_arrive(&bars.kfull[slot]);
+              }
+              continue;
+            }
+            if constexpr (kFmt == kCacheFp4) {
+              const int half = lane & 1;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int a = at[r0 + 16 * i + (lane >> 1)];
+                const uint8_t* r = p.kv.cache + (int64_t)a * kFp4Row;
+                v[i] = make_uint4(0, 0, 0, 0), sc[i] = 0;
+                if (a >= 0 && guard_span(p.err, G_STEP_IN, r, kFp4Row, p.kv.cache, cache_bytes)) {
+                  v[i] = *reinterpret_cast<const uint4*>(r + 32 * k + 16 * half);
+                  sc[i] = *reinterpret_cast<const uint16_t*>(r + kFp4Codes + 4 * k + 2 * half);
+                }
+              }
+            } else if constexpr (kFmt == kCacheE4m3) {
+#pragma unroll
+              for (int i = 0; i < kVec; ++i) {
+                const int a = at[r0 + 8 * i + (lane >> 2)];
+                const uint8_t* src = p.kv.cache + (int64_t)a * kDk + 64 * k + 16 * (lane & 3);
+                v[i] = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint4*>(src)
+                                                                                               : make_uint4(0, 0, 0, 0);
+              }
+            }
+            if (!flush()) { live = false; break; }
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) ready[i] = v[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ready_sc[i] = sc[i];
+            due = kbox;
+            pending = true;
+          }
+          if (live) warp_arrive(&bars.rfree[rslot]);
+        }
+      }
+    }
+    if (live) flush();
+    cp_async_wait_all();                         // no copy into this CTA outlives it
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) tmem_dealloc(tbase, kTmemCols);
+}
+
+// Several chunks of query rows: a range's sums are those of the CTAs that had units of it, in their order.  A CTA per range.
+__global__ void __launch_bounds__(kSub * kTile) key_weights_sum_kernel(const __grid_constant__ KeyWeightsParams p, int shares, int per_request) {
+  const int64_t table = (int64_t)p.kv.max_pages * p.kv.page_size, cap = table < p.width ? table : p.width;
+  const int chunks = (p.s * p.H + kTile - 1) / kTile;
+  const int b = blockIdx.x / per_request, r = blockIdx.x - b * per_request, i = threadIdx.x / kTile;
+  const int len = paged_len(p.kv, p.err, b, cap, false), t0 = r * kSub, nt = min(tiles_of(len) - t0, kSub);
+  if (i >= nt) return;
+  const int64_t total = (int64_t)p.before[2 * p.kv.B] * chunks, u0 = ((int64_t)p.before[2 * b] + t0) * chunks, range = p.before[2 * b + 1] + r;
+  const int j = (t0 + i) * kTile + (threadIdx.x & (kTile - 1));
+  if (j >= len) return;
+  float sum = 0.f;
+  int s = (int)(((u0 + 1) * shares - 1) / total);         // the share that has unit u0
+  for (; s < shares; ++s) {
+    const int64_t lo = total * s / shares - u0, hi = total * (s + 1) / shares - u0;
+    if (lo >= (int64_t)nt * chunks) break;
+    const int64_t c = lo <= i ? 0 : (lo - i + nt - 1) / nt;  // its first chunk of this tile
+    if (c >= chunks || c * nt + i >= hi) continue;
+    const float* part = p.part + ((range + s) * kSub + i) * kTile + (threadIdx.x & (kTile - 1));
+    if (guard_span(p.err, G_PART_O, part, 4, p.part, p.part_bytes)) sum += *part;
+  }
+  float* w = p.weights + b * p.stride + j;
+  if (guard_span(p.err, G_STEP_OUT, w, 4, p.weights, ((uint64_t)(p.kv.B - 1) * p.stride + p.width) * 4))
+    *w = p.decay == 0.f ? sum : fmaf(p.decay, *w, sum);
+}
+
+}  // namespace
+
+// the most ranges of kSub tiles that requests of `width` keys have
+static int64_t most_ranges(int B, int64_t width) { return B * ((width + kSub * kTile - 1) / (kSub * kTile)); }
+
+size_t key_weights_scratch(int B, int64_t rows, int64_t width, size_t* before) {
+  *before = 0;
+  if (rows <= kTile || B <= 0 || width <= 0) return 0;
+  *before = ((size_t)2 * B + 2) * sizeof(int32_t);
+  return (size_t)(most_ranges(B, width) + device_sm_count()) * kSub * kTile * sizeof(float);
+}
+
+cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream) {
+  static PerDeviceOnce attrs;
+  cudaError_t e = attrs.run([] {
+    cudaError_t r = cudaSuccess;
+    for (const void* fn : {(const void*)key_weights_kernel<kCacheBf16>, (const void*)key_weights_kernel<kCacheE4m3>, (const void*)key_weights_kernel<kCacheFp4>})
+      if (r == cudaSuccess) r = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  // no more CTAs than tiles there can be
+  const int64_t table = (int64_t)p.kv.max_pages * p.kv.page_size, cap = table < p.width ? table : p.width;
+  const int64_t most = p.kv.B * ((cap + kTile - 1) / kTile);
+  if (most == 0) return cudaSuccess;
+  const unsigned grid = (unsigned)(most < device_sm_count() ? most : device_sm_count());
+  if (p.format == kCacheBf16) key_weights_kernel<kCacheBf16><<<grid, kThreads, kSmem, stream>>>(p);
+  else if (p.format == kCacheE4m3) key_weights_kernel<kCacheE4m3><<<grid, kThreads, kSmem, stream>>>(p);
+  else key_weights_kernel<kCacheFp4><<<grid, kThreads, kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess && (int64_t)p.s * p.H > kTile) {
+    const int64_t ranges = most_ranges(p.kv.B, cap);
+    key_weights_sum_kernel<<<(unsigned)ranges, kSub * kTile, 0, stream>>>(p, (int)grid, (int)(ranges / p.kv.B));
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace mla

@@ -1,7 +1,7 @@
 // The serving step around the latent attention: parameters and launchers of the slot map, the RMS
 // norm, the cache append by slots and the products with 4-bit weights.
 #pragma once
-#include "mla_internal.h"
+#include "mla_cache.h"
 
 namespace mla {
 
@@ -42,7 +42,6 @@ constexpr int kNormMaxD = 32768;    // a row's values stay in one CTA's register
 cudaError_t launch_rms_norm(const RmsNormParams& p, cudaStream_t stream);
 
 // cache rows [norm(c_kv) w | rotated k_pe] by slot, rotated q_pe into the fused query
-enum CacheFormat : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheFp4 = 2 };
 struct KvAppendParams {
   const __nv_bfloat16* c_kv;       // [T, 512] rows
   const __nv_bfloat16* k_pe;       // [T, 64] rows

@@ -101,7 +101,9 @@ def test_workspaces_are_required(L):
     for call in (append, decode, weights, select, compact):
         assert call(L, ws=None) == 6 and call(L, wsb=255) == 6
     assert L.mla_decode_fp4_workspace_size(64, 1, 128, 0) >= 256
-    assert L.mla_key_weights_workspace_size(64, 1, 128) == L.mla_select_keys_workspace_size(64) == 256
+    assert L.mla_key_weights_workspace_size(64, 1, 128, 32768) == L.mla_select_keys_workspace_size(64) == 256
+    assert L.mla_key_weights_workspace_size(64, 2, 128, 32768) >= 256 + 64 * 32768 * 4
+    assert weights(L, s=9, wsb=4096) == 6
     assert L.mla_compact_rows_workspace_size(64) == L.mla_kv_append_fp4_workspace_size(64) == 256
 
 

@@ -392,6 +392,13 @@ def test_weights_scales(fmt, scale, decay):
     _check_weights(fmt, [200, 65, 1], 16, scale=scale, decay=decay, seed=80)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lens,s", [([60000], 1), ([30000, 5, 21000], 2), ([20500], 200)])
+def test_weights_long(fmt, lens, s):
+    """Several tiles for each CTA, with one chunk of query rows and with more."""
+    _check_weights(fmt, lens, 1, s=s, seed=70)
+
+
 def test_weights_with_sinks_and_many_requests():
     _check_weights("bf16", [3, 70, 1, 0] * 60, 4, page=16, seed=81, sinks=np.array([0.0, 2.0, -np.inf, 8.0]))
 
