@@ -10,7 +10,7 @@
 // A CTA per SM takes an equal share of all tiles.  16 warps:
 //   0-3   a key a thread: S from tensor memory, exponentials, the weight's update
 //   4     MMAs (one thread): nine 64-column boxes of K against those of Q
-//   5     rows of the next tiles through the block table, their lines asked for in L2, and the chunk's log-sum-exps
+//   5     rows of the next tiles through the block table, and the chunk's log-sum-exps
 //   6-15  producers, two for each stage of the ring, 64 rows each: bf16 rows by cp.async; e4m3 and 4-bit rows through
 //         registers into f16 (exact), with q in f16 too, the next box's loads out before the last one's are converted; the RoPE
 //         columns of 4-bit rows stay bf16.  A stage has producers of its own, as a parity tells no more than the last phase.
@@ -72,7 +72,7 @@ struct Shares {
   __device__ Shares(const KeyWeightsParams& prm, int64_t cap_, const Bars& bars, int chunks_)
       : p(&prm), cap(cap_), left(bars.share), range(bars.start_range), b(bars.start_b), t0(bars.start_t), o(bars.start_o), from(bars.start_o),
         chunks(chunks_) {}
-  __device__ bool next(Segment& s) {
+  __device__ __noinline__ bool next(Segment& s) {       // one copy for all roles: the loops should stay in the instruction cache
     while (left > 0 && b < p->kv.B) {
       const int len = paged_len(p->kv, p->err, b, cap, false), all = tiles_of(len) - t0;
       if (all <= 0) {
@@ -93,7 +93,7 @@ struct Shares {
 
 // Where this CTA's share starts; by all threads.  With several chunks the first CTA puts down the tiles and ranges before each
 // request.
-__device__ __forceinline__ void find_share(const KeyWeightsParams& p, int64_t cap, int chunks, Bars& bars, int32_t* sums) {
+__device__ __noinline__ void find_share(const KeyWeightsParams& p, int64_t cap, int chunks, Bars& bars, int32_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.kv.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.kv.B), b1 = min(b0 + per, p.kv.B);
   int64_t tiles = 0, ranges = 0;
@@ -153,8 +153,7 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   return v;
 }
 
-constexpr int kNoRow = -1, kZeroRow = -2;
-
+constexpr int kNoRow = -1;                       // no key there, or its page is none
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -250,34 +249,39 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
       ++c_all;
     }
   } else if (warp == 4) {
-    // ---------------- MMAs ----------------
-    if (lane == 0) {
-      if (p.debug_stall) live = live && wait.one(&bars.stall, 0, W_STALL);
-      uint32_t kbox = 0;
-      for (; live && shares.next(it); ++c_all) {
-        const uint32_t n = (uint32_t)(min(rows - it.c * kTile, kTile) + 31) & ~31u;
-        const uint32_t id_f16 = idesc_f16_f32(kTile, n, false, false), id_bf16 = idesc_bf16_f32(kTile, n, false, false);
-        for (int i = it.i0; i < it.i1 && live; ++i, ++u) {
-          const int buf = u & 1;
-          if (!wait.one(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, W_SFREE)) { live = false; break; }
-          for (int k = 0; k < kBoxes; ++k, ++kbox) {
-            const uint32_t slot = kbox % kStages;
-            if (i == it.i0 && !wait.one(&bars.qfull[k], c_all & 1, W_QFULL)) { live = false; break; }
-            if (!wait.one(&bars.kfull[slot], (kbox / kStages) & 1, W_KFULL)) { live = false; break; }
-            tc_fence_after();
-            if constexpr (kFmt == kCacheBf16) fence_proxy_async_smem();    // copies that other threads issued
+    // ---------------- MMAs (the whole warp waits, one lane issues) ----------------
+    // (not unrolled: nine copies pass the instruction cache, 284 against 211 us for 4096 query rows and 32768 keys in 4 bits)
+    if (p.debug_stall) live = live && wait.warp(&bars.stall, 0, W_STALL);
+    const uint64_t kdesc = sdesc_sw128(smem_u32(smem + kOffK), 16, 1024), qdesc = sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024);
+    uint32_t slot = 0, phase = 0;
+    for (; live && shares.next(it); ++c_all) {
+      const uint32_t n = (uint32_t)(min(rows - it.c * kTile, kTile) + 31) & ~31u;
+      const uint32_t id_f16 = idesc_f16_f32(kTile, n, false, false), id_bf16 = idesc_bf16_f32(kTile, n, false, false);
+      for (int i = it.i0; i < it.i1 && live; ++i, ++u) {
+        const int buf = u & 1;
+        const uint32_t d = tbase + buf * kTile;
+        const bool first = i == it.i0, last = i == it.i1 - 1;
+        if (!wait.warp(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, W_SFREE)) { live = false; break; }
+#pragma unroll 1
+        for (int k = 0; k < kBoxes; ++k) {
+          if (first && !wait.warp(&bars.qfull[k], c_all & 1, W_QFULL)) { live = false; break; }
+          if (!wait.warp(&bars.kfull[slot], phase, W_KFULL)) { live = false; break; }
+          tc_fence_after();
+          if constexpr (kFmt == kCacheBf16) fence_proxy_async_smem();    // copies that other threads issued
+          if (elect_one()) {
             const bool bf = kFmt == kCacheBf16 || (kFmt == kCacheFp4 && k == kBoxes - 1);
-            mma_box64(tbase + buf * kTile, sdesc_sw128(smem_u32(smem + kOffK + slot * kBoxBytes), 16, 1024),
-                      sdesc_sw128(smem_u32(smem + kOffQ + k * kBoxBytes), 16, 1024), bf ? id_bf16 : id_f16, k > 0 ? 1u : 0u);
+            mma_box64(d, kdesc + slot * (kBoxBytes / 16), qdesc + k * (kBoxBytes / 16), bf ? id_bf16 : id_f16, k > 0 ? 1u : 0u);
             mma_commit(&bars.kempty[slot]);
-            if (i == it.i1 - 1) mma_commit(&bars.qempty[k]);
+            if (last) mma_commit(&bars.qempty[k]);
+            if (k == kBoxes - 1) mma_commit(&bars.sfull[buf]);
           }
-          if (live) mma_commit(&bars.sfull[buf]);
+          __syncwarp();
+          if (++slot == kStages) slot = 0, phase ^= 1;
         }
       }
-      mma_commit(&bars.drain);                   // what was issued is done before tensor memory is given back
-      mbar_drain(&bars.drain, 0);
     }
+    if (elect_one()) mma_commit(&bars.drain);    // what was issued is done before tensor memory is given back
+    mbar_drain(&bars.drain, 0);
     __syncwarp();
   } else if (warp == 5) {
     // ---------------- rows of the tiles to come ----------------
@@ -302,10 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
           if (j < it.len) {
             const int pg = j / p.kv.page_size;
             const int page = guarded_int(p.err, p.kv.block_table, (int64_t)it.b * p.kv.max_pages + pg, (int64_t)p.kv.B * p.kv.max_pages);
-            at[r] = kZeroRow;
             if (page >= 0 && page < p.kv.num_pages) at[r] = page * p.kv.page_size + (j - pg * p.kv.page_size);
             else record_error(p.err, DEV_RANGE_BASE | Y_PAGE);
-            if (at[r] >= 0) bulk_prefetch_l2(p.kv.cache + (int64_t)at[r] * p.kv.row_bytes, p.kv.row_bytes);
           }
         }
         if (!wait.warp(&bars.rfree[slot], ((u / kRowSlots) & 1) ^ 1, W_RFREE)) { live = false; break; }
@@ -318,131 +320,140 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     // ---------------- producers ----------------
     const uint32_t me = (warp - kFirstProducer) % kStages;
     const int r0 = (warp - kFirstProducer) / kStages * 64;     // this warp's rows of a box
-    uint32_t kbox = 0, due = 0;
+    uint64_t* const kempty = &bars.kempty[me];
+    uint64_t* const kfull = &bars.kfull[me];
+    const uint32_t kslot = smem_u32(smem + kOffK + me * kBoxBytes);
+    uint32_t made = 0;                            // boxes of this stage so far
     // a box whose loads are out: 4-bit rows two lanes a row, 32 columns each; e4m3 four lanes a row, 16 columns each
     constexpr int kVec = kFmt == kCacheFp4 ? 4 : 8;
-    uint4 v[kVec], ready[kVec];
-    uint32_t sc[4], ready_sc[4];
-    bool pending = false;
-    auto flush = [&]() -> bool {                  // converts the box `due`
-      if (!pending) return true;
-      pending = false;
-      const uint32_t slot = due % kStages, box = smem_u32(smem + kOffK + slot * kBoxBytes);
-      if (!wait.warp(&bars.kempty[slot], ((due / kStages) & 1) ^ 1, W_KEMPTY)) return false;
+    uint4 v[2][kVec];
+    uint32_t sc[2][4];
+    int held = -1;                                // which of the two holds a box
+    auto convert = [&](const uint4 (&ready)[kVec], const uint32_t (&ready_sc)[4]) -> bool {
+      held = -1;
+      if (!wait.warp(kempty, (made & 1) ^ 1, W_KEMPTY)) return false;
+      ++made;
       if constexpr (kFmt == kCacheFp4) {
         const int half = lane & 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = r0 + 16 * i + (lane >> 1);
           const uint2 s = fp4_scales2(ready_sc[i]);
-          st_shared16(box_unit(box, r, 4 * half), fp4x8_to_f16(ready[i].x, s.x));
-          st_shared16(box_unit(box, r, 4 * half + 1), fp4x8_to_f16(ready[i].y, s.x));
-          st_shared16(box_unit(box, r, 4 * half + 2), fp4x8_to_f16(ready[i].z, s.y));
-          st_shared16(box_unit(box, r, 4 * half + 3), fp4x8_to_f16(ready[i].w, s.y));
+          st_shared16(box_unit(kslot, r, 4 * half), fp4x8_to_f16(ready[i].x, s.x));
+          st_shared16(box_unit(kslot, r, 4 * half + 1), fp4x8_to_f16(ready[i].y, s.x));
+          st_shared16(box_unit(kslot, r, 4 * half + 2), fp4x8_to_f16(ready[i].z, s.y));
+          st_shared16(box_unit(kslot, r, 4 * half + 3), fp4x8_to_f16(ready[i].w, s.y));
         }
       } else {
         const int quarter = lane & 3;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           const int r = r0 + 8 * i + (lane >> 2);
-          st_shared16(box_unit(box, r, 2 * quarter), e4m3x8_to_f16(ready[i].x, ready[i].y));
-          st_shared16(box_unit(box, r, 2 * quarter + 1), e4m3x8_to_f16(ready[i].z, ready[i].w));
+          st_shared16(box_unit(kslot, r, 2 * quarter), e4m3x8_to_f16(ready[i].x, ready[i].y));
+          st_shared16(box_unit(kslot, r, 2 * quarter + 1), e4m3x8_to_f16(ready[i].z, ready[i].w));
         }
       }
       fence_proxy_async_smem();
-      warp_arrive(&bars.kfull[slot]);
+      warp_arrive(kfull);
       return true;
     };
+    // (two copies of the code: a register that a load is on its way to is not moved without waiting for it)
+    auto flush = [&]() -> bool { return held < 0 || (held == 0 ? convert(v[0], sc[0]) : convert(v[1], sc[1])); };
+    int k0 = me;                                   // this stage's first box of the unit
     for (; live && shares.next(it); ++c_all) {
-      {
-        const int n = min(rows - it.c * kTile, kTile), n32 = (n + 31) & ~31;
-        const __nv_bfloat16* qsrc = p.q + ((int64_t)it.b * rows + it.c * kTile) * kDk;
-        const uint64_t q_bytes = (uint64_t)p.kv.B * rows * kDk * 2;
-        for (int t = it.i0; t < it.i1 && live; ++t, ++u) {
-          const int rslot = u % kRowSlots;
-          bool have_rows = false;
-          for (int k = 0; k < kBoxes; ++k, ++kbox) {
-            if (t == it.i0 && k % kStages == me) {
-              // ---- a box of query rows ----
-              const uint32_t box = smem_u32(smem + kOffQ + k * kBoxBytes);
-              if (!flush() || !wait.warp(&bars.qempty[k], (c_all & 1) ^ 1, W_QEMPTY)) { live = false; break; }
-              const int unit = lane & 7, rend = min(n32, r0 + 64);
-              for (int r = r0 + (lane >> 3); r < rend; r += 4) {
-                const __nv_bfloat16* src = qsrc + (int64_t)r * kDk + 64 * k + 8 * unit;
-                const bool in = r < n && guard_span(p.err, G_STEP_IN, src, 16, p.q, q_bytes);
-                cp_async16_zfill(box_unit(box, r, unit), in ? src : p.q, in ? 16u : 0u);
-              }
-              if constexpr (kFmt == kCacheBf16) {
-                cp_async_arrive_noinc(&bars.qfull[k]);
-              } else {                                   // each lane puts its own copies into f16 where they lie
-                cp_async_wait_all();
-                if (kFmt == kCacheE4m3 || k < kBoxes - 1)
-                  for (int r = r0 + (lane >> 3); r < rend; r += 4) {
-                    const uint32_t at = box_unit(box, r, unit);
-                    st_shared16(at, bf16x8_to_f16(ld_shared16(at)));
-                  }
-                fence_proxy_async_smem();
-                warp_arrive(&bars.qfull[k]);
-              }
+      const int n = min(rows - it.c * kTile, kTile), n32 = (n + 31) & ~31;
+      const __nv_bfloat16* qsrc = p.q + ((int64_t)it.b * rows + it.c * kTile) * kDk;
+      const uint64_t q_bytes = (uint64_t)p.kv.B * rows * kDk * 2;
+      const int unit = lane & 7;
+      // the query rows' boxes me and me + 5, in the first unit each before the keys' box of its column
+      int kq = me;
+      auto query_box = [&](int k) -> bool {
+        const uint32_t box = smem_u32(smem + kOffQ + k * kBoxBytes);
+        if (!flush() || !wait.warp(&bars.qempty[k], (c_all & 1) ^ 1, W_QEMPTY)) return false;
+        for (int r = r0 + (lane >> 3); r < min(n32, r0 + 64); r += 4) {
+          const __nv_bfloat16* src = qsrc + (int64_t)r * kDk + 64 * k + 8 * unit;
+          const bool in = r < n && guard_span(p.err, G_STEP_IN, src, 16, p.q, q_bytes);
+          cp_async16_zfill(box_unit(box, r, unit), in ? src : p.q, in ? 16u : 0u);
+        }
+        if constexpr (kFmt == kCacheBf16) {
+          cp_async_arrive_noinc(&bars.qfull[k]);
+        } else {                                   // each lane puts its own copies into f16 where they lie
+          cp_async_wait_all();
+          if (kFmt == kCacheE4m3 || k < kBoxes - 1)
+            for (int r = r0 + (lane >> 3); r < min(n32, r0 + 64); r += 4) {
+              const uint32_t at = box_unit(box, r, unit);
+              st_shared16(at, bf16x8_to_f16(ld_shared16(at)));
             }
-            if (kbox % kStages != me) continue;
-            // ---- a box of keys ----
-            if (!have_rows && !wait.warp(&bars.rfull[rslot], (u / kRowSlots) & 1, W_RFULL)) { live = false; break; }
-            have_rows = true;
-            const int32_t* at = row_slots + rslot * kTile;
-            if (kFmt == kCacheBf16 || (kFmt == kCacheFp4 && k == kBoxes - 1)) {
-              const uint32_t slot = kbox % kStages, box = smem_u32(smem + kOffK + slot * kBoxBytes);
-              if (!flush() || !wait.warp(&bars.kempty[slot], ((kbox / kStages) & 1) ^ 1, W_KEMPTY)) { live = false; break; }
-              const int unit = lane & 7;
-              const uint32_t off = (kFmt == kCacheBf16 ? 128 * k : kFp4Pe) + 16 * unit;
-#pragma unroll 8
-              for (int r = r0 + (lane >> 3); r < r0 + 64; r += 4) {
-                const int a = at[r];
-                if (a == kNoRow) continue;               // the row's lane is not looked at
-                const uint8_t* src = p.kv.cache + (int64_t)a * p.kv.row_bytes + off;
-                const bool in = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes);
-                cp_async16_zfill(box_unit(box, r, unit), in ? src : (const uint8_t*)p.q, in ? 16u : 0u);
-              }
-              if constexpr (kFmt == kCacheBf16) {
-                cp_async_arrive_noinc(&bars.kfull[slot]);
-              } else {
-                cp_async_wait_all();
-                fence_proxy_async_smem();
-                warp_arrive(&bars.kfull[slot]);
-              }
-              continue;
+          fence_proxy_async_smem();
+          warp_arrive(&bars.qfull[k]);
+        }
+        return true;
+      };
+      for (int t = it.i0; t < it.i1 && live; ++t, ++u) {
+        const int rslot = u % kRowSlots;
+        if (!wait.warp(&bars.rfull[rslot], (u / kRowSlots) & 1, W_RFULL)) { live = false; break; }
+        const int32_t* at = row_slots + rslot * kTile + r0;
+        int k = k0;
+        for (; k < kBoxes; k += kStages) {
+          for (; kq <= k && live; kq += kStages) live = query_box(kq);
+          if (!live) break;
+          if (kFmt == kCacheBf16 || (kFmt == kCacheFp4 && k == kBoxes - 1)) {
+            int32_t a[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a[i] = at[(lane >> 3) + 4 * i];
+            if (!flush() || !wait.warp(kempty, (made & 1) ^ 1, W_KEMPTY)) { live = false; break; }
+            ++made;
+            const uint32_t off = (kFmt == kCacheBf16 ? 128 * k : kFp4Pe) + 16 * unit;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint8_t* src = p.kv.cache + (int64_t)a[i] * p.kv.row_bytes + off;
+              const bool in = a[i] >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes);
+              // (a row of zeros where there is none)
+              cp_async16_zfill256(box_unit(kslot, r0 + (lane >> 3) + 4 * i, unit), in ? src : (const uint8_t*)p.q, in ? 16u : 0u);
             }
+            if constexpr (kFmt == kCacheBf16) {
+              cp_async_arrive_noinc(kfull);
+            } else {
+              cp_async_wait_all();
+              fence_proxy_async_smem();
+              warp_arrive(kfull);
+            }
+            continue;
+          }
+          auto load = [&](uint4 (&x)[kVec], uint32_t (&xs)[4]) {
             if constexpr (kFmt == kCacheFp4) {
               const int half = lane & 1;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int a = at[r0 + 16 * i + (lane >> 1)];
+                const int a = at[16 * i + (lane >> 1)];
                 const uint8_t* r = p.kv.cache + (int64_t)a * kFp4Row;
-                v[i] = make_uint4(0, 0, 0, 0), sc[i] = 0;
+                x[i] = make_uint4(0, 0, 0, 0), xs[i] = 0;
                 if (a >= 0 && guard_span(p.err, G_STEP_IN, r, kFp4Row, p.kv.cache, cache_bytes)) {
-                  v[i] = *reinterpret_cast<const uint4*>(r + 32 * k + 16 * half);
-                  sc[i] = *reinterpret_cast<const uint16_t*>(r + kFp4Codes + 4 * k + 2 * half);
+                  x[i] = *reinterpret_cast<const uint4*>(r + 32 * k + 16 * half);
+                  xs[i] = *reinterpret_cast<const uint16_t*>(r + kFp4Codes + 4 * k + 2 * half);
                 }
               }
-            } else if constexpr (kFmt == kCacheE4m3) {
+            } else {
 #pragma unroll
               for (int i = 0; i < kVec; ++i) {
-                const int a = at[r0 + 8 * i + (lane >> 2)];
+                const int a = at[8 * i + (lane >> 2)];
                 const uint8_t* src = p.kv.cache + (int64_t)a * kDk + 64 * k + 16 * (lane & 3);
-                v[i] = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint4*>(src)
+                x[i] = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint4*>(src)
                                                                                                : make_uint4(0, 0, 0, 0);
               }
             }
+          };
+          if constexpr (kFmt != kCacheBf16) {
+            const int into = held == 0 ? 1 : 0;
+            if (into == 0) load(v[0], sc[0]);
+            else load(v[1], sc[1]);
             if (!flush()) { live = false; break; }
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) ready[i] = v[i];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ready_sc[i] = sc[i];
-            due = kbox;
-            pending = true;
+            held = into;
           }
-          if (live) warp_arrive(&bars.rfree[rslot]);
         }
+        for (; kq < kBoxes && live; kq += kStages) live = query_box(kq);
+        k0 = k - kBoxes;                           // the ring goes on with the next unit's first box
+        if (live) warp_arrive(&bars.rfree[rslot]);
       }
     }
     if (live) flush();

@@ -201,6 +201,12 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst_smem, const void* 
                : "memory");
 }
 
+// The same, and the other 16-byte pieces of the 256 around it asked for in L2: rows that are read in columns one after the other.
+__device__ __forceinline__ void cp_async16_zfill256(uint32_t dst_smem, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(src_bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // One arrival on `bar` once every cp.async this thread issued before has landed; the
@@ -475,6 +481,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// One lane of a converged warp.  Where the compiler knows that one lane is left, descriptors stay in uniform registers: four
+// MMAs of a box go out in 364 cycles, against 534 under `lane == 0`.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ bool elect_lane0() { return (threadIdx.x & 31u) == 0u; }
 
 // TMA gather of four rows (tile::gather4; the tensor map's box is one row high): rows y0..y3

@@ -5,21 +5,26 @@
 
 namespace mla {
 
+// The part of a wait behind its first test, out of line: a kernel has dozens of waits, and its loops should stay in the
+// instruction cache.
+static __device__ __noinline__ bool tile_wait_on(uint64_t* bar, uint32_t parity, uint32_t* abort, uint32_t* err, uint32_t site,
+                                                 uint32_t spin_limit, bool cluster) {
+  if (mbar_wait_inline(bar, parity, abort, site, spin_limit, cluster)) return true;
+  atomicCAS(abort, 0u, DEV_TIMEOUT_BASE | site);
+  record_error(err, DEV_TIMEOUT_BASE | site);
+  return false;
+}
+
 struct TileWaits {
   uint32_t* abort;     // shared memory, 0 at the start
   uint32_t* err;       // the call's status word
   uint32_t spin_limit;
 
-  // by one thread
-  __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity, uint32_t site, bool cluster = false) const {
-    if (mbar_wait(bar, parity, abort, site, spin_limit, cluster)) return true;
-    atomicCAS(abort, 0u, DEV_TIMEOUT_BASE | site);
-    record_error(err, DEV_TIMEOUT_BASE | site);
-    return false;
-  }
   // by a warp, with one answer for all of it
   __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity, uint32_t site, bool cluster = false) const {
-    const bool ok = one(bar, parity, site, cluster);
+    const uint32_t a = smem_u32(bar);
+    if (__all_sync(0xffffffffu, cluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity))) return true;
+    const bool ok = tile_wait_on(bar, parity, abort, err, site, spin_limit, cluster);
     return __all_sync(0xffffffffu, ok);
   }
 };
