@@ -35,9 +35,23 @@ struct DecodeFp4Params {
   uint32_t* err;
   float scale;                   // scale * kv_scale
   float kv_scale;
+  uint32_t spin_limit, debug_stall;
   int s, H;
+  int row_tiles;                 // groups of up to 128 query rows a request has
+  int part_rows;                 // rows of a partial
+  int64_t groups;
+  int64_t* before;               // ws: [groups + 1] tiles before each group
+  float* part_lse;               // ws: [groups + pairs, part_rows]
+  float* part_o;                 // ws: [groups + pairs, part_rows, 512]
+  uint64_t part_lse_bytes, part_o_bytes;
 };
-cudaError_t launch_decode_fp4(const DecodeFp4Params& p, cudaStream_t stream);
+struct DecodeFp4Scratch {
+  int pairs, row_tiles, part_rows;
+  int64_t groups;
+  size_t before, part_lse, part_o;     // bytes
+};
+DecodeFp4Scratch decode_fp4_scratch(int B, int s, int H, int num_splits);
+cudaError_t launch_decode_fp4(const DecodeFp4Params& p, int pairs, cudaStream_t stream);
 
 struct KeyWeightsParams {
   PagedRows kv;

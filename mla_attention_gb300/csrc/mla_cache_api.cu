@@ -50,8 +50,9 @@ extern "C" {
 
 // ---------------------------------------------------------------------------
 size_t mla_decode_fp4_workspace_size(int B, int q_per_req, int H, int num_splits) {
-  (void)B, (void)q_per_req, (void)H, (void)num_splits;
-  return kWsHeader;
+  if (B < 0 || q_per_req < 1 || H < 1 || num_splits < 0) return kWsHeader;
+  const DecodeFp4Scratch w = decode_fp4_scratch(B, q_per_req, H, num_splits);
+  return kWsHeader + w.before + w.part_lse + w.part_o;
 }
 
 mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4, float kv_scale, int64_t num_pages,
@@ -80,9 +81,21 @@ mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4
   p.err = reinterpret_cast<uint32_t*>(workspace);
   p.scale = scale * kv_scale;
   p.kv_scale = kv_scale;
+  p.spin_limit = spin_limit();
+  p.debug_stall = debug_stall();
   p.s = q_per_req;
   p.H = H;
-  return finish(launch_decode_fp4(p, reinterpret_cast<cudaStream_t>(stream)), "mla_decode_fp4");
+  const DecodeFp4Scratch w = decode_fp4_scratch(B, q_per_req, H, num_splits);
+  p.row_tiles = w.row_tiles;
+  p.part_rows = w.part_rows;
+  p.groups = w.groups;
+  char* at = reinterpret_cast<char*>(workspace) + kWsHeader;
+  p.before = reinterpret_cast<int64_t*>(at);
+  p.part_lse = reinterpret_cast<float*>(at + w.before);
+  p.part_o = reinterpret_cast<float*>(at + w.before + w.part_lse);
+  p.part_lse_bytes = w.part_lse;
+  p.part_o_bytes = w.part_o;
+  return finish(launch_decode_fp4(p, w.pairs, reinterpret_cast<cudaStream_t>(stream)), "mla_decode_fp4");
 }
 
 // ---------------------------------------------------------------------------

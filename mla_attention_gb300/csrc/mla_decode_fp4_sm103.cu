@@ -1,0 +1,655 @@
+// Decode over a 4-bit latent cache (sm_103a: tcgen05 on pairs of SMs, TMEM).
+//   S = scale k . q,  P = softmax(S),  O = P V with V the key's latent columns; a sink is one more key with no value.
+//
+// A cluster of two CTAs works on 128 query rows (token, head) of one request, 64 in each CTA, and goes through the request's keys
+// 128 at a time.  Both products are MMAs of the pair (cta_group::2, M = 128): each CTA holds the scores, P and O of its own
+// rows - 128 lanes of tensor memory with half of the columns each - so that P never crosses to the other SM, O of 512
+// columns takes half of a tensor memory and two buffers of scores fit beside it; and each CTA brings half of either B
+// operand, so that a key's row is taken apart once for the scores and once for the values.  CTA c has the tile's keys
+// 64 c .. 64 c + 63 for the scores and the latent columns 128 c .. and 256 + 128 c .. of all its keys for the values.
+//
+// A code times its scale has at most six bits and is exact in f16; q and P are f16 too (P a weight of at most 2^8), the RoPE
+// columns stay bf16 as their MMA's operands, sums are fp32.  15 warps a CTA:
+//   0-3   rows: lanes L and L + 64 of tensor memory hold the same row's scores of 64 keys each; maximum through shared
+//         memory, lazy rescale of O (by more than 2^8), exponentials, P
+//   4, 5  MMAs, in the first CTA alone (one lane issues for both): scores; values
+//   6-13  4-bit rows into f16: K column box w and V (key half w / 4, column box w % 4); the loads of a tile go out before
+//         the last one's are converted
+//   14    the tiles' rows through the block table, and the RoPE columns
+// The tiles of all requests are dealt to the pairs in equal shares; fp32 partials of a request that several pairs share
+// are merged by decode_fp4_reduce_kernel.
+#include <math_constants.h>
+
+#include "fp4_rows.cuh"
+#include "softmax_rows.cuh"
+#include "tile_waits.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kTile = 128, kHalf = 64;                // keys a tile, and the part that one CTA brings for the scores
+constexpr int kThreads = 480, kConverters = 8, kFirstConverter = 6, kRowWarp = 14;
+constexpr int kBox = 64 * 128;                        // 64 rows of 128 bytes
+constexpr int kRowSlots = 3;
+constexpr uint32_t kTmemO = 0, kTmemS = 256;          // O: 256 columns; S: two buffers of 64
+constexpr float kRescale = 8.f;                       // P passes 1 by 2^8 at most
+
+constexpr int kOffQ = 0;                              // 9 boxes
+constexpr int kOffK = 9 * kBox;                       // 9 boxes
+constexpr int kOffV = 18 * kBox;                      // 2 halves of 4 boxes
+constexpr int kOffP = 26 * kBox;                      // 2 boxes
+constexpr int kOffRows = 28 * kBox;
+constexpr int kOffMax = kOffRows + kRowSlots * kTile * 4;   // [2][2][64]
+constexpr int kOffBars = kOffMax + 4 * 64 * 4;
+
+struct Bars {
+  // in the first CTA, with arrivals from both
+  uint64_t kfull[3], vfull[2], qfull, pfull, sfree[2], ofree;
+  // in each CTA, by commits to both
+  uint64_t kempty[3], vempty[2], qempty, sfull[2], pvdone;
+  // in each CTA
+  uint64_t rfull[kRowSlots], rfree[kRowSlots];
+  uint64_t pair[2];                                   // warps w and w + 2
+  uint64_t drain[2], stall;
+  uint32_t tmem_base, abort;
+  int64_t share, start_t;
+  int32_t start_g;
+};
+constexpr int kSmem = kOffBars + 512;
+static_assert(sizeof(Bars) <= 512, "barrier block too large");
+static_assert(kSmem <= 232448, "shared memory over the sm_103a limit");
+
+enum : uint32_t { D_KFULL = 0x1C0, D_VFULL, D_QFULL, D_PFULL, D_SFREE, D_OFREE, D_KEMPTY, D_VEMPTY, D_QEMPTY, D_SFULL, D_PVDONE, D_RFULL,
+                  D_RFREE, D_PAIR, D_STALL, D_ALIGN };
+
+// ---- query groups: up to 128 (token, head) rows of a request ----
+struct Group {
+  int b, row0, rows;       // request, first row among the request's s * H, rows
+  int len;                 // keys of the request
+  int keys;                // keys that its last token sees
+};
+__device__ __forceinline__ Group group_of(const DecodeFp4Params& p, int64_t g, bool report) {
+  Group r;
+  r.b = (int)(g / p.row_tiles);
+  r.row0 = (int)(g - (int64_t)r.b * p.row_tiles) * kRows;
+  r.rows = min(p.s * p.H - r.row0, kRows);
+  r.len = paged_len(p.kv, p.err, r.b, (int64_t)p.kv.max_pages * p.kv.page_size, report);
+  r.keys = max(0, r.len - p.s + 1 + (r.row0 + r.rows - 1) / p.H);
+  return r;
+}
+
+// A pair's part of one group: tiles t0 .. t1 - 1.
+struct Part {
+  Group g;
+  int64_t id;
+  int t0, t1;
+};
+struct Shares {
+  const DecodeFp4Params* p;
+  int64_t g, t, left;
+  __device__ Shares(const DecodeFp4Params& prm, const Bars& bars) : p(&prm), g(bars.start_g), t(bars.start_t), left(bars.share) {}
+  __device__ __noinline__ bool next(Part& it) {
+    while (left > 0 && g < p->groups) {
+      it.g = group_of(*p, g, false);
+      const int64_t n = (it.g.keys + kTile - 1) / kTile - t;
+      if (n <= 0) {
+        ++g, t = 0;
+        continue;
+      }
+      it.id = g, it.t0 = (int)t, it.t1 = (int)(t + min(n, left));
+      left -= it.t1 - it.t0, t = it.t1;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Where this pair's share starts, and (first CTA of all) the tiles before each group; by all threads.
+__device__ __noinline__ void find_share(const DecodeFp4Params& p, Bars& bars, int64_t* sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t per = (p.groups + kThreads - 1) / kThreads, g0 = min(tid * per, p.groups), g1 = min(g0 + per, p.groups);
+  int64_t mine = 0;
+  for (int64_t g = g0; g < g1; ++g) mine += (group_of(p, g, blockIdx.x == 0).keys + kTile - 1) / kTile;
+  int64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t v = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int64_t at = upto - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) at += sums[w];
+    total += sums[w];
+  }
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2, lo = total * pair / pairs, hi = total * (pair + 1) / pairs;
+  if (tid == 0) bars.share = hi - lo;
+  const bool tell = blockIdx.x == 0, here = lo < hi && at <= lo && lo < at + mine;
+  auto put = [&](int64_t g, int64_t v) {
+    if (guard_span(p.err, G_TILE_PREFIX, p.before + g, 8, p.before, (uint64_t)(p.groups + 1) * 8)) p.before[g] = v;
+  };
+  if (tell && tid == 0) put(p.groups, total);
+  if (tell || here) {
+    for (int64_t g = g0; g < g1; ++g) {
+      const int n = (group_of(p, g, false).keys + kTile - 1) / kTile;
+      if (tell) put(g, at);
+      if (lo < hi && at <= lo && lo < at + n) bars.start_g = (int)g, bars.start_t = lo - at;
+      at += n;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t box_unit(uint32_t box, int row, int unit) {   // 16 bytes of a swizzled 128-byte row
+  return box + row * 128 + ((unit ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// ---- MMAs of the pair ----
+#define MLA_MMA2(D, X, Y, ID, P) "tcgen05.mma.cta_group::2.kind::f16 [" D "], " X ", " Y ", " ID ", " P ";\n\t"
+#define MLA_STEP2(P, ID) MLA_MMA2("%0", "x", "y", ID, P) "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
+#define MLA_BOX2(P, ID) MLA_STEP2(P, ID) MLA_STEP2("t", ID) MLA_STEP2("t", ID) MLA_MMA2("%0", "x", "y", ID, "t") \
+  "add.s64 x, x, 506;\n\tadd.s64 y, y, 506;\n\t"
+// S (+)= Q K^T over three boxes of 64 columns, 64 rows each in either CTA; the last box with an instruction descriptor of its own
+__device__ __forceinline__ void mma2_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t id_last, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
+      MLA_BOX2("p", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%4") "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(id_last), "r"(accumulate)
+      : "memory");
+}
+#define MLA_PV2(P) MLA_MMA2("%0", "x", "y", "%4", P) MLA_MMA2("%5", "x", "z", "%4", P) \
+  "add.s64 x, x, 2;\n\tadd.s64 y, y, 128;\n\tadd.s64 z, z, 128;\n\t"
+// O (+)= P V over 64 keys: two MMAs of 256 columns (128 from either CTA) for each 16 keys
+__device__ __forceinline__ void mma2_values(uint32_t d0, uint32_t d1, uint64_t a, uint64_t b0, uint64_t b1, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y, z;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tsetp.eq.u32 t, %4, %4;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\tmov.b64 z, %3;\n\t"
+      MLA_PV2("p") MLA_PV2("t") MLA_PV2("t") MLA_PV2("t") "}" ::"r"(d0),
+      "l"(a), "l"(b0), "l"(b1), "r"(id), "r"(d1), "r"(accumulate)
+      : "memory");
+}
+#undef MLA_MMA2
+#undef MLA_STEP2
+#undef MLA_BOX2
+#undef MLA_PV2
+// arrives on the barrier at this offset in both CTAs once the MMAs that this thread issued are done
+__device__ __forceinline__ void commit2(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+
+// Raw 64 x 64 box of 4-bit values: two lanes a row, 32 columns each; the four scales of rows lane and 32 + lane.
+struct Raw {
+  uint4 v[4];
+  uint32_t sc[2];
+};
+__device__ __forceinline__ void load_raw(const DecodeFp4Params& p, Raw& x, const int32_t* at, int col, int lane, uint64_t cache_bytes) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = at[16 * i + (lane >> 1)];
+    const uint8_t* r = p.kv.cache + (int64_t)a * kFp4Row + col / 2 + 16 * (lane & 1);
+    x.v[i] = a >= 0 && guard_span(p.err, G_STEP_IN, r, 16, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint4*>(r) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int a = at[32 * i + lane];
+    const uint8_t* r = p.kv.cache + (int64_t)a * kFp4Row + kFp4Codes + col / 16;
+    x.sc[i] = a >= 0 && guard_span(p.err, G_STEP_IN, r, 4, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint32_t*>(r) : 0u;
+  }
+}
+__device__ __forceinline__ void convert_raw(const Raw& x, uint32_t box, int lane) {
+  const int half = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 16 * i + (lane >> 1);
+    const uint32_t four = __shfl_sync(0xffffffffu, x.sc[i >> 1], r & 31);
+    const uint2 s = fp4_scales2(half ? four >> 16 : four);
+    st_shared16(box_unit(box, r, 4 * half), fp4x8_to_f16(x.v[i].x, s.x));
+    st_shared16(box_unit(box, r, 4 * half + 1), fp4x8_to_f16(x.v[i].y, s.x));
+    st_shared16(box_unit(box, r, 4 * half + 2), fp4x8_to_f16(x.v[i].z, s.y));
+    st_shared16(box_unit(box, r, 4 * half + 3), fp4x8_to_f16(x.v[i].w, s.y));
+  }
+}
+// box k of this CTA's 64 query rows (in f16 but for the RoPE columns); rows behind the group's are zeros
+__device__ __noinline__ void load_query_box(const DecodeFp4Params& p, const Group& g, int first, uint32_t box, int k, int lane) {
+  const uint64_t q_bytes = (uint64_t)p.kv.B * p.s * p.H * kDk * 2;
+  const int unit = lane & 7;
+#pragma unroll 1
+  for (int r0 = lane >> 3; r0 < kHalf; r0 += 32) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = first + r0 + 4 * i;
+      const __nv_bfloat16* src = p.q + ((int64_t)g.b * p.s * p.H + g.row0 + r) * kDk + 64 * k + 8 * unit;
+      x[i] = r < g.rows && guard_span(p.err, G_Q, src, 16, p.q, q_bytes) ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st_shared16(box_unit(box, r0 + 4 * i, unit), k == 8 ? x[i] : bf16x8_to_f16(x[i]));
+  }
+}
+
+// O of this lane's row times a (its 256 columns)
+__device__ __noinline__ void rescale_o(uint32_t to, float a) {
+#pragma unroll 1
+  for (int c = 0; c < 256; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(to + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+    tmem_st32(to + c, o);
+  }
+  tmem_wait_st();
+}
+// partial of this lane's row: columns 128 hh .. and 256 + 128 hh ..
+__device__ __noinline__ void store_part(const DecodeFp4Params& p, uint32_t to, int64_t slot_row, int hh, float inv, bool live) {
+#pragma unroll 1
+  for (int c = 0; c < 256; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(to + c, o);
+    tmem_wait_ld();
+    float* dst = p.part_o + slot_row * kLatent + (c < 128 ? 0 : 128) + 128 * hh + c;
+    if (live && guard_span(p.err, G_PART_O, dst, 128, p.part_o, p.part_o_bytes))
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        *reinterpret_cast<float4*>(dst + i) = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
+                                                          __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+  }
+}
+
+template <bool kUp>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_fp4_kernel(const __grid_constant__ DecodeFp4Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + kOffBars);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t cta = cluster_ctarank();
+  const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * kFp4Row;
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(&bars.kfull[i], 6), mbar_init(&bars.kempty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.vfull[i], 8), mbar_init(&bars.vempty[i], 1);
+      mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 8);
+      mbar_init(&bars.pair[i], 2), mbar_init(&bars.drain[i], 1);
+    }
+    mbar_init(&bars.qfull, 2 * (kConverters + 1)), mbar_init(&bars.qempty, 1);
+    mbar_init(&bars.pfull, 8), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 8);
+    for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], kConverters);
+    mbar_init(&bars.stall, 1);
+    bars.abort = 0;
+    if (smem_u32(smem) & 1023u) bars.abort = DEV_TIMEOUT_BASE | D_ALIGN, record_error(p.err, bars.abort);
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bars.tmem_base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  find_share(p, bars, reinterpret_cast<int64_t*>(smem + kOffRows));    // no row is there yet
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tbase = bars.tmem_base;
+  const TileWaits wait{&bars.abort, p.err, p.spin_limit};
+  int32_t* row_slots = reinterpret_cast<int32_t*>(smem + kOffRows);
+  Shares shares(p, bars);
+  Part it;
+  uint32_t u = 0, n = 0;                              // tiles and parts gone through
+  bool live = bars.abort == 0;
+
+  if (warp < 4) {
+    // ---------------- rows ----------------
+    const int hh = warp >> 1, r = (warp & 1) * 32 + lane;            // key half, row of this CTA
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const float c = p.scale * 1.4426950408889634f, c2 = c == 0.f ? 1e-30f : c;    // see mask_piece
+    const uint64_t c22 = f32x2(c2, c2);
+    float* tile_max = reinterpret_cast<float*>(smem + kOffMax);
+    const uint32_t r_sfree[2] = {map_to_rank(smem_u32(&bars.sfree[0]), 0), map_to_rank(smem_u32(&bars.sfree[1]), 0)};
+    const uint32_t r_pfull = map_to_rank(smem_u32(&bars.pfull), 0), r_ofree = map_to_rank(smem_u32(&bars.ofree), 0);
+    const uint32_t prow = smem_u32(smem + kOffP + hh * kBox);
+    uint32_t pairs = 0;                               // exchanges with the other half's warp
+    auto exchange = [&](float mine, float& other) -> bool {
+      float* x = tile_max + (pairs & 1) * 128;
+      x[hh * 64 + r] = mine;
+      warp_arrive(&bars.pair[warp & 1]);
+      if (!wait.warp(&bars.pair[warp & 1], pairs & 1, D_PAIR)) return false;
+      other = x[(hh ^ 1) * 64 + r];
+      ++pairs;
+      return true;
+    };
+    for (; live && shares.next(it); ++n) {
+      const int row = (int)cta * kHalf + r;            // of the group
+      const int seen = row < it.g.rows ? max(0, it.g.len - p.s + 1 + (it.g.row0 + row) / p.H) : 0;
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int t = it.t0; t < it.t1; ++t, ++u) {
+        const int buf = u & 1, visible = seen - t * kTile - hh * kHalf;
+        if (!wait.warp(&bars.sfull[buf], (u >> 1) & 1, D_SFULL, true)) { live = false; break; }
+        tc_fence_after();
+        uint32_t s0[32], s1[32];
+        tmem_ld32(tbase + lanes + kTmemS + buf * 64, s0);
+        tmem_ld32(tbase + lanes + kTmemS + buf * 64 + 32, s1);
+        tmem_wait_ld();
+        tc_fence_before();
+        warp_arrive_remote(r_sfree[buf]);
+        mask_piece<kUp>(s0, visible);
+        mask_piece<kUp>(s1, visible - 32);
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = kUp ? -CUDART_INF_F : CUDART_INF_F;
+        row_extreme<kUp>(s0, e);
+        row_extreme<kUp>(s1, e);
+        float mt = visible > 0 ? extreme4<kUp>(e) * c2 : -CUDART_INF_F, other;
+        if (!exchange(mt, other)) { live = false; break; }
+        mt = fmaxf(mt, other);
+        float a = 1.f;
+        if (mt > m + kRescale || m == -CUDART_INF_F) {
+          a = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mt);
+          m = mt;
+        }
+        l *= a;
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        const uint64_t nref = f32x2(-ref, -ref);
+        uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+        // packed in place: words 0 .. 15 of either piece hold its P
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float x0, x1;
+          f32x2_split(fma_f32x2(f32x2(__uint_as_float(s0[i]), __uint_as_float(s0[i + 1])), c22, nref), x0, x1);
+          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+          sum[0] = add_f32x2(sum[0], f32x2(x0, x1));
+          s0[i / 2] = pack_f16x2(x0, x1);
+          f32x2_split(fma_f32x2(f32x2(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])), c22, nref), x0, x1);
+          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+          sum[1] = add_f32x2(sum[1], f32x2(x0, x1));
+          s1[i / 2] = pack_f16x2(x0, x1);
+        }
+        float l0, l1;
+        f32x2_split(add_f32x2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
+        // the last tile's P V is done: P may be written over, O be scaled
+        if (u > 0 && !wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE, true)) { live = false; break; }
+        if (t > it.t0 && __any_sync(~0u, a != 1.f)) {
+          tc_fence_after();
+          rescale_o(tbase + lanes + kTmemO, a);
+          tc_fence_before();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          st_shared16(box_unit(prow, r, i), make_uint4(s0[4 * i], s0[4 * i + 1], s0[4 * i + 2], s0[4 * i + 3]));
+          st_shared16(box_unit(prow, r, 4 + i), make_uint4(s1[4 * i], s1[4 * i + 1], s1[4 * i + 2], s1[4 * i + 3]));
+        }
+        fence_proxy_async_smem();
+        warp_arrive_remote(r_pfull);
+      }
+      if (!live) break;
+      float l_other;
+      if (!exchange(l, l_other)) break;
+      l = hh ? l_other + l : l + l_other;              // the same order in both halves
+      if (!wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE, true)) break;
+      tc_fence_after();
+      const int64_t slot_row = (it.id + blockIdx.x / 2) * p.part_rows + row;
+      const bool mine = row < it.g.rows;
+      store_part(p, tbase + lanes + kTmemO, slot_row, hh, l == 0.f ? 0.f : 1.f / l, mine);
+      if (mine && hh == 0 && guard_span(p.err, G_PART_LSE, p.part_lse + slot_row, 4, p.part_lse, p.part_lse_bytes))
+        p.part_lse[slot_row] = l == 0.f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.f : m) * 0.6931471805599453f + logf(l);
+      tc_fence_before();
+      warp_arrive_remote(r_ofree);
+    }
+  } else if (warp == 4) {
+    // ---------------- scores ----------------
+    if (cta == 0) {
+      if (p.debug_stall) live = live && wait.warp(&bars.stall, 0, D_STALL);
+      const uint64_t qdesc = sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024), kdesc = sdesc_sw128(smem_u32(smem + kOffK), 16, 1024);
+      const uint32_t id = idesc_f16_f32(kRows, kTile, false, false), id_pe = idesc_bf16_f32(kRows, kTile, false, false);
+      for (; live && shares.next(it); ++n) {
+        if (!wait.warp(&bars.qfull, n & 1, D_QFULL, true)) break;
+        for (int t = it.t0; t < it.t1; ++t, ++u) {
+          const int buf = u & 1;
+          if (!wait.warp(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, D_SFREE, true)) { live = false; break; }
+#pragma unroll 1
+          for (int g = 0; g < 3; ++g) {
+            if (!wait.warp(&bars.kfull[g], u & 1, D_KFULL, true)) { live = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              mma2_scores(tbase + kTmemS + buf * 64, qdesc + g * (3 * kBox / 16), kdesc + g * (3 * kBox / 16), id, g == 2 ? id_pe : id, g > 0 ? 1u : 0u);
+              commit2(&bars.kempty[g]);
+              if (g == 2) commit2(&bars.sfull[buf]);
+              if (g == 2 && t == it.t1 - 1) commit2(&bars.qempty);
+            }
+            __syncwarp();
+          }
+          if (!live) break;
+        }
+      }
+      if (elect_one()) commit2(&bars.drain[0]);       // what was issued is done before anything is given back
+      mbar_drain(&bars.drain[0], 0);
+      __syncwarp();
+    }
+  } else if (warp == 5) {
+    // ---------------- values ----------------
+    if (cta == 0) {
+      const uint32_t pst = smem_u32(smem + kOffP), vst = smem_u32(smem + kOffV);
+      const uint32_t id = idesc_f16_f32(kRows, 256, false, true);
+      for (; live && shares.next(it); ++n) {
+        if (n > 0 && !wait.warp(&bars.ofree, (n - 1) & 1, D_OFREE, true)) break;
+        for (int t = it.t0; t < it.t1; ++t, ++u) {
+          if (!wait.warp(&bars.pfull, u & 1, D_PFULL, true)) { live = false; break; }
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (!wait.warp(&bars.vfull[h], u & 1, D_VFULL, true)) { live = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              mma2_values(tbase + kTmemO, tbase + kTmemO + 128, sdesc_sw128(pst + h * kBox, 16, 1024), sdesc_sw128(vst + h * 4 * kBox, kBox, 1024),
+                          sdesc_sw128(vst + h * 4 * kBox + 2 * kBox, kBox, 1024), id, t > it.t0 || h > 0 ? 1u : 0u);
+              commit2(&bars.vempty[h]);
+              if (h == 1) commit2(&bars.pvdone);
+            }
+            __syncwarp();
+          }
+          if (!live) break;
+        }
+      }
+      if (elect_one()) commit2(&bars.drain[1]);
+      mbar_drain(&bars.drain[1], 0);
+      __syncwarp();
+    }
+  } else if (warp < kRowWarp) {
+    // ---------------- 4-bit rows into f16 ----------------
+    const int w = warp - kFirstConverter, group = w / 3, h = w >> 2, vb = w & 3;
+    const int kcol = 64 * w, vcol = (vb < 2 ? 0 : 256) + 128 * (int)cta + 64 * (vb & 1);
+    const uint32_t kbox = smem_u32(smem + kOffK + w * kBox), vbox = smem_u32(smem + kOffV + (h * 4 + vb) * kBox);
+    const uint32_t r_kfull = map_to_rank(smem_u32(&bars.kfull[group]), 0), r_vfull = map_to_rank(smem_u32(&bars.vfull[h]), 0);
+    const uint32_t r_qfull = map_to_rank(smem_u32(&bars.qfull), 0);
+    uint32_t loaded = 0;                              // tiles whose loads are out
+    Raw ka, va, kb, vb2;
+    // one tile: the next one's loads go out, then this one's are converted
+    auto rows_of = [&](uint32_t tile) -> const int32_t* { return row_slots + (tile % kRowSlots) * kTile; };
+    auto load_k = [&](Raw& x) -> bool {
+      if (!wait.warp(&bars.rfull[loaded % kRowSlots], (loaded / kRowSlots) & 1, D_RFULL)) return false;
+      load_raw(p, x, rows_of(loaded) + cta * kHalf, kcol, lane, cache_bytes);
+      return true;
+    };
+    auto load_v = [&](Raw& x) {
+      load_raw(p, x, rows_of(loaded) + h * kHalf, vcol, lane, cache_bytes);
+      warp_arrive(&bars.rfree[loaded % kRowSlots]);
+      ++loaded;
+    };
+    auto step = [&](Raw& k, Raw& v, Raw& k_next, Raw& v_next, bool more) -> bool {
+      if (more && !load_k(k_next)) return false;
+      if (!wait.warp(&bars.kempty[group], (u & 1) ^ 1, D_KEMPTY, true)) return false;
+      convert_raw(k, kbox, lane);
+      fence_proxy_async_smem();
+      warp_arrive_remote(r_kfull);
+      if (more) load_v(v_next);
+      if (!wait.warp(&bars.vempty[h], (u & 1) ^ 1, D_VEMPTY, true)) return false;
+      convert_raw(v, vbox, lane);
+      fence_proxy_async_smem();
+      warp_arrive_remote(r_vfull);
+      ++u;
+      return true;
+    };
+    for (; live && shares.next(it); ++n) {
+      if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY, true)) break;
+      load_query_box(p, it.g, (int)cta * kHalf, smem_u32(smem + kOffQ + w * kBox), w, lane);
+      fence_proxy_async_smem();
+      warp_arrive_remote(r_qfull);
+      if (!load_k(ka)) break;
+      load_v(va);
+      for (int t = it.t0; t < it.t1 && live; t += 2) {
+        live = step(ka, va, kb, vb2, t + 1 < it.t1);
+        if (live && t + 1 < it.t1) live = step(kb, vb2, ka, va, t + 2 < it.t1);
+      }
+    }
+  } else {
+    // ---------------- rows through the block table; RoPE columns ----------------
+    const uint32_t r_kfull = map_to_rank(smem_u32(&bars.kfull[2]), 0), r_qfull = map_to_rank(smem_u32(&bars.qfull), 0);
+    const uint32_t box = smem_u32(smem + kOffK + 8 * kBox);
+    const int unit = lane & 7;
+    uint32_t ahead = 0;                               // tiles whose rows are down
+    auto rows_down = [&](int t) -> bool {
+      int32_t at[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = t * kTile + 32 * i + lane;
+        at[i] = -1;
+        if (j < it.g.keys) {
+          const int pg = j / p.kv.page_size;
+          const int page = guarded_int(p.err, p.kv.block_table, (int64_t)it.g.b * p.kv.max_pages + pg, (int64_t)p.kv.B * p.kv.max_pages);
+          if (page >= 0 && page < p.kv.num_pages) at[i] = page * p.kv.page_size + (j - pg * p.kv.page_size);
+          else record_error(p.err, DEV_RANGE_BASE | Y_PAGE);
+        }
+      }
+      const uint32_t slot = ahead % kRowSlots;
+      if (!wait.warp(&bars.rfree[slot], ((ahead / kRowSlots) & 1) ^ 1, D_RFREE)) return false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row_slots[slot * kTile + 32 * i + lane] = at[i];
+      warp_arrive(&bars.rfull[slot]);
+      ++ahead;
+      return true;
+    };
+    uint4 x[16];
+    // the tile whose rows were put down last: this CTA's 64 keys
+    auto load_pe = [&]() {
+      const int32_t* at = row_slots + ((ahead - 1) % kRowSlots) * kTile + cta * kHalf + (lane >> 3);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int a = at[4 * i];
+        const uint8_t* src = p.kv.cache + (int64_t)a * kFp4Row + kFp4Pe + 16 * unit;
+        x[i] = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    for (; live && shares.next(it); ++n) {
+      if (!rows_down(it.t0)) break;
+      load_pe();
+      if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY, true)) break;
+      load_query_box(p, it.g, (int)cta * kHalf, smem_u32(smem + kOffQ + 8 * kBox), 8, lane);
+      fence_proxy_async_smem();
+      warp_arrive_remote(r_qfull);
+      for (int t = it.t0; t < it.t1; ++t, ++u) {
+        if (t + 1 < it.t1 && !rows_down(t + 1)) { live = false; break; }
+        if (!wait.warp(&bars.kempty[2], (u & 1) ^ 1, D_KEMPTY, true)) { live = false; break; }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st_shared16(box_unit(box, (lane >> 3) + 4 * i, unit), x[i]);
+        fence_proxy_async_smem();
+        warp_arrive_remote(r_kfull);
+        if (t + 1 < it.t1) load_pe();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                     // no MMA of the pair is left, no arrival on its way
+  if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tbase) : "memory");
+}
+
+// A warp a row: the partials of the pairs that had tiles of its group, by their log-sum-exp, and the sink.
+__global__ void __launch_bounds__(256) decode_fp4_reduce_kernel(const __grid_constant__ DecodeFp4Params p, int pairs) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)p.kv.B * p.s * p.H, item = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  if (item >= rows) return;
+  const int64_t b = item / (p.s * p.H);
+  const int row = (int)(item - b * (p.s * p.H));
+  const int64_t g = b * p.row_tiles + row / kRows;
+  auto before = [&](int64_t i) -> int64_t {
+    return guard_span(p.err, G_TILE_PREFIX, p.before + i, 8, p.before, (uint64_t)(p.groups + 1) * 8) ? p.before[i] : 0;
+  };
+  const int64_t total = before(p.groups), t0 = before(g), t1 = before(g + 1);
+  const float sink = p.sinks && guard_span(p.err, G_SINKS, p.sinks + row % p.H, 4, p.sinks, (uint64_t)p.H * 4) ? p.sinks[row % p.H] : -CUDART_INF_F;
+  // pairs whose share meets tiles t0 .. t1 - 1; those in between have one
+  const int64_t p0 = t1 > t0 ? ((t0 + 1) * pairs - 1) / total : 0, p1 = t1 > t0 ? (t1 * pairs - 1) / total : -1;
+  auto lse_of = [&](int64_t q) -> float {
+    if (total * q / pairs >= total * (q + 1) / pairs) return -CUDART_INF_F;      // an empty share
+    const float* s = p.part_lse + (g + q) * p.part_rows + (row & (kRows - 1));
+    return guard_span(p.err, G_PART_LSE, s, 4, p.part_lse, p.part_lse_bytes) ? *s : -CUDART_INF_F;
+  };
+  float m = sink;
+  bool nan = false;
+  for (int64_t q = p0; q <= p1; ++q) {
+    const float l = lse_of(q);
+    nan |= l != l;
+    m = fmaxf(m, l);
+  }
+  float wsum = sink == -CUDART_INF_F ? 0.f : expf(sink - m), acc[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int64_t q = p0; q <= p1; ++q) {
+    const float l = lse_of(q);
+    if (l == -CUDART_INF_F) continue;
+    const float* src = p.part_o + ((g + q) * p.part_rows + (row & (kRows - 1))) * kLatent;
+    if (!guard_span(p.err, G_PART_O, src, kLatent * 4, p.part_o, p.part_o_bytes)) continue;
+    const float w = expf(l - m);
+    wsum += w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = reinterpret_cast<const float4*>(src)[lane + 32 * k];
+      acc[4 * k] += w * v.x, acc[4 * k + 1] += w * v.y, acc[4 * k + 2] += w * v.z, acc[4 * k + 3] += w * v.w;
+    }
+  }
+  const float inv = nan ? CUDART_NAN_F : wsum > 0.f ? p.kv_scale / wsum : 0.f;
+  __nv_bfloat16* out = p.out + item * kLatent;
+  if (guard_span(p.err, G_OUT, out, kLatent * 2, p.out, (uint64_t)rows * kLatent * 2))
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      reinterpret_cast<uint2*>(out)[lane + 32 * k] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv), pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+  if (lane == 0 && p.lse && guard_span(p.err, G_LSE, p.lse + item, 4, p.lse, (uint64_t)rows * 4))
+    p.lse[item] = nan ? CUDART_NAN_F : wsum > 0.f ? m + logf(wsum) : -CUDART_INF_F;
+}
+
+}  // namespace
+
+DecodeFp4Scratch decode_fp4_scratch(int B, int s, int H, int num_splits) {
+  DecodeFp4Scratch r;
+  const int sms = device_sm_count();
+  r.pairs = num_splits > 0 ? num_splits : sms / 2 > 1 ? sms / 2 : 1;
+  const int64_t rows = (int64_t)s * H;
+  r.row_tiles = (int)((rows + kRows - 1) / kRows);
+  r.part_rows = rows < kRows ? (int)rows : kRows;
+  r.groups = (int64_t)B * r.row_tiles;
+  const size_t slots = (size_t)(r.groups + r.pairs) * r.part_rows;
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  r.before = up((size_t)(r.groups + 1) * 8);
+  r.part_lse = up(slots * 4);
+  r.part_o = up(slots * kLatent * 4);
+  return r;
+}
+
+cudaError_t launch_decode_fp4(const DecodeFp4Params& p, int pairs, cudaStream_t stream) {
+  static PerDeviceOnce attrs;
+  cudaError_t e = attrs.run([] {
+    cudaError_t r = cudaFuncSetAttribute((const void*)decode_fp4_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return r == cudaSuccess ? cudaFuncSetAttribute((const void*)decode_fp4_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) : r;
+  });
+  if (e != cudaSuccess) return e;
+  if (p.scale >= 0.f) decode_fp4_kernel<true><<<2 * pairs, kThreads, kSmem, stream>>>(p);
+  else decode_fp4_kernel<false><<<2 * pairs, kThreads, kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  decode_fp4_reduce_kernel<<<(unsigned)(((int64_t)p.kv.B * p.s * p.H + 7) / 8), 256, 0, stream>>>(p, pairs);
+  return cudaGetLastError();
+}
+
+}  // namespace mla
