@@ -39,15 +39,14 @@ struct DecodeFp4Params {
   int s, H;
   int row_tiles;                 // groups of up to 128 query rows a request has
   int part_rows;                 // rows of a partial
-  int64_t groups;
+  int groups;
   int64_t* before;               // ws: [groups + 1] tiles before each group
   float* part_lse;               // ws: [groups + pairs, part_rows]
   float* part_o;                 // ws: [groups + pairs, part_rows, 512]
   uint64_t part_lse_bytes, part_o_bytes;
 };
 struct DecodeFp4Scratch {
-  int pairs, row_tiles, part_rows;
-  int64_t groups;
+  int pairs, row_tiles, part_rows, groups;
   size_t before, part_lse, part_o;     // bytes
 };
 DecodeFp4Scratch decode_fp4_scratch(int B, int s, int H, int num_splits);

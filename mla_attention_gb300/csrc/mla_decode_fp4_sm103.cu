@@ -9,13 +9,14 @@
 // 64 c .. 64 c + 63 for the scores and the latent columns 128 c .. and 256 + 128 c .. of all its keys for the values.
 //
 // A code times its scale has at most six bits and is exact in f16; q and P are f16 too (P a weight of at most 2^8), the RoPE
-// columns stay bf16 as their MMA's operands, sums are fp32.  15 warps a CTA:
+// columns stay bf16 as their MMA's operands, sums are fp32.  24 warps a CTA:
 //   0-3   rows: lanes L and L + 64 of tensor memory hold the same row's scores of 64 keys each; maximum through shared
 //         memory, lazy rescale of O (by more than 2^8), exponentials, P
-//   4, 5  MMAs, in the first CTA alone (one lane issues for both): scores; values
-//   6-13  4-bit rows into f16: K column box w and V (key half w / 4, column box w % 4); the loads of a tile go out before
-//         the last one's are converted
-//   14    the tiles' rows through the block table, and the RoPE columns
+//   4, 5  first CTA: MMAs (one lane issues for both CTAs), scores and values; second CTA: its warps' arrivals passed on.  An
+//         arrival in another CTA waits for all of the thread's loads on their way: 1900 cycles under the next tile's
+//   6, 7  the RoPE columns, 32 keys each; warp 6 also the tiles' rows through the block table
+//   8-23  4-bit rows into f16: column box w of K; column box w % 4 of key half w / 4 of V.  The loads of a tile go out before the
+//         last one's are converted.  Latency bounds them: with 8 warps that do both a tile took 9200 cycles
 // The tiles of all requests are dealt to the pairs in equal shares; fp32 partials of a request that several pairs share
 // are merged by decode_fp4_reduce_kernel.
 #include <math_constants.h>
@@ -28,7 +29,7 @@ namespace mla {
 namespace {
 
 constexpr int kTile = 128, kHalf = 64;                // keys a tile, and the part that one CTA brings for the scores
-constexpr int kThreads = 480, kConverters = 8, kFirstConverter = 6, kRowWarp = 14;
+constexpr int kThreads = 768, kFirstK = 8, kFirstV = 16;
 constexpr int kBox = 64 * 128;                        // 64 rows of 128 bytes
 constexpr int kRowSlots = 3;
 constexpr uint32_t kTmemO = 0, kTmemS = 256;          // O: 256 columns; S: two buffers of 64
@@ -43,7 +44,7 @@ constexpr int kOffMax = kOffRows + kRowSlots * kTile * 4;   // [2][2][64]
 constexpr int kOffBars = kOffMax + 4 * 64 * 4;
 
 struct Bars {
-  // in the first CTA, with arrivals from both
+  // in each CTA, with arrivals of its own warps; in the first also the second's as one
   uint64_t kfull[3], vfull[2], qfull, pfull, sfree[2], ofree;
   // in each CTA, by commits to both
   uint64_t kempty[3], vempty[2], qempty, sfull[2], pvdone;
@@ -52,8 +53,8 @@ struct Bars {
   uint64_t pair[2];                                   // warps w and w + 2
   uint64_t drain[2], stall;
   uint32_t tmem_base, abort;
-  int64_t share, start_t;
-  int32_t start_g;
+  int64_t share;
+  int32_t start_g, start_t;
 };
 constexpr int kSmem = kOffBars + 512;
 static_assert(sizeof(Bars) <= 512, "barrier block too large");
@@ -68,35 +69,35 @@ struct Group {
   int len;                 // keys of the request
   int keys;                // keys that its last token sees
 };
-__device__ __forceinline__ Group group_of(const DecodeFp4Params& p, int64_t g, bool report) {
+__device__ __forceinline__ Group group_of(const DecodeFp4Params& p, int g, bool report) {
   Group r;
-  r.b = (int)(g / p.row_tiles);
-  r.row0 = (int)(g - (int64_t)r.b * p.row_tiles) * kRows;
+  r.b = p.row_tiles == 1 ? g : g / p.row_tiles;
+  r.row0 = (g - r.b * p.row_tiles) * kRows;
   r.rows = min(p.s * p.H - r.row0, kRows);
   r.len = paged_len(p.kv, p.err, r.b, (int64_t)p.kv.max_pages * p.kv.page_size, report);
-  r.keys = max(0, r.len - p.s + 1 + (r.row0 + r.rows - 1) / p.H);
+  r.keys = p.s == 1 ? r.len : max(0, r.len - p.s + 1 + (r.row0 + r.rows - 1) / p.H);
   return r;
 }
 
 // A pair's part of one group: tiles t0 .. t1 - 1.
 struct Part {
   Group g;
-  int64_t id;
-  int t0, t1;
+  int id, t0, t1;
 };
 struct Shares {
   const DecodeFp4Params* p;
-  int64_t g, t, left;
+  int g, t;
+  int64_t left;
   __device__ Shares(const DecodeFp4Params& prm, const Bars& bars) : p(&prm), g(bars.start_g), t(bars.start_t), left(bars.share) {}
   __device__ __noinline__ bool next(Part& it) {
     while (left > 0 && g < p->groups) {
       it.g = group_of(*p, g, false);
-      const int64_t n = (it.g.keys + kTile - 1) / kTile - t;
+      const int n = (it.g.keys + kTile - 1) / kTile - t;
       if (n <= 0) {
         ++g, t = 0;
         continue;
       }
-      it.id = g, it.t0 = (int)t, it.t1 = (int)(t + min(n, left));
+      it.id = g, it.t0 = t, it.t1 = (int)(t + min((int64_t)n, left));
       left -= it.t1 - it.t0, t = it.t1;
       return true;
     }
@@ -107,9 +108,9 @@ struct Shares {
 // Where this pair's share starts, and (first CTA of all) the tiles before each group; by all threads.
 __device__ __noinline__ void find_share(const DecodeFp4Params& p, Bars& bars, int64_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t per = (p.groups + kThreads - 1) / kThreads, g0 = min(tid * per, p.groups), g1 = min(g0 + per, p.groups);
+  const int per = (p.groups + kThreads - 1) / kThreads, g0 = min(tid * per, p.groups), g1 = min(g0 + per, p.groups);
   int64_t mine = 0;
-  for (int64_t g = g0; g < g1; ++g) mine += (group_of(p, g, blockIdx.x == 0).keys + kTile - 1) / kTile;
+  for (int g = g0; g < g1; ++g) mine += (group_of(p, g, blockIdx.x == 0).keys + kTile - 1) / kTile;
   int64_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -123,7 +124,9 @@ __device__ __noinline__ void find_share(const DecodeFp4Params& p, Bars& bars, in
     if (w < warp) at += sums[w];
     total += sums[w];
   }
-  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2, lo = total * pair / pairs, hi = total * (pair + 1) / pairs;
+  // no more shares than tiles: none is empty but those of the pairs behind them
+  const int64_t pair = blockIdx.x / 2, pairs = max((int64_t)1, min((int64_t)(gridDim.x / 2), total));
+  const int64_t lo = pair < pairs ? total * pair / pairs : total, hi = pair < pairs ? total * (pair + 1) / pairs : total;
   if (tid == 0) bars.share = hi - lo;
   const bool tell = blockIdx.x == 0, here = lo < hi && at <= lo && lo < at + mine;
   auto put = [&](int64_t g, int64_t v) {
@@ -131,10 +134,10 @@ __device__ __noinline__ void find_share(const DecodeFp4Params& p, Bars& bars, in
   };
   if (tell && tid == 0) put(p.groups, total);
   if (tell || here) {
-    for (int64_t g = g0; g < g1; ++g) {
+    for (int g = g0; g < g1; ++g) {
       const int n = (group_of(p, g, false).keys + kTile - 1) / kTile;
       if (tell) put(g, at);
-      if (lo < hi && at <= lo && lo < at + n) bars.start_g = (int)g, bars.start_t = lo - at;
+      if (lo < hi && at <= lo && lo < at + n) bars.start_g = g, bars.start_t = (int)(lo - at);
       at += n;
     }
   }
@@ -215,22 +218,27 @@ __device__ __forceinline__ void convert_raw(const Raw& x, uint32_t box, int lane
     st_shared16(box_unit(box, r, 4 * half + 3), fp4x8_to_f16(x.v[i].w, s.y));
   }
 }
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 // box k of this CTA's 64 query rows (in f16 but for the RoPE columns); rows behind the group's are zeros
 __device__ __noinline__ void load_query_box(const DecodeFp4Params& p, const Group& g, int first, uint32_t box, int k, int lane) {
   const uint64_t q_bytes = (uint64_t)p.kv.B * p.s * p.H * kDk * 2;
   const int unit = lane & 7;
-#pragma unroll 1
-  for (int r0 = lane >> 3; r0 < kHalf; r0 += 32) {
-    uint4 x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = first + r0 + 4 * i;
-      const __nv_bfloat16* src = p.q + ((int64_t)g.b * p.s * p.H + g.row0 + r) * kDk + 64 * k + 8 * unit;
-      x[i] = r < g.rows && guard_span(p.err, G_Q, src, 16, p.q, q_bytes) ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) st_shared16(box_unit(box, r0 + 4 * i, unit), k == 8 ? x[i] : bf16x8_to_f16(x[i]));
+  const __nv_bfloat16* q = p.q + ((int64_t)g.b * p.s * p.H + g.row0 + first) * kDk + 64 * k + 8 * unit;
+#pragma unroll 4
+  for (int r = lane >> 3; r < kHalf; r += 4) {
+    const __nv_bfloat16* src = q + (int64_t)r * kDk;
+    const bool in = first + r < g.rows && guard_span(p.err, G_Q, src, 16, p.q, q_bytes);
+    cp_async16_zfill(box_unit(box, r, unit), in ? src : p.q, in ? 16u : 0u);
   }
+  cp_async_wait_all();
+  if (k < 8)                                          // each lane puts its own copies into f16 where they lie
+#pragma unroll 4
+    for (int r = lane >> 3; r < kHalf; r += 4) st_shared16(box_unit(box, r, unit), bf16x8_to_f16(ld_shared16(box_unit(box, r, unit))));
+  fence_proxy_async_smem();
 }
 
 // O of this lane's row times a (its 256 columns)
@@ -246,19 +254,27 @@ __device__ __noinline__ void rescale_o(uint32_t to, float a) {
   }
   tmem_wait_st();
 }
-// partial of this lane's row: columns 128 hh .. and 256 + 128 hh ..
-__device__ __noinline__ void store_part(const DecodeFp4Params& p, uint32_t to, int64_t slot_row, int hh, float inv, bool live) {
+// Partials of this warp's 32 rows: columns 128 hh .. and 256 + 128 hh .., 32 at a time through 4 KB of shared memory so that a
+// store brings whole lines.
+__device__ __noinline__ void store_part(const DecodeFp4Params& p, uint32_t to, int64_t slot_row0, int rows, int hh, float inv, uint32_t stage, int lane) {
 #pragma unroll 1
   for (int c = 0; c < 256; c += 32) {
     uint32_t o[32];
     tmem_ld32(to + c, o);
     tmem_wait_ld();
-    float* dst = p.part_o + slot_row * kLatent + (c < 128 ? 0 : 128) + 128 * hh + c;
-    if (live && guard_span(p.err, G_PART_O, dst, 128, p.part_o, p.part_o_bytes))
 #pragma unroll
-      for (int i = 0; i < 32; i += 4)
-        *reinterpret_cast<float4*>(dst + i) = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                                          __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+    for (int i = 0; i < 8; ++i)
+      st_shared16(box_unit(stage, lane, i), make_uint4(__float_as_uint(__uint_as_float(o[4 * i]) * inv), __float_as_uint(__uint_as_float(o[4 * i + 1]) * inv),
+                                                       __float_as_uint(__uint_as_float(o[4 * i + 2]) * inv), __float_as_uint(__uint_as_float(o[4 * i + 3]) * inv)));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      float* dst = p.part_o + (slot_row0 + r) * kLatent + (c < 128 ? 0 : 128) + 128 * hh + c + 4 * (lane & 7);
+      const uint4 v = ld_shared16(box_unit(stage, r, lane & 7));
+      if (r < rows && guard_span(p.err, G_PART_O, dst, 16, p.part_o, p.part_o_bytes)) *reinterpret_cast<uint4*>(dst) = v;
+    }
+    __syncwarp();
   }
 }
 
@@ -270,15 +286,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   const uint32_t cta = cluster_ctarank();
   const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * kFp4Row;
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(&bars.kfull[i], 6), mbar_init(&bars.kempty[i], 1);
+    const uint32_t more = cta == 0 ? 1 : 0;           // the second CTA's
+    for (int i = 0; i < 3; ++i) mbar_init(&bars.kfull[i], (i < 2 ? 3 : 4) + more), mbar_init(&bars.kempty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.vfull[i], 8), mbar_init(&bars.vempty[i], 1);
-      mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 8);
+      mbar_init(&bars.vfull[i], 4 + more), mbar_init(&bars.vempty[i], 1);
+      mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 4 + more);
       mbar_init(&bars.pair[i], 2), mbar_init(&bars.drain[i], 1);
     }
-    mbar_init(&bars.qfull, 2 * (kConverters + 1)), mbar_init(&bars.qempty, 1);
-    mbar_init(&bars.pfull, 8), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 8);
-    for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], kConverters);
+    mbar_init(&bars.qfull, 9 + more), mbar_init(&bars.qempty, 1);
+    mbar_init(&bars.pfull, 4 + more), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 4 + more);
+    for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], 18);
     mbar_init(&bars.stall, 1);
     bars.abort = 0;
     if (smem_u32(smem) & 1023u) bars.abort = DEV_TIMEOUT_BASE | D_ALIGN, record_error(p.err, bars.abort);
@@ -308,8 +325,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     const float c = p.scale * 1.4426950408889634f, c2 = c == 0.f ? 1e-30f : c;    // see mask_piece
     const uint64_t c22 = f32x2(c2, c2);
     float* tile_max = reinterpret_cast<float*>(smem + kOffMax);
-    const uint32_t r_sfree[2] = {map_to_rank(smem_u32(&bars.sfree[0]), 0), map_to_rank(smem_u32(&bars.sfree[1]), 0)};
-    const uint32_t r_pfull = map_to_rank(smem_u32(&bars.pfull), 0), r_ofree = map_to_rank(smem_u32(&bars.ofree), 0);
     const uint32_t prow = smem_u32(smem + kOffP + hh * kBox);
     uint32_t pairs = 0;                               // exchanges with the other half's warp
     auto exchange = [&](float mine, float& other) -> bool {
@@ -327,21 +342,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       float m = -CUDART_INF_F, l = 0.f;
       for (int t = it.t0; t < it.t1; ++t, ++u) {
         const int buf = u & 1, visible = seen - t * kTile - hh * kHalf;
-        if (!wait.warp(&bars.sfull[buf], (u >> 1) & 1, D_SFULL, true)) { live = false; break; }
+        if (!wait.warp(&bars.sfull[buf], (u >> 1) & 1, D_SFULL)) { live = false; break; }
         tc_fence_after();
-        uint32_t s0[32], s1[32];
-        tmem_ld32(tbase + lanes + kTmemS + buf * 64, s0);
-        tmem_ld32(tbase + lanes + kTmemS + buf * 64 + 32, s1);
-        tmem_wait_ld();
-        tc_fence_before();
-        warp_arrive_remote(r_sfree[buf]);
-        mask_piece<kUp>(s0, visible);
-        mask_piece<kUp>(s1, visible - 32);
+        const uint32_t from = tbase + lanes + kTmemS + buf * 64;
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = kUp ? -CUDART_INF_F : CUDART_INF_F;
-        row_extreme<kUp>(s0, e);
-        row_extreme<kUp>(s1, e);
+#pragma unroll 1
+        for (int q = 0; q < 64; q += 32) {
+          uint32_t s[32];
+          tmem_ld32(from + q, s);
+          tmem_wait_ld();
+          mask_piece<kUp>(s, visible - q);
+          row_extreme<kUp>(s, e);
+        }
         float mt = visible > 0 ? extreme4<kUp>(e) * c2 : -CUDART_INF_F, other;
         if (!exchange(mt, other)) { live = false; break; }
         mt = fmaxf(mt, other);
@@ -354,50 +368,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const uint64_t nref = f32x2(-ref, -ref);
         uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-        // packed in place: words 0 .. 15 of either piece hold its P
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float x0, x1;
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(s0[i]), __uint_as_float(s0[i + 1])), c22, nref), x0, x1);
-          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
-          sum[0] = add_f32x2(sum[0], f32x2(x0, x1));
-          s0[i / 2] = pack_f16x2(x0, x1);
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])), c22, nref), x0, x1);
-          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
-          sum[1] = add_f32x2(sum[1], f32x2(x0, x1));
-          s1[i / 2] = pack_f16x2(x0, x1);
-        }
-        float l0, l1;
-        f32x2_split(add_f32x2(sum[0], sum[1]), l0, l1);
-        l += l0 + l1;
         // the last tile's P V is done: P may be written over, O be scaled
-        if (u > 0 && !wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE, true)) { live = false; break; }
+        if (u > 0 && !wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) { live = false; break; }
         if (t > it.t0 && __any_sync(~0u, a != 1.f)) {
           tc_fence_after();
           rescale_o(tbase + lanes + kTmemO, a);
-          tc_fence_before();
         }
+#pragma unroll 1
+        for (int q = 0; q < 64; q += 32) {
+          uint32_t s[32];
+          tmem_ld32(from + q, s);
+          tmem_wait_ld();
+          mask_piece<kUp>(s, visible - q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          st_shared16(box_unit(prow, r, i), make_uint4(s0[4 * i], s0[4 * i + 1], s0[4 * i + 2], s0[4 * i + 3]));
-          st_shared16(box_unit(prow, r, 4 + i), make_uint4(s1[4 * i], s1[4 * i + 1], s1[4 * i + 2], s1[4 * i + 3]));
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              float x0, x1;
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i + 2 * v]), __uint_as_float(s[i + 2 * v + 1])), c22, nref), x0, x1);
+              x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+              sum[v & 1] = add_f32x2(sum[v & 1], f32x2(x0, x1));
+              w[v] = pack_f16x2(x0, x1);
+            }
+            st_shared16(box_unit(prow, r, (q + i) / 8), make_uint4(w[0], w[1], w[2], w[3]));
+          }
         }
+        tc_fence_before();
+        warp_arrive(&bars.sfree[buf]);
         fence_proxy_async_smem();
-        warp_arrive_remote(r_pfull);
+        warp_arrive(&bars.pfull);
+        float l0, l1;
+        f32x2_split(add_f32x2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
       }
       if (!live) break;
       float l_other;
       if (!exchange(l, l_other)) break;
       l = hh ? l_other + l : l + l_other;              // the same order in both halves
-      if (!wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE, true)) break;
+      if (!wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) break;
       tc_fence_after();
-      const int64_t slot_row = (it.id + blockIdx.x / 2) * p.part_rows + row;
-      const bool mine = row < it.g.rows;
-      store_part(p, tbase + lanes + kTmemO, slot_row, hh, l == 0.f ? 0.f : 1.f / l, mine);
-      if (mine && hh == 0 && guard_span(p.err, G_PART_LSE, p.part_lse + slot_row, 4, p.part_lse, p.part_lse_bytes))
+      const int64_t slot_row = (int64_t)(it.id + (int)(blockIdx.x / 2)) * p.part_rows + row;
+      // P's place is free until the next tile's, and these warps write that
+      store_part(p, tbase + lanes + kTmemO, slot_row - lane, it.g.rows - (row - lane), hh, l == 0.f ? 0.f : 1.f / l,
+                 smem_u32(smem + kOffP + warp * 4096), lane);
+      if (row < it.g.rows && hh == 0 && guard_span(p.err, G_PART_LSE, p.part_lse + slot_row, 4, p.part_lse, p.part_lse_bytes))
         p.part_lse[slot_row] = l == 0.f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.f : m) * 0.6931471805599453f + logf(l);
       tc_fence_before();
-      warp_arrive_remote(r_ofree);
+      warp_arrive(&bars.ofree);
     }
   } else if (warp == 4) {
     // ---------------- scores ----------------
@@ -428,6 +446,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (elect_one()) commit2(&bars.drain[0]);       // what was issued is done before anything is given back
       mbar_drain(&bars.drain[0], 0);
       __syncwarp();
+    } else {
+      auto pass_on = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+        if (!wait.warp(bar, parity, site)) return false;
+        warp_arrive_remote(map_to_rank(smem_u32(bar), 0));
+        return true;
+      };
+      for (; live && shares.next(it); ++n) {
+        live = pass_on(&bars.qfull, n & 1, D_QFULL);
+        for (int t = it.t0; t < it.t1 && live; ++t, ++u)
+          for (int g = 0; g < 3 && live; ++g) live = pass_on(&bars.kfull[g], u & 1, D_KFULL);
+      }
     }
   } else if (warp == 5) {
     // ---------------- values ----------------
@@ -456,60 +485,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (elect_one()) commit2(&bars.drain[1]);
       mbar_drain(&bars.drain[1], 0);
       __syncwarp();
+    } else {
+      auto pass_on = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+        if (!wait.warp(bar, parity, site)) return false;
+        warp_arrive_remote(map_to_rank(smem_u32(bar), 0));
+        return true;
+      };
+      for (; live && shares.next(it); ++n) {
+        for (int t = it.t0; t < it.t1 && live; ++t, ++u)
+          live = pass_on(&bars.sfree[u & 1], (u >> 1) & 1, D_SFREE) && pass_on(&bars.pfull, u & 1, D_PFULL) &&
+                 pass_on(&bars.vfull[0], u & 1, D_VFULL) && pass_on(&bars.vfull[1], u & 1, D_VFULL);
+        if (live) live = pass_on(&bars.ofree, n & 1, D_OFREE);
+      }
     }
-  } else if (warp < kRowWarp) {
+  } else if (warp >= kFirstK) {
     // ---------------- 4-bit rows into f16 ----------------
-    const int w = warp - kFirstConverter, group = w / 3, h = w >> 2, vb = w & 3;
-    const int kcol = 64 * w, vcol = (vb < 2 ? 0 : 256) + 128 * (int)cta + 64 * (vb & 1);
-    const uint32_t kbox = smem_u32(smem + kOffK + w * kBox), vbox = smem_u32(smem + kOffV + (h * 4 + vb) * kBox);
-    const uint32_t r_kfull = map_to_rank(smem_u32(&bars.kfull[group]), 0), r_vfull = map_to_rank(smem_u32(&bars.vfull[h]), 0);
-    const uint32_t r_qfull = map_to_rank(smem_u32(&bars.qfull), 0);
-    uint32_t loaded = 0;                              // tiles whose loads are out
-    Raw ka, va, kb, vb2;
-    // one tile: the next one's loads go out, then this one's are converted
-    auto rows_of = [&](uint32_t tile) -> const int32_t* { return row_slots + (tile % kRowSlots) * kTile; };
-    auto load_k = [&](Raw& x) -> bool {
-      if (!wait.warp(&bars.rfull[loaded % kRowSlots], (loaded / kRowSlots) & 1, D_RFULL)) return false;
-      load_raw(p, x, rows_of(loaded) + cta * kHalf, kcol, lane, cache_bytes);
+    const bool is_k = warp < kFirstV;
+    const int w = (warp - kFirstK) & 7, part = is_k ? w / 3 : w >> 2, vb = w & 3;
+    const int col = is_k ? 64 * w : (vb < 2 ? 0 : 256) + 128 * (int)cta + 64 * (vb & 1);
+    const int first = is_k ? (int)cta * kHalf : part * kHalf;      // of the tile's keys
+    const uint32_t box = smem_u32(smem + (is_k ? kOffK : kOffV) + w * kBox);
+    uint64_t* const empty = is_k ? &bars.kempty[part] : &bars.vempty[part];
+    uint64_t* const full = is_k ? &bars.kfull[part] : &bars.vfull[part];
+    uint32_t slot = 0, turn = 0;                      // of the next tile's rows
+    Raw xa, xb;
+    auto load = [&](Raw& x) -> bool {
+      if (!wait.warp(&bars.rfull[slot], turn, D_RFULL)) return false;
+      load_raw(p, x, row_slots + slot * kTile + first, col, lane, cache_bytes);
+      warp_arrive(&bars.rfree[slot]);
+      if (++slot == kRowSlots) slot = 0, turn ^= 1;
       return true;
     };
-    auto load_v = [&](Raw& x) {
-      load_raw(p, x, rows_of(loaded) + h * kHalf, vcol, lane, cache_bytes);
-      warp_arrive(&bars.rfree[loaded % kRowSlots]);
-      ++loaded;
-    };
-    auto step = [&](Raw& k, Raw& v, Raw& k_next, Raw& v_next, bool more) -> bool {
-      if (more && !load_k(k_next)) return false;
-      if (!wait.warp(&bars.kempty[group], (u & 1) ^ 1, D_KEMPTY, true)) return false;
-      convert_raw(k, kbox, lane);
+    // the next tile's loads go out, then this one's are converted
+    auto step = [&](const Raw& x, Raw& next, bool more) -> bool {
+      if (more && !load(next)) return false;
+      if (!wait.warp(empty, (u & 1) ^ 1, D_KEMPTY)) return false;
+      convert_raw(x, box, lane);
       fence_proxy_async_smem();
-      warp_arrive_remote(r_kfull);
-      if (more) load_v(v_next);
-      if (!wait.warp(&bars.vempty[h], (u & 1) ^ 1, D_VEMPTY, true)) return false;
-      convert_raw(v, vbox, lane);
-      fence_proxy_async_smem();
-      warp_arrive_remote(r_vfull);
+      warp_arrive(full);
       ++u;
       return true;
     };
     for (; live && shares.next(it); ++n) {
-      if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY, true)) break;
-      load_query_box(p, it.g, (int)cta * kHalf, smem_u32(smem + kOffQ + w * kBox), w, lane);
-      fence_proxy_async_smem();
-      warp_arrive_remote(r_qfull);
-      if (!load_k(ka)) break;
-      load_v(va);
+      if (!load(xa)) break;
+      if (is_k) {
+        if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY)) break;
+        load_query_box(p, it.g, (int)cta * kHalf, smem_u32(smem + kOffQ + w * kBox), w, lane);
+        warp_arrive(&bars.qfull);
+      }
       for (int t = it.t0; t < it.t1 && live; t += 2) {
-        live = step(ka, va, kb, vb2, t + 1 < it.t1);
-        if (live && t + 1 < it.t1) live = step(kb, vb2, ka, va, t + 2 < it.t1);
+        live = step(xa, xb, t + 1 < it.t1);
+        if (live && t + 1 < it.t1) live = step(xb, xa, t + 2 < it.t1);
       }
     }
   } else {
-    // ---------------- rows through the block table; RoPE columns ----------------
-    const uint32_t r_kfull = map_to_rank(smem_u32(&bars.kfull[2]), 0), r_qfull = map_to_rank(smem_u32(&bars.qfull), 0);
+    // ---------------- RoPE columns of 32 keys; rows through the block table ----------------
     const uint32_t box = smem_u32(smem + kOffK + 8 * kBox);
-    const int unit = lane & 7;
-    uint32_t ahead = 0;                               // tiles whose rows are down
+    const int unit = lane & 7, r0 = (warp & 1) * 32 + (lane >> 3);
+    uint32_t down = 0, slot = 0, turn = 0;            // tiles whose rows are down (warp 6); the next tile's rows
     auto rows_down = [&](int t) -> bool {
       int32_t at[4];
 #pragma unroll
@@ -523,42 +556,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
           else record_error(p.err, DEV_RANGE_BASE | Y_PAGE);
         }
       }
-      const uint32_t slot = ahead % kRowSlots;
-      if (!wait.warp(&bars.rfree[slot], ((ahead / kRowSlots) & 1) ^ 1, D_RFREE)) return false;
+      const uint32_t into = down % kRowSlots;
+      if (!wait.warp(&bars.rfree[into], ((down / kRowSlots) & 1) ^ 1, D_RFREE)) return false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) row_slots[slot * kTile + 32 * i + lane] = at[i];
-      warp_arrive(&bars.rfull[slot]);
-      ++ahead;
+      for (int i = 0; i < 4; ++i) row_slots[into * kTile + 32 * i + lane] = at[i];
+      warp_arrive(&bars.rfull[into]);
+      ++down;
       return true;
     };
-    uint4 x[16];
-    // the tile whose rows were put down last: this CTA's 64 keys
-    auto load_pe = [&]() {
-      const int32_t* at = row_slots + ((ahead - 1) % kRowSlots) * kTile + cta * kHalf + (lane >> 3);
+    uint4 x[8];
+    auto load_pe = [&]() -> bool {
+      if (!wait.warp(&bars.rfull[slot], turn, D_RFULL)) return false;
+      const int32_t* at = row_slots + slot * kTile + cta * kHalf + r0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const int a = at[4 * i];
         const uint8_t* src = p.kv.cache + (int64_t)a * kFp4Row + kFp4Pe + 16 * unit;
         x[i] = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
       }
+      warp_arrive(&bars.rfree[slot]);
+      if (++slot == kRowSlots) slot = 0, turn ^= 1;
+      return true;
     };
     for (; live && shares.next(it); ++n) {
-      if (!rows_down(it.t0)) break;
-      load_pe();
-      if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY, true)) break;
-      load_query_box(p, it.g, (int)cta * kHalf, smem_u32(smem + kOffQ + 8 * kBox), 8, lane);
-      fence_proxy_async_smem();
-      warp_arrive_remote(r_qfull);
+      if (warp == 6 && !rows_down(it.t0)) break;
+      if (!load_pe()) break;
+      if (warp == 7) {
+        if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY)) break;
+        load_query_box(p, it.g, (int)cta * kHalf, smem_u32(smem + kOffQ + 8 * kBox), 8, lane);
+        warp_arrive(&bars.qfull);
+      }
       for (int t = it.t0; t < it.t1; ++t, ++u) {
-        if (t + 1 < it.t1 && !rows_down(t + 1)) { live = false; break; }
-        if (!wait.warp(&bars.kempty[2], (u & 1) ^ 1, D_KEMPTY, true)) { live = false; break; }
+        if (warp == 6 && t + 1 < it.t1 && !rows_down(t + 1)) { live = false; break; }
+        if (!wait.warp(&bars.kempty[2], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st_shared16(box_unit(box, (lane >> 3) + 4 * i, unit), x[i]);
+        for (int i = 0; i < 8; ++i) st_shared16(box_unit(box, r0 + 4 * i, unit), x[i]);
         fence_proxy_async_smem();
-        warp_arrive_remote(r_kfull);
-        if (t + 1 < it.t1) load_pe();
+        warp_arrive(&bars.kfull[2]);
+        if (t + 1 < it.t1 && !load_pe()) { live = false; break; }
       }
     }
+    cp_async_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -566,56 +604,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tbase) : "memory");
 }
 
-// A warp a row: the partials of the pairs that had tiles of its group, by their log-sum-exp, and the sink.
-__global__ void __launch_bounds__(256) decode_fp4_reduce_kernel(const __grid_constant__ DecodeFp4Params p, int pairs) {
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)p.kv.B * p.s * p.H, item = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  if (item >= rows) return;
+// A CTA a row, four columns a thread: the partials of the pairs that had tiles of its group, by their log-sum-exp, and the
+// sink.  A thread a pair finds the weights (a pass over kPairs of them), eight partials' loads go out together: a warp that
+// took the partials one after the other spent 63 us on one request's 33.
+constexpr int kPairs = 128;
+__global__ void __launch_bounds__(kPairs) decode_fp4_reduce_kernel(const __grid_constant__ DecodeFp4Params p, int pairs) {
+  __shared__ float weight[kPairs], red[8];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t rows = (int64_t)p.kv.B * p.s * p.H, item = blockIdx.x;
   const int64_t b = item / (p.s * p.H);
   const int row = (int)(item - b * (p.s * p.H));
-  const int64_t g = b * p.row_tiles + row / kRows;
+  const int g = (int)(b * p.row_tiles + row / kRows);
   auto before = [&](int64_t i) -> int64_t {
     return guard_span(p.err, G_TILE_PREFIX, p.before + i, 8, p.before, (uint64_t)(p.groups + 1) * 8) ? p.before[i] : 0;
   };
   const int64_t total = before(p.groups), t0 = before(g), t1 = before(g + 1);
   const float sink = p.sinks && guard_span(p.err, G_SINKS, p.sinks + row % p.H, 4, p.sinks, (uint64_t)p.H * 4) ? p.sinks[row % p.H] : -CUDART_INF_F;
-  // pairs whose share meets tiles t0 .. t1 - 1; those in between have one
-  const int64_t p0 = t1 > t0 ? ((t0 + 1) * pairs - 1) / total : 0, p1 = t1 > t0 ? (t1 * pairs - 1) / total : -1;
-  auto lse_of = [&](int64_t q) -> float {
-    if (total * q / pairs >= total * (q + 1) / pairs) return -CUDART_INF_F;      // an empty share
-    const float* s = p.part_lse + (g + q) * p.part_rows + (row & (kRows - 1));
+  // pairs whose share meets tiles t0 .. t1 - 1
+  const int64_t shares = min((int64_t)pairs, total);
+  const int p0 = t1 > t0 ? (int)(((t0 + 1) * shares - 1) / total) : 0, p1 = t1 > t0 ? (int)((t1 * shares - 1) / total) : -1;
+  auto lse_of = [&](int q) -> float {
+    if (q > p1) return -CUDART_INF_F;
+    const float* s = p.part_lse + (int64_t)(g + q) * p.part_rows + (row & (kRows - 1));
     return guard_span(p.err, G_PART_LSE, s, 4, p.part_lse, p.part_lse_bytes) ? *s : -CUDART_INF_F;
   };
   float m = sink;
   bool nan = false;
-  for (int64_t q = p0; q <= p1; ++q) {
+  for (int q = p0 + tid; q <= p1; q += kPairs) {
     const float l = lse_of(q);
     nan |= l != l;
     m = fmaxf(m, l);
   }
-  float wsum = sink == -CUDART_INF_F ? 0.f : expf(sink - m), acc[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int64_t q = p0; q <= p1; ++q) {
-    const float l = lse_of(q);
-    if (l == -CUDART_INF_F) continue;
-    const float* src = p.part_o + ((g + q) * p.part_rows + (row & (kRows - 1))) * kLatent;
-    if (!guard_span(p.err, G_PART_O, src, kLatent * 4, p.part_o, p.part_o_bytes)) continue;
-    const float w = expf(l - m);
-    wsum += w;
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+  if (lane == 0) red[tid >> 5] = m;
+  nan = __syncthreads_or(nan);
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float wsum = sink == -CUDART_INF_F ? 0.f : expf(sink - m);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q0 = p0; q0 <= p1; q0 += kPairs) {
+    __syncthreads();
+    const float l = lse_of(q0 + tid);
+    weight[tid] = l == -CUDART_INF_F ? 0.f : expf(l - m);
+    __syncthreads();
+    const int n = min(kPairs, p1 - q0 + 1);
+    for (int i0 = 0; i0 < n; i0 += 8) {
+      float4 v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = reinterpret_cast<const float4*>(src)[lane + 32 * k];
-      acc[4 * k] += w * v.x, acc[4 * k + 1] += w * v.y, acc[4 * k + 2] += w * v.z, acc[4 * k + 3] += w * v.w;
+      for (int i = 0; i < 8; ++i) {
+        const float* src = p.part_o + ((int64_t)(g + q0 + i0 + i) * p.part_rows + (row & (kRows - 1))) * kLatent + 4 * tid;
+        const bool in = i0 + i < n && weight[i0 + i] != 0.f && guard_span(p.err, G_PART_O, src, 16, p.part_o, p.part_o_bytes);
+        v[i] = in ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = i0 + i < n ? weight[i0 + i] : 0.f;
+        wsum += w;
+        acc.x += w * v[i].x, acc.y += w * v[i].y, acc.z += w * v[i].z, acc.w += w * v[i].w;
+      }
     }
   }
   const float inv = nan ? CUDART_NAN_F : wsum > 0.f ? p.kv_scale / wsum : 0.f;
-  __nv_bfloat16* out = p.out + item * kLatent;
-  if (guard_span(p.err, G_OUT, out, kLatent * 2, p.out, (uint64_t)rows * kLatent * 2))
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      reinterpret_cast<uint2*>(out)[lane + 32 * k] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv), pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
-  if (lane == 0 && p.lse && guard_span(p.err, G_LSE, p.lse + item, 4, p.lse, (uint64_t)rows * 4))
+  __nv_bfloat16* out = p.out + item * kLatent + 4 * tid;
+  if (guard_span(p.err, G_OUT, out, 8, p.out, (uint64_t)rows * kLatent * 2))
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (tid == 0 && p.lse && guard_span(p.err, G_LSE, p.lse + item, 4, p.lse, (uint64_t)rows * 4))
     p.lse[item] = nan ? CUDART_NAN_F : wsum > 0.f ? m + logf(wsum) : -CUDART_INF_F;
 }
 
@@ -628,7 +681,7 @@ DecodeFp4Scratch decode_fp4_scratch(int B, int s, int H, int num_splits) {
   const int64_t rows = (int64_t)s * H;
   r.row_tiles = (int)((rows + kRows - 1) / kRows);
   r.part_rows = rows < kRows ? (int)rows : kRows;
-  r.groups = (int64_t)B * r.row_tiles;
+  r.groups = B * r.row_tiles;
   const size_t slots = (size_t)(r.groups + r.pairs) * r.part_rows;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   r.before = up((size_t)(r.groups + 1) * 8);
@@ -648,7 +701,7 @@ cudaError_t launch_decode_fp4(const DecodeFp4Params& p, int pairs, cudaStream_t 
   else decode_fp4_kernel<false><<<2 * pairs, kThreads, kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  decode_fp4_reduce_kernel<<<(unsigned)(((int64_t)p.kv.B * p.s * p.H + 7) / 8), 256, 0, stream>>>(p, pairs);
+  decode_fp4_reduce_kernel<<<(unsigned)((int64_t)p.kv.B * p.s * p.H), kPairs, 0, stream>>>(p, pairs);
   return cudaGetLastError();
 }
 
