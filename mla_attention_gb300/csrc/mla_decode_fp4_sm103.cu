@@ -15,8 +15,8 @@
 //   4, 5  first CTA: MMAs (one lane issues for both CTAs), scores and values; second CTA: its warps' arrivals passed on.  An
 //         arrival in another CTA waits for all of the thread's loads on their way: 1900 cycles under the next tile's
 //   6, 7  the RoPE columns, 32 keys each; warp 6 also the tiles' rows through the block table
-//   8-23  4-bit rows into f16: column box w of K; column box w % 4 of key half w / 4 of V.  The loads of a tile go out before the
-//         last one's are converted.  Latency bounds them: with 8 warps that do both a tile took 9200 cycles
+//   8-23  4-bit rows into f16, 32 keys and 128 columns each: of K and of V .  The loads of a tile go out
+//         before the last one's are converted.  Latency bounds them: with 8 warps that do both a tile took 9200 cycles
 // The tiles of all requests are dealt to the pairs in equal shares; fp32 partials of a request that several pairs share
 // are merged by decode_fp4_reduce_kernel.
 #include <math_constants.h>
@@ -45,9 +45,9 @@ constexpr int kOffBars = kOffMax + 4 * 64 * 4;
 
 struct Bars {
   // in each CTA, with arrivals of its own warps; in the first also the second's as one
-  uint64_t kfull[3], vfull[2], qfull, pfull, sfree[2], ofree;
+  uint64_t kfull[2], vfull[2], qfull, pfull, sfree[2], ofree;
   // in each CTA, by commits to both
-  uint64_t kempty[3], vempty[2], qempty, sfull[2], pvdone;
+  uint64_t kempty[2], vempty[2], qempty, sfull[2], pvdone;
   // in each CTA
   uint64_t rfull[kRowSlots], rfree[kRowSlots];
   uint64_t pair[2];                                   // warps w and w + 2
@@ -155,13 +155,22 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
 #define MLA_STEP2(P, ID) MLA_MMA2("%0", "x", "y", ID, P) "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
 #define MLA_BOX2(P, ID) MLA_STEP2(P, ID) MLA_STEP2("t", ID) MLA_STEP2("t", ID) MLA_MMA2("%0", "x", "y", ID, "t") \
   "add.s64 x, x, 506;\n\tadd.s64 y, y, 506;\n\t"
-// S (+)= Q K^T over three boxes of 64 columns, 64 rows each in either CTA; the last box with an instruction descriptor of its own
-__device__ __forceinline__ void mma2_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t id_last, uint32_t accumulate) {
+// S = Q K^T over four boxes of 64 columns, 64 rows each in either CTA
+__device__ __forceinline__ void mma2_scores4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
-      MLA_BOX2("p", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%4") "}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(id_last), "r"(accumulate)
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
+      MLA_BOX2("p", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+// S += over the other four and the RoPE columns, whose operands are bf16
+__device__ __forceinline__ void mma2_scores5(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t id_pe) {
+  asm volatile(
+      "{\n\t.reg .pred t;\n\t.reg .b64 x, y;\n\t"
+      "setp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
+      MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%4") "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(id_pe)
       : "memory");
 }
 #define MLA_PV2(P) MLA_MMA2("%0", "x", "y", "%4", P) MLA_MMA2("%5", "x", "z", "%4", P) \
@@ -186,36 +195,41 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
                : "memory");
 }
 
-// Raw 64 x 64 box of 4-bit values: two lanes a row, 32 columns each; the four scales of rows lane and 32 + lane.
+// 32 rows of 128 columns as they lie: four lanes a row, 32 columns each, and their two scales.  (Two lanes a row and 64
+// columns ask the first-level cache for twice as many lines: 0.486 against 0.42 ms.)
 struct Raw {
   uint4 v[4];
-  uint32_t sc[2];
+  uint32_t sc[4];
 };
 __device__ __forceinline__ void load_raw(const DecodeFp4Params& p, Raw& x, const int32_t* at, int col, int lane, uint64_t cache_bytes) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int a = at[16 * i + (lane >> 1)];
-    const uint8_t* r = p.kv.cache + (int64_t)a * kFp4Row + col / 2 + 16 * (lane & 1);
-    x.v[i] = a >= 0 && guard_span(p.err, G_STEP_IN, r, 16, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint4*>(r) : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int a = at[32 * i + lane];
-    const uint8_t* r = p.kv.cache + (int64_t)a * kFp4Row + kFp4Codes + col / 16;
-    x.sc[i] = a >= 0 && guard_span(p.err, G_STEP_IN, r, 4, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint32_t*>(r) : 0u;
+    const int a = at[8 * i + (lane >> 2)];
+    const uint8_t* r = p.kv.cache + (int64_t)a * kFp4Row;
+    x.v[i] = make_uint4(0, 0, 0, 0), x.sc[i] = 0;
+    if (a >= 0 && guard_span(p.err, G_STEP_IN, r, kFp4Row, p.kv.cache, cache_bytes)) {
+      x.v[i] = *reinterpret_cast<const uint4*>(r + col / 2 + 16 * (lane & 3));
+      x.sc[i] = *reinterpret_cast<const uint16_t*>(r + kFp4Codes + col / 16 + 2 * (lane & 3));
+    }
   }
 }
-__device__ __forceinline__ void convert_raw(const Raw& x, uint32_t box, int lane) {
-  const int half = lane & 1;
+// into two boxes of 64 columns, rows r0 .. r0 + 31 (r0 a multiple of 8).  The lanes of the second box store their
+// 16-byte pieces in another order, so that eight lanes meet eight banks.
+__device__ __forceinline__ void convert_raw(const Raw& x, uint32_t boxes, int r0, int lane) {
+  const int second = (lane >> 1) & 1, half = lane & 1, r = lane >> 2;
+  const uint32_t row = boxes + second * kBox + (r0 + r) * 128;
+  uint32_t to[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) to[j] = row + (((4 * half + (j ^ (2 * second))) ^ (r & 7)) << 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = 16 * i + (lane >> 1);
-    const uint32_t four = __shfl_sync(0xffffffffu, x.sc[i >> 1], r & 31);
-    const uint2 s = fp4_scales2(half ? four >> 16 : four);
-    st_shared16(box_unit(box, r, 4 * half), fp4x8_to_f16(x.v[i].x, s.x));
-    st_shared16(box_unit(box, r, 4 * half + 1), fp4x8_to_f16(x.v[i].y, s.x));
-    st_shared16(box_unit(box, r, 4 * half + 2), fp4x8_to_f16(x.v[i].z, s.y));
-    st_shared16(box_unit(box, r, 4 * half + 3), fp4x8_to_f16(x.v[i].w, s.y));
+    uint2 s = fp4_scales2(x.sc[i]);
+    uint4 v = x.v[i];
+    if (second) s = make_uint2(s.y, s.x), v = make_uint4(v.z, v.w, v.x, v.y);
+    st_shared16(to[0] + i * 1024, fp4x8_to_f16(v.x, s.x));
+    st_shared16(to[1] + i * 1024, fp4x8_to_f16(v.y, s.x));
+    st_shared16(to[2] + i * 1024, fp4x8_to_f16(v.z, s.y));
+    st_shared16(to[3] + i * 1024, fp4x8_to_f16(v.w, s.y));
   }
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
@@ -287,7 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * kFp4Row;
   if (tid == 0) {
     const uint32_t more = cta == 0 ? 1 : 0;           // the second CTA's
-    for (int i = 0; i < 3; ++i) mbar_init(&bars.kfull[i], (i < 2 ? 3 : 4) + more), mbar_init(&bars.kempty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.kfull[i], (i == 0 ? 4 : 6) + more), mbar_init(&bars.kempty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.vfull[i], 4 + more), mbar_init(&bars.vempty[i], 1);
       mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 4 + more);
@@ -428,19 +442,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         for (int t = it.t0; t < it.t1; ++t, ++u) {
           const int buf = u & 1;
           if (!wait.warp(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, D_SFREE, true)) { live = false; break; }
-#pragma unroll 1
-          for (int g = 0; g < 3; ++g) {
-            if (!wait.warp(&bars.kfull[g], u & 1, D_KFULL, true)) { live = false; break; }
-            tc_fence_after();
-            if (elect_one()) {
-              mma2_scores(tbase + kTmemS + buf * 64, qdesc + g * (3 * kBox / 16), kdesc + g * (3 * kBox / 16), id, g == 2 ? id_pe : id, g > 0 ? 1u : 0u);
-              commit2(&bars.kempty[g]);
-              if (g == 2) commit2(&bars.sfull[buf]);
-              if (g == 2 && t == it.t1 - 1) commit2(&bars.qempty);
-            }
-            __syncwarp();
+          if (!wait.warp(&bars.kfull[0], u & 1, D_KFULL, true)) { live = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            mma2_scores4(tbase + kTmemS + buf * 64, qdesc, kdesc, id, 0u);
+            commit2(&bars.kempty[0]);
           }
-          if (!live) break;
+          __syncwarp();
+          if (!wait.warp(&bars.kfull[1], u & 1, D_KFULL, true)) { live = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            mma2_scores5(tbase + kTmemS + buf * 64, qdesc + 4 * kBox / 16, kdesc + 4 * kBox / 16, id, id_pe);
+            commit2(&bars.kempty[1]);
+            commit2(&bars.sfull[buf]);
+            if (t == it.t1 - 1) commit2(&bars.qempty);
+          }
+          __syncwarp();
         }
       }
       if (elect_one()) commit2(&bars.drain[0]);       // what was issued is done before anything is given back
@@ -455,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       for (; live && shares.next(it); ++n) {
         live = pass_on(&bars.qfull, n & 1, D_QFULL);
         for (int t = it.t0; t < it.t1 && live; ++t, ++u)
-          for (int g = 0; g < 3 && live; ++g) live = pass_on(&bars.kfull[g], u & 1, D_KFULL);
+          for (int g = 0; g < 2 && live; ++g) live = pass_on(&bars.kfull[g], u & 1, D_KFULL);
       }
     }
   } else if (warp == 5) {
@@ -501,10 +518,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   } else if (warp >= kFirstK) {
     // ---------------- 4-bit rows into f16 ----------------
     const bool is_k = warp < kFirstV;
-    const int w = (warp - kFirstK) & 7, part = is_k ? w / 3 : w >> 2, vb = w & 3;
-    const int col = is_k ? 64 * w : (vb < 2 ? 0 : 256) + 128 * (int)cta + 64 * (vb & 1);
-    const int first = is_k ? (int)cta * kHalf : part * kHalf;      // of the tile's keys
-    const uint32_t box = smem_u32(smem + (is_k ? kOffK : kOffV) + w * kBox);
+    // K: 32 rows w % 2 of this CTA's keys, columns 128 (w / 2); V: rows w % 2 of key half w / 4, the CTA's columns (w / 2) % 2
+    const int w = (warp - kFirstK) & 7, part = w >> 2, r0 = (w & 1) * 32;
+    const int col = is_k ? 128 * (w >> 1) : 256 * ((w >> 1) & 1) + 128 * (int)cta;
+    const int first = (is_k ? (int)cta : part) * kHalf + r0;       // of the tile's keys
+    const uint32_t boxes = smem_u32(smem + (is_k ? kOffK : kOffV) + 2 * (w >> 1) * kBox);
     uint64_t* const empty = is_k ? &bars.kempty[part] : &bars.vempty[part];
     uint64_t* const full = is_k ? &bars.kfull[part] : &bars.vfull[part];
     uint32_t slot = 0, turn = 0;                      // of the next tile's rows
@@ -520,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     auto step = [&](const Raw& x, Raw& next, bool more) -> bool {
       if (more && !load(next)) return false;
       if (!wait.warp(empty, (u & 1) ^ 1, D_KEMPTY)) return false;
-      convert_raw(x, box, lane);
+      convert_raw(x, boxes, r0, lane);
       fence_proxy_async_smem();
       warp_arrive(full);
       ++u;
@@ -588,11 +606,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       }
       for (int t = it.t0; t < it.t1; ++t, ++u) {
         if (warp == 6 && t + 1 < it.t1 && !rows_down(t + 1)) { live = false; break; }
-        if (!wait.warp(&bars.kempty[2], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
+        if (!wait.warp(&bars.kempty[1], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
 #pragma unroll
         for (int i = 0; i < 8; ++i) st_shared16(box_unit(box, r0 + 4 * i, unit), x[i]);
         fence_proxy_async_smem();
-        warp_arrive(&bars.kfull[2]);
+        warp_arrive(&bars.kfull[1]);
         if (t + 1 < it.t1 && !load_pe()) { live = false; break; }
       }
     }
