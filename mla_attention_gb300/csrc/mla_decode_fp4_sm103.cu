@@ -14,7 +14,8 @@
 //         memory, lazy rescale of O (by more than 2^8), exponentials, P
 //   4, 5  first CTA: MMAs (one lane issues for both CTAs), scores and values; second CTA: its warps' arrivals passed on.  An
 //         arrival in another CTA waits for all of the thread's loads on their way: 1900 cycles under the next tile's
-//   6, 7  the RoPE columns, 32 keys each; warp 6 also the tiles' rows through the block table
+//   6     the tiles' rows through the block table, up to three tiles ahead
+//   7     the RoPE columns
 //   8-23  4-bit rows into f16, 32 keys and 128 columns each: of K and of V .  The loads of a tile go out
 //         before the last one's are converted.  Latency bounds them: with 8 warps that do both a tile took 9200 cycles
 // The tiles of all requests are dealt to the pairs in equal shares; fp32 partials of a request that several pairs share
@@ -45,9 +46,9 @@ constexpr int kOffBars = kOffMax + 4 * 64 * 4;
 
 struct Bars {
   // in each CTA, with arrivals of its own warps; in the first also the second's as one
-  uint64_t kfull[2], vfull[2], qfull, pfull, sfree[2], ofree;
+  uint64_t kfull[4], vfull[2], qfull, pfull, sfree[2], ofree;
   // in each CTA, by commits to both
-  uint64_t kempty[2], vempty[2], qempty, sfull[2], pvdone;
+  uint64_t kempty[4], vempty[2], qempty, sfull[2], pvdone;
   // in each CTA
   uint64_t rfull[kRowSlots], rfree[kRowSlots];
   uint64_t pair[2];                                   // warps w and w + 2
@@ -105,6 +106,14 @@ struct Shares {
   }
 };
 
+// Tiles before share i of n: total * i / n (a 64-bit quotient takes hundreds of cycles, and the kernel waits for it).
+__device__ __forceinline__ int64_t share_start(int64_t total, int64_t i, int64_t n) {
+  if (i >= n) return total;
+  if (total >= 1ll << 31) return total * i / n;
+  const uint32_t t = (uint32_t)total, m = (uint32_t)n, q = t / m, r = t - q * m;
+  return (int64_t)((uint64_t)q * (uint32_t)i + (uint32_t)(r * (uint32_t)i) / m);    // r i < n^2 <= 2^32
+}
+
 // Where this pair's share starts, and (first CTA of all) the tiles before each group; by all threads.
 __device__ __noinline__ void find_share(const DecodeFp4Params& p, Bars& bars, int64_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -125,8 +134,8 @@ __device__ __noinline__ void find_share(const DecodeFp4Params& p, Bars& bars, in
     total += sums[w];
   }
   // no more shares than tiles: none is empty but those of the pairs behind them
-  const int64_t pair = blockIdx.x / 2, pairs = max((int64_t)1, min((int64_t)(gridDim.x / 2), total));
-  const int64_t lo = pair < pairs ? total * pair / pairs : total, hi = pair < pairs ? total * (pair + 1) / pairs : total;
+  const int64_t pair = blockIdx.x / 2, pairs = min((int64_t)(gridDim.x / 2), total);
+  const int64_t lo = share_start(total, pair, pairs), hi = share_start(total, pair + 1, pairs);
   if (tid == 0) bars.share = hi - lo;
   const bool tell = blockIdx.x == 0, here = lo < hi && at <= lo && lo < at + mine;
   auto put = [&](int64_t g, int64_t v) {
@@ -155,21 +164,21 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
 #define MLA_STEP2(P, ID) MLA_MMA2("%0", "x", "y", ID, P) "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
 #define MLA_BOX2(P, ID) MLA_STEP2(P, ID) MLA_STEP2("t", ID) MLA_STEP2("t", ID) MLA_MMA2("%0", "x", "y", ID, "t") \
   "add.s64 x, x, 506;\n\tadd.s64 y, y, 506;\n\t"
-// S = Q K^T over four boxes of 64 columns, 64 rows each in either CTA
-__device__ __forceinline__ void mma2_scores4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+// S (+)= Q K^T over two boxes of 64 columns, 64 rows each in either CTA
+__device__ __forceinline__ void mma2_scores2(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
-      MLA_BOX2("p", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") "}" ::"r"(d),
+      MLA_BOX2("p", "%3") MLA_BOX2("t", "%3") "}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(accumulate)
       : "memory");
 }
-// S += over the other four and the RoPE columns, whose operands are bf16
-__device__ __forceinline__ void mma2_scores5(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t id_pe) {
+// S += over the last two and the RoPE columns, whose operands are bf16
+__device__ __forceinline__ void mma2_scores3(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t id_pe) {
   asm volatile(
       "{\n\t.reg .pred t;\n\t.reg .b64 x, y;\n\t"
       "setp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
-      MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%4") "}" ::"r"(d),
+      MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%4") "}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(id_pe)
       : "memory");
 }
@@ -237,8 +246,8 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// box k of this CTA's 64 query rows (in f16 but for the RoPE columns); rows behind the group's are zeros
-__device__ __noinline__ void load_query_box(const DecodeFp4Params& p, const Group& g, int first, uint32_t box, int k, int lane) {
+// Box k of this CTA's 64 query rows; rows behind the group's are zeros.  The copies go out ...
+__device__ __forceinline__ void ask_query_box(const DecodeFp4Params& p, const Group& g, int first, uint32_t box, int k, int lane) {
   const uint64_t q_bytes = (uint64_t)p.kv.B * p.s * p.H * kDk * 2;
   const int unit = lane & 7;
   const __nv_bfloat16* q = p.q + ((int64_t)g.b * p.s * p.H + g.row0 + first) * kDk + 64 * k + 8 * unit;
@@ -248,8 +257,12 @@ __device__ __noinline__ void load_query_box(const DecodeFp4Params& p, const Grou
     const bool in = first + r < g.rows && guard_span(p.err, G_Q, src, 16, p.q, q_bytes);
     cp_async16_zfill(box_unit(box, r, unit), in ? src : p.q, in ? 16u : 0u);
   }
+}
+// ... and each lane puts its own into f16 where they lie (the RoPE columns stay)
+__device__ __forceinline__ void take_query_box(uint32_t box, int k, int lane) {
+  const int unit = lane & 7;
   cp_async_wait_all();
-  if (k < 8)                                          // each lane puts its own copies into f16 where they lie
+  if (k < 8)
 #pragma unroll 4
     for (int r = lane >> 3; r < kHalf; r += 4) st_shared16(box_unit(box, r, unit), bf16x8_to_f16(ld_shared16(box_unit(box, r, unit))));
   fence_proxy_async_smem();
@@ -301,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * kFp4Row;
   if (tid == 0) {
     const uint32_t more = cta == 0 ? 1 : 0;           // the second CTA's
-    for (int i = 0; i < 2; ++i) mbar_init(&bars.kfull[i], (i == 0 ? 4 : 6) + more), mbar_init(&bars.kempty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.kfull[i], (i < 3 ? 2 : 3) + more), mbar_init(&bars.kempty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.vfull[i], 4 + more), mbar_init(&bars.vempty[i], 1);
       mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 4 + more);
@@ -309,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     }
     mbar_init(&bars.qfull, 9 + more), mbar_init(&bars.qempty, 1);
     mbar_init(&bars.pfull, 4 + more), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 4 + more);
-    for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], 18);
+    for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], 17);
     mbar_init(&bars.stall, 1);
     bars.abort = 0;
     if (smem_u32(smem) & 1023u) bars.abort = DEV_TIMEOUT_BASE | D_ALIGN, record_error(p.err, bars.abort);
@@ -442,18 +455,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         for (int t = it.t0; t < it.t1; ++t, ++u) {
           const int buf = u & 1;
           if (!wait.warp(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, D_SFREE, true)) { live = false; break; }
-          if (!wait.warp(&bars.kfull[0], u & 1, D_KFULL, true)) { live = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
-            mma2_scores4(tbase + kTmemS + buf * 64, qdesc, kdesc, id, 0u);
-            commit2(&bars.kempty[0]);
+#pragma unroll 1
+          for (int g = 0; g < 3; ++g) {
+            if (!wait.warp(&bars.kfull[g], u & 1, D_KFULL, true)) { live = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              mma2_scores2(tbase + kTmemS + buf * 64, qdesc + g * (2 * kBox / 16), kdesc + g * (2 * kBox / 16), id, g > 0 ? 1u : 0u);
+              commit2(&bars.kempty[g]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          if (!wait.warp(&bars.kfull[1], u & 1, D_KFULL, true)) { live = false; break; }
+          if (!live || !wait.warp(&bars.kfull[3], u & 1, D_KFULL, true)) { live = false; break; }
           tc_fence_after();
           if (elect_one()) {
-            mma2_scores5(tbase + kTmemS + buf * 64, qdesc + 4 * kBox / 16, kdesc + 4 * kBox / 16, id, id_pe);
-            commit2(&bars.kempty[1]);
+            mma2_scores3(tbase + kTmemS + buf * 64, qdesc + 6 * kBox / 16, kdesc + 6 * kBox / 16, id, id_pe);
+            commit2(&bars.kempty[3]);
             commit2(&bars.sfull[buf]);
             if (t == it.t1 - 1) commit2(&bars.qempty);
           }
@@ -472,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       for (; live && shares.next(it); ++n) {
         live = pass_on(&bars.qfull, n & 1, D_QFULL);
         for (int t = it.t0; t < it.t1 && live; ++t, ++u)
-          for (int g = 0; g < 2 && live; ++g) live = pass_on(&bars.kfull[g], u & 1, D_KFULL);
+          for (int g = 0; g < 4 && live; ++g) live = pass_on(&bars.kfull[g], u & 1, D_KFULL);
       }
     }
   } else if (warp == 5) {
@@ -519,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     // ---------------- 4-bit rows into f16 ----------------
     const bool is_k = warp < kFirstV;
     // K: 32 rows w % 2 of this CTA's keys, columns 128 (w / 2); V: rows w % 2 of key half w / 4, the CTA's columns (w / 2) % 2
-    const int w = (warp - kFirstK) & 7, part = w >> 2, r0 = (w & 1) * 32;
+    const int w = (warp - kFirstK) & 7, part = is_k ? w >> 1 : w >> 2, r0 = (w & 1) * 32;
     const int col = is_k ? 128 * (w >> 1) : 256 * ((w >> 1) & 1) + 128 * (int)cta;
     const int first = (is_k ? (int)cta : part) * kHalf + r0;       // of the tile's keys
     const uint32_t boxes = smem_u32(smem + (is_k ? kOffK : kOffV) + 2 * (w >> 1) * kBox);
@@ -545,10 +561,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       return true;
     };
     for (; live && shares.next(it); ++n) {
-      if (!load(xa)) break;
+      const uint32_t qbox = smem_u32(smem + kOffQ + w * kBox);
       if (is_k) {
         if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY)) break;
-        load_query_box(p, it.g, (int)cta * kHalf, smem_u32(smem + kOffQ + w * kBox), w, lane);
+        ask_query_box(p, it.g, (int)cta * kHalf, qbox, w, lane);
+      }
+      if (!load(xa)) break;
+      if (is_k) {
+        take_query_box(qbox, w, lane);
         warp_arrive(&bars.qfull);
       }
       for (int t = it.t0; t < it.t1 && live; t += 2) {
@@ -556,62 +576,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         if (live && t + 1 < it.t1) live = step(xb, xa, t + 2 < it.t1);
       }
     }
-  } else {
-    // ---------------- RoPE columns of 32 keys; rows through the block table ----------------
-    const uint32_t box = smem_u32(smem + kOffK + 8 * kBox);
-    const int unit = lane & 7, r0 = (warp & 1) * 32 + (lane >> 3);
-    uint32_t down = 0, slot = 0, turn = 0;            // tiles whose rows are down (warp 6); the next tile's rows
-    auto rows_down = [&](int t) -> bool {
-      int32_t at[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = t * kTile + 32 * i + lane;
-        at[i] = -1;
-        if (j < it.g.keys) {
-          const int pg = j / p.kv.page_size;
-          const int page = guarded_int(p.err, p.kv.block_table, (int64_t)it.g.b * p.kv.max_pages + pg, (int64_t)p.kv.B * p.kv.max_pages);
-          if (page >= 0 && page < p.kv.num_pages) at[i] = page * p.kv.page_size + (j - pg * p.kv.page_size);
-          else record_error(p.err, DEV_RANGE_BASE | Y_PAGE);
-        }
-      }
-      const uint32_t into = down % kRowSlots;
-      if (!wait.warp(&bars.rfree[into], ((down / kRowSlots) & 1) ^ 1, D_RFREE)) return false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) row_slots[into * kTile + 32 * i + lane] = at[i];
-      warp_arrive(&bars.rfull[into]);
-      ++down;
-      return true;
-    };
-    uint4 x[8];
-    auto load_pe = [&]() -> bool {
-      if (!wait.warp(&bars.rfull[slot], turn, D_RFULL)) return false;
-      const int32_t* at = row_slots + slot * kTile + cta * kHalf + r0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int a = at[4 * i];
-        const uint8_t* src = p.kv.cache + (int64_t)a * kFp4Row + kFp4Pe + 16 * unit;
-        x[i] = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes) ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-      }
-      warp_arrive(&bars.rfree[slot]);
-      if (++slot == kRowSlots) slot = 0, turn ^= 1;
-      return true;
-    };
+  } else if (warp == 6) {
+    // ---------------- rows through the block table ----------------
     for (; live && shares.next(it); ++n) {
-      if (warp == 6 && !rows_down(it.t0)) break;
-      if (!load_pe()) break;
-      if (warp == 7) {
-        if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY)) break;
-        load_query_box(p, it.g, (int)cta * kHalf, smem_u32(smem + kOffQ + 8 * kBox), 8, lane);
-        warp_arrive(&bars.qfull);
-      }
       for (int t = it.t0; t < it.t1; ++t, ++u) {
-        if (warp == 6 && t + 1 < it.t1 && !rows_down(t + 1)) { live = false; break; }
-        if (!wait.warp(&bars.kempty[1], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
+        int32_t at[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st_shared16(box_unit(box, r0 + 4 * i, unit), x[i]);
+        for (int i = 0; i < 4; ++i) {
+          const int j = t * kTile + 32 * i + lane;
+          at[i] = -1;
+          if (j < it.g.keys) {
+            const int pg = j / p.kv.page_size;
+            const int page = guarded_int(p.err, p.kv.block_table, (int64_t)it.g.b * p.kv.max_pages + pg, (int64_t)p.kv.B * p.kv.max_pages);
+            if (page >= 0 && page < p.kv.num_pages) at[i] = page * p.kv.page_size + (j - pg * p.kv.page_size);
+            else record_error(p.err, DEV_RANGE_BASE | Y_PAGE);
+          }
+        }
+        const uint32_t slot = u % kRowSlots;
+        if (!wait.warp(&bars.rfree[slot], ((u / kRowSlots) & 1) ^ 1, D_RFREE)) { live = false; break; }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row_slots[slot * kTile + 32 * i + lane] = at[i];
+        warp_arrive(&bars.rfull[slot]);
+      }
+    }
+  } else {
+    // ---------------- RoPE columns of this CTA's keys ----------------
+    const uint32_t box = smem_u32(smem + kOffK + 8 * kBox), qbox = smem_u32(smem + kOffQ + 8 * kBox);
+    const int unit = lane & 7;
+    for (; live && shares.next(it); ++n) {
+      if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY)) break;
+      ask_query_box(p, it.g, (int)cta * kHalf, qbox, 8, lane);
+      take_query_box(qbox, 8, lane);
+      warp_arrive(&bars.qfull);
+      for (int t = it.t0; t < it.t1; ++t, ++u) {
+        const uint32_t slot = u % kRowSlots;
+        if (!wait.warp(&bars.rfull[slot], (u / kRowSlots) & 1, D_RFULL) || !wait.warp(&bars.kempty[3], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
+        const int32_t* at = row_slots + slot * kTile + cta * kHalf + (lane >> 3);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int a = at[4 * i];
+          const uint8_t* src = p.kv.cache + (int64_t)a * kFp4Row + kFp4Pe + 16 * unit;
+          const bool in = a >= 0 && guard_span(p.err, G_STEP_IN, src, 16, p.kv.cache, cache_bytes);
+          cp_async16_zfill(box_unit(box, (lane >> 3) + 4 * i, unit), in ? src : (const uint8_t*)p.q, in ? 16u : 0u);
+        }
+        warp_arrive(&bars.rfree[slot]);
+        cp_async_wait_all();
         fence_proxy_async_smem();
-        warp_arrive(&bars.kfull[1]);
-        if (t + 1 < it.t1 && !load_pe()) { live = false; break; }
+        warp_arrive(&bars.kfull[3]);
       }
     }
     cp_async_wait_all();
