@@ -12,8 +12,7 @@
 // columns stay bf16 as their MMA's operands, sums are fp32.  24 warps a CTA:
 //   0-3   rows: lanes L and L + 64 of tensor memory hold the same row's scores of 64 keys each; maximum through shared
 //         memory, lazy rescale of O (by more than 2^8), exponentials, P
-//   4, 5  first CTA: MMAs (one lane issues for both CTAs), scores and values; second CTA: its warps' arrivals passed on.  An
-//         arrival in another CTA waits for all of the thread's loads on their way: 1900 cycles under the next tile's
+//   4, 5  MMAs, in the first CTA alone (one lane issues for both): scores; values
 //   6     the tiles' rows through the block table, up to three tiles ahead
 //   7     the RoPE columns
 //   8-23  4-bit rows into f16, 32 keys and 128 columns each: of K and of V .  The loads of a tile go out
@@ -45,7 +44,7 @@ constexpr int kOffMax = kOffRows + kRowSlots * kTile * 4;   // [2][2][64]
 constexpr int kOffBars = kOffMax + 4 * 64 * 4;
 
 struct Bars {
-  // in each CTA, with arrivals of its own warps; in the first also the second's as one
+  // in the first CTA, with arrivals of both CTAs' warps
   uint64_t kfull[4], vfull[2], qfull, pfull, sfree[2], ofree;
   // in each CTA, by commits to both
   uint64_t kempty[4], vempty[2], qempty, sfull[2], pvdone;
@@ -160,6 +159,16 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
 }
 
 // ---- MMAs of the pair ----
+// One arrival for the warp on a barrier of the first CTA.  What it tells of lies in this CTA's own shared or tensor memory, where this
+// SM's tensor core reads it: ordered within the CTA, as the default is.  (A release at cluster scope waits for the loads on
+// their way: 1900 cycles under the next tile's; passed on by another warp it still cost 0.1 ms of 0.42.)
+__device__ __forceinline__ void first_cta_arrive(uint64_t* bar, uint32_t cta) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    if (cta == 0) mbar_arrive(bar);
+    else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(smem_u32(bar), 0)) : "memory");
+  }
+}
 #define MLA_MMA2(D, X, Y, ID, P) "tcgen05.mma.cta_group::2.kind::f16 [" D "], " X ", " Y ", " ID ", " P ";\n\t"
 #define MLA_STEP2(P, ID) MLA_MMA2("%0", "x", "y", ID, P) "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
 #define MLA_BOX2(P, ID) MLA_STEP2(P, ID) MLA_STEP2("t", ID) MLA_STEP2("t", ID) MLA_MMA2("%0", "x", "y", ID, "t") \
@@ -313,15 +322,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   const uint32_t cta = cluster_ctarank();
   const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * kFp4Row;
   if (tid == 0) {
-    const uint32_t more = cta == 0 ? 1 : 0;           // the second CTA's
-    for (int i = 0; i < 4; ++i) mbar_init(&bars.kfull[i], (i < 3 ? 2 : 3) + more), mbar_init(&bars.kempty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.kfull[i], 2 * (i < 3 ? 2 : 3)), mbar_init(&bars.kempty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.vfull[i], 4 + more), mbar_init(&bars.vempty[i], 1);
-      mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 4 + more);
+      mbar_init(&bars.vfull[i], 8), mbar_init(&bars.vempty[i], 1);
+      mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 8);
       mbar_init(&bars.pair[i], 2), mbar_init(&bars.drain[i], 1);
     }
-    mbar_init(&bars.qfull, 9 + more), mbar_init(&bars.qempty, 1);
-    mbar_init(&bars.pfull, 4 + more), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 4 + more);
+    mbar_init(&bars.qfull, 18), mbar_init(&bars.qempty, 1);
+    mbar_init(&bars.pfull, 8), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 8);
     for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], 17);
     mbar_init(&bars.stall, 1);
     bars.abort = 0;
@@ -395,36 +403,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const uint64_t nref = f32x2(-ref, -ref);
         uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+        // P of the 64 keys, packed; then the scores' buffer is free (before the wait below: the next but one tile's scores run
+        // beside this tile's values: 0.436 against 0.30 ms)
+        uint32_t w[32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t s[32];
+          tmem_ld32(from + 32 * q, s);
+          tmem_wait_ld();
+          mask_piece<kUp>(s, visible - 32 * q);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x0, x1;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c22, nref), x0, x1);
+            x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+            sum[i & 1] = add_f32x2(sum[i & 1], f32x2(x0, x1));
+            w[16 * q + i] = pack_f16x2(x0, x1);
+          }
+        }
+        tc_fence_before();
+        first_cta_arrive(&bars.sfree[buf], cta);
         // the last tile's P V is done: P may be written over, O be scaled
         if (u > 0 && !wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) { live = false; break; }
         if (t > it.t0 && __any_sync(~0u, a != 1.f)) {
           tc_fence_after();
           rescale_o(tbase + lanes + kTmemO, a);
+          tc_fence_before();
         }
-#pragma unroll 1
-        for (int q = 0; q < 64; q += 32) {
-          uint32_t s[32];
-          tmem_ld32(from + q, s);
-          tmem_wait_ld();
-          mask_piece<kUp>(s, visible - q);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              float x0, x1;
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i + 2 * v]), __uint_as_float(s[i + 2 * v + 1])), c22, nref), x0, x1);
-              x0 = ex2_approx(x0), x1 = ex2_approx(x1);
-              sum[v & 1] = add_f32x2(sum[v & 1], f32x2(x0, x1));
-              w[v] = pack_f16x2(x0, x1);
-            }
-            st_shared16(box_unit(prow, r, (q + i) / 8), make_uint4(w[0], w[1], w[2], w[3]));
-          }
-        }
-        tc_fence_before();
-        warp_arrive(&bars.sfree[buf]);
+        for (int i = 0; i < 8; ++i) st_shared16(box_unit(prow, r, i), make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
         fence_proxy_async_smem();
-        warp_arrive(&bars.pfull);
+        first_cta_arrive(&bars.pfull, cta);
         float l0, l1;
         f32x2_split(add_f32x2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
@@ -442,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (row < it.g.rows && hh == 0 && guard_span(p.err, G_PART_LSE, p.part_lse + slot_row, 4, p.part_lse, p.part_lse_bytes))
         p.part_lse[slot_row] = l == 0.f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.f : m) * 0.6931471805599453f + logf(l);
       tc_fence_before();
-      warp_arrive(&bars.ofree);
+      first_cta_arrive(&bars.ofree, cta);
     }
   } else if (warp == 4) {
     // ---------------- scores ----------------
@@ -479,17 +488,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (elect_one()) commit2(&bars.drain[0]);       // what was issued is done before anything is given back
       mbar_drain(&bars.drain[0], 0);
       __syncwarp();
-    } else {
-      auto pass_on = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-        if (!wait.warp(bar, parity, site)) return false;
-        warp_arrive_remote(map_to_rank(smem_u32(bar), 0));
-        return true;
-      };
-      for (; live && shares.next(it); ++n) {
-        live = pass_on(&bars.qfull, n & 1, D_QFULL);
-        for (int t = it.t0; t < it.t1 && live; ++t, ++u)
-          for (int g = 0; g < 4 && live; ++g) live = pass_on(&bars.kfull[g], u & 1, D_KFULL);
-      }
     }
   } else if (warp == 5) {
     // ---------------- values ----------------
@@ -518,18 +516,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (elect_one()) commit2(&bars.drain[1]);
       mbar_drain(&bars.drain[1], 0);
       __syncwarp();
-    } else {
-      auto pass_on = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-        if (!wait.warp(bar, parity, site)) return false;
-        warp_arrive_remote(map_to_rank(smem_u32(bar), 0));
-        return true;
-      };
-      for (; live && shares.next(it); ++n) {
-        for (int t = it.t0; t < it.t1 && live; ++t, ++u)
-          live = pass_on(&bars.sfree[u & 1], (u >> 1) & 1, D_SFREE) && pass_on(&bars.pfull, u & 1, D_PFULL) &&
-                 pass_on(&bars.vfull[0], u & 1, D_VFULL) && pass_on(&bars.vfull[1], u & 1, D_VFULL);
-        if (live) live = pass_on(&bars.ofree, n & 1, D_OFREE);
-      }
     }
   } else if (warp >= kFirstK) {
     // ---------------- 4-bit rows into f16 ----------------
@@ -556,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (!wait.warp(empty, (u & 1) ^ 1, D_KEMPTY)) return false;
       convert_raw(x, boxes, r0, lane);
       fence_proxy_async_smem();
-      warp_arrive(full);
+      first_cta_arrive(full, cta);
       ++u;
       return true;
     };
@@ -569,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (!load(xa)) break;
       if (is_k) {
         take_query_box(qbox, w, lane);
-        warp_arrive(&bars.qfull);
+        first_cta_arrive(&bars.qfull, cta);
       }
       for (int t = it.t0; t < it.t1 && live; t += 2) {
         live = step(xa, xb, t + 1 < it.t1);
@@ -607,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY)) break;
       ask_query_box(p, it.g, (int)cta * kHalf, qbox, 8, lane);
       take_query_box(qbox, 8, lane);
-      warp_arrive(&bars.qfull);
+      first_cta_arrive(&bars.qfull, cta);
       for (int t = it.t0; t < it.t1; ++t, ++u) {
         const uint32_t slot = u % kRowSlots;
         if (!wait.warp(&bars.rfull[slot], (u / kRowSlots) & 1, D_RFULL) || !wait.warp(&bars.kempty[3], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
@@ -622,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         warp_arrive(&bars.rfree[slot]);
         cp_async_wait_all();
         fence_proxy_async_smem();
-        warp_arrive(&bars.kfull[3]);
+        first_cta_arrive(&bars.kfull[3], cta);
       }
     }
     cp_async_wait_all();
