@@ -41,13 +41,13 @@ struct DecodeFp4Params {
   int part_rows;                 // rows of a partial
   int groups;
   int64_t* before;               // ws: [groups + 1] tiles before each group
-  float* part_lse;               // ws: [groups + pairs, part_rows]
+  float* part_stat;              // ws: [groups + pairs, part_rows][8]: maximum, four sums
   float* part_o;                 // ws: [groups + pairs, part_rows, 512]
-  uint64_t part_lse_bytes, part_o_bytes;
+  uint64_t part_stat_bytes, part_o_bytes;
 };
 struct DecodeFp4Scratch {
   int pairs, row_tiles, part_rows, groups;
-  size_t before, part_lse, part_o;     // bytes
+  size_t before, part_stat, part_o;     // bytes
 };
 DecodeFp4Scratch decode_fp4_scratch(int B, int s, int H, int num_splits);
 cudaError_t launch_decode_fp4(const DecodeFp4Params& p, int pairs, cudaStream_t stream);

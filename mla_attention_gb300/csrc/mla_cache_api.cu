@@ -52,7 +52,7 @@ extern "C" {
 size_t mla_decode_fp4_workspace_size(int B, int q_per_req, int H, int num_splits) {
   if (B < 0 || q_per_req < 1 || H < 1 || num_splits < 0) return kWsHeader;
   const DecodeFp4Scratch w = decode_fp4_scratch(B, q_per_req, H, num_splits);
-  return kWsHeader + w.before + w.part_lse + w.part_o;
+  return kWsHeader + w.before + w.part_stat + w.part_o;
 }
 
 mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4, float kv_scale, int64_t num_pages,
@@ -91,9 +91,9 @@ mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4
   p.groups = w.groups;
   char* at = reinterpret_cast<char*>(workspace) + kWsHeader;
   p.before = reinterpret_cast<int64_t*>(at);
-  p.part_lse = reinterpret_cast<float*>(at + w.before);
-  p.part_o = reinterpret_cast<float*>(at + w.before + w.part_lse);
-  p.part_lse_bytes = w.part_lse;
+  p.part_stat = reinterpret_cast<float*>(at + w.before);
+  p.part_o = reinterpret_cast<float*>(at + w.before + w.part_stat);
+  p.part_stat_bytes = w.part_stat;
   p.part_o_bytes = w.part_o;
   return finish(launch_decode_fp4(p, w.pairs, reinterpret_cast<cudaStream_t>(stream)), "mla_decode_fp4");
 }

@@ -9,14 +9,15 @@
 // 64 c .. 64 c + 63 for the scores and the latent columns 128 c .. and 256 + 128 c .. of all its keys for the values.
 //
 // A code times its scale has at most six bits and is exact in f16; q and P are f16 too (P a weight of at most 2^8), the RoPE
-// columns stay bf16 as their MMA's operands, sums are fp32.  24 warps a CTA:
-//   0-3   rows: lanes L and L + 64 of tensor memory hold the same row's scores of 64 keys each; maximum through shared
-//         memory, lazy rescale of O (by more than 2^8), exponentials, P
-//   4, 5  MMAs, in the first CTA alone (one lane issues for both): scores; values
-//   6     the tiles' rows through the block table, up to three tiles ahead
-//   7     the RoPE columns
-//   8-23  4-bit rows into f16, 32 keys and 128 columns each: of K and of V .  The loads of a tile go out
-//         before the last one's are converted.  Latency bounds them: with 8 warps that do both a tile took 9200 cycles
+// columns stay bf16 as their MMA's operands, sums are fp32.  28 warps a CTA:
+//   0-7    rows: lanes L and L + 64 of tensor memory hold the same row's scores of 64 keys each, 32 of them a warp; maximum
+//          through shared memory, lazy rescale of O (by more than 2^8), exponentials, P
+//   8, 9   MMAs, in the first CTA alone (one lane issues for both): scores; values
+//   10     the tiles' rows through the block table, up to three tiles ahead
+//   11     the RoPE columns
+//   12-27  4-bit rows into f16, 32 keys and 128 columns each: of K and of V.  The loads of a tile go out before the last one's are
+//          converted
+// Latency bounds it: of 5000 cycles a tile (64 requests at 4K to 32K tokens, 128 heads) the tensor pipe has 2200.
 // The tiles of all requests are dealt to the pairs in equal shares; fp32 partials of a request that several pairs share
 // are merged by decode_fp4_reduce_kernel.
 #include <math_constants.h>
@@ -29,7 +30,7 @@ namespace mla {
 namespace {
 
 constexpr int kTile = 128, kHalf = 64;                // keys a tile, and the part that one CTA brings for the scores
-constexpr int kThreads = 768, kFirstK = 8, kFirstV = 16;
+constexpr int kThreads = 896, kMmaS = 8, kMmaV = 9, kTableWarp = 10, kFirstK = 12, kFirstV = 20;
 constexpr int kBox = 64 * 128;                        // 64 rows of 128 bytes
 constexpr int kRowSlots = 3;
 constexpr uint32_t kTmemO = 0, kTmemS = 256;          // O: 256 columns; S: two buffers of 64
@@ -40,8 +41,8 @@ constexpr int kOffK = 9 * kBox;                       // 9 boxes
 constexpr int kOffV = 18 * kBox;                      // 2 halves of 4 boxes
 constexpr int kOffP = 26 * kBox;                      // 2 boxes
 constexpr int kOffRows = 28 * kBox;
-constexpr int kOffMax = kOffRows + kRowSlots * kTile * 4;   // [2][2][64]
-constexpr int kOffBars = kOffMax + 4 * 64 * 4;
+constexpr int kOffMax = kOffRows + kRowSlots * kTile * 4;   // [3][64]
+constexpr int kOffBars = kOffMax + 3 * 64 * 4;
 
 struct Bars {
   // in the first CTA, with arrivals of both CTAs' warps
@@ -50,7 +51,7 @@ struct Bars {
   uint64_t kempty[4], vempty[2], qempty, sfull[2], pvdone;
   // in each CTA
   uint64_t rfull[kRowSlots], rfree[kRowSlots];
-  uint64_t pair[2];                                   // warps w and w + 2
+  uint64_t same[2];                                   // the four warps that hold the same rows
   uint64_t drain[2], stall;
   uint32_t tmem_base, abort;
   int64_t share;
@@ -277,10 +278,10 @@ __device__ __forceinline__ void take_query_box(uint32_t box, int k, int lane) {
   fence_proxy_async_smem();
 }
 
-// O of this lane's row times a (its 256 columns)
+// 128 columns of O of this lane's row times a
 __device__ __noinline__ void rescale_o(uint32_t to, float a) {
 #pragma unroll 1
-  for (int c = 0; c < 256; c += 32) {
+  for (int c = 0; c < 128; c += 32) {
     uint32_t o[32];
     tmem_ld32(to + c, o);
     tmem_wait_ld();
@@ -290,29 +291,34 @@ __device__ __noinline__ void rescale_o(uint32_t to, float a) {
   }
   tmem_wait_st();
 }
-// Partials of this warp's 32 rows: columns 128 hh .. and 256 + 128 hh .., 32 at a time through 4 KB of shared memory so that a
-// store brings whole lines.
-__device__ __noinline__ void store_part(const DecodeFp4Params& p, uint32_t to, int64_t slot_row0, int rows, int hh, float inv, uint32_t stage, int lane) {
-#pragma unroll 1
-  for (int c = 0; c < 256; c += 32) {
-    uint32_t o[32];
-    tmem_ld32(to + c, o);
+// 128 columns of this warp's 32 rows as they are (weights relative to the row's maximum), 16 at a time through 2 KB of
+// shared memory so that a store brings whole sectors
+__device__ __noinline__ void store_part(const DecodeFp4Params& p, uint32_t to, int64_t slot_row0, int rows, int col, uint32_t stage, int lane) {
+#pragma unroll 2
+  for (int c = 0; c < 128; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(to + c, o);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      st_shared16(box_unit(stage, lane, i), make_uint4(__float_as_uint(__uint_as_float(o[4 * i]) * inv), __float_as_uint(__uint_as_float(o[4 * i + 1]) * inv),
-                                                       __float_as_uint(__uint_as_float(o[4 * i + 2]) * inv), __float_as_uint(__uint_as_float(o[4 * i + 3]) * inv)));
+    for (int i = 0; i < 4; ++i)
+      st_shared16(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      float* dst = p.part_o + (slot_row0 + r) * kLatent + (c < 128 ? 0 : 128) + 128 * hh + c + 4 * (lane & 7);
-      const uint4 v = ld_shared16(box_unit(stage, r, lane & 7));
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), unit = lane & 3;
+      float* dst = p.part_o + (slot_row0 + r) * kLatent + col + c + 4 * unit;
+      const uint4 v = ld_shared16(stage + r * 64 + ((unit ^ ((r >> 1) & 3)) << 4));
       if (r < rows && guard_span(p.err, G_PART_O, dst, 16, p.part_o, p.part_o_bytes)) *reinterpret_cast<uint4*>(dst) = v;
     }
     __syncwarp();
   }
 }
+// a float's order as an integer's
+__device__ __forceinline__ int32_t ordered(float f) {
+  const int32_t i = __float_as_int(f);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int32_t i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 template <bool kUp>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_fp4_kernel(const __grid_constant__ DecodeFp4Params p) {
@@ -325,18 +331,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     for (int i = 0; i < 4; ++i) mbar_init(&bars.kfull[i], 2 * (i < 3 ? 2 : 3)), mbar_init(&bars.kempty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.vfull[i], 8), mbar_init(&bars.vempty[i], 1);
-      mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 8);
-      mbar_init(&bars.pair[i], 2), mbar_init(&bars.drain[i], 1);
+      mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 16);
+      mbar_init(&bars.same[i], 4), mbar_init(&bars.drain[i], 1);
     }
     mbar_init(&bars.qfull, 18), mbar_init(&bars.qempty, 1);
-    mbar_init(&bars.pfull, 8), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 8);
+    mbar_init(&bars.pfull, 16), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 16);
     for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], 17);
     mbar_init(&bars.stall, 1);
     bars.abort = 0;
     if (smem_u32(smem) & 1023u) bars.abort = DEV_TIMEOUT_BASE | D_ALIGN, record_error(p.err, bars.abort);
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (tid < 192) reinterpret_cast<int32_t*>(smem + kOffMax)[tid] = INT32_MIN;
+  if (warp == kMmaS) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bars.tmem_base)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
@@ -353,107 +360,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   uint32_t u = 0, n = 0;                              // tiles and parts gone through
   bool live = bars.abort == 0;
 
-  if (warp < 4) {
+  if (warp < kMmaS) {
     // ---------------- rows ----------------
-    const int hh = warp >> 1, r = (warp & 1) * 32 + lane;            // key half, row of this CTA
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    // key half hh, 32 of its keys (cc), row r of this CTA; the lanes' 128 columns cc of O
+    const int hh = (warp >> 1) & 1, cc = warp >> 2, r = (warp & 1) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float c = p.scale * 1.4426950408889634f, c2 = c == 0.f ? 1e-30f : c;    // see mask_piece
     const uint64_t c22 = f32x2(c2, c2);
-    float* tile_max = reinterpret_cast<float*>(smem + kOffMax);
+    int32_t* const tile_max = reinterpret_cast<int32_t*>(smem + kOffMax) + r;
     const uint32_t prow = smem_u32(smem + kOffP + hh * kBox);
-    uint32_t pairs = 0;                               // exchanges with the other half's warp
-    auto exchange = [&](float mine, float& other) -> bool {
-      float* x = tile_max + (pairs & 1) * 128;
-      x[hh * 64 + r] = mine;
-      warp_arrive(&bars.pair[warp & 1]);
-      if (!wait.warp(&bars.pair[warp & 1], pairs & 1, D_PAIR)) return false;
-      other = x[(hh ^ 1) * 64 + r];
-      ++pairs;
-      return true;
-    };
+    uint32_t into = 0;                                // tile_max's next third
     for (; live && shares.next(it); ++n) {
       const int row = (int)cta * kHalf + r;            // of the group
       const int seen = row < it.g.rows ? max(0, it.g.len - p.s + 1 + (it.g.row0 + row) / p.H) : 0;
       float m = -CUDART_INF_F, l = 0.f;
       for (int t = it.t0; t < it.t1; ++t, ++u) {
-        const int buf = u & 1, visible = seen - t * kTile - hh * kHalf;
+        const int buf = u & 1;
         if (!wait.warp(&bars.sfull[buf], (u >> 1) & 1, D_SFULL)) { live = false; break; }
         tc_fence_after();
-        const uint32_t from = tbase + lanes + kTmemS + buf * 64;
+        uint32_t s[32];
+        tmem_ld32(tbase + lanes + kTmemS + buf * 64 + 32 * cc, s);
+        tmem_wait_ld();
+        tc_fence_before();
+        first_cta_arrive(&bars.sfree[buf], cta);
+        const int visible = seen - t * kTile - hh * kHalf - 32 * cc;
+        mask_piece<kUp>(s, visible);
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = kUp ? -CUDART_INF_F : CUDART_INF_F;
-#pragma unroll 1
-        for (int q = 0; q < 64; q += 32) {
-          uint32_t s[32];
-          tmem_ld32(from + q, s);
-          tmem_wait_ld();
-          mask_piece<kUp>(s, visible - q);
-          row_extreme<kUp>(s, e);
-        }
-        float mt = visible > 0 ? extreme4<kUp>(e) * c2 : -CUDART_INF_F, other;
-        if (!exchange(mt, other)) { live = false; break; }
-        mt = fmaxf(mt, other);
+        row_extreme<kUp>(s, e);
+        float mt = visible > 0 ? extreme4<kUp>(e) * c2 : -CUDART_INF_F;
+        // the largest of the four warps' (the third that comes next was read by all before they came here)
+        const uint32_t next = into == 2 ? 0 : into + 1;
+        atomicMax(tile_max + 64 * into, ordered(mt));
+        if (hh == 0 && cc == 0) tile_max[64 * next] = INT32_MIN;
+        warp_arrive(&bars.same[warp & 1]);
+        if (!wait.warp(&bars.same[warp & 1], u & 1, D_PAIR)) { live = false; break; }
+        mt = unordered(*reinterpret_cast<volatile int32_t*>(tile_max + 64 * into));
+        into = next;
         float a = 1.f;
         if (mt > m + kRescale || m == -CUDART_INF_F) {
           a = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mt);
           m = mt;
         }
-        l *= a;
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const uint64_t nref = f32x2(-ref, -ref);
         uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-        // P of the 64 keys, packed; then the scores' buffer is free (before the wait below: the next but one tile's scores run
-        // beside this tile's values: 0.436 against 0.30 ms)
-        uint32_t w[32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t s[32];
-          tmem_ld32(from + 32 * q, s);
-          tmem_wait_ld();
-          mask_piece<kUp>(s, visible - 32 * q);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c22, nref), x0, x1);
-            x0 = ex2_approx(x0), x1 = ex2_approx(x1);
-            sum[i & 1] = add_f32x2(sum[i & 1], f32x2(x0, x1));
-            w[16 * q + i] = pack_f16x2(x0, x1);
-          }
+        for (int i = 0; i < 16; ++i) {                 // packed into the first sixteen words
+          float x0, x1;
+          f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c22, nref), x0, x1);
+          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+          sum[i & 1] = add_f32x2(sum[i & 1], f32x2(x0, x1));
+          s[i] = pack_f16x2(x0, x1);
         }
-        tc_fence_before();
-        first_cta_arrive(&bars.sfree[buf], cta);
+        float l0, l1;
+        f32x2_split(add_f32x2(sum[0], sum[1]), l0, l1);
+        l = l * a + (l0 + l1);
         // the last tile's P V is done: P may be written over, O be scaled
         if (u > 0 && !wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) { live = false; break; }
         if (t > it.t0 && __any_sync(~0u, a != 1.f)) {
           tc_fence_after();
-          rescale_o(tbase + lanes + kTmemO, a);
+          rescale_o(tbase + lanes + kTmemO + 128 * cc, a);
           tc_fence_before();
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st_shared16(box_unit(prow, r, i), make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+        for (int i = 0; i < 4; ++i) st_shared16(box_unit(prow, r, 4 * cc + i), make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]));
         fence_proxy_async_smem();
         first_cta_arrive(&bars.pfull, cta);
-        float l0, l1;
-        f32x2_split(add_f32x2(sum[0], sum[1]), l0, l1);
-        l += l0 + l1;
       }
       if (!live) break;
-      float l_other;
-      if (!exchange(l, l_other)) break;
-      l = hh ? l_other + l : l + l_other;              // the same order in both halves
       if (!wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) break;
       tc_fence_after();
       const int64_t slot_row = (int64_t)(it.id + (int)(blockIdx.x / 2)) * p.part_rows + row;
-      // P's place is free until the next tile's, and these warps write that
-      store_part(p, tbase + lanes + kTmemO, slot_row - lane, it.g.rows - (row - lane), hh, l == 0.f ? 0.f : 1.f / l,
-                 smem_u32(smem + kOffP + warp * 4096), lane);
-      if (row < it.g.rows && hh == 0 && guard_span(p.err, G_PART_LSE, p.part_lse + slot_row, 4, p.part_lse, p.part_lse_bytes))
-        p.part_lse[slot_row] = l == 0.f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.f : m) * 0.6931471805599453f + logf(l);
+      // the place of P of these 32 rows and keys: free until the same four warps, all done with it, meet over the next tile's maximum
+      store_part(p, tbase + lanes + kTmemO + 128 * cc, slot_row - lane, it.g.rows - (row - lane), 256 * cc + 128 * hh,
+                 smem_u32(smem + kOffP + hh * kBox + (warp & 1) * 4096 + cc * 2048), lane);
+      float* stat = p.part_stat + slot_row * 8;       // the maximum and the four sums
+      if (row < it.g.rows && guard_span(p.err, G_PART_LSE, stat, 32, p.part_stat, p.part_stat_bytes)) {
+        stat[1 + 2 * hh + cc] = l;
+        if (hh == 0 && cc == 0) stat[0] = m;
+      }
       tc_fence_before();
       first_cta_arrive(&bars.ofree, cta);
     }
-  } else if (warp == 4) {
+  } else if (warp == kMmaS) {
     // ---------------- scores ----------------
     if (cta == 0) {
       if (p.debug_stall) live = live && wait.warp(&bars.stall, 0, D_STALL);
@@ -489,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       mbar_drain(&bars.drain[0], 0);
       __syncwarp();
     }
-  } else if (warp == 5) {
+  } else if (warp == kMmaV) {
     // ---------------- values ----------------
     if (cta == 0) {
       const uint32_t pst = smem_u32(smem + kOffP), vst = smem_u32(smem + kOffV);
@@ -562,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         if (live && t + 1 < it.t1) live = step(xb, xa, t + 2 < it.t1);
       }
     }
-  } else if (warp == 6) {
+  } else if (warp == kTableWarp) {
     // ---------------- rows through the block table ----------------
     for (; live && shares.next(it); ++n) {
       for (int t = it.t0; t < it.t1; ++t, ++u) {
@@ -616,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                     // no MMA of the pair is left, no arrival on its way
-  if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tbase) : "memory");
+  if (warp == kMmaS) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tbase) : "memory");
 }
 
 // A CTA a row, four columns a thread: the partials of the pairs that had tiles of its group, by their log-sum-exp, and the
@@ -624,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
 // took the partials one after the other spent 63 us on one request's 33.
 constexpr int kPairs = 128;
 __global__ void __launch_bounds__(kPairs) decode_fp4_reduce_kernel(const __grid_constant__ DecodeFp4Params p, int pairs) {
-  __shared__ float weight[kPairs], red[8];
+  __shared__ float weight[kPairs], sums[kPairs], red[8];
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t rows = (int64_t)p.kv.B * p.s * p.H, item = blockIdx.x;
   const int64_t b = item / (p.s * p.H);
@@ -638,29 +629,37 @@ __global__ void __launch_bounds__(kPairs) decode_fp4_reduce_kernel(const __grid_
   // pairs whose share meets tiles t0 .. t1 - 1
   const int64_t shares = min((int64_t)pairs, total);
   const int p0 = t1 > t0 ? (int)(((t0 + 1) * shares - 1) / total) : 0, p1 = t1 > t0 ? (int)((t1 * shares - 1) / total) : -1;
-  auto lse_of = [&](int q) -> float {
-    if (q > p1) return -CUDART_INF_F;
-    const float* s = p.part_lse + (int64_t)(g + q) * p.part_rows + (row & (kRows - 1));
-    return guard_span(p.err, G_PART_LSE, s, 4, p.part_lse, p.part_lse_bytes) ? *s : -CUDART_INF_F;
+  // maximum (of scores in powers of two) and sum of pair q's weights
+  auto stat_of = [&](int q, float& sum) -> float {
+    sum = 0.f;
+    const float* s = p.part_stat + ((int64_t)(g + q) * p.part_rows + (row & (kRows - 1))) * 8;
+    if (q > p1 || !guard_span(p.err, G_PART_LSE, s, 32, p.part_stat, p.part_stat_bytes)) return -CUDART_INF_F;
+    const float4 a = *reinterpret_cast<const float4*>(s);
+    sum = (a.y + a.z) + (a.w + s[4]);
+    return a.x;
   };
-  float m = sink;
+  const float sink2 = sink * 1.4426950408889634f;
+  float m = -CUDART_INF_F;
   bool nan = false;
   for (int q = p0 + tid; q <= p1; q += kPairs) {
-    const float l = lse_of(q);
+    float l;
+    m = fmaxf(m, stat_of(q, l));
     nan |= l != l;
-    m = fmaxf(m, l);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
   if (lane == 0) red[tid >> 5] = m;
   nan = __syncthreads_or(nan);
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float wsum = sink == -CUDART_INF_F ? 0.f : expf(sink - m);
+  const float keys_m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));    // -inf: the row sees no key
+  m = fmaxf(keys_m, sink2);
+  float wsum = sink == -CUDART_INF_F ? 0.f : exp2f(sink2 - m);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int q0 = p0; q0 <= p1; q0 += kPairs) {
     __syncthreads();
-    const float l = lse_of(q0 + tid);
-    weight[tid] = l == -CUDART_INF_F ? 0.f : expf(l - m);
+    float l;
+    const float mq = stat_of(q0 + tid, l);
+    weight[tid] = mq == -CUDART_INF_F ? 0.f : exp2f(mq - m);
+    sums[tid] = l;
     __syncthreads();
     const int n = min(kPairs, p1 - q0 + 1);
     for (int i0 = 0; i0 < n; i0 += 8) {
@@ -674,7 +673,7 @@ __global__ void __launch_bounds__(kPairs) decode_fp4_reduce_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float w = i0 + i < n ? weight[i0 + i] : 0.f;
-        wsum += w;
+        wsum += i0 + i < n ? w * sums[i0 + i] : 0.f;
         acc.x += w * v[i].x, acc.y += w * v[i].y, acc.z += w * v[i].z, acc.w += w * v[i].w;
       }
     }
@@ -684,7 +683,7 @@ __global__ void __launch_bounds__(kPairs) decode_fp4_reduce_kernel(const __grid_
   if (guard_span(p.err, G_OUT, out, 8, p.out, (uint64_t)rows * kLatent * 2))
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (tid == 0 && p.lse && guard_span(p.err, G_LSE, p.lse + item, 4, p.lse, (uint64_t)rows * 4))
-    p.lse[item] = nan ? CUDART_NAN_F : wsum > 0.f ? m + logf(wsum) : -CUDART_INF_F;
+    p.lse[item] = nan ? CUDART_NAN_F : keys_m == -CUDART_INF_F ? sink : wsum > 0.f ? fmaf(m, 0.6931471805599453f, logf(wsum)) : -CUDART_INF_F;
 }
 
 }  // namespace
@@ -700,7 +699,7 @@ DecodeFp4Scratch decode_fp4_scratch(int B, int s, int H, int num_splits) {
   const size_t slots = (size_t)(r.groups + r.pairs) * r.part_rows;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   r.before = up((size_t)(r.groups + 1) * 8);
-  r.part_lse = up(slots * 4);
+  r.part_stat = up(slots * 32);
   r.part_o = up(slots * kLatent * 4);
   return r;
 }
