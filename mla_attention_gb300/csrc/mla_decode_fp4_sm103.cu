@@ -13,10 +13,9 @@
 //   0-7    rows: lanes L and L + 64 of tensor memory hold the same row's scores of 64 keys each, 32 of them a warp; maximum
 //          through shared memory, lazy rescale of O (by more than 2^8), exponentials, P
 //   8, 9   MMAs, in the first CTA alone (one lane issues for both): scores; values
-//   10     the tiles' rows through the block table, up to three tiles ahead
+//   10     the tiles' rows through the block table, up to three tiles ahead, and their lines asked for in L2
 //   11     the RoPE columns
-//   12-27  4-bit rows into f16, 32 keys and 128 columns each: of K and of V.  The loads of a tile go out before the last one's are
-//          converted
+//   12-27  4-bit rows into f16, 32 keys and 128 columns each: of K and of V
 // Latency bounds it: of 5000 cycles a tile (64 requests at 4K to 32K tokens, 128 heads) the tensor pipe has 2200.
 // The tiles of all requests are dealt to the pairs in equal shares; fp32 partials of a request that several pairs share
 // are merged by decode_fp4_reduce_kernel.
@@ -519,22 +518,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     uint64_t* const empty = is_k ? &bars.kempty[part] : &bars.vempty[part];
     uint64_t* const full = is_k ? &bars.kfull[part] : &bars.vfull[part];
     uint32_t slot = 0, turn = 0;                      // of the next tile's rows
-    Raw xa, xb;
-    auto load = [&](Raw& x) -> bool {
+    Raw x;
+    auto load = [&]() -> bool {
       if (!wait.warp(&bars.rfull[slot], turn, D_RFULL)) return false;
       load_raw(p, x, row_slots + slot * kTile + first, col, lane, cache_bytes);
       warp_arrive(&bars.rfree[slot]);
       if (++slot == kRowSlots) slot = 0, turn ^= 1;
-      return true;
-    };
-    // the next tile's loads go out, then this one's are converted
-    auto step = [&](const Raw& x, Raw& next, bool more) -> bool {
-      if (more && !load(next)) return false;
-      if (!wait.warp(empty, (u & 1) ^ 1, D_KEMPTY)) return false;
-      convert_raw(x, boxes, r0, lane);
-      fence_proxy_async_smem();
-      first_cta_arrive(full, cta);
-      ++u;
       return true;
     };
     for (; live && shares.next(it); ++n) {
@@ -543,14 +532,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY)) break;
         ask_query_box(p, it.g, (int)cta * kHalf, qbox, w, lane);
       }
-      if (!load(xa)) break;
+      if (!load()) break;
       if (is_k) {
         take_query_box(qbox, w, lane);
         first_cta_arrive(&bars.qfull, cta);
       }
-      for (int t = it.t0; t < it.t1 && live; t += 2) {
-        live = step(xa, xb, t + 1 < it.t1);
-        if (live && t + 1 < it.t1) live = step(xb, xa, t + 2 < it.t1);
+      for (int t = it.t0; t < it.t1; ++t, ++u) {
+        if (!wait.warp(empty, (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
+        convert_raw(x, boxes, r0, lane);
+        fence_proxy_async_smem();
+        first_cta_arrive(full, cta);
+        // the next tile's loads go out while its place is not free yet
+        if (t + 1 < it.t1 && !load()) { live = false; break; }
       }
     }
   } else if (warp == kTableWarp) {
@@ -567,6 +560,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
             const int page = guarded_int(p.err, p.kv.block_table, (int64_t)it.g.b * p.kv.max_pages + pg, (int64_t)p.kv.B * p.kv.max_pages);
             if (page >= 0 && page < p.kv.num_pages) at[i] = page * p.kv.page_size + (j - pg * p.kv.page_size);
             else record_error(p.err, DEV_RANGE_BASE | Y_PAGE);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {                  // either CTA asks for the keys of its scores
+          const int a = cta == 0 ? at[i] : at[2 + i];
+          if (a >= 0) {
+            const uint8_t* row = p.kv.cache + (int64_t)a * kFp4Row;
+            for (int o = 0; o < kFp4Row; o += 128) prefetch_l2(row + o);
+            prefetch_l2(row + kFp4Row - 1);
           }
         }
         const uint32_t slot = u % kRowSlots;
