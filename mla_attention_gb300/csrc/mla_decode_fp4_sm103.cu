@@ -15,7 +15,7 @@
 //   8, 9   MMAs, in the first CTA alone (one lane issues for both): scores; values
 //   10     the tiles' rows through the block table, up to three tiles ahead, and their lines asked for in L2
 //   11     the RoPE columns
-//   12-27  4-bit rows into f16, 32 keys and 128 columns each: of K and of V
+//   12-27  4-bit rows into f16, 16 keys and 256 columns each: of K and of V
 // Latency bounds it: of 5000 cycles a tile (64 requests at 4K to 32K tokens, 128 heads) the tensor pipe has 2200.
 // The tiles of all requests are dealt to the pairs in equal shares; fp32 partials of a request that several pairs share
 // are merged by decode_fp4_reduce_kernel.
@@ -45,9 +45,9 @@ constexpr int kOffBars = kOffMax + 3 * 64 * 4;
 
 struct Bars {
   // in the first CTA, with arrivals of both CTAs' warps
-  uint64_t kfull[4], vfull[2], qfull, pfull, sfree[2], ofree;
+  uint64_t kfull[2], vfull[2], qfull, pfull[2], sfree[2], ofree;
   // in each CTA, by commits to both
-  uint64_t kempty[4], vempty[2], qempty, sfull[2], pvdone;
+  uint64_t kempty[2], vempty[2], qempty, sfull[2], pvdone;
   // in each CTA
   uint64_t rfull[kRowSlots], rfree[kRowSlots];
   uint64_t same[2];                                   // the four warps that hold the same rows
@@ -173,21 +173,21 @@ __device__ __forceinline__ void first_cta_arrive(uint64_t* bar, uint32_t cta) {
 #define MLA_STEP2(P, ID) MLA_MMA2("%0", "x", "y", ID, P) "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
 #define MLA_BOX2(P, ID) MLA_STEP2(P, ID) MLA_STEP2("t", ID) MLA_STEP2("t", ID) MLA_MMA2("%0", "x", "y", ID, "t") \
   "add.s64 x, x, 506;\n\tadd.s64 y, y, 506;\n\t"
-// S (+)= Q K^T over two boxes of 64 columns, 64 rows each in either CTA
-__device__ __forceinline__ void mma2_scores2(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+// S = Q K^T over four boxes of 64 columns, 64 rows each in either CTA
+__device__ __forceinline__ void mma2_scores4(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
   asm volatile(
-      "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
-      MLA_BOX2("p", "%3") MLA_BOX2("t", "%3") "}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      "{\n\t.reg .pred f, t;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.u32 f, %3, %3;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
+      MLA_BOX2("f", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id)
       : "memory");
 }
-// S += over the last two and the RoPE columns, whose operands are bf16
-__device__ __forceinline__ void mma2_scores3(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t id_pe) {
+// S += over the other four and the RoPE columns, whose operands are bf16
+__device__ __forceinline__ void mma2_scores5(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t id_pe) {
   asm volatile(
       "{\n\t.reg .pred t;\n\t.reg .b64 x, y;\n\t"
       "setp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
-      MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%4") "}" ::"r"(d),
+      MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%3") MLA_BOX2("t", "%4") "}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(id_pe)
       : "memory");
 }
@@ -213,8 +213,9 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
                : "memory");
 }
 
-// 32 rows of 128 columns as they lie: four lanes a row, 32 columns each, and their two scales.  (Two lanes a row and 64
-// columns ask the first-level cache for twice as many lines: 0.486 against 0.42 ms.)
+// 16 rows of 256 columns as they lie: eight lanes a row, 32 columns each, and their two scales.  (Fewer lanes a row ask the
+// first-level cache for more lines, and its data pipe, which the tensor core's operands and the stores below pass too, was what
+// bounded the kernel: four lanes a row 0.350 ms, two 0.39.)
 struct Raw {
   uint4 v[4];
   uint32_t sc[4];
@@ -222,32 +223,34 @@ struct Raw {
 __device__ __forceinline__ void load_raw(const DecodeFp4Params& p, Raw& x, const int32_t* at, int col, int lane, uint64_t cache_bytes) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int a = at[8 * i + (lane >> 2)];
+    const int a = at[4 * i + (lane >> 3)];
     const uint8_t* r = p.kv.cache + (int64_t)a * kFp4Row;
     x.v[i] = make_uint4(0, 0, 0, 0), x.sc[i] = 0;
     if (a >= 0 && guard_span(p.err, G_STEP_IN, r, kFp4Row, p.kv.cache, cache_bytes)) {
-      x.v[i] = *reinterpret_cast<const uint4*>(r + col / 2 + 16 * (lane & 3));
-      x.sc[i] = *reinterpret_cast<const uint16_t*>(r + kFp4Codes + col / 16 + 2 * (lane & 3));
+      x.v[i] = *reinterpret_cast<const uint4*>(r + col / 2);
+      x.sc[i] = *reinterpret_cast<const uint16_t*>(r + kFp4Codes + col / 16);
     }
   }
 }
-// into two boxes of 64 columns, rows r0 .. r0 + 31 (r0 a multiple of 8).  The lanes of the second box store their
-// 16-byte pieces in another order, so that eight lanes meet eight banks.
+// into four boxes of 64 columns, rows r0 .. r0 + 15.  A lane stores its four 16-byte pieces from its box's number on, so that
+// the eight lanes of a row meet eight banks.
 __device__ __forceinline__ void convert_raw(const Raw& x, uint32_t boxes, int r0, int lane) {
-  const int second = (lane >> 1) & 1, half = lane & 1, r = lane >> 2;
-  const uint32_t row = boxes + second * kBox + (r0 + r) * 128;
-  uint32_t to[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) to[j] = row + (((4 * half + (j ^ (2 * second))) ^ (r & 7)) << 4);
+  const int b = (lane >> 1) & 3, half = lane & 1;
+  const bool odd = b & 1, high = b & 2;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint2 s = fp4_scales2(x.sc[i]);
+    const int r = r0 + 4 * i + (lane >> 3);
+    const uint32_t row = boxes + b * kBox + r * 128;
+    const uint2 s = fp4_scales2(x.sc[i]);
     uint4 v = x.v[i];
-    if (second) s = make_uint2(s.y, s.x), v = make_uint4(v.z, v.w, v.x, v.y);
-    st_shared16(to[0] + i * 1024, fp4x8_to_f16(v.x, s.x));
-    st_shared16(to[1] + i * 1024, fp4x8_to_f16(v.y, s.x));
-    st_shared16(to[2] + i * 1024, fp4x8_to_f16(v.z, s.y));
-    st_shared16(to[3] + i * 1024, fp4x8_to_f16(v.w, s.y));
+    if (odd) v = make_uint4(v.y, v.z, v.w, v.x);
+    if (high) v = make_uint4(v.z, v.w, v.x, v.y);
+    // pieces b, b + 1, b + 2, b + 3 (mod 4); 0 and 1 have the first scale
+    const uint32_t s0 = high ? s.y : s.x, s1 = odd != high ? s.y : s.x, s2 = high ? s.x : s.y, s3 = odd != high ? s.x : s.y;
+    st_shared16(row + (((4 * half + b) ^ (r & 7)) << 4), fp4x8_to_f16(v.x, s0));
+    st_shared16(row + (((4 * half + ((b + 1) & 3)) ^ (r & 7)) << 4), fp4x8_to_f16(v.y, s1));
+    st_shared16(row + (((4 * half + (b ^ 2)) ^ (r & 7)) << 4), fp4x8_to_f16(v.z, s2));
+    st_shared16(row + (((4 * half + ((b + 3) & 3)) ^ (r & 7)) << 4), fp4x8_to_f16(v.w, s3));
   }
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
@@ -327,14 +330,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   const uint32_t cta = cluster_ctarank();
   const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * kFp4Row;
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&bars.kfull[i], 2 * (i < 3 ? 2 : 3)), mbar_init(&bars.kempty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.kfull[i], 2 * (4 + i)), mbar_init(&bars.kempty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.vfull[i], 8), mbar_init(&bars.vempty[i], 1);
+      mbar_init(&bars.vfull[i], 8), mbar_init(&bars.vempty[i], 1), mbar_init(&bars.pfull[i], 8);
       mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 16);
       mbar_init(&bars.same[i], 4), mbar_init(&bars.drain[i], 1);
     }
     mbar_init(&bars.qfull, 18), mbar_init(&bars.qempty, 1);
-    mbar_init(&bars.pfull, 16), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 16);
+    mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 16);
     for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], 17);
     mbar_init(&bars.stall, 1);
     bars.abort = 0;
@@ -416,9 +419,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         float l0, l1;
         f32x2_split(add_f32x2(sum[0], sum[1]), l0, l1);
         l = l * a + (l0 + l1);
-        // the last tile's P V is done: P may be written over, O be scaled
-        if (u > 0 && !wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) { live = false; break; }
+        // the last tile's P V of this key half is done: P of the half may be written over (and O be scaled when all of it is)
+        if (u > 0 && !wait.warp(&bars.vempty[hh], (u - 1) & 1, D_VEMPTY)) { live = false; break; }
         if (t > it.t0 && __any_sync(~0u, a != 1.f)) {
+          if (!wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) { live = false; break; }
           tc_fence_after();
           rescale_o(tbase + lanes + kTmemO + 128 * cc, a);
           tc_fence_before();
@@ -426,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
 #pragma unroll
         for (int i = 0; i < 4; ++i) st_shared16(box_unit(prow, r, 4 * cc + i), make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]));
         fence_proxy_async_smem();
-        first_cta_arrive(&bars.pfull, cta);
+        first_cta_arrive(&bars.pfull[hh], cta);
       }
       if (!live) break;
       if (!wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) break;
@@ -454,21 +458,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         for (int t = it.t0; t < it.t1; ++t, ++u) {
           const int buf = u & 1;
           if (!wait.warp(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, D_SFREE, true)) { live = false; break; }
-#pragma unroll 1
-          for (int g = 0; g < 3; ++g) {
-            if (!wait.warp(&bars.kfull[g], u & 1, D_KFULL, true)) { live = false; break; }
-            tc_fence_after();
-            if (elect_one()) {
-              mma2_scores2(tbase + kTmemS + buf * 64, qdesc + g * (2 * kBox / 16), kdesc + g * (2 * kBox / 16), id, g > 0 ? 1u : 0u);
-              commit2(&bars.kempty[g]);
-            }
-            __syncwarp();
-          }
-          if (!live || !wait.warp(&bars.kfull[3], u & 1, D_KFULL, true)) { live = false; break; }
+          if (!wait.warp(&bars.kfull[0], u & 1, D_KFULL, true)) { live = false; break; }
           tc_fence_after();
           if (elect_one()) {
-            mma2_scores3(tbase + kTmemS + buf * 64, qdesc + 6 * kBox / 16, kdesc + 6 * kBox / 16, id, id_pe);
-            commit2(&bars.kempty[3]);
+            mma2_scores4(tbase + kTmemS + buf * 64, qdesc, kdesc, id);
+            commit2(&bars.kempty[0]);
+          }
+          __syncwarp();
+          if (!wait.warp(&bars.kfull[1], u & 1, D_KFULL, true)) { live = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            mma2_scores5(tbase + kTmemS + buf * 64, qdesc + 4 * kBox / 16, kdesc + 4 * kBox / 16, id, id_pe);
+            commit2(&bars.kempty[1]);
             commit2(&bars.sfull[buf]);
             if (t == it.t1 - 1) commit2(&bars.qempty);
           }
@@ -487,10 +488,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       for (; live && shares.next(it); ++n) {
         if (n > 0 && !wait.warp(&bars.ofree, (n - 1) & 1, D_OFREE, true)) break;
         for (int t = it.t0; t < it.t1; ++t, ++u) {
-          if (!wait.warp(&bars.pfull, u & 1, D_PFULL, true)) { live = false; break; }
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            if (!wait.warp(&bars.vfull[h], u & 1, D_VFULL, true)) { live = false; break; }
+            if (!wait.warp(&bars.vfull[h], u & 1, D_VFULL, true) || !wait.warp(&bars.pfull[h], u & 1, D_PFULL, true)) { live = false; break; }
             tc_fence_after();
             if (elect_one()) {
               mma2_values(tbase + kTmemO, tbase + kTmemO + 128, sdesc_sw128(pst + h * kBox, 16, 1024), sdesc_sw128(vst + h * 4 * kBox, kBox, 1024),
@@ -510,11 +510,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   } else if (warp >= kFirstK) {
     // ---------------- 4-bit rows into f16 ----------------
     const bool is_k = warp < kFirstV;
-    // K: 32 rows w % 2 of this CTA's keys, columns 128 (w / 2); V: rows w % 2 of key half w / 4, the CTA's columns (w / 2) % 2
-    const int w = (warp - kFirstK) & 7, part = is_k ? w >> 1 : w >> 2, r0 = (w & 1) * 32;
-    const int col = is_k ? 128 * (w >> 1) : 256 * ((w >> 1) & 1) + 128 * (int)cta;
+    // 16 rows w % 4: of K this CTA's keys and columns 256 (w / 4) ..; of V key half w / 4 and the CTA's columns
+    const int w = (warp - kFirstK) & 7, part = w >> 2, r0 = (w & 3) * 16, chunk = lane & 7;
+    const int col = is_k ? 256 * part + 32 * chunk : 256 * (chunk >> 2) + 128 * (int)cta + 32 * (chunk & 3);
     const int first = (is_k ? (int)cta : part) * kHalf + r0;       // of the tile's keys
-    const uint32_t boxes = smem_u32(smem + (is_k ? kOffK : kOffV) + 2 * (w >> 1) * kBox);
+    const uint32_t boxes = smem_u32(smem + (is_k ? kOffK : kOffV) + 4 * part * kBox);
     uint64_t* const empty = is_k ? &bars.kempty[part] : &bars.vempty[part];
     uint64_t* const full = is_k ? &bars.kfull[part] : &bars.vfull[part];
     uint32_t slot = 0, turn = 0;                      // of the next tile's rows
@@ -589,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       first_cta_arrive(&bars.qfull, cta);
       for (int t = it.t0; t < it.t1; ++t, ++u) {
         const uint32_t slot = u % kRowSlots;
-        if (!wait.warp(&bars.rfull[slot], (u / kRowSlots) & 1, D_RFULL) || !wait.warp(&bars.kempty[3], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
+        if (!wait.warp(&bars.rfull[slot], (u / kRowSlots) & 1, D_RFULL) || !wait.warp(&bars.kempty[1], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
         const int32_t* at = row_slots + slot * kTile + cta * kHalf + (lane >> 3);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -601,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         warp_arrive(&bars.rfree[slot]);
         cp_async_wait_all();
         fence_proxy_async_smem();
-        first_cta_arrive(&bars.kfull[3], cta);
+        first_cta_arrive(&bars.kfull[1], cta);
       }
     }
     cp_async_wait_all();
