@@ -91,6 +91,7 @@ struct CompactParams {
   const int32_t* count;          // [B]
   float* weights;                // [B, width] rows at stride, or null
   uint32_t* err;
+  uint32_t spin_limit, debug_stall;
   int64_t stride;
   int K, width;
 };

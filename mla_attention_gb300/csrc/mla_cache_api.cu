@@ -210,6 +210,8 @@ mla_status mla_compact_rows(void* kv_cache, int row_bytes, int64_t num_pages, in
   p.count = count;
   p.weights = weights;
   p.err = reinterpret_cast<uint32_t*>(workspace);
+  p.spin_limit = spin_limit();
+  p.debug_stall = debug_stall();
   p.stride = weights_stride;
   p.K = K;
   p.width = width;
