@@ -46,14 +46,14 @@ __device__ __forceinline__ bool moving(const CompactParams& p, int64_t i, int co
   return false;
 }
 // cache row of row j of request b, -1 where its page is none
-__device__ __forceinline__ int64_t row_at(const CompactParams& p, int b, int j, bool report) {
+__device__ __forceinline__ int row_at(const CompactParams& p, int b, int j, bool report) {
   const int pg = j / p.kv.page_size;
   const int page = guarded_int(p.err, p.kv.block_table, (int64_t)b * p.kv.max_pages + pg, (int64_t)p.kv.B * p.kv.max_pages);
   if (page < 0 || page >= p.kv.num_pages) {
     if (report) record_error(p.err, DEV_RANGE_BASE | Y_COMPACT);
     return -1;
   }
-  return (int64_t)page * p.kv.page_size + (j - pg * p.kv.page_size);
+  return page * p.kv.page_size + (j - pg * p.kv.page_size);
 }
 
 __device__ __forceinline__ void move_weights(const CompactParams& p, int b, int rank, int ranks, int count, int64_t limit) {
@@ -81,7 +81,7 @@ __device__ __forceinline__ void move_weights(const CompactParams& p, int b, int 
 // A cluster: request and slice, `units` 16-byte columns of its rows (the slice behind the last one: the weights).
 __global__ void __launch_bounds__(kThreads, 2) compact_rows_kernel(const __grid_constant__ CompactParams p, int units, int slices, int ranks) {
   extern __shared__ __align__(16) uint4 pieces[];     // [stage][piece of a thread][mover]
-  __shared__ longlong2 moves[kRing][kMaxRows];        // cache rows (from, to), from < 0: stays
+  __shared__ int2 moves[kRing][kMaxRows];        // cache rows (from, to), from < 0: stays
   __shared__ Bars bars;
   const int group = blockIdx.x / ranks, rank = blockIdx.x - group * ranks, all_slices = slices + (p.weights ? 1 : 0);
   const int b = group / all_slices, slice = group - b * all_slices, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -125,9 +125,9 @@ __global__ void __launch_bounds__(kThreads, 2) compact_rows_kernel(const __grid_
       for (int k = 0; k < kLooks; ++k) {
         if (k * 32 + lane >= rows) continue;
         const int64_t i = place(c, k);
-        longlong2 m = make_longlong2(-1, -1);
+        int2 m = make_int2(-1, -1);
         if (moving(p, i, count, en[k], limit, report)) {
-          m = make_longlong2(row_at(p, b, en[k].y, report), row_at(p, b, (int)i, report));
+          m = make_int2(row_at(p, b, en[k].y, report), row_at(p, b, (int)i, report));
           if (m.y < 0) m.x = -1;
         }
         moves[slot][k * 32 + lane] = m;
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, 2) compact_rows_kernel(const __grid_
       const uint32_t stage = smem_u32(pieces + (c % kStages) * kPer * kMovers + tid);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const int64_t from = at[k] >= 0 ? moves[c % kRing][at[k]].x : -1;
-        const uint8_t* s = cache + from * p.kv.row_bytes + off[k];
+        const int from = at[k] >= 0 ? moves[c % kRing][at[k]].x : -1;
+        const uint8_t* s = cache + (int64_t)from * p.kv.row_bytes + off[k];
         if (from >= 0 && guard_span(p.err, G_STEP_IN, s, 16, p.kv.cache, ext)) cp_async16_zfill(stage + k * kMovers * 16, s, 16);
       }
       cp_async_arrive_noinc(&bars.landed[c % kStages]);
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 2) compact_rows_kernel(const __grid_
       const uint4* stage = pieces + (c % kStages) * kPer * kMovers + tid;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const longlong2 m = at[k] >= 0 ? moves[c % kRing][at[k]] : make_longlong2(-1, -1);
-        uint8_t* d = cache + m.y * p.kv.row_bytes + off[k];
+        const int2 m = at[k] >= 0 ? moves[c % kRing][at[k]] : make_int2(-1, -1);
+        uint8_t* d = cache + (int64_t)m.y * p.kv.row_bytes + off[k];
         if (m.x >= 0 && guard_span(p.err, G_STEP_OUT, d, 16, p.kv.cache, ext)) *reinterpret_cast<uint4*>(d) = stage[k * kMovers];
       }
       warp_arrive(&bars.free[c % kRing]);
