@@ -614,8 +614,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
 
 // A CTA a row, four columns a thread: the partials of the pairs that had tiles of its group, by their log-sum-exp, and the
 // sink.  A thread a pair finds the weights (a pass over kPairs of them), eight partials' loads go out together: a warp that
-// took the partials one after the other spent 63 us on one request's 33.
-constexpr int kPairs = 128;
+// took the partials one after the other spent 63 us on one request's 33.  Up to kFew partials, as among many requests, need no
+// pass of their own for the weights (8192 rows 20 -> 14 us; eight in registers 22).
+constexpr int kPairs = 128, kFew = 4;
 __global__ void __launch_bounds__(kPairs) decode_fp4_reduce_kernel(const __grid_constant__ DecodeFp4Params p, int pairs) {
   __shared__ float weight[kPairs], sums[kPairs], red[8];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -641,42 +642,68 @@ __global__ void __launch_bounds__(kPairs) decode_fp4_reduce_kernel(const __grid_
     return a.x;
   };
   const float sink2 = sink * 1.4426950408889634f;
-  float m = -CUDART_INF_F;
-  bool nan = false;
-  for (int q = p0 + tid; q <= p1; q += kPairs) {
-    float l;
-    m = fmaxf(m, stat_of(q, l));
-    nan |= l != l;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-  if (lane == 0) red[tid >> 5] = m;
-  nan = __syncthreads_or(nan);
-  const float keys_m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));    // -inf: the row sees no key
-  m = fmaxf(keys_m, sink2);
-  float wsum = sink == -CUDART_INF_F ? 0.f : exp2f(sink2 - m);
+  float m = -CUDART_INF_F, keys_m = -CUDART_INF_F;      // -inf: the row sees no key
+  float wsum;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int q0 = p0; q0 <= p1; q0 += kPairs) {
-    __syncthreads();
-    float l;
-    const float mq = stat_of(q0 + tid, l);
-    weight[tid] = mq == -CUDART_INF_F ? 0.f : exp2f(mq - m);
-    sums[tid] = l;
-    __syncthreads();
-    const int n = min(kPairs, p1 - q0 + 1);
-    for (int i0 = 0; i0 < n; i0 += 8) {
-      float4 v[8];
+  bool nan = false;
+  auto part_at = [&](int q) { return p.part_o + ((int64_t)(g + q) * p.part_rows + (row & (kRows - 1))) * kLatent + 4 * tid; };
+  if (p1 - p0 < kFew) {
+    // few partials: each thread takes them all, statistics and columns asked for together
+    float of_m[kFew], of_sum[kFew];
+    float4 v[kFew];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float* src = p.part_o + ((int64_t)(g + q0 + i0 + i) * p.part_rows + (row & (kRows - 1))) * kLatent + 4 * tid;
-        const bool in = i0 + i < n && weight[i0 + i] != 0.f && guard_span(p.err, G_PART_O, src, 16, p.part_o, p.part_o_bytes);
-        v[i] = in ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+    for (int i = 0; i < kFew; ++i) {
+      of_m[i] = stat_of(p0 + i, of_sum[i]);
+      const float* src = part_at(p0 + i);
+      const bool in = p0 + i <= p1 && guard_span(p.err, G_PART_O, src, 16, p.part_o, p.part_o_bytes);
+      v[i] = in ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = i0 + i < n ? weight[i0 + i] : 0.f;
-        wsum += i0 + i < n ? w * sums[i0 + i] : 0.f;
-        acc.x += w * v[i].x, acc.y += w * v[i].y, acc.z += w * v[i].z, acc.w += w * v[i].w;
+    for (int i = 0; i < kFew; ++i) keys_m = fmaxf(keys_m, of_m[i]), nan |= of_sum[i] != of_sum[i];
+    m = fmaxf(keys_m, sink2);
+    wsum = sink == -CUDART_INF_F ? 0.f : exp2f(sink2 - m);
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+      if (of_m[i] == -CUDART_INF_F) continue;
+      const float w = exp2f(of_m[i] - m);
+      wsum += w * of_sum[i];
+      if (w != 0.f) acc.x += w * v[i].x, acc.y += w * v[i].y, acc.z += w * v[i].z, acc.w += w * v[i].w;
+    }
+  } else {
+    for (int q = p0 + tid; q <= p1; q += kPairs) {
+      float l;
+      m = fmaxf(m, stat_of(q, l));
+      nan |= l != l;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    if (lane == 0) red[tid >> 5] = m;
+    nan = __syncthreads_or(nan);
+    keys_m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    m = fmaxf(keys_m, sink2);
+    wsum = sink == -CUDART_INF_F ? 0.f : exp2f(sink2 - m);
+    for (int q0 = p0; q0 <= p1; q0 += kPairs) {
+      __syncthreads();
+      float l;
+      const float mq = stat_of(q0 + tid, l);
+      weight[tid] = mq == -CUDART_INF_F ? 0.f : exp2f(mq - m);
+      sums[tid] = l;
+      __syncthreads();
+      const int n = min(kPairs, p1 - q0 + 1);
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float* src = part_at(q0 + i0 + i);
+          const bool in = i0 + i < n && weight[i0 + i] != 0.f && guard_span(p.err, G_PART_O, src, 16, p.part_o, p.part_o_bytes);
+          v[i] = in ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float w = i0 + i < n ? weight[i0 + i] : 0.f;
+          wsum += i0 + i < n ? w * sums[i0 + i] : 0.f;
+          acc.x += w * v[i].x, acc.y += w * v[i].y, acc.z += w * v[i].z, acc.w += w * v[i].w;
+        }
       }
     }
   }
