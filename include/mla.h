@@ -483,7 +483,7 @@ mla_status mla_kv_append_fp4(const void* c_kv, int64_t c_kv_stride, const void* 
  * 2^-14 keep an absolute error of 2^-25) and those of the RoPE part on bf16 ones; sums are fp32.  A page id outside
  * [0, num_pages) reads as keys of zeros, a length outside [0, max_pages * page_size] is cut to it; both
  * record MLA_ERR_DEVICE_RANGE (details 0x207a, 0x207b).  Rows of the block table behind a request's last page
- * are not read.
+ * are not read.  With several tokens a request, a NaN in a row that the later ones see makes the earlier ones' outputs NaN too.
  * workspace_bytes >= mla_decode_fp4_workspace_size(B, q_per_req, H, num_splits).
  */
 size_t mla_decode_fp4_workspace_size(int B, int q_per_req, int H, int num_splits);
@@ -544,7 +544,8 @@ mla_status mla_select_keys(const float* weights, int64_t weights_stride, int wid
  * weights  (nullable) fp32 [B, width] at row stride weights_stride >= width.
  * An entry that is not above the one before it, lies below its own place i or outside the table (or the weights' width), or
  * whose pages are not in [0, num_pages), is skipped and recorded (MLA_ERR_DEVICE_RANGE, 0x207d), as is a request whose
- * count is not in [0, K].  workspace: >= 256 bytes (the status word).
+ * count is not in [0, K].  A call that ends in MLA_ERR_TIMEOUT may have moved part of a request's rows.
+ * workspace: >= 256 bytes (the status word).
  */
 size_t mla_compact_rows_workspace_size(int B);
 mla_status mla_compact_rows(void* kv_cache, int row_bytes, int64_t num_pages, int page_size, const int32_t* block_table,

@@ -24,19 +24,6 @@ __device__ __forceinline__ int paged_len(const PagedRows& kv, uint32_t* err, int
   return (int)n;
 }
 
-// row of key j of request b, null (and recorded) where its page is none
-__device__ __forceinline__ const uint8_t* paged_row(const PagedRows& kv, uint32_t* err, int b, int j) {
-  const int pg = j / kv.page_size;
-  const int page = guarded_int(err, kv.block_table, (int64_t)b * kv.max_pages + pg, (int64_t)kv.B * kv.max_pages);
-  if (page < 0 || page >= kv.num_pages) {
-    record_error(err, DEV_RANGE_BASE | Y_PAGE);
-    return nullptr;
-  }
-  const uint8_t* row = kv.cache + ((int64_t)page * kv.page_size + (j - pg * kv.page_size)) * kv.row_bytes;
-  const bool in = guard_span(err, G_STEP_IN, row, kv.row_bytes, kv.cache, (uint64_t)kv.num_pages * kv.page_size * kv.row_bytes);
-  return in ? row : nullptr;
-}
-
 // eight codes (a word, lowest four bits first) times a scale, in f16: exact, a product has at most six bits
 __device__ __forceinline__ uint4 fp4x8_to_f16(uint32_t w, uint32_t scale2) {
   uint32_t r[4];
@@ -63,11 +50,6 @@ __device__ __forceinline__ uint4 bf16x8_to_f16(const uint4& v) {
   return make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
 }
 
-// two codes (low half first) as f16
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
-  return (uint32_t)h.x | (uint32_t)h.y << 16;
-}
 __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
 }

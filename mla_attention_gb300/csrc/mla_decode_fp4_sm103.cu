@@ -16,7 +16,11 @@
 //   10     the tiles' rows through the block table, up to three tiles ahead, and their lines asked for in L2
 //   11     the RoPE columns
 //   12-27  4-bit rows into f16, 16 keys and 256 columns each: of K and of V
-// Latency bounds it: of 5000 cycles a tile (64 requests at 4K to 32K tokens, 128 heads) the tensor pipe has 2200.
+// 64 requests of 4096 to 32768 keys with 128 heads: 0.347 ms, 0.95 PFLOP/s.  No pipe is full: of 5000 cycles a tile the tensor
+// pipe has 2200 (36 % with 32 requests), the issue slots 40 %, the first-level cache's data pipe 64 %, DRAM 19 %, and without any one
+// of the parts it takes some 5 % less; what is left is the chain rows, conversion, scores, exponentials, values of two tiles at a
+// time.  A second set of row registers a converting warp: 0.362.  One request of 4097 keys: 25 us, of which 5.5 join the partials and 18
+// are one chain of loads through the lengths, the table and the rows, the products and the partials' way out.
 // The tiles of all requests are dealt to the pairs in equal shares; fp32 partials of a request that several pairs share
 // are merged by decode_fp4_reduce_kernel.
 #include <math_constants.h>
@@ -213,9 +217,8 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
                : "memory");
 }
 
-// 16 rows of 256 columns as they lie: eight lanes a row, 32 columns each, and their two scales.  (Fewer lanes a row ask the
-// first-level cache for more lines, and its data pipe, which the tensor core's operands and the stores below pass too, was what
-// bounded the kernel: four lanes a row 0.350 ms, two 0.39.)
+// 16 rows of 256 columns as they lie: eight lanes a row, 32 columns each, and their two scales (four lanes a row ask the
+// first-level cache for twice as many lines; 0.350 ms for 0.349)
 struct Raw {
   uint4 v[4];
   uint32_t sc[4];

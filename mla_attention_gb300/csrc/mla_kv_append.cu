@@ -19,7 +19,8 @@
 // the warp's heads.
 // Prefill of 8192 tokens with 128 heads and the rows written too 47.4 us, 93 % of the copy's bandwidth (the cache
 // stays partly in L2); 32768 rows to e4m3 without heads 14.1 to 14.8 us, 65 to 68 %, bound by issue and load latency; a decode
-// step of 64 tokens with 128 heads 2.4 to 2.6 us.
+// step of 64 tokens with 128 heads 2.4 to 2.6 us.  To 4 bits the prefill takes 54 us, 81 % (two roundings of each code), the
+// decode step 3.3.
 #include "fp4_rows.cuh"
 #include "mla_step.h"
 #include "row_vec.cuh"
