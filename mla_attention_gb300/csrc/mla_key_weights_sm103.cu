@@ -479,24 +479,25 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
   if (warp == 4) tmem_dealloc(tbase, kTmemCols);
 }
 
-// Several chunks of query rows: a range's sums are those of the CTAs that had units of it, in their order.  A CTA per range.
-__global__ void __launch_bounds__(kSub * kTile) key_weights_sum_kernel(const __grid_constant__ KeyWeightsParams p, int shares, int per_request) {
+// Several chunks of query rows: a range's sums are those of the CTAs that had units of it, in their order.  A CTA per tile.
+__global__ void __launch_bounds__(kTile) key_weights_sum_kernel(const __grid_constant__ KeyWeightsParams p, int shares, int per_request) {
   const int64_t table = (int64_t)p.kv.max_pages * p.kv.page_size, cap = table < p.width ? table : p.width;
   const int chunks = (p.s * p.H + kTile - 1) / kTile;
-  const int b = blockIdx.x / per_request, r = blockIdx.x - b * per_request, i = threadIdx.x / kTile;
+  const int at = blockIdx.x / kSub, i = blockIdx.x - at * kSub, b = at / per_request, r = at - b * per_request;
   const int len = paged_len(p.kv, p.err, b, cap, false), t0 = r * kSub, nt = min(tiles_of(len) - t0, kSub);
   if (i >= nt) return;
   const int64_t total = (int64_t)p.before[2 * p.kv.B] * chunks, u0 = ((int64_t)p.before[2 * b] + t0) * chunks, range = p.before[2 * b + 1] + r;
-  const int j = (t0 + i) * kTile + (threadIdx.x & (kTile - 1));
+  const int j = (t0 + i) * kTile + threadIdx.x;
   if (j >= len) return;
   float sum = 0.f;
   int s = (int)(((u0 + 1) * shares - 1) / total);         // the share that has unit u0
+  int64_t lo, hi = total * s / shares - u0;
   for (; s < shares; ++s) {
-    const int64_t lo = total * s / shares - u0, hi = total * (s + 1) / shares - u0;
+    lo = hi, hi = total * (s + 1) / shares - u0;
     if (lo >= (int64_t)nt * chunks) break;
     const int64_t c = lo <= i ? 0 : (lo - i + nt - 1) / nt;  // its first chunk of this tile
     if (c >= chunks || c * nt + i >= hi) continue;
-    const float* part = p.part + ((range + s) * kSub + i) * kTile + (threadIdx.x & (kTile - 1));
+    const float* part = p.part + ((range + s) * kSub + i) * kTile + threadIdx.x;
     if (guard_span(p.err, G_PART_O, part, 4, p.part, p.part_bytes)) sum += *part;
   }
   float* w = p.weights + b * p.stride + j;
@@ -536,7 +537,7 @@ cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e == cudaSuccess && (int64_t)p.s * p.H > kTile) {
     const int64_t ranges = most_ranges(p.kv.B, cap);
-    key_weights_sum_kernel<<<(unsigned)ranges, kSub * kTile, 0, stream>>>(p, (int)grid, (int)(ranges / p.kv.B));
+    key_weights_sum_kernel<<<(unsigned)(ranges * kSub), kTile, 0, stream>>>(p, (int)grid, (int)(ranges / p.kv.B));
     e = cudaGetLastError();
   }
   return e;
