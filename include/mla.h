@@ -525,6 +525,7 @@ mla_status mla_key_weights(const void* q, int q_per_req, const float* lse, const
  *
  * weights  fp32 [B, width] at row stride weights_stride >= width; lens, keep DEVICE int32 [B]; idx int32 [B, K]
  *          contiguous; count, dropped int32 [B].  first, recent, K >= 0; K, width < 2^31 - 2^16.
+ * count and dropped may be lens and keep themselves, in either order.
  * A request with lens[b] outside [0, width], keep[b] < 0 or n > K is refused: count = dropped = 0, idx -1, and
  * MLA_ERR_DEVICE_RANGE recorded (0x207c).  workspace: >= 256 bytes (the status word).
  */

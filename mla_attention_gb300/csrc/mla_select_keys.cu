@@ -31,6 +31,14 @@ __device__ __forceinline__ void cluster_barrier() {
   __syncwarp();
   cluster_sync();
 }
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // larger weights have larger keys; -0 is 0, a NaN of either sign the largest
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -57,15 +65,17 @@ __global__ void __launch_bounds__(kThreads, 2) select_keys_kernel(const __grid_c
   const int n = min(len, keep);
   int32_t* idx = p.idx + (int64_t)b * p.K;
   const bool ok = len >= 0 && len <= p.width && keep >= 0 && n <= p.K;
+  cluster_arrive();                                 // this thread has the length and the budget
+  auto put = [&](int64_t i, int v) {
+    if (guard_span(p.err, G_STEP_OUT, idx + i, 4, p.idx, (uint64_t)p.B * p.K * 4)) idx[i] = v;
+  };
+  for (int64_t i = (ok ? n : 0) + own; i < p.K; i += step) put(i, -1);
+  cluster_wait();                                   // all have: count or dropped may be the same memory
   if (own == 0) {
     if (!ok) record_error(p.err, DEV_RANGE_BASE | Y_SELECT);
     if (guard_span(p.err, G_STEP_OUT, p.count + b, 4, p.count, (uint64_t)p.B * 4)) p.count[b] = ok ? n : 0;
     if (guard_span(p.err, G_STEP_OUT, p.dropped + b, 4, p.dropped, (uint64_t)p.B * 4)) p.dropped[b] = ok ? n - len : 0;
   }
-  auto put = [&](int64_t i, int v) {
-    if (guard_span(p.err, G_STEP_OUT, idx + i, 4, p.idx, (uint64_t)p.B * p.K * 4)) idx[i] = v;
-  };
-  for (int64_t i = (ok ? n : 0) + own; i < p.K; i += step) put(i, -1);
   if (!ok) return;
   if (n == len) {
     for (int64_t i = own; i < n; i += step) put(i, (int)i);

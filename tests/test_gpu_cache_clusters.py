@@ -8,9 +8,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.cache_oracle as co
 import tests.test_gpu_cache as cases
 from mla_attention_gb300 import (MLAError, check_device_status, inject_stall, mla_compact_rows, mla_decode_fp4, mla_key_weights,
-                                 set_spin_limit)
+                                 mla_select_keys, set_spin_limit)
 from tests.helpers import dev
 
 pytestmark = pytest.mark.gpu
@@ -35,6 +36,27 @@ def test_compact_one_long_request(n, keep):
     cases._check_compact([n], 48, 64, [keep], n + keep)
 
 
+@pytest.mark.parametrize("fmt", cases.FORMATS)
+@pytest.mark.parametrize("s,H", [(129, 1), (2, 80), (7, 23), (3, 85), (2, 128), (257, 1), (17, 16), (3, 100)])
+def test_weights_around_two_chunks(fmt, s, H):
+    """Query rows around 128 and 256 (129, 160, 161, 255, 256, 257, 272, 300), keys around 128, 256 and a range of 2048."""
+    cases._check_weights(fmt, [0, 1, 127, 129, 255, 256, 257, 2048, 2300, 600], H, s=s, page=16, seed=s + H)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "fp4"])
+def test_weights_of_many_chunks_repeat_bit_for_bit(fmt):
+    cache, table, keys = cases._paged(fmt, [5000, 300, 2049], 64, 4, poison=False)
+    q, L = cases._query(3, 12, 128, 4).to(dev()), cases._i32([5000, 300, 2049])
+    lse = torch.full((3, 12, 128), 5.0, device=dev())
+    first = None
+    for _ in range(10):
+        w = torch.zeros((3, 5000), device=dev())
+        mla_key_weights(q, lse, cache, table, L, 0.07, w, decay=0.0)
+        cases._done()
+        first = w if first is None else first
+        assert torch.equal(w, first)
+
+
 @pytest.mark.parametrize("B", [1, 19, 20, 38, 39, 76, 77, 152, 153])
 def test_select_by_requests(B):
     g = torch.Generator().manual_seed(B)
@@ -53,6 +75,25 @@ def test_select_keys_that_one_cta_cannot_hold():
     lens[5], keep[5] = 26000, 25000
     lens[7], keep[7] = 25999, 900
     cases._check_select(w, lens, keep, 25000, 4, 100)
+
+
+@pytest.mark.parametrize("B", [1, 30, 200])
+@pytest.mark.parametrize("swap", [False, True])
+def test_select_counts_in_place(B, swap):
+    """count in the place of lens and dropped in that of keep, or the other way round: read by all before they are written."""
+    g = torch.Generator().manual_seed(B)
+    w = torch.rand((B, 3000), generator=g)
+    lens = torch.randint(0, 3000, (B,), generator=g)
+    keep = torch.randint(0, 3000, (B,), generator=g)
+    lens[0], keep[0] = 3000, 1700
+    ref = co.select_keys(w.double().numpy(), lens.tolist(), keep.tolist(), 3000, 3, 9)
+    d, first = w.to(dev()), [lens.int().to(dev()), keep.int().to(dev())]
+    for _ in range(20):
+        L, K = (t.clone() for t in first)
+        idx, count, dropped = mla_select_keys(d, L, K, 3000, first=3, recent=9, count=K if swap else L, dropped=L if swap else K)
+        cases._done()
+        for a, b in zip((idx, count, dropped), ref):
+            np.testing.assert_array_equal(a.cpu().numpy(), b)
 
 
 FIRST = """
