@@ -163,16 +163,6 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
 }
 
 // ---- MMAs of the pair ----
-// One arrival for the warp on a barrier of the first CTA.  What it tells of lies in this CTA's own shared or tensor memory, where this
-// SM's tensor core reads it: ordered within the CTA, as the default is.  (A release at cluster scope waits for the loads on
-// their way: 1900 cycles under the next tile's; passed on by another warp it still cost 0.1 ms of 0.42.)
-__device__ __forceinline__ void first_cta_arrive(uint64_t* bar, uint32_t cta) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    if (cta == 0) mbar_arrive(bar);
-    else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(smem_u32(bar), 0)) : "memory");
-  }
-}
 #define MLA_MMA2(D, X, Y, ID, P) "tcgen05.mma.cta_group::2.kind::f16 [" D "], " X ", " Y ", " ID ", " P ";\n\t"
 #define MLA_STEP2(P, ID) MLA_MMA2("%0", "x", "y", ID, P) "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
 #define MLA_BOX2(P, ID) MLA_STEP2(P, ID) MLA_STEP2("t", ID) MLA_STEP2("t", ID) MLA_MMA2("%0", "x", "y", ID, "t") \
@@ -210,12 +200,6 @@ __device__ __forceinline__ void mma2_values(uint32_t d0, uint32_t d1, uint64_t a
 #undef MLA_STEP2
 #undef MLA_BOX2
 #undef MLA_PV2
-// arrives on the barrier at this offset in both CTAs once the MMAs that this thread issued are done
-__device__ __forceinline__ void commit2(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-               "h"((uint16_t)3)
-               : "memory");
-}
 
 // 16 rows of 256 columns as they lie: eight lanes a row, 32 columns each, and their two scales (four lanes a row ask the
 // first-level cache for twice as many lines; 0.350 ms for 0.349)
@@ -465,21 +449,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
           tc_fence_after();
           if (elect_one()) {
             mma2_scores4(tbase + kTmemS + buf * 64, qdesc, kdesc, id);
-            commit2(&bars.kempty[0]);
+            commit<2>(&bars.kempty[0]);
           }
           __syncwarp();
           if (!wait.warp(&bars.kfull[1], u & 1, D_KFULL, true)) { live = false; break; }
           tc_fence_after();
           if (elect_one()) {
             mma2_scores5(tbase + kTmemS + buf * 64, qdesc + 4 * kBox / 16, kdesc + 4 * kBox / 16, id, id_pe);
-            commit2(&bars.kempty[1]);
-            commit2(&bars.sfull[buf]);
-            if (t == it.t1 - 1) commit2(&bars.qempty);
+            commit<2>(&bars.kempty[1]);
+            commit<2>(&bars.sfull[buf]);
+            if (t == it.t1 - 1) commit<2>(&bars.qempty);
           }
           __syncwarp();
         }
       }
-      if (elect_one()) commit2(&bars.drain[0]);       // what was issued is done before anything is given back
+      if (elect_one()) commit<2>(&bars.drain[0]);       // what was issued is done before anything is given back
       mbar_drain(&bars.drain[0], 0);
       __syncwarp();
     }
@@ -498,15 +482,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
             if (elect_one()) {
               mma2_values(tbase + kTmemO, tbase + kTmemO + 128, sdesc_sw128(pst + h * kBox, 16, 1024), sdesc_sw128(vst + h * 4 * kBox, kBox, 1024),
                           sdesc_sw128(vst + h * 4 * kBox + 2 * kBox, kBox, 1024), id, t > it.t0 || h > 0 ? 1u : 0u);
-              commit2(&bars.vempty[h]);
-              if (h == 1) commit2(&bars.pvdone);
+              commit<2>(&bars.vempty[h]);
+              if (h == 1) commit<2>(&bars.pvdone);
             }
             __syncwarp();
           }
           if (!live) break;
         }
       }
-      if (elect_one()) commit2(&bars.drain[1]);
+      if (elect_one()) commit<2>(&bars.drain[1]);
       mbar_drain(&bars.drain[1], 0);
       __syncwarp();
     }
@@ -611,6 +595,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == kMmaS) mbar_drain(&bars.drain[0], 0), mbar_drain(&bars.drain[1], 0);    // the last arrivals in either CTA
+  __syncwarp();
   cluster_sync();                                     // no MMA of the pair is left, no arrival on its way
   if (warp == kMmaS) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tbase) : "memory");
 }

@@ -2,22 +2,25 @@
 //   weights[b, j] = decay weights[b, j] + sum_{i, h} exp(scale q_{b,i,h} . k_j - lse_{b,i,h})
 //
 // Scores are taken the other way round, S^T = K Q^T with 128 keys as the rows of a tile and up to 128 query rows (token, head) as
-// its columns: a key is then a lane of tensor memory and its sum over the query rows stays in one thread, with neither
+// its columns (a pair of SMs: 256 of either): a key is then a lane of tensor memory and its sum over the query rows stays in one thread, with neither
 // shuffles nor atomics.  The query rows of a request stay in shared memory while its keys stream past.  More than 128 of
 // them are taken a chunk after the other over a few tiles at a time (kSub), so that the keys come from L2 again; a CTA's
 // part of such a range's sums goes to the workspace, and key_weights_sum_kernel adds the parts up in their order.
 //
-// A CTA per SM takes an equal share of all tiles.  16 warps:
+// More than 128 query rows over e4m3 or 4-bit rows go to clusters of two CTAs: MMAs of the pair (cta_group::2, M = N = 256), each CTA
+// with 128 keys and half of the query rows, so that a key made f16 meets twice as many of them.
+//
+// A CTA (or pair) per SM takes an equal share of all tiles.  16 warps:
 //   0-3   a key a thread: S from tensor memory, exponentials, the weight's update
-//   4     MMAs (one thread): nine 64-column boxes of K against those of Q
+//   4     MMAs (one thread, of the first CTA): nine 64-column boxes of K against those of Q
 //   5     rows of the next tiles through the block table, and the chunk's log-sum-exps
 //   6-15  producers, two for each stage of the ring, 64 rows each: bf16 rows by cp.async; e4m3 and 4-bit rows through
 //         registers into f16 (exact), with q in f16 too, the next box's loads out before the last one's are converted; the RoPE
 //         columns of 4-bit rows stay bf16.  A stage has producers of its own, as a parity tells no more than the last phase.
 //
-// One new token of 128 heads and request over bf16 rows is HBM-bound: 64 requests of 4096 to 32768 keys 0.224 ms, 6.2 TB/s.  The conversion to
-// f16 bounds the others: 32 such requests 0.111 ms with e4m3 rows, 0.127 with 4-bit ones, and 4096 query rows over 32768 4-bit keys,
-// where each chunk of 128 converts the keys again, 0.21 ms, 0.73 PFLOP/s.
+// One new token of 128 heads and request over bf16 rows is HBM-bound: 64 requests of 4096 to 32768 keys 0.224 ms, 6.2 TB/s.  The
+// first-level cache (rows, their f16 form, the MMAs' operands) bounds the others: 32 such requests 0.111 ms with e4m3 rows, 0.127 with
+// 4-bit ones; 4096 query rows over 32768 4-bit keys 0.119 ms, 1.30 PFLOP/s (without pairs 0.211).
 #include <math_constants.h>
 
 #include "fp4_rows.cuh"
@@ -26,14 +29,13 @@
 namespace mla {
 namespace {
 
-constexpr int kTile = 128;                       // keys a tile, query rows a chunk
+constexpr int kTile = 128;                       // a CTA's keys of a tile, and its query rows of a chunk
 constexpr int kBoxes = kDk / 64;
 constexpr int kBoxBytes = kTile * 128;
 constexpr int kStages = 5;                       // K boxes on their way
 constexpr int kRowSlots = 3;                     // tiles whose rows are known
 constexpr int kSub = 8;                          // tiles before the next chunk of query rows
 constexpr int kThreads = 512, kProducers = 2 * kStages, kFirstProducer = 6;
-constexpr uint32_t kTmemCols = 256;
 
 constexpr int kOffQ = 0;
 constexpr int kOffK = kBoxes * kBoxBytes;
@@ -65,10 +67,12 @@ struct Segment {
   int from;                // and the first unit (c * nt + tile) of it that this CTA has
 };
 
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+template <int kCtas>
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile * kCtas - 1) / (kTile * kCtas); }
 
 // This CTA's share of the units (tile, chunk): request by request, kSub tiles at a time, a chunk of query rows after the other
 // over them.  With one chunk a segment is all of a request that the share has.
+template <int kCtas>
 struct Shares {
   const KeyWeightsParams* p;
   int64_t cap, left, range;
@@ -78,7 +82,7 @@ struct Shares {
         chunks(chunks_) {}
   __device__ __noinline__ bool next(Segment& s) {       // one copy for all roles: the loops should stay in the instruction cache
     while (left > 0 && b < p->kv.B) {
-      const int len = paged_len(p->kv, p->err, b, cap, false), all = tiles_of(len) - t0;
+      const int len = paged_len(p->kv, p->err, b, cap, false), all = tiles_of<kCtas>(len) - t0;
       if (all <= 0) {
         ++b, t0 = 0;
         continue;
@@ -97,12 +101,13 @@ struct Shares {
 
 // Where this CTA's share starts; by all threads.  With several chunks the first CTA puts down the tiles and ranges before each
 // request.
+template <int kCtas>
 __device__ __noinline__ void find_share(const KeyWeightsParams& p, int64_t cap, int chunks, Bars& bars, int32_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.kv.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.kv.B), b1 = min(b0 + per, p.kv.B);
   int64_t tiles = 0, ranges = 0;
   for (int b = b0; b < b1; ++b) {
-    const int n = tiles_of(paged_len(p.kv, p.err, b, cap, blockIdx.x == 0));
+    const int n = tiles_of<kCtas>(paged_len(p.kv, p.err, b, cap, blockIdx.x == 0));
     tiles += n, ranges += (n + kSub - 1) / kSub;
   }
   int64_t t_upto = tiles, r_upto = ranges;
@@ -119,12 +124,12 @@ __device__ __noinline__ void find_share(const KeyWeightsParams& p, int64_t cap, 
     total += sums[2 * w];
   }
   total *= chunks;
-  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  const int64_t share = blockIdx.x / kCtas, all = gridDim.x / kCtas, lo = total * share / all, hi = total * (share + 1) / all;
   if (tid == 0) bars.share = hi - lo;
   const bool tell = chunks > 1 && blockIdx.x == 0, here = lo < hi && t_at * chunks <= lo && lo < (t_at + tiles) * chunks;
   if (tell || here) {
     for (int b = b0; b < b1; ++b) {
-      const int n = tiles_of(paged_len(p.kv, p.err, b, cap, false));
+      const int n = tiles_of<kCtas>(paged_len(p.kv, p.err, b, cap, false));
       if (tell) {
         p.before[2 * b] = (int32_t)t_at, p.before[2 * b + 1] = (int32_t)r_at;
         if (b == p.kv.B - 1) p.before[2 * b + 2] = (int32_t)(t_at + n);
@@ -158,20 +163,25 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
 }
 
 constexpr int kNoRow = -1;                       // no key there, or its page is none
-template <int kFmt>
+// kCtas 2: a cluster of two CTAs, MMAs of the pair
+template <int kFmt, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsParams p) {
+  static_assert(kCtas == 1 || kFmt != kCacheBf16, "the copies' arrivals stay in their CTA");
+  constexpr int kChunk = kCtas * kTile, kLseSlots = 2 / kCtas;      // query rows a chunk
+  constexpr uint32_t kTmemCols = 2 * kChunk;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bars = *reinterpret_cast<Bars*>(smem + kOffBars);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t table = (int64_t)p.kv.max_pages * p.kv.page_size, cap = table < p.width ? table : p.width;
-  const int rows = p.s * p.H, chunks = (rows + kTile - 1) / kTile;
+  const int rows = p.s * p.H, chunks = (rows + kChunk - 1) / kChunk;
+  const int cta = kCtas == 1 ? 0 : (int)cluster_ctarank(), share = blockIdx.x / kCtas;
   const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * p.kv.row_bytes;
   // bf16: every lane of both producers arrives when its copies have landed
   constexpr uint32_t kArrivals = kFmt == kCacheBf16 ? 64 : 2;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars.kfull[i], kArrivals), mbar_init(&bars.kempty[i], 1);
-    for (int i = 0; i < kBoxes; ++i) mbar_init(&bars.qfull[i], kArrivals), mbar_init(&bars.qempty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 4);
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars.kfull[i], kCtas * kArrivals), mbar_init(&bars.kempty[i], 1);
+    for (int i = 0; i < kBoxes; ++i) mbar_init(&bars.qfull[i], kCtas * kArrivals), mbar_init(&bars.qempty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 4 * kCtas);
     for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], kProducers);
     for (int i = 0; i < 2; ++i) mbar_init(&bars.lfull[i], 1), mbar_init(&bars.lfree[i], 4);
     mbar_init(&bars.drain, 1);
@@ -181,21 +191,32 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     fence_mbar_init();
   }
   if (warp == 4) {
-    tmem_alloc(&bars.tmem_base, kTmemCols);
-    tmem_relinquish();
+    if constexpr (kCtas == 1) {
+      tmem_alloc(&bars.tmem_base, kTmemCols);
+      tmem_relinquish();
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem_base)), "n"(kTmemCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
   }
-  find_share(p, cap, chunks, bars, reinterpret_cast<int32_t*>(smem + kOffRows));   // no row is there yet
+  find_share<kCtas>(p, cap, chunks, bars, reinterpret_cast<int32_t*>(smem + kOffRows));   // no row is there yet
   tc_fence_before();
   __syncthreads();
+  if constexpr (kCtas == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tbase = bars.tmem_base;
   const TileWaits wait{&bars.abort, p.err, p.spin_limit};
   int32_t* row_slots = reinterpret_cast<int32_t*>(smem + kOffRows);
   float* lse_slots = reinterpret_cast<float*>(smem + kOffLse);
-  Shares shares(p, cap, bars, chunks);
+  Shares<kCtas> shares(p, cap, bars, chunks);
   Segment it;
   uint32_t u = 0, c_all = 0;                     // units and segments gone through
   bool live = bars.abort == 0;
+  // what the MMAs of the pair wait for, in the first CTA
+  auto tell = [&](uint64_t* bar) {
+    if constexpr (kCtas == 1) warp_arrive(bar);
+    else first_cta_arrive(bar, cta);
+  };
 
   if (warp < 4) {
     // ---------------- a key a thread ----------------
@@ -203,30 +224,31 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     const float c2 = p.scale * 1.4426950408889634f;
     const uint64_t c22 = f32x2(c2, c2);
     while (live && shares.next(it)) {
-      const float* minus_lse = lse_slots + (c_all & 1) * kTile;
-      if (!wait.warp(&bars.lfull[c_all & 1], (c_all >> 1) & 1, W_LFULL)) break;
-      const int n = min(rows - it.c * kTile, kTile);
+      const uint32_t lslot = c_all % kLseSlots;
+      const float* minus_lse = lse_slots + lslot * kChunk;
+      if (!wait.warp(&bars.lfull[lslot], (c_all / kLseSlots) & 1, W_LFULL)) break;
+      const int n = min(rows - it.c * kChunk, kChunk);
       for (int i = it.i0; i < it.i1; ++i, ++u) {
-        const int j = (it.t0 + i) * kTile + tid, buf = u & 1;
+        const int j = ((it.t0 + i) * kCtas + cta) * kTile + tid, buf = u & 1;
         bool mine = j < it.len, first;
         float* w;
         if (chunks == 1) {
           w = p.weights + it.b * p.stride + j, first = p.decay == 0.f;
           mine = mine && guard_span(p.err, G_STEP_OUT, w, 4, p.weights, ((uint64_t)(p.kv.B - 1) * p.stride + p.width) * 4);
         } else {       // this CTA's part of the range's sums
-          w = p.part + ((it.range + blockIdx.x) * kSub + i) * kTile + tid, first = it.c * it.nt + i - it.nt < it.from;
+          w = p.part + ((it.range + share) * kSub + i) * kChunk + cta * kTile + tid, first = it.c * it.nt + i - it.nt < it.from;
           mine = mine && guard_span(p.err, G_PART_O, w, 4, p.part, p.part_bytes);
         }
         const float old = mine && !first ? *w : 0.f;
         // query rows below `hidden` do not see the key
-        const int hidden = (int)max((int64_t)0, (int64_t)(j - (it.len - p.s)) * p.H - it.c * kTile);
+        const int hidden = (int)max((int64_t)0, (int64_t)(j - (it.len - p.s)) * p.H - it.c * kChunk);
         const bool any_hidden = __any_sync(~0u, j < it.len && hidden > 0);
         if (!wait.warp(&bars.sfull[buf], (u >> 1) & 1, W_SFULL)) { live = false; break; }
         tc_fence_after();
         uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
         for (int n0 = 0; n0 < n; n0 += 32) {
           uint32_t s[32];
-          tmem_ld32(tbase + lanes + buf * kTile + n0, s);
+          tmem_ld32(tbase + lanes + buf * kChunk + n0, s);
           tmem_wait_ld();
 #pragma unroll
           for (int i4 = 0; i4 < 32; i4 += 4) {
@@ -244,68 +266,69 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
           }
         }
         tc_fence_before();
-        warp_arrive(&bars.sfree[buf]);
+        tell(&bars.sfree[buf]);
         float a, b;
         f32x2_split(add_f32x2(sum2[0], sum2[1]), a, b);
         if (mine) *w = first ? a + b : chunks == 1 ? fmaf(p.decay, old, a + b) : old + (a + b);
       }
-      if (live) warp_arrive(&bars.lfree[c_all & 1]);
+      if (live) warp_arrive(&bars.lfree[lslot]);
       ++c_all;
     }
   } else if (warp == 4) {
     // ---------------- MMAs (the whole warp waits, one lane issues) ----------------
-    // (not unrolled: nine copies pass the instruction cache, 284 against 211 us for 4096 query rows and 32768 keys in 4 bits)
+    // (not unrolled: nine copies pass the instruction cache, without pairs 284 against 211 us for 4096 query rows and 32768 keys in 4 bits)
     if (p.debug_stall) live = live && wait.warp(&bars.stall, 0, W_STALL);
-    const uint64_t kdesc = sdesc_sw128(smem_u32(smem + kOffK), 16, 1024), qdesc = sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024);
-    uint32_t slot = 0, phase = 0;
-    for (; live && shares.next(it); ++c_all) {
-      const uint32_t n = (uint32_t)(min(rows - it.c * kTile, kTile) + 31) & ~31u;
-      const uint32_t id_f16 = idesc_f16_f32(kTile, n, false, false), id_bf16 = idesc_bf16_f32(kTile, n, false, false);
-      for (int i = it.i0; i < it.i1 && live; ++i, ++u) {
-        const int buf = u & 1;
-        const uint32_t d = tbase + buf * kTile;
-        const bool first = i == it.i0, last = i == it.i1 - 1;
-        if (!wait.warp(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, W_SFREE)) { live = false; break; }
+    if (cta == 0) {
+      const uint64_t kdesc = sdesc_sw128(smem_u32(smem + kOffK), 16, 1024), qdesc = sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024);
+      uint32_t slot = 0, phase = 0;
+      for (; live && shares.next(it); ++c_all) {
+        const uint32_t n = (uint32_t)(min(rows - it.c * kChunk, kChunk) + 31) & ~31u;
+        const uint32_t id_f16 = idesc_f16_f32(kChunk, n, false, false), id_bf16 = idesc_bf16_f32(kChunk, n, false, false);
+        for (int i = it.i0; i < it.i1 && live; ++i, ++u) {
+          const int buf = u & 1;
+          const uint32_t d = tbase + buf * kChunk;
+          const bool first = i == it.i0, last = i == it.i1 - 1;
+          if (!wait.warp(&bars.sfree[buf], ((u >> 1) & 1) ^ 1, W_SFREE, kCtas == 2)) { live = false; break; }
 #pragma unroll 1
-        for (int k = 0; k < kBoxes; ++k) {
-          if (first && !wait.warp(&bars.qfull[k], c_all & 1, W_QFULL)) { live = false; break; }
-          if (!wait.warp(&bars.kfull[slot], phase, W_KFULL)) { live = false; break; }
-          tc_fence_after();
-          if constexpr (kFmt == kCacheBf16) fence_proxy_async_smem();    // copies that other threads issued
-          if (elect_one()) {
-            const bool bf = kFmt == kCacheBf16 || (kFmt == kCacheFp4 && k == kBoxes - 1);
-            mma_box64(d, kdesc + slot * (kBoxBytes / 16), qdesc + k * (kBoxBytes / 16), bf ? id_bf16 : id_f16, k > 0 ? 1u : 0u);
-            mma_commit(&bars.kempty[slot]);
-            if (last) mma_commit(&bars.qempty[k]);
-            if (k == kBoxes - 1) mma_commit(&bars.sfull[buf]);
+          for (int k = 0; k < kBoxes; ++k) {
+            if (first && !wait.warp(&bars.qfull[k], c_all & 1, W_QFULL, kCtas == 2)) { live = false; break; }
+            if (!wait.warp(&bars.kfull[slot], phase, W_KFULL, kCtas == 2)) { live = false; break; }
+            tc_fence_after();
+            if constexpr (kFmt == kCacheBf16) fence_proxy_async_smem();    // copies that other threads issued
+            if (elect_one()) {
+              const bool bf = kFmt == kCacheBf16 || (kFmt == kCacheFp4 && k == kBoxes - 1);
+              mma_box64<kCtas>(d, kdesc + slot * (kBoxBytes / 16), qdesc + k * (kBoxBytes / 16), bf ? id_bf16 : id_f16, k > 0 ? 1u : 0u);
+              commit<kCtas>(&bars.kempty[slot]);
+              if (last) commit<kCtas>(&bars.qempty[k]);
+              if (k == kBoxes - 1) commit<kCtas>(&bars.sfull[buf]);
+            }
+            __syncwarp();
+            if (++slot == kStages) slot = 0, phase ^= 1;
           }
-          __syncwarp();
-          if (++slot == kStages) slot = 0, phase ^= 1;
         }
       }
+      if (elect_one()) commit<kCtas>(&bars.drain);    // what was issued is done before tensor memory is given back
+      mbar_drain(&bars.drain, 0);
+      __syncwarp();
     }
-    if (elect_one()) mma_commit(&bars.drain);    // what was issued is done before tensor memory is given back
-    mbar_drain(&bars.drain, 0);
-    __syncwarp();
   } else if (warp == 5) {
     // ---------------- rows of the tiles to come ----------------
     for (; live && shares.next(it); ++c_all) {
-      if (!wait.warp(&bars.lfree[c_all & 1], ((c_all >> 1) & 1) ^ 1, W_LFREE)) break;
+      const uint32_t lslot = c_all % kLseSlots;
+      float l[kChunk / 32];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = it.c * kTile + 32 * i + lane;
+      for (int i = 0; i < kChunk / 32; ++i) {
+        const int r = it.c * kChunk + 32 * i + lane;
         const float* src = p.lse + (int64_t)it.b * rows + r;
-        float l = -CUDART_INF_F;
-        if (r < rows && guard_span(p.err, G_STEP_IN, src, 4, p.lse, (uint64_t)p.kv.B * rows * 4)) l = *src;
-        lse_slots[(c_all & 1) * kTile + 32 * i + lane] = l == -CUDART_INF_F ? -CUDART_INF_F : -l * 1.4426950408889634f;
+        l[i] = -CUDART_INF_F;
+        if (r < rows && guard_span(p.err, G_STEP_IN, src, 4, p.lse, (uint64_t)p.kv.B * rows * 4)) l[i] = *src;
       }
-      warp_arrive(&bars.lfull[c_all & 1]);
       for (int i = it.i0; i < it.i1; ++i, ++u) {
         const int slot = u % kRowSlots;
         int32_t at[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int j = (it.t0 + i) * kTile + 32 * r + lane;
+          const int j = ((it.t0 + i) * kCtas + cta) * kTile + 32 * r + lane;
           at[r] = kNoRow;
           if (j < it.len) {
             const int pg = j / p.kv.page_size;
@@ -329,6 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
 #pragma unroll
         for (int r = 0; r < 4; ++r) row_slots[slot * kTile + 32 * r + lane] = at[r];
         warp_arrive(&bars.rfull[slot]);
+        // the rows of two tiles go ahead of the log-sum-exps, whose place may be in use still
+        if (i == min(it.i0 + 1, it.i1 - 1)) {
+          if (!wait.warp(&bars.lfree[lslot], ((c_all / kLseSlots) & 1) ^ 1, W_LFREE)) { live = false; break; }
+#pragma unroll
+          for (int i = 0; i < kChunk / 32; ++i)
+            lse_slots[lslot * kChunk + 32 * i + lane] = l[i] == -CUDART_INF_F ? -CUDART_INF_F : -l[i] * 1.4426950408889634f;
+          warp_arrive(&bars.lfull[lslot]);
+        }
       }
     }
   } else {
@@ -369,15 +400,15 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         }
       }
       fence_proxy_async_smem();
-      warp_arrive(kfull);
+      tell(kfull);
       return true;
     };
     // (two copies of the code: a register that a load is on its way to is not moved without waiting for it)
     auto flush = [&]() -> bool { return held < 0 || (held == 0 ? convert(v[0], sc[0]) : convert(v[1], sc[1])); };
     int k0 = me;                                   // this stage's first box of the unit
     for (; live && shares.next(it); ++c_all) {
-      const int n = min(rows - it.c * kTile, kTile), n32 = (n + 31) & ~31;
-      const __nv_bfloat16* qsrc = p.q + ((int64_t)it.b * rows + it.c * kTile) * kDk;
+      const int n = min(rows - it.c * kChunk, kChunk), own = ((n + 31) & ~31) / kCtas;    // this CTA's query rows
+      const __nv_bfloat16* qsrc = p.q + ((int64_t)it.b * rows + it.c * kChunk + cta * own) * kDk;
       const uint64_t q_bytes = (uint64_t)p.kv.B * rows * kDk * 2;
       const int unit = lane & 7;
       // the query rows' boxes me and me + 5, in the first unit each before the keys' box of its column
@@ -385,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
       auto query_box = [&](int k) -> bool {
         const uint32_t box = smem_u32(smem + kOffQ + k * kBoxBytes);
         if (!flush() || !wait.warp(&bars.qempty[k], (c_all & 1) ^ 1, W_QEMPTY)) return false;
-        for (int r = r0 + (lane >> 3); r < min(n32, r0 + 64); r += 4) {
+        for (int r = r0 + (lane >> 3); r < min(own, r0 + 64); r += 4) {
           const __nv_bfloat16* src = qsrc + (int64_t)r * kDk + 64 * k + 8 * unit;
-          const bool in = r < n && guard_span(p.err, G_STEP_IN, src, 16, p.q, q_bytes);
+          const bool in = cta * own + r < n && guard_span(p.err, G_STEP_IN, src, 16, p.q, q_bytes);
           cp_async16_zfill(box_unit(box, r, unit), in ? src : p.q, in ? 16u : 0u);
         }
         if constexpr (kFmt == kCacheBf16) {
@@ -395,12 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         } else {                                   // each lane puts its own copies into f16 where they lie
           cp_async_wait_all();
           if (kFmt == kCacheE4m3 || k < kBoxes - 1)
-            for (int r = r0 + (lane >> 3); r < min(n32, r0 + 64); r += 4) {
+            for (int r = r0 + (lane >> 3); r < min(own, r0 + 64); r += 4) {
               const uint32_t at = box_unit(box, r, unit);
               st_shared16(at, bf16x8_to_f16(ld_shared16(at)));
             }
           fence_proxy_async_smem();
-          warp_arrive(&bars.qfull[k]);
+          tell(&bars.qfull[k]);
         }
         return true;
       };
@@ -431,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             } else {
               cp_async_wait_all();
               fence_proxy_async_smem();
-              warp_arrive(kfull);
+              tell(kfull);
             }
             continue;
           }
@@ -476,18 +507,27 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) tmem_dealloc(tbase, kTmemCols);
+  if constexpr (kCtas == 1) {
+    if (warp == 4) tmem_dealloc(tbase, kTmemCols);
+  } else {
+    if (warp == 4) mbar_drain(&bars.drain, 0);   // the last arrival in either CTA
+    __syncwarp();
+    cluster_sync();                              // no MMA of the pair is left, no arrival on its way
+    if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "n"(kTmemCols) : "memory");
+  }
 }
 
 // Several chunks of query rows: a range's sums are those of the CTAs that had units of it, in their order.  A CTA per tile.
-__global__ void __launch_bounds__(kTile) key_weights_sum_kernel(const __grid_constant__ KeyWeightsParams p, int shares, int per_request) {
+template <int kCtas>
+__global__ void __launch_bounds__(kTile * kCtas) key_weights_sum_kernel(const __grid_constant__ KeyWeightsParams p, int shares, int per_request) {
   const int64_t table = (int64_t)p.kv.max_pages * p.kv.page_size, cap = table < p.width ? table : p.width;
-  const int chunks = (p.s * p.H + kTile - 1) / kTile;
+  constexpr int kChunk = kTile * kCtas;
+  const int chunks = (p.s * p.H + kChunk - 1) / kChunk;
   const int at = blockIdx.x / kSub, i = blockIdx.x - at * kSub, b = at / per_request, r = at - b * per_request;
-  const int len = paged_len(p.kv, p.err, b, cap, false), t0 = r * kSub, nt = min(tiles_of(len) - t0, kSub);
+  const int len = paged_len(p.kv, p.err, b, cap, false), t0 = r * kSub, nt = min(tiles_of<kCtas>(len) - t0, kSub);
   if (i >= nt) return;
   const int64_t total = (int64_t)p.before[2 * p.kv.B] * chunks, u0 = ((int64_t)p.before[2 * b] + t0) * chunks, range = p.before[2 * b + 1] + r;
-  const int j = (t0 + i) * kTile + threadIdx.x;
+  const int j = (t0 + i) * kChunk + threadIdx.x;
   if (j >= len) return;
   float sum = 0.f;
   int s = (int)(((u0 + 1) * shares - 1) / total);         // the share that has unit u0
@@ -497,7 +537,7 @@ __global__ void __launch_bounds__(kTile) key_weights_sum_kernel(const __grid_con
     if (lo >= (int64_t)nt * chunks) break;
     const int64_t c = lo <= i ? 0 : (lo - i + nt - 1) / nt;  // its first chunk of this tile
     if (c >= chunks || c * nt + i >= hi) continue;
-    const float* part = p.part + ((range + s) * kSub + i) * kTile + threadIdx.x;
+    const float* part = p.part + ((range + s) * kSub + i) * kChunk + threadIdx.x;
     if (guard_span(p.err, G_PART_O, part, 4, p.part, p.part_bytes)) sum += *part;
   }
   float* w = p.weights + b * p.stride + j;
@@ -508,39 +548,56 @@ __global__ void __launch_bounds__(kTile) key_weights_sum_kernel(const __grid_con
 }  // namespace
 
 // the most ranges of kSub tiles that requests of `width` keys have
-static int64_t most_ranges(int B, int64_t width) { return B * ((width + kSub * kTile - 1) / (kSub * kTile)); }
+static int64_t most_ranges(int B, int64_t width, int ctas) {
+  const int64_t keys = (int64_t)kSub * kTile * ctas;
+  return B * ((width + keys - 1) / keys);
+}
 
 size_t key_weights_scratch(int B, int64_t rows, int64_t width, size_t* before) {
   *before = 0;
   if (rows <= kTile || B <= 0 || width <= 0) return 0;
   *before = ((size_t)2 * B + 2) * sizeof(int32_t);
-  return (size_t)(most_ranges(B, width) + device_sm_count()) * kSub * kTile * sizeof(float);
+  const int sms = device_sm_count();             // of CTAs alone and of pairs
+  const size_t one = (size_t)(most_ranges(B, width, 1) + sms), two = 2 * (size_t)(most_ranges(B, width, 2) + sms / 2);
+  return (one > two ? one : two) * kSub * kTile * sizeof(float);
 }
 
-cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream) {
+namespace {
+template <int kFmt, int kCtas>
+cudaError_t launch(const KeyWeightsParams& p, int64_t cap, cudaStream_t stream) {
   static PerDeviceOnce attrs;
-  cudaError_t e = attrs.run([] {
-    cudaError_t r = cudaSuccess;
-    for (const void* fn : {(const void*)key_weights_kernel<kCacheBf16>, (const void*)key_weights_kernel<kCacheE4m3>, (const void*)key_weights_kernel<kCacheFp4>})
-      if (r == cudaSuccess) r = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    return r;
-  });
+  const void* fn = (const void*)key_weights_kernel<kFmt, kCtas>;
+  cudaError_t e = attrs.run([fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
   if (e != cudaSuccess) return e;
-  // no more CTAs than tiles there can be
+  // no more shares than tiles there can be
+  const int64_t most = p.kv.B * ((cap + kTile * kCtas - 1) / (kTile * kCtas)), room = device_sm_count() / kCtas;
+  const int shares = (int)(most < room ? most : room);
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3((unsigned)(shares * kCtas));
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = kSmem;
+  config.stream = stream;
+  cudaLaunchAttribute cluster{};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = kCtas, cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  config.attrs = &cluster;
+  config.numAttrs = 1;
+  e = cudaLaunchKernelEx(&config, key_weights_kernel<kFmt, kCtas>, p);
+  if (e != cudaSuccess || (int64_t)p.s * p.H <= kTile * kCtas) return e;
+  const int64_t ranges = most_ranges(p.kv.B, cap, kCtas);
+  key_weights_sum_kernel<kCtas><<<(unsigned)(ranges * kSub), kTile * kCtas, 0, stream>>>(p, shares, (int)(ranges / p.kv.B));
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream) {
   const int64_t table = (int64_t)p.kv.max_pages * p.kv.page_size, cap = table < p.width ? table : p.width;
-  const int64_t most = p.kv.B * ((cap + kTile - 1) / kTile);
-  if (most == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)(most < device_sm_count() ? most : device_sm_count());
-  if (p.format == kCacheBf16) key_weights_kernel<kCacheBf16><<<grid, kThreads, kSmem, stream>>>(p);
-  else if (p.format == kCacheE4m3) key_weights_kernel<kCacheE4m3><<<grid, kThreads, kSmem, stream>>>(p);
-  else key_weights_kernel<kCacheFp4><<<grid, kThreads, kSmem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e == cudaSuccess && (int64_t)p.s * p.H > kTile) {
-    const int64_t ranges = most_ranges(p.kv.B, cap);
-    key_weights_sum_kernel<<<(unsigned)(ranges * kSub), kTile, 0, stream>>>(p, (int)grid, (int)(ranges / p.kv.B));
-    e = cudaGetLastError();
-  }
-  return e;
+  if (p.kv.B == 0 || cap == 0) return cudaSuccess;
+    // (of up to 128 query rows a pair gains 2 % over 4-bit rows and loses 1 % over e4m3 ones)
+  const bool pair = (int64_t)p.s * p.H > kTile && device_sm_count() > 1;
+  if (p.format == kCacheBf16) return launch<kCacheBf16, 1>(p, cap, stream);
+  if (p.format == kCacheE4m3) return pair ? launch<kCacheE4m3, 2>(p, cap, stream) : launch<kCacheE4m3, 1>(p, cap, stream);
+  return pair ? launch<kCacheFp4, 2>(p, cap, stream) : launch<kCacheFp4, 1>(p, cap, stream);
 }
 
 }  // namespace mla

@@ -29,17 +29,39 @@ struct TileWaits {
   }
 };
 
-// D (+)= A B over a 64-column box of 16-bit values: four K16 steps along 128-byte swizzled rows of both operands
-__device__ __forceinline__ void mma_box64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\tadd.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\tadd.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\tadd.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+// One arrival for the warp on a barrier of the first CTA.  What it tells of lies in this CTA's own shared or tensor memory, where this
+// SM's tensor core reads it: ordered within the CTA, as the default is.  (A release at cluster scope waits for the loads on
+// their way: 1900 cycles under the next tile's; passed on by another warp it still cost 0.1 ms of 0.42.)
+__device__ __forceinline__ void first_cta_arrive(uint64_t* bar, uint32_t cta) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    if (cta == 0) mbar_arrive(bar);
+    else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(smem_u32(bar), 0)) : "memory");
+  }
 }
+// arrives on the barrier once the MMAs that this thread issued are done; of a pair, at this offset in both CTAs
+template <int kCtas>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (kCtas == 1) mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+
+#define MLA_BOX64(G, P) "tcgen05.mma.cta_group::" G ".kind::f16 [%0], x, y, %3, " P ";\n\t"
+#define MLA_BOX64_4(G) \
+  "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t" \
+  "setp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.b64 x, %1;\n\tmov.b64 y, %2;\n\t" \
+  MLA_BOX64(G, "p") "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t" MLA_BOX64(G, "t") "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t" \
+  MLA_BOX64(G, "t") "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t" MLA_BOX64(G, "t") "}"
+// D (+)= A B over a 64-column box of 16-bit values: four K16 steps along 128-byte swizzled rows of both operands
+template <int kCtas>
+__device__ __forceinline__ void mma_box64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kCtas == 1) asm volatile(MLA_BOX64_4("1") ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+  else asm volatile(MLA_BOX64_4("2") ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+#undef MLA_BOX64
+#undef MLA_BOX64_4
 
 }  // namespace mla
