@@ -7,7 +7,7 @@
 // them are taken a chunk after the other over a few tiles at a time (kSub), so that the keys come from L2 again; a CTA's
 // part of such a range's sums goes to the workspace, and key_weights_sum_kernel adds the parts up in their order.
 //
-// More than 128 query rows over e4m3 or 4-bit rows go to clusters of two CTAs: MMAs of the pair (cta_group::2, M = N = 256), each CTA
+// More than 128 query rows go to clusters of two CTAs: MMAs of the pair (cta_group::2, M = N = 256), each CTA
 // with 128 keys and half of the query rows, so that a key made f16 meets twice as many of them.
 //
 // A CTA (or pair) per SM takes an equal share of all tiles.  16 warps:
@@ -166,7 +166,6 @@ constexpr int kNoRow = -1;                       // no key there, or its page is
 // kCtas 2: a cluster of two CTAs, MMAs of the pair
 template <int kFmt, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsParams p) {
-  static_assert(kCtas == 1 || kFmt != kCacheBf16, "the copies' arrivals stay in their CTA");
   constexpr int kChunk = kCtas * kTile, kLseSlots = 2 / kCtas;      // query rows a chunk
   constexpr uint32_t kTmemCols = 2 * kChunk;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -176,11 +175,11 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
   const int rows = p.s * p.H, chunks = (rows + kChunk - 1) / kChunk;
   const int cta = kCtas == 1 ? 0 : (int)cluster_ctarank(), share = blockIdx.x / kCtas;
   const uint64_t cache_bytes = (uint64_t)p.kv.num_pages * p.kv.page_size * p.kv.row_bytes;
-  // bf16: every lane of both producers arrives when its copies have landed
-  constexpr uint32_t kArrivals = kFmt == kCacheBf16 ? 64 : 2;
+  // bf16: every lane of both producers arrives when its copies have landed, in its own CTA; warp 4 of the second CTA hands that on
+  const uint32_t arrivals = kFmt == kCacheBf16 ? (kCtas == 2 && cta == 0 ? 65 : 64) : 2 * kCtas;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars.kfull[i], kCtas * kArrivals), mbar_init(&bars.kempty[i], 1);
-    for (int i = 0; i < kBoxes; ++i) mbar_init(&bars.qfull[i], kCtas * kArrivals), mbar_init(&bars.qempty[i], 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars.kfull[i], arrivals), mbar_init(&bars.kempty[i], 1);
+    for (int i = 0; i < kBoxes; ++i) mbar_init(&bars.qfull[i], arrivals), mbar_init(&bars.qempty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 4 * kCtas);
     for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], kProducers);
     for (int i = 0; i < 2; ++i) mbar_init(&bars.lfull[i], 1), mbar_init(&bars.lfree[i], 4);
@@ -310,6 +309,21 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
       if (elect_one()) commit<kCtas>(&bars.drain);    // what was issued is done before tensor memory is given back
       mbar_drain(&bars.drain, 0);
       __syncwarp();
+    } else if constexpr (kFmt == kCacheBf16) {
+      uint32_t slot = 0, phase = 0;
+      for (; live && shares.next(it); ++c_all)
+        for (int i = it.i0; i < it.i1 && live; ++i)
+          for (int k = 0; k < kBoxes; ++k) {
+            if (i == it.i0) {
+              if (!wait.warp(&bars.qfull[k], c_all & 1, W_QFULL)) { live = false; break; }
+              fence_proxy_async_smem();
+              first_cta_arrive(&bars.qfull[k], cta);
+            }
+            if (!wait.warp(&bars.kfull[slot], phase, W_KFULL)) { live = false; break; }
+            fence_proxy_async_smem();
+            first_cta_arrive(&bars.kfull[slot], cta);
+            if (++slot == kStages) slot = 0, phase ^= 1;
+          }
     }
   } else if (warp == 5) {
     // ---------------- rows of the tiles to come ----------------
@@ -595,7 +609,7 @@ cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream) {
   if (p.kv.B == 0 || cap == 0) return cudaSuccess;
     // (of up to 128 query rows a pair gains 2 % over 4-bit rows and loses 1 % over e4m3 ones)
   const bool pair = (int64_t)p.s * p.H > kTile && device_sm_count() > 1;
-  if (p.format == kCacheBf16) return launch<kCacheBf16, 1>(p, cap, stream);
+  if (p.format == kCacheBf16) return pair ? launch<kCacheBf16, 2>(p, cap, stream) : launch<kCacheBf16, 1>(p, cap, stream);
   if (p.format == kCacheE4m3) return pair ? launch<kCacheE4m3, 2>(p, cap, stream) : launch<kCacheE4m3, 1>(p, cap, stream);
   return pair ? launch<kCacheFp4, 2>(p, cap, stream) : launch<kCacheFp4, 1>(p, cap, stream);
 }
