@@ -53,7 +53,7 @@ def compact_cases():
     cases.test_compact_skips_and_records_bad_entries()
     clusters.test_compact_by_requests(20, 1152)
     clusters.test_compact_by_requests(153, 416)
-    clusters.test_compact_wide_rows(30736, 3)
+    clusters.test_compact_wide_rows(1921 * 16, 3)
 
 
 def append_cases():

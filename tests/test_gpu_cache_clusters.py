@@ -26,7 +26,7 @@ def test_compact_by_requests(B, row):
     cases._check_compact(lens, row, 16, [int(n * 0.7) for n in lens], B)
 
 
-@pytest.mark.parametrize("row,B", [(65536, 2), (30720, 1), (30736, 3), (128, 1), (144, 40)])
+@pytest.mark.parametrize("row,B", [(65536, 2), (1920 * 16, 1), (1921 * 16, 3), (128, 1), (144, 40)])
 def test_compact_wide_rows(row, B):
     cases._check_compact([60, 13, 33][:min(B, 3)] + [5] * (B - 3), row, 4, [40, 6, 33][:min(B, 3)] + [2] * (B - 3), row, weights=B != 2)
 
