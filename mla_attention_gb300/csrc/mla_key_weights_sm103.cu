@@ -583,8 +583,10 @@ cudaError_t launch(const KeyWeightsParams& p, int64_t cap, cudaStream_t stream) 
   const void* fn = (const void*)key_weights_kernel<kFmt, kCtas>;
   cudaError_t e = attrs.run([fn] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
   if (e != cudaSuccess) return e;
-  // no more shares than tiles there can be
-  const int64_t most = p.kv.B * ((cap + kTile * kCtas - 1) / (kTile * kCtas)), room = device_sm_count() / kCtas;
+  // no more shares than tiles there can be, once for each chunk (1280 query rows over 464 4-bit keys: 41 us
+  // with two shares, 23 with ten)
+  const int64_t chunks = ((int64_t)p.s * p.H + kTile * kCtas - 1) / (kTile * kCtas);
+  const int64_t most = p.kv.B * ((cap + kTile * kCtas - 1) / (kTile * kCtas)) * chunks, room = device_sm_count() / kCtas;
   const int shares = (int)(most < room ? most : room);
   cudaLaunchConfig_t config{};
   config.gridDim = dim3((unsigned)(shares * kCtas));
