@@ -283,7 +283,8 @@ __device__ __noinline__ void rescale_o(uint32_t to, float a) {
 // 128 columns of this warp's 32 rows as they are (weights relative to the row's maximum), 16 at a time through 2 KB of
 // shared memory so that a store brings whole sectors
 __device__ __noinline__ void store_part(const DecodeFp4Params& p, uint32_t to, int64_t slot_row0, int rows, int col, uint32_t stage, int lane) {
-#pragma unroll 2
+  if (rows <= 0) return;                              // (17 requests of 32 query rows 53.3 -> 51.3 us)
+#pragma unroll 1
   for (int c = 0; c < 128; c += 16) {
     uint32_t o[16];
     tmem_ld16(to + c, o);
