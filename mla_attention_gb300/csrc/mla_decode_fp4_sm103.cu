@@ -49,7 +49,7 @@ constexpr int kOffBars = kOffMax + 3 * 64 * 4;
 
 struct Bars {
   // in the first CTA, with arrivals of both CTAs' warps
-  uint64_t kfull[2], vfull[2], qfull, pfull[2], sfree[2], ofree;
+  uint64_t kfull[2], vfull[2], qfull, pfull, sfree[2], ofree;
   // in each CTA, by commits to both
   uint64_t kempty[2], vempty[2], qempty, sfull[2], pvdone;
   // in each CTA
@@ -320,12 +320,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) mbar_init(&bars.kfull[i], 2 * (4 + i)), mbar_init(&bars.kempty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.vfull[i], 8), mbar_init(&bars.vempty[i], 1), mbar_init(&bars.pfull[i], 8);
+      mbar_init(&bars.vfull[i], 8), mbar_init(&bars.vempty[i], 1);
       mbar_init(&bars.sfull[i], 1), mbar_init(&bars.sfree[i], 16);
       mbar_init(&bars.same[i], 4), mbar_init(&bars.drain[i], 1);
     }
     mbar_init(&bars.qfull, 18), mbar_init(&bars.qempty, 1);
-    mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 16);
+    mbar_init(&bars.pfull, 16), mbar_init(&bars.pvdone, 1), mbar_init(&bars.ofree, 16);
     for (int i = 0; i < kRowSlots; ++i) mbar_init(&bars.rfull[i], 1), mbar_init(&bars.rfree[i], 17);
     mbar_init(&bars.stall, 1);
     bars.abort = 0;
@@ -418,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
 #pragma unroll
         for (int i = 0; i < 4; ++i) st_shared16(box_unit(prow, r, 4 * cc + i), make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]));
         fence_proxy_async_smem();
-        first_cta_arrive(&bars.pfull[hh], cta);
+        first_cta_arrive(&bars.pfull, cta);
       }
       if (!live) break;
       if (!wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) break;
@@ -476,9 +476,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       for (; live && shares.next(it); ++n) {
         if (n > 0 && !wait.warp(&bars.ofree, (n - 1) & 1, D_OFREE, true)) break;
         for (int t = it.t0; t < it.t1; ++t, ++u) {
+          // All row warps have scaled O ahead of either half: the MMAs over one half of the keys add to every lane of O, also
+          // to those of the warps that bring P of the other half.
+          if (!wait.warp(&bars.pfull, u & 1, D_PFULL, true)) { live = false; break; }
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            if (!wait.warp(&bars.vfull[h], u & 1, D_VFULL, true) || !wait.warp(&bars.pfull[h], u & 1, D_PFULL, true)) { live = false; break; }
+            if (!wait.warp(&bars.vfull[h], u & 1, D_VFULL, true)) { live = false; break; }
             tc_fence_after();
             if (elect_one()) {
               mma2_values(tbase + kTmemO, tbase + kTmemO + 128, sdesc_sw128(pst + h * kBox, 16, 1024), sdesc_sw128(vst + h * 4 * kBox, kBox, 1024),
