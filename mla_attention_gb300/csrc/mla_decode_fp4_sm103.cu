@@ -372,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         tmem_ld32(tbase + lanes + kTmemS + buf * 64 + 32 * cc, s);
         tmem_wait_ld();
         tc_fence_before();
-        first_cta_arrive(&bars.sfree[buf], cta);
+        first_cta_arrive<false>(&bars.sfree[buf], cta);
         const int visible = seen - t * kTile - hh * kHalf - 32 * cc;
         mask_piece<kUp>(s, visible);
         float e[4];
@@ -418,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
 #pragma unroll
         for (int i = 0; i < 4; ++i) st_shared16(box_unit(prow, r, 4 * cc + i), make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]));
         fence_proxy_async_smem();
-        first_cta_arrive(&bars.pfull, cta);
+        first_cta_arrive<true>(&bars.pfull, cta);
       }
       if (!live) break;
       if (!wait.warp(&bars.pvdone, (u - 1) & 1, D_PVDONE)) break;
@@ -433,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         if (hh == 0 && cc == 0) stat[0] = m;
       }
       tc_fence_before();
-      first_cta_arrive(&bars.ofree, cta);
+      first_cta_arrive<false>(&bars.ofree, cta);
     }
   } else if (warp == kMmaS) {
     // ---------------- scores ----------------
@@ -526,13 +526,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (!load()) break;
       if (is_k) {
         take_query_box(qbox, w, lane);
-        first_cta_arrive(&bars.qfull, cta);
+        first_cta_arrive<true>(&bars.qfull, cta);
       }
       for (int t = it.t0; t < it.t1; ++t, ++u) {
         if (!wait.warp(empty, (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
         convert_raw(x, boxes, r0, lane);
         fence_proxy_async_smem();
-        first_cta_arrive(full, cta);
+        first_cta_arrive<true>(full, cta);
         // the next tile's loads go out while its place is not free yet
         if (t + 1 < it.t1 && !load()) { live = false; break; }
       }
@@ -577,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       if (!wait.warp(&bars.qempty, (n & 1) ^ 1, D_QEMPTY)) break;
       ask_query_box(p, it.g, (int)cta * kHalf, qbox, 8, lane);
       take_query_box(qbox, 8, lane);
-      first_cta_arrive(&bars.qfull, cta);
+      first_cta_arrive<true>(&bars.qfull, cta);
       for (int t = it.t0; t < it.t1; ++t, ++u) {
         const uint32_t slot = u % kRowSlots;
         if (!wait.warp(&bars.rfull[slot], (u / kRowSlots) & 1, D_RFULL) || !wait.warp(&bars.kempty[1], (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
@@ -592,7 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         warp_arrive(&bars.rfree[slot]);
         cp_async_wait_all();
         fence_proxy_async_smem();
-        first_cta_arrive(&bars.kfull[1], cta);
+        first_cta_arrive<true>(&bars.kfull[1], cta);
       }
     }
     cp_async_wait_all();

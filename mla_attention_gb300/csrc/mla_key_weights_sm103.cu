@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
   // what the MMAs of the pair wait for, in the first CTA
   auto tell = [&](uint64_t* bar) {
     if constexpr (kCtas == 1) warp_arrive(bar);
-    else first_cta_arrive(bar, cta);
+    else first_cta_arrive<true>(bar, cta);
   };
 
   if (warp < 4) {
@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
           }
         }
         tc_fence_before();
-        tell(&bars.sfree[buf]);
+        if constexpr (kCtas == 1) warp_arrive(&bars.sfree[buf]);
+        else first_cta_arrive<false>(&bars.sfree[buf], cta);
         float a, b;
         f32x2_split(add_f32x2(sum2[0], sum2[1]), a, b);
         if (mine) *w = first ? a + b : chunks == 1 ? fmaf(p.decay, old, a + b) : old + (a + b);
@@ -317,11 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             if (i == it.i0) {
               if (!wait.warp(&bars.qfull[k], c_all & 1, W_QFULL)) { live = false; break; }
               fence_proxy_async_smem();
-              first_cta_arrive(&bars.qfull[k], cta);
+              first_cta_arrive<true>(&bars.qfull[k], cta);
             }
             if (!wait.warp(&bars.kfull[slot], phase, W_KFULL)) { live = false; break; }
             fence_proxy_async_smem();
-            first_cta_arrive(&bars.kfull[slot], cta);
+            first_cta_arrive<true>(&bars.kfull[slot], cta);
             if (++slot == kStages) slot = 0, phase ^= 1;
           }
     }
