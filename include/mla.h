@@ -480,7 +480,8 @@ mla_status mla_kv_append_fp4(const void* c_kv, int64_t c_kv_stride, const void* 
  * [B, q_per_req, H, 576]; out bf16 [B, q_per_req, H, 512]; lse fp32 [B, q_per_req, H] or NULL), with any
  * page_size >= 1, num_pages * page_size below 2^31 and 2^-100 <= kv_scale <= 2^100.  The products of the latent part run on f16
  * operands (a code times its scale is exact there; q is rounded to f16: |q| must stay below 65504, values below
- * 2^-14 keep an absolute error of 2^-25) and those of the RoPE part on bf16 ones; sums are fp32.  A page id outside
+ * 2^-14 keep an absolute error of 2^-25) and those of the RoPE part on bf16 ones; sums are fp32.  A key's softmax weight meets its
+ * value in f16: below 2^-21 of a row's largest it keeps an absolute error of 2^-32 of that.  A page id outside
  * [0, num_pages) reads as keys of zeros, a length outside [0, max_pages * page_size] is cut to it; both
  * record MLA_ERR_DEVICE_RANGE (details 0x207a, 0x207b).  Rows of the block table behind a request's last page
  * are not read.  With several tokens a request, a NaN in a row that the later ones see makes the earlier ones' outputs NaN too.

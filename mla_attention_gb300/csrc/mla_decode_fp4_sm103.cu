@@ -8,7 +8,7 @@
 // operand, so that a key's row is taken apart once for the scores and once for the values.  CTA c has the tile's keys
 // 64 c .. 64 c + 63 for the scores and the latent columns 128 c .. and 256 + 128 c .. of all its keys for the values.
 //
-// A code times its scale has at most six bits and is exact in f16; q and P are f16 too (P a weight of at most 2^8), the RoPE
+// A code times its scale has at most six bits and is exact in f16; q and P are f16 too (P a weight of at most 2^8, times 2^7), the RoPE
 // columns stay bf16 as their MMA's operands, sums are fp32.  28 warps a CTA:
 //   0-7    rows: lanes L and L + 64 of tensor memory hold the same row's scores of 64 keys each, 32 of them a warp; maximum
 //          through shared memory, lazy rescale of O (by more than 2^8), exponentials, P
@@ -37,7 +37,8 @@ constexpr int kThreads = 896, kMmaS = 8, kMmaV = 9, kTableWarp = 10, kFirstK = 1
 constexpr int kBox = 64 * 128;                        // 64 rows of 128 bytes
 constexpr int kRowSlots = 3;
 constexpr uint32_t kTmemO = 0, kTmemS = 256;          // O: 256 columns; S: two buffers of 64
-constexpr float kRescale = 8.f;                       // P passes 1 by 2^8 at most
+constexpr float kRescale = 8.f;                       // a weight passes 1 by 2^8 at most
+constexpr float kLift = 7.f;                          // P and O are held times 2^7: P is below f16's 2^16, its last bit 2^-31 of the largest
 
 constexpr int kOffQ = 0;                              // 9 boxes
 constexpr int kOffK = 9 * kBox;                       // 9 boxes
@@ -394,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
           m = mt;
         }
         const float ref = m == -CUDART_INF_F ? 0.f : m;
-        const uint64_t nref = f32x2(-ref, -ref);
+        const uint64_t nref = f32x2(kLift - ref, kLift - ref);
         uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {                 // packed into the first sixteen words
@@ -429,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
                  smem_u32(smem + kOffP + hh * kBox + (warp & 1) * 4096 + cc * 2048), lane);
       float* stat = p.part_stat + slot_row * 8;       // the maximum and the four sums
       if (row < it.g.rows && guard_span(p.err, G_PART_LSE, stat, 32, p.part_stat, p.part_stat_bytes)) {
-        stat[1 + 2 * hh + cc] = l;
+        stat[1 + 2 * hh + cc] = l * 0x1p-7f;
         if (hh == 0 && cc == 0) stat[0] = m;
       }
       tc_fence_before();
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(kPairs) decode_fp4_reduce_kernel(const __grid_
       }
     }
   }
-  const float inv = nan ? CUDART_NAN_F : wsum > 0.f ? p.kv_scale / wsum : 0.f;
+  const float inv = nan ? CUDART_NAN_F : wsum > 0.f ? p.kv_scale * 0x1p-7f / wsum : 0.f;    // O has P's 2^7
   __nv_bfloat16* out = p.out + item * kLatent + 4 * tid;
   if (guard_span(p.err, G_OUT, out, 8, p.out, (uint64_t)rows * kLatent * 2))
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
