@@ -484,7 +484,7 @@ mla_status mla_kv_append_fp4(const void* c_kv, int64_t c_kv_stride, const void* 
  * value in f16: below 2^-21 of a row's largest it keeps an absolute error of 2^-32 of that.  A page id outside
  * [0, num_pages) reads as keys of zeros, a length outside [0, max_pages * page_size] is cut to it; both
  * record MLA_ERR_DEVICE_RANGE (details 0x207a, 0x207b).  Rows of the block table behind a request's last page
- * are not read.  With several tokens a request, a NaN in a row that the later ones see makes the earlier ones' outputs NaN too.
+ * are not read.  A NaN in a row makes the outputs and lse of the tokens that see it NaN, and of no others.
  * workspace_bytes >= mla_decode_fp4_workspace_size(B, q_per_req, H, num_splits).
  */
 size_t mla_decode_fp4_workspace_size(int B, int q_per_req, int H, int num_splits);

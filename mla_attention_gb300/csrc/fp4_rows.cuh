@@ -41,6 +41,13 @@ __device__ __forceinline__ uint2 fp4_scales2(uint32_t two) {
   const uint32_t h = e4m3x2_to_f16x2((uint16_t)two);
   return make_uint2(__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232));
 }
+// the same with `cap`, in both halves, in the place of a NaN: the largest scale, or a NaN again
+constexpr uint32_t kScaleNan = 0x7fff7fffu, kScale448 = 0x5f005f00u;
+__device__ __forceinline__ uint2 fp4_scales2(uint32_t two, uint32_t cap) {
+  uint32_t h = e4m3x2_to_f16x2((uint16_t)two);
+  asm("min.f16x2 %0, %0, %1;" : "+r"(h) : "r"(cap));          // of a number and a NaN the number
+  return make_uint2(__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232));
+}
 // eight e4m3 values as f16
 __device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t a, uint32_t b) {
   return make_uint4(e4m3x2_to_f16x2((uint16_t)a), e4m3x2_to_f16x2((uint16_t)(a >> 16)), e4m3x2_to_f16x2((uint16_t)b),

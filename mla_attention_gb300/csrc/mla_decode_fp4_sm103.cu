@@ -221,15 +221,16 @@ __device__ __forceinline__ void load_raw(const DecodeFp4Params& p, Raw& x, const
   }
 }
 // into four boxes of 64 columns, rows r0 .. r0 + 15.  A lane stores its four 16-byte pieces from its box's number on, so that
-// the eight lanes of a row meet eight banks.
-__device__ __forceinline__ void convert_raw(const Raw& x, uint32_t boxes, int r0, int lane) {
+// the eight lanes of a row meet eight banks.  Of values a NaN scale becomes a finite one: the key's score is a NaN already, and so is the
+// result of each row that sees it; a row from which the key is hidden (weight 0) has nothing of it.
+__device__ __forceinline__ void convert_raw(const Raw& x, uint32_t boxes, int r0, int lane, uint32_t cap) {
   const int b = (lane >> 1) & 3, half = lane & 1;
   const bool odd = b & 1, high = b & 2;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + 4 * i + (lane >> 3);
     const uint32_t row = boxes + b * kBox + r * 128;
-    const uint2 s = fp4_scales2(x.sc[i]);
+    const uint2 s = fp4_scales2(x.sc[i], cap);
     uint4 v = x.v[i];
     if (odd) v = make_uint4(v.y, v.z, v.w, v.x);
     if (high) v = make_uint4(v.z, v.w, v.x, v.y);
@@ -531,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       }
       for (int t = it.t0; t < it.t1; ++t, ++u) {
         if (!wait.warp(empty, (u & 1) ^ 1, D_KEMPTY)) { live = false; break; }
-        convert_raw(x, boxes, r0, lane);
+        convert_raw(x, boxes, r0, lane, is_k ? kScaleNan : kScale448);
         fence_proxy_async_smem();
         first_cta_arrive<true>(full, cta);
         // the next tile's loads go out while its place is not free yet

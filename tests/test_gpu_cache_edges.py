@@ -61,3 +61,24 @@ def test_decode_a_heavy_key_and_a_long_tail(below):
     assert (bo < 0.1 * ro + 1e-9).mean() > 0.9 if below < 19 else True
     cases._within(lse, rl, bl, "lse")
     cases._within(out, ro, bo, "out")
+
+
+@pytest.mark.parametrize("s,H,scale", [(3, 16, 0.07), (3, 16, -0.07), (10, 16, 0.07), (2, 128, 0.07), (130, 1, 0.07)])
+@pytest.mark.parametrize("nan", [0x7F, 0xFF])
+def test_decode_a_nan_reaches_the_tokens_that_see_it_alone(s, H, scale, nan):
+    """A NaN scale in a request's last key, in the last but one, and in one that all tokens see."""
+    lens, page = [200, 200, 200, 200], 16
+    cache, table, keys = cases._paged("fp4", lens, page, 91)
+    raw = cache.cpu()
+    for b, j in ((0, 199), (1, 198), (2, 200 - s)):
+        pg, r = _rows(raw, table, b, [j])
+        raw[pg[0], r[0], 256 + 7 * b] = nan
+    q = cases._query(4, s, H, 91)
+    ro, rl = co.decode(to_np(q), keys, scale)
+    out, lse = mla_decode_fp4(q.to(dev()), raw.to(dev()), 1.0, table, cases._i32(lens), scale)
+    cases._done()
+    bo, bl = cases._decode_bounds(to_np(q), keys, scale, None, ro, rl)
+    for b, seen in ((0, s - 1), (1, s - 2), (2, 0), (3, s)):       # tokens from `seen` on see the NaN
+        cases._within(out[b, :seen], ro[b, :seen], bo[b, :seen], "out")
+        cases._within(lse[b, :seen], rl[b, :seen], bl[b, :seen], "lse")
+        assert torch.isnan(out[b, seen:]).all() and torch.isnan(lse[b, seen:]).all()
