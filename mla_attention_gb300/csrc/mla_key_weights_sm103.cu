@@ -51,6 +51,7 @@ struct Bars {
   uint64_t lfull[2], lfree[2];
   uint64_t drain, stall;
   uint32_t tmem_base, abort;
+  uint32_t skips[2];             // a chunk of query rows has some that add nothing
   int32_t start_b, start_t, start_o;
   int64_t share, start_range;
 };
@@ -162,6 +163,46 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   return v;
 }
 
+// Sums of exp2(score c2 + addend) over 32 query rows of this lane's key, without those that `none` tells.
+template <class None>
+__device__ __forceinline__ void key_sums32(uint32_t from, uint64_t c22, const float* addends, uint64_t (&sum2)[2], None none) {
+  uint32_t s[32];
+  tmem_ld32(from, s);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(addends + i);
+    float x0, x1, x2, x3;
+    f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c22, f32x2(l.x, l.y)), x0, x1);
+    f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c22, f32x2(l.z, l.w)), x2, x3);
+    x0 = ex2_approx(x0), x1 = ex2_approx(x1), x2 = ex2_approx(x2), x3 = ex2_approx(x3);
+    x0 = none(i, l.x) ? 0.f : x0, x1 = none(i + 1, l.y) ? 0.f : x1, x2 = none(i + 2, l.z) ? 0.f : x2, x3 = none(i + 3, l.w) ? 0.f : x3;
+    sum2[0] = add_f32x2(sum2[0], f32x2(x0, x1));
+    sum2[1] = add_f32x2(sum2[1], f32x2(x2, x3));
+  }
+}
+__device__ __forceinline__ float sum_of(const uint64_t (&sum2)[2]) {
+  float a, b;
+  f32x2_split(add_f32x2(sum2[0], sum2[1]), a, b);
+  return a + b;
+}
+// n query rows, of which the last 32 may be less
+__device__ __forceinline__ float key_sum(uint32_t from, int n, uint64_t c22, const float* addends) {
+  uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+  int n0 = 0;
+  for (; n0 + 32 <= n; n0 += 32) key_sums32(from + n0, c22, addends + n0, sum2, [](int, float) { return false; });
+  if (n0 < n) key_sums32(from + n0, c22, addends + n0, sum2, [=](int i, float) { return n0 + i >= n; });
+  return sum_of(sum2);
+}
+// The same without the rows below `hidden` and those whose addend is -inf, whatever their score is (an infinite one, or a NaN, is
+// not made nothing by the addend).  Out of line, for the tiles that need it: the loop stays in the instruction cache.
+__device__ __noinline__ float key_sum_of_some(uint32_t from, int n, uint64_t c22, const float* addends, int hidden) {
+  uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+  for (int n0 = 0; n0 < n; n0 += 32)
+    key_sums32(from + n0, c22, addends + n0, sum2, [=](int i, float l) { return n0 + i < hidden || l == -CUDART_INF_F; });
+  return sum_of(sum2);
+}
+
 constexpr int kNoRow = -1;                       // no key there, or its page is none
 // kCtas 2: a cluster of two CTAs, MMAs of the pair
 template <int kFmt, int kCtas>
@@ -226,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
       const uint32_t lslot = c_all % kLseSlots;
       const float* minus_lse = lse_slots + lslot * kChunk;
       if (!wait.warp(&bars.lfull[lslot], (c_all / kLseSlots) & 1, W_LFULL)) break;
+      const bool skips = bars.skips[lslot] != 0;
       const int n = min(rows - it.c * kChunk, kChunk);
       for (int i = it.i0; i < it.i1; ++i, ++u) {
         const int j = ((it.t0 + i) * kCtas + cta) * kTile + tid, buf = u & 1;
@@ -241,35 +283,15 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         const float old = mine && !first ? *w : 0.f;
         // query rows below `hidden` do not see the key
         const int hidden = (int)max((int64_t)0, (int64_t)(j - (it.len - p.s)) * p.H - it.c * kChunk);
-        const bool any_hidden = __any_sync(~0u, j < it.len && hidden > 0);
+        const bool choose = __any_sync(~0u, j < it.len && hidden > 0) || skips;
         if (!wait.warp(&bars.sfull[buf], (u >> 1) & 1, W_SFULL)) { live = false; break; }
         tc_fence_after();
-        uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-        for (int n0 = 0; n0 < n; n0 += 32) {
-          uint32_t s[32];
-          tmem_ld32(tbase + lanes + buf * kChunk + n0, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i4 = 0; i4 < 32; i4 += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(minus_lse + n0 + i4);
-            float x0, x1, x2, x3;
-            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i4]), __uint_as_float(s[i4 + 1])), c22, f32x2(l.x, l.y)), x0, x1);
-            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i4 + 2]), __uint_as_float(s[i4 + 3])), c22, f32x2(l.z, l.w)), x2, x3);
-            x0 = ex2_approx(x0), x1 = ex2_approx(x1), x2 = ex2_approx(x2), x3 = ex2_approx(x3);
-            if (any_hidden) {
-              x0 = n0 + i4 < hidden ? 0.f : x0, x1 = n0 + i4 + 1 < hidden ? 0.f : x1;
-              x2 = n0 + i4 + 2 < hidden ? 0.f : x2, x3 = n0 + i4 + 3 < hidden ? 0.f : x3;
-            }
-            sum2[0] = add_f32x2(sum2[0], f32x2(x0, x1));
-            sum2[1] = add_f32x2(sum2[1], f32x2(x2, x3));
-          }
-        }
+        const uint32_t from = tbase + lanes + buf * kChunk;
+        const float sum = choose ? key_sum_of_some(from, n, c22, minus_lse, hidden) : key_sum(from, n, c22, minus_lse);
         tc_fence_before();
         if constexpr (kCtas == 1) warp_arrive(&bars.sfree[buf]);
         else first_cta_arrive<false>(&bars.sfree[buf], cta);
-        float a, b;
-        f32x2_split(add_f32x2(sum2[0], sum2[1]), a, b);
-        if (mine) *w = first ? a + b : chunks == 1 ? fmaf(p.decay, old, a + b) : old + (a + b);
+        if (mine) *w = first ? sum : chunks == 1 ? fmaf(p.decay, old, sum) : old + sum;
       }
       if (live) warp_arrive(&bars.lfree[lslot]);
       ++c_all;
@@ -370,9 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         // the rows of two tiles go ahead of the log-sum-exps, whose place may be in use still
         if (i == min(it.i0 + 1, it.i1 - 1)) {
           if (!wait.warp(&bars.lfree[lslot], ((c_all / kLseSlots) & 1) ^ 1, W_LFREE)) { live = false; break; }
+          bool none = false;
 #pragma unroll
-          for (int i = 0; i < kChunk / 32; ++i)
-            lse_slots[lslot * kChunk + 32 * i + lane] = l[i] == -CUDART_INF_F ? -CUDART_INF_F : -l[i] * 1.4426950408889634f;
+          for (int i = 0; i < kChunk / 32; ++i) {
+            const float minus = l[i] == -CUDART_INF_F ? -CUDART_INF_F : -l[i] * 1.4426950408889634f;
+            lse_slots[lslot * kChunk + 32 * i + lane] = minus;
+            none |= minus == -CUDART_INF_F && it.c * kChunk + 32 * i + lane < rows;
+          }
+          none = __any_sync(~0u, none);
+          if (lane == 0) bars.skips[lslot] = none;
           warp_arrive(&bars.lfull[lslot]);
         }
       }

@@ -6,7 +6,7 @@ import torch
 
 import oracle.cache_oracle as co
 import tests.test_gpu_cache as cases
-from mla_attention_gb300 import mla_decode_fp4
+from mla_attention_gb300 import mla_decode_fp4, mla_key_weights
 from tests.helpers import dev, to_np
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +82,87 @@ def test_decode_a_nan_reaches_the_tokens_that_see_it_alone(s, H, scale, nan):
         cases._within(out[b, :seen], ro[b, :seen], bo[b, :seen], "out")
         cases._within(lse[b, :seen], rl[b, :seen], bl[b, :seen], "lse")
         assert torch.isnan(out[b, seen:]).all() and torch.isnan(lse[b, seen:]).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# the keys' weights
+# ---------------------------------------------------------------------------------------------
+def _with_bf16(cache, table, fmt, keys, b, j, column, value):
+    """The cache with RoPE column `column` of a key set, bf16 in both formats."""
+    raw = cache.cpu()
+    if fmt == "fp4":
+        _put_pe(raw, table, b, j, column, value)
+    else:
+        pg, r = _rows(raw, table, b, [j])
+        raw[pg[0], r[0], 512 + column] = value
+    keys[b][j, 512 + column] = value
+    return raw.to(dev())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+@pytest.mark.parametrize("s,H", [(1, 16), (1, 32), (1, 40), (1, 128), (3, 16), (2, 80), (3, 100), (9, 64)])
+def test_weights_of_an_infinite_key(fmt, s, H):
+    """A key with scores of -inf in every row has the weight 0, whatever the number of rows."""
+    lens, n = [300, 70], 60
+    cache, table, keys = cases._paged(fmt, lens, 64, 92)
+    q = cases._query(2, s, H, 92)
+    q[..., 512] = q[..., 512].abs() + 0.5
+    qn = to_np(q)
+    cache = _with_bf16(cache, table, fmt, keys, 0, n, 0, -float("inf"))
+    cache = _with_bf16(cache, table, fmt, keys, 1, n, 0, -float("inf"))
+    _, rl = co.decode(qn, [np.delete(k, n, 0) for k in keys], 0.07)
+    w = torch.ones((2, 300), device=dev())
+    mla_key_weights(q.to(dev()), torch.tensor(rl, dtype=torch.float32).to(dev()), cache, table, cases._i32(lens), 0.07, w, decay=0.5)
+    cases._done()
+    assert w[0, n] == 0.5 and w[1, n] == 0.5 and torch.isfinite(w).all()
+    ref = co.key_weights(qn, rl, keys, 0.07, np.ones((2, 300)), 0.5)
+    finite = [np.nan_to_num(k, neginf=0.0) for k in keys]
+    cases._within(w, ref, cases._weight_bounds(qn, rl, finite, 0.07, ref), "weights")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "fp4"])
+@pytest.mark.parametrize("s,H", [(1, 16), (1, 32), (1, 128), (2, 128), (3, 100), (5, 64)])
+def test_weights_rows_with_an_infinite_lse_add_nothing(fmt, s, H):
+    """-inf and +inf add nothing over a NaN key either; a NaN key shows in its weight where a row of a finite one sees it."""
+    lens, n = [300, 300], 61
+    cache, table, keys = cases._paged(fmt, lens, 64, 93)
+    raw = cache.cpu().view(torch.uint8)
+    for b in range(2):
+        pg, r = _rows(raw, table, b, [n])
+        raw[pg[0], r[0], 256 if fmt == "fp4" else 0] = 0x7F
+        if fmt == "bf16":
+            raw[pg[0], r[0], 0], raw[pg[0], r[0], 1] = 0xC0, 0x7F
+    cache = raw.to(dev()).view(cache.dtype)
+    q = cases._query(2, s, H, 93)
+    qn = to_np(q)
+    _, rl = co.decode(qn, [np.delete(k, n, 0) for k in keys], 0.07)
+    rl[0] = -np.inf
+    rl[0, :, 1::2] = np.inf
+    rl[1, :, ::3] = -np.inf
+    w = torch.ones((2, 300), device=dev())
+    mla_key_weights(q.to(dev()), torch.tensor(rl, dtype=torch.float32).to(dev()), cache, table, cases._i32(lens), 0.07, w)
+    cases._done()
+    assert (w[0] == 1).all()
+    assert torch.isnan(w[1, n])
+    w[1, n], ref = 1, co.key_weights(qn, rl, keys, 0.07, np.ones((2, 300)), 1.0)
+    ref[1, n] = 1
+    cases._within(w, ref, cases._weight_bounds(qn, rl, keys, 0.07, ref), "weights")
+
+
+def test_weights_of_a_score_that_gave_an_infinite_lse():
+    """A key with a score of +inf, and the log-sum-exp of +inf that it leads to: the row adds nothing, to that key neither."""
+    lens, n = [150], 33
+    cache, table, keys = cases._paged("bf16", lens, 64, 94)
+    q = cases._query(1, 1, 32, 94)
+    q[..., 512] = torch.where(torch.arange(32) % 2 == 0, 1.0, -1.0).bfloat16()
+    qn = to_np(q)
+    cache = _with_bf16(cache, table, "bf16", keys, 0, n, 0, float("inf"))
+    _, rl = co.decode(qn, [np.delete(k, n, 0) for k in keys], 0.07)
+    rl[:, :, ::2] = np.inf
+    w = torch.zeros((1, 150), device=dev())
+    mla_key_weights(q.to(dev()), torch.tensor(rl, dtype=torch.float32).to(dev()), cache, table, cases._i32(lens), 0.07, w)
+    cases._done()
+    assert w[0, n] == 0
+    odd = co.key_weights(qn[:, :, 1::2], rl[:, :, 1::2], keys, 0.07, np.zeros((1, 150)), 1.0)
+    finite = [np.nan_to_num(k, posinf=0.0) for k in keys]
+    cases._within(w, odd, cases._weight_bounds(qn, rl, finite, 0.07, odd), "weights")
