@@ -67,7 +67,9 @@ __device__ __forceinline__ void move_weights(const CompactParams& p, int b, int 
     for (int u = 0; u < kMany; ++u) {
       const int64_t i = i0 + ((int64_t)rank * kMany + u) * kThreads + threadIdx.x;
       const int2 en = entry(p, b, i, count);
-      to[u] = moving(p, i, count, en, limit, false) && guard_span(p.err, G_STEP_IN, w + en.y, 4, p.weights, ext) ? (int)i : -1;
+      // with its row: where that has no page, or its place has none, neither moves
+      const bool moves = moving(p, i, count, en, limit, false) && row_at(p, b, en.y, false) >= 0 && row_at(p, b, (int)i, false) >= 0;
+      to[u] = moves && guard_span(p.err, G_STEP_IN, w + en.y, 4, p.weights, ext) ? (int)i : -1;
       if (to[u] >= 0) v[u] = __ldcg(w + en.y);
     }
     __syncwarp();

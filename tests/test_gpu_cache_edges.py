@@ -6,7 +6,7 @@ import torch
 
 import oracle.cache_oracle as co
 import tests.test_gpu_cache as cases
-from mla_attention_gb300 import mla_decode_fp4, mla_key_weights
+from mla_attention_gb300 import mla_compact_rows, mla_decode_fp4, mla_key_weights
 from tests.helpers import dev, to_np
 
 pytestmark = pytest.mark.gpu
@@ -166,3 +166,30 @@ def test_weights_of_a_score_that_gave_an_infinite_lse():
     odd = co.key_weights(qn[:, :, 1::2], rl[:, :, 1::2], keys, 0.07, np.zeros((1, 150)), 1.0)
     finite = [np.nan_to_num(k, posinf=0.0) for k in keys]
     cases._within(w, odd, cases._weight_bounds(qn, rl, finite, 0.07, odd), "weights")
+
+
+# ---------------------------------------------------------------------------------------------
+# the moves
+# ---------------------------------------------------------------------------------------------
+def test_compact_weights_stay_with_rows_whose_page_is_none():
+    """Rows that are not moved, since they or their places have no page, keep their weights."""
+    page, lens = 4, 12
+    cache = torch.arange(8 * page * 16, dtype=torch.int32).reshape(8, page, 16).to(torch.uint8)
+    w0 = torch.rand((3, lens), generator=torch.Generator().manual_seed(95))
+    table = cases._i32([[0, 8, 2], [-1, 4, 5], [6, 7, 1]])           # the second page of request 0, the first of request 1 are none
+    idx = [[5, 6, 8, 9, 10, 11], [4, 5, 6, 8, 9, 11], [1, 2, 3, 5, 8, 11]]
+    for K in (6, 300):
+        wide = torch.full((3, K), -1, dtype=torch.int32)
+        wide[:, :6] = torch.tensor(idx, dtype=torch.int32)
+        d, w = cache.to(dev()), w0.to(dev())
+        mla_compact_rows(d, table, wide.to(dev()), cases._i32([6, 6, 6]), weights=w)
+        assert "0x7d" in cases._faults()
+        ref, rw = cache.clone(), w0.clone()
+        host = table.cpu()
+        for b in range(3):
+            for i, j in enumerate(idx[b]):
+                src, dst = int(host[b, j // page]), int(host[b, i // page])
+                if 0 <= src < 8 and 0 <= dst < 8:
+                    ref[dst, i % page] = ref[src, j % page]
+                    rw[b, i] = rw[b, j]
+        assert torch.equal(d.cpu(), ref) and torch.equal(w.cpu(), rw)
