@@ -485,7 +485,8 @@ mla_status mla_kv_append_fp4(const void* c_kv, int64_t c_kv_stride, const void* 
  * [0, num_pages) reads as keys of zeros, a length outside [0, max_pages * page_size] is cut to it; both
  * record MLA_ERR_DEVICE_RANGE (details 0x207a, 0x207b).  Rows of the block table behind a request's last page
  * are not read.  A NaN in a row makes the outputs and lse of the tokens that see it NaN, and of no others.
- * workspace_bytes >= mla_decode_fp4_workspace_size(B, q_per_req, H, num_splits).
+ * workspace_bytes >= mla_decode_fp4_workspace_size(B, q_per_req, H, num_splits); another workspace than the attention calls'
+ * (as for mla_slot_map): what is recorded in it ends no wait of this call, but it would end theirs.
  */
 size_t mla_decode_fp4_workspace_size(int B, int q_per_req, int H, int num_splits);
 mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4, float kv_scale, int64_t num_pages,
@@ -509,7 +510,7 @@ mla_status mla_decode_fp4(const void* q, int q_per_req, const void* kv_cache_fp4
  * Formats 1 and 2 round q to f16 for the latent (1: all) columns, as mla_decode_fp8 and mla_decode_fp4 do.
  * No atomics: the same inputs give the same weights.
  * workspace_bytes >= mla_key_weights_workspace_size(B, q_per_req, H, width): 256 for up to 128 query rows (tokens times
- * heads) a request.
+ * heads) a request; another workspace than the attention calls', as for mla_decode_fp4.
  */
 size_t mla_key_weights_workspace_size(int B, int q_per_req, int H, int width);
 mla_status mla_key_weights(const void* q, int q_per_req, const float* lse, const void* kv_cache, int cache_format,

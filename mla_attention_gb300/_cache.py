@@ -22,6 +22,12 @@ def _paged(kv_cache, block_table, dev, B):
     return pages, page, max_pages, _dense(block_table, "block_table", _I32, dev, (B, max_pages))
 
 
+def _scratch(nbytes, dev):
+    """The device's scratch buffer of mla_decode_fp4 and mla_key_weights.  It is not the attention's, whose kernels give up their
+    waits while their word is set: a length that was cut is recorded in this one."""
+    return _lib.grown(_lib._scratch_cache, nbytes, torch.device("cuda", dev))
+
+
 def _query(q):
     """q as [B, s, H, 576], its device and whether it came as [B, H, 576]."""
     try:
@@ -97,7 +103,7 @@ def mla_decode_fp4(q, kv_cache_fp4, kv_scale: float, block_table, lens, scale: f
     if not 0 <= num_splits <= 65535:
         raise MLAError(1, f"num_splits must be between 0 and 65535, got {num_splits}")
     if ws is None:
-        ws = _lib.workspace(_lib.lib().mla_decode_fp4_workspace_size(B, s, H, num_splits), torch.device("cuda", dev))
+        ws = _scratch(_lib.lib().mla_decode_fp4_workspace_size(B, s, H, num_splits), dev)
     _call("mla_decode_fp4", dev, stream, pq, s, pc, float(kv_scale), pages, page, pt, max_pages, pl, B, H, float(scale), ps,
           num_splits, po, pe, *_workspace(ws, dev))
     if single:
@@ -125,7 +131,7 @@ def mla_key_weights(q, lse, kv_cache, block_table, lens, scale: float, weights, 
         raise MLAError(1, f"weights has too many columns ({width})")
     pw = _rows(weights, "weights", _F32, dev, (B, width))
     if ws is None and s * H > 128:
-        ws = _lib.workspace(_lib.lib().mla_key_weights_workspace_size(B, s, H, width), torch.device("cuda", dev))
+        ws = _scratch(_lib.lib().mla_key_weights_workspace_size(B, s, H, width), dev)
     _call("mla_key_weights", dev, stream, pq, s, pe, pc, fmt, float(kv_scale), pages, page, pt, max_pages,
           _dense(lens, "lens", _I32, dev, (B,)), B, H, float(scale), float(decay), pw, weights.stride(0), width,
           *_workspace(ws, dev))

@@ -167,6 +167,7 @@ def _need(t: torch.Tensor, name: str, dtype, device=None, contiguous: bool = Tru
 # workspace: caller-owned scratch, cached per device; first bytes = status word
 # ---------------------------------------------------------------------------
 _ws_cache = {}
+_scratch_cache = {}    # of the calls over a smaller cache (see _cache), whose range codes end none of their waits, but would the attention's
 _ws_outgrown = []      # replaced by larger ones; a captured graph may still hold their addresses
 _status_cache = {}     # status words of the calls around the attention (see _step), one buffer per device
 
@@ -174,11 +175,15 @@ _status_cache = {}     # status words of the calls around the attention (see _st
 def workspace(nbytes: int, device: torch.device) -> torch.Tensor:
     """The device's scratch buffer of at least this size.  It grows by doubling, so that the outgrown ones together stay
     below the present one; where memory does not hold twice the size, by what the call needs."""
+    return grown(_ws_cache, nbytes, device)
+
+
+def grown(cache: dict, nbytes: int, device: torch.device) -> torch.Tensor:
     key = (device.type, device.index)
-    ws = _ws_cache.get(key)
+    ws = cache.get(key)
     if ws is None or ws.numel() < nbytes:
         with _lock:
-            ws = _ws_cache.get(key)
+            ws = cache.get(key)
             if ws is None or ws.numel() < nbytes:
                 need = max(int(nbytes), 256)
                 try:
@@ -187,22 +192,22 @@ def workspace(nbytes: int, device: torch.device) -> torch.Tensor:
                     new = torch.zeros(need, dtype=torch.uint8, device=device)
                 if ws is not None:
                     _ws_outgrown.append(ws)
-                ws = _ws_cache[key] = new
+                ws = cache[key] = new
     return ws
 
 
 def check_device_status(ws: Optional[torch.Tensor] = None, device=None, stream=None) -> int:
     """Read and clear the device status word; raise MLAError if a kernel reported a fault.  Without a
-    workspace: the device's own, those that it outgrew and the one of the calls around the attention (several faults in one
-    error, with the first's status)."""
+    workspace: the device's own, those that it outgrew and those of the calls around the attention and over a smaller cache
+    (several faults in one error, with the first's status)."""
     words = [ws]
     if ws is None:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         words = [workspace(256, device)]
         words += [w for w in _ws_outgrown if w.device == words[0].device]    # a captured graph reports in the one that it holds
         step = _status_cache.get(torch.cuda.current_device() if device.index is None else device.index)
-        if step is not None:
-            words.append(step)
+        scratch = _scratch_cache.get((words[0].device.type, words[0].device.index))
+        words += [w for w in (step, scratch) if w is not None]
     faults, found = [], 0
     for w in words:
         detail = c_uint32(0)

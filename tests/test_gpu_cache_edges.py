@@ -6,7 +6,7 @@ import torch
 
 import oracle.cache_oracle as co
 import tests.test_gpu_cache as cases
-from mla_attention_gb300 import mla_compact_rows, mla_decode_fp4, mla_key_weights
+from mla_attention_gb300 import mla_compact_rows, mla_decode_ex, mla_decode_fp4, mla_key_weights, mla_prefill
 from tests.helpers import dev, to_np
 
 pytestmark = pytest.mark.gpu
@@ -193,3 +193,30 @@ def test_compact_weights_stay_with_rows_whose_page_is_none():
                     ref[dst, i % page] = ref[src, j % page]
                     rw[b, i] = rw[b, j]
         assert torch.equal(d.cpu(), ref) and torch.equal(w.cpu(), rw)
+
+
+# ---------------------------------------------------------------------------------------------
+# status words
+# ---------------------------------------------------------------------------------------------
+def test_what_is_recorded_ends_no_attention_call():
+    """A length that decode and weights cut, not asked for yet: the attention calls that follow are as ever."""
+    lens, page = [300, 77], 16
+    cache, table, _ = cases._paged("bf16", lens, page, 96, poison=False)
+    small, small_table, _ = cases._paged("fp4", lens, page, 96, poison=False)
+    q = cases._query(2, 2, 128, 96).to(dev())
+    L, bad = cases._i32(lens), cases._i32([1 << 20, 77])
+    x, kv = torch.randn((1000, 16, 576), device=dev()).bfloat16(), torch.randn((1000, 576), device=dev()).bfloat16()
+
+    def attention():
+        return (*mla_decode_ex(q, cache, table, L, 0.07), *mla_prefill(x, kv, 0.07))
+
+    want = attention()
+    cases._done()
+    w = torch.zeros((2, 320), device=dev())
+    mla_decode_fp4(q, small, 1.0, small_table, bad, 0.07)
+    mla_key_weights(q, torch.zeros((2, 2, 128), device=dev()), cache, table, bad, 0.07, w)
+    for _ in range(3):
+        for a, b in zip(attention(), want):
+            assert torch.equal(a, b)
+    assert "0x7b" in cases._faults()
+    cases._done()
