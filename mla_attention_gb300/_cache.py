@@ -8,7 +8,7 @@ import torch
 
 from . import _lib
 from ._lib import MLAError
-from ._step import (_BF16, _E4M3, _F32, _I32, _INT_MAX, _U8, _call, _dense, _device, _empty, _rows, _shape, _workspace)
+from ._step import (_BF16, _E4M3, _F32, _I32, _INT_MAX, _U8, _call, _dense, _device, _empty, _on, _rows, _shape, _workspace)
 
 FP4_ROW = 416     # bytes of a 4-bit cache row: 256 of codes, 32 scales, 64 RoPE columns in bf16
 
@@ -22,10 +22,18 @@ def _paged(kv_cache, block_table, dev, B):
     return pages, page, max_pages, _dense(block_table, "block_table", _I32, dev, (B, max_pages))
 
 
-def _scratch(nbytes, dev):
+def _scratch(nbytes, dev, stream):
     """The device's scratch buffer of mla_decode_fp4 and mla_key_weights.  It is not the attention's, whose kernels give up their
-    waits while their word is set: a length that was cut is recorded in this one."""
-    return _lib.grown(_lib._scratch_cache, nbytes, torch.device("cuda", dev))
+    waits while their word is set: a length that was cut is recorded in this one.  A new one is filled on the call's stream: in a
+    capture the zeros are a node of the graph, which comes before the call's."""
+    device = torch.device("cuda", dev)
+    ws = _lib._scratch_cache.get(("cuda", dev))
+    if ws is not None and ws.numel() >= nbytes:
+        return ws
+    if stream is None:
+        return _lib.grown(_lib._scratch_cache, nbytes, device)
+    with _on(stream, device):
+        return _lib.grown(_lib._scratch_cache, nbytes, device)
 
 
 def _query(q):
@@ -103,7 +111,7 @@ def mla_decode_fp4(q, kv_cache_fp4, kv_scale: float, block_table, lens, scale: f
     if not 0 <= num_splits <= 65535:
         raise MLAError(1, f"num_splits must be between 0 and 65535, got {num_splits}")
     if ws is None:
-        ws = _scratch(_lib.lib().mla_decode_fp4_workspace_size(B, s, H, num_splits), dev)
+        ws = _scratch(_lib.lib().mla_decode_fp4_workspace_size(B, s, H, num_splits), dev, stream)
     _call("mla_decode_fp4", dev, stream, pq, s, pc, float(kv_scale), pages, page, pt, max_pages, pl, B, H, float(scale), ps,
           num_splits, po, pe, *_workspace(ws, dev))
     if single:
@@ -131,7 +139,7 @@ def mla_key_weights(q, lse, kv_cache, block_table, lens, scale: float, weights, 
         raise MLAError(1, f"weights has too many columns ({width})")
     pw = _rows(weights, "weights", _F32, dev, (B, width))
     if ws is None and s * H > 128:
-        ws = _scratch(_lib.lib().mla_key_weights_workspace_size(B, s, H, width), dev)
+        ws = _scratch(_lib.lib().mla_key_weights_workspace_size(B, s, H, width), dev, stream)
     _call("mla_key_weights", dev, stream, pq, s, pe, pc, fmt, float(kv_scale), pages, page, pt, max_pages,
           _dense(lens, "lens", _I32, dev, (B,)), B, H, float(scale), float(decay), pw, weights.stride(0), width,
           *_workspace(ws, dev))

@@ -190,6 +190,9 @@ def grown(cache: dict, nbytes: int, device: torch.device) -> torch.Tensor:
                     new = torch.zeros(max(need, 0 if ws is None else 2 * ws.numel()), dtype=torch.uint8, device=device)
                 except torch.cuda.OutOfMemoryError:
                     new = torch.zeros(need, dtype=torch.uint8, device=device)
+                # the call may be issued on another stream than the one that fills it
+                if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream(device).synchronize()
                 if ws is not None:
                     _ws_outgrown.append(ws)
                 ws = cache[key] = new

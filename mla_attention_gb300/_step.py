@@ -78,15 +78,20 @@ def _shape(t, name, dims):
     return shape
 
 
+def _on(stream, device):
+    """torch.cuda.stream(stream) for whatever a call takes as one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _empty(shape, dtype, dev, stream):
     """An output in the memory of the stream that writes it, as under torch.cuda.stream(stream)."""
     device = torch.device("cuda", dev)
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = int(getattr(stream, "cuda_stream", stream))
-        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    with _on(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -15,6 +15,21 @@ class OnGpu(torch.Tensor):
         return 0
 
 
+class On:
+    """torch.cuda.stream: which is current."""
+
+    now = "current"
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        self.was, On.now = On.now, self.stream
+
+    def __exit__(self, *_):
+        On.now = self.was
+
+
 @pytest.fixture
 def calls(monkeypatch):
     """The C calls stand-ins record what they get; buffers are host memory."""
@@ -33,12 +48,15 @@ def calls(monkeypatch):
     monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k).as_subclass(OnGpu))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(synchronize=lambda: None))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda dev=None: 0)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, dev=None: handle)
+    monkeypatch.setattr(torch.cuda, "stream", On)
     return got
 
 
-def _decode():
+def _decode(stream=0):
     _cache.mla_decode_fp4(bf16(2, 2, 128, 576), Shaped(torch.uint8, 8, 16, 416), 1.0, i32(2, 4), i32(2), 0.1, out=bf16(2, 2, 128, 512),
-                          lse=Shaped(torch.float32, 2, 2, 128), stream=0)
+                          lse=Shaped(torch.float32, 2, 2, 128), stream=stream)
 
 
 def _weights():
@@ -71,3 +89,26 @@ def test_what_the_scratch_records_is_told(calls, monkeypatch):
         _lib.check_device_status(device="cuda:0", stream=0)
     assert e.value.status == 5 and "0x207b" in str(e.value)
     assert _lib.check_device_status(device="cuda:0", stream=0) == 0
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_new_buffer_is_filled_before_the_call_that_asked_for_it(calls, monkeypatch, capturing):
+    """The call may be on another stream than the current one, on which the zeros are written; a capture cannot wait."""
+    waited = []
+    stream = types.SimpleNamespace(synchronize=lambda: waited.append(dict(calls)))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    _decode()
+    assert waited == ([] if capturing else [{}])         # once, before the call
+    _decode()
+    _lib.workspace(100, torch.device("cuda", 0))
+    assert len(waited) == (0 if capturing else 2)
+
+
+@pytest.mark.parametrize("stream", [0, 1 << 40])
+def test_a_new_buffer_is_filled_on_the_streams_of_the_call(calls, monkeypatch, stream):
+    """In a capture with several streams the zeros come before the call's kernels, not beside them at each replay."""
+    zeros, on = torch.zeros, []
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: on.append(On.now) or zeros(*a, **k))
+    _decode(stream)
+    assert on == [stream] and On.now == "current"
