@@ -538,15 +538,17 @@ mla_status mla_select_keys(const float* weights, int64_t weights_stride, int wid
 
 /*
  * The kept rows moved to the front of their request, in place: row i of request b becomes its row idx[b, i], for
- * i < count[b]; with weights also weights[b, i] = weights[b, idx[b, i]].  The rows behind are left as they are.  RoPE is in
- * the rows already: later tokens keep their positions and go on behind row count[b].
+ * i < count[b]; with weights also weights[b, i] = weights[b, idx[b, i]].  The rows and weights behind are left as they are: set
+ * weights[b, count[b] ..] to 0 before the next tokens come there, or those start with the old rows' weights (mla_key_weights
+ * with decay > 0).  RoPE is in the rows already: later tokens go on behind row count[b] with the positions that they would have had,
+ * those of mla_slot_map plus the rows of the request that have been dropped so far.
  *
  * kv_cache [num_pages, page_size, row_bytes] contiguous, 16-byte aligned, row_bytes a multiple of 16 up to
  *          65536 (1152 bf16, 576 e4m3, 416 4-bit rows); a page belongs to one request.
  * idx      int32 [B, K] contiguous, ascending as mla_select_keys writes them; count DEVICE int32 [B]; B <= 65535.
  * weights  (nullable) fp32 [B, width] at row stride weights_stride >= width.
  * An entry that is not above the one before it, lies below its own place i or outside the table (or the weights' width), or
- * whose pages are not in [0, num_pages), is skipped and recorded (MLA_ERR_DEVICE_RANGE, 0x207d), as is a request whose
+ * whose pages (its row's, its place's) are not in [0, num_pages), is skipped with its weight and recorded (MLA_ERR_DEVICE_RANGE, 0x207d), as is a request whose
  * count is not in [0, K].  A call that ends in MLA_ERR_TIMEOUT may have moved part of a request's rows.
  * workspace: >= 256 bytes (the status word).
  */

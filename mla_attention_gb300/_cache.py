@@ -172,7 +172,8 @@ def mla_select_keys(weights, lens, keep, K: int, first: int = 0, recent: int = 0
 
 def mla_compact_rows(kv_cache, block_table, idx, count, weights=None, ws=None, stream=None):
     """Row i of request b becomes its row idx[b, i] (i < count[b]), in place in kv_cache [pages,page,row] (any type, rows of a
-    multiple of 16 bytes) and, if given, in weights fp32 [B,W].  idx as mla_select_keys gives it."""
+    multiple of 16 bytes) and, if given, in weights fp32 [B,W].  idx as mla_select_keys gives it.  Weights behind count are the old
+    rows' still: set them to 0 before new tokens come there."""
     dev, (B, K) = _device(idx, "idx", 2)
     pages, page, max_pages, pt = _paged(kv_cache, block_table, dev, B)
     row = kv_cache.shape[2] * kv_cache.element_size()

@@ -8,6 +8,7 @@
 //   warp 12      says to the cluster's CTAs that this one's pieces of a chunk are there.  It has no load or store of its own
 //                on its way, which a release to the cluster would wait for
 //   warps 13-15  look up where rows come from and go to, up to six chunks ahead
+// Weights have a cluster of their own, and move where their rows do.
 //
 // Bound by the bytes on their way (up to 90 KB a CTA, two CTAs a SM) and at many requests by the longest of them: 64 of 4096
 // to 16384 kept 4-bit rows take 0.118 ms, 4.3 TB/s; 21845 bf16 rows of one request 17 us, 2.9 TB/s.  Measured instead: a CTA
@@ -198,8 +199,9 @@ cudaError_t launch_compact_rows(const CompactParams& p, cudaStream_t stream) {
     return r == cudaSuccess ? cudaFuncSetAttribute((const void*)compact_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) : r;
   });
   if (e != cudaSuccess) return e;
-  // As many CTAs as run at once: a request's rows to a cluster of up to sixteen, then their columns, so many that a chunk of
-  // theirs has kMaxRows rows.  (One request in clusters of eight: 28 us for 17.)
+  // No more CTAs than run at once: a request's rows to a cluster of up to sixteen, then their columns, in no more slices than
+  // leave a chunk full with kMaxRows rows (one request: 96 CTAs for bf16 rows, 48 for e4m3, 32 for 4-bit ones, and 16 for the
+  // weights, of 304).  (One request in clusters of eight: 28 us for 17.)
   const int columns = p.kv.row_bytes / 16, room = 2 * device_sm_count();
   int ranks = 16;
   while (ranks > 1 && (int64_t)ranks * p.kv.B > room) ranks /= 2;

@@ -12,12 +12,12 @@
 // columns stay bf16 as their MMA's operands, sums are fp32.  28 warps a CTA:
 //   0-7    rows: lanes L and L + 64 of tensor memory hold the same row's scores of 64 keys each, 32 of them a warp; maximum
 //          through shared memory, lazy rescale of O (by more than 2^8), exponentials, P
-//   8, 9   MMAs, in the first CTA alone (one lane issues for both): scores; values
+//   8, 9   MMAs, in the first CTA alone (one lane issues for both): scores; values, once all row warps have scaled O and stored P
 //   10     the tiles' rows through the block table, up to three tiles ahead, and their lines asked for in L2
 //   11     the RoPE columns
 //   12-27  4-bit rows into f16, 16 keys and 256 columns each: of K and of V
-// 64 requests of 4096 to 32768 keys with 128 heads: 0.347 ms, 0.95 PFLOP/s.  No pipe is full: of 5000 cycles a tile the tensor
-// pipe has 2200 (36 % with 32 requests), the issue slots 40 %, the first-level cache's data pipe 64 %, DRAM 19 %, and without any one
+// 64 requests of 4096 to 32768 keys with 128 heads: 0.345 ms, 0.95 PFLOP/s.  No pipe is full: of 5000 cycles a tile the tensor
+// pipe has 2200 (37 % with 32 requests), the issue slots 38 %, the first-level cache's data pipe 65 %, DRAM 19 %, and without any one
 // of the parts it takes some 5 % less; what is left is the chain rows, conversion, scores, exponentials, values of two tiles at a
 // time.  A second set of row registers a converting warp: 0.362.  One request of 4097 keys: 25 us, of which 5.5 join the partials and 18
 // are one chain of loads through the lengths, the table and the rows, the products and the partials' way out.

@@ -18,8 +18,8 @@
 //         registers into f16 (exact), with q in f16 too, the next box's loads out before the last one's are converted; the RoPE
 //         columns of 4-bit rows stay bf16.  A stage has producers of its own, as a parity tells no more than the last phase.
 //
-// One new token of 128 heads and request over bf16 rows is HBM-bound: 64 requests of 4096 to 32768 keys 0.224 ms, 6.2 TB/s.  The
-// first-level cache (rows, their f16 form, the MMAs' operands) bounds the others: 32 such requests 0.111 ms with e4m3 rows, 0.127 with
+// One new token of 128 heads and request over bf16 rows is HBM-bound: 64 requests of 4096 to 32768 keys 0.224 to 0.229 ms, 6.0 to 6.2 TB/s.  The
+// first-level cache (rows, their f16 form, the MMAs' operands) bounds the others: 32 such requests 0.110 ms with e4m3 rows, 0.128 with
 // 4-bit ones; 4096 query rows over 32768 4-bit keys 0.119 ms, 1.30 PFLOP/s (without pairs 0.211).
 #include <math_constants.h>
 

@@ -193,7 +193,7 @@ cudaError_t launch_select_keys(const SelectParams& p, cudaStream_t stream) {
     return r == cudaSuccess ? cudaFuncSetAttribute((const void*)select_keys_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) : r;
   });
   if (e != cudaSuccess) return e;
-  // as many CTAs as run at once (one request with four: 24 us for 12)
+  // clusters so large that all run at once (one request with four CTAs: 24 us for 12)
   int ranks = kMaxRanks;
   while (ranks > 1 && (int64_t)ranks * p.B > 2 * device_sm_count()) ranks /= 2;
   cudaLaunchConfig_t config{};
