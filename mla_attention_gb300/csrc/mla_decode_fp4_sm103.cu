@@ -358,7 +358,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     const int hh = (warp >> 1) & 1, cc = warp >> 2, r = (warp & 1) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float c = p.scale * 1.4426950408889634f, c2 = c == 0.f ? 1e-30f : c;    // see mask_piece
-    const uint64_t c22 = f32x2(c2, c2);
+    // Maxima are those of the scores as they come (their minimum, negated, where the scale is negative), and exponents are
+    // (score - maximum) c: that difference is exact next to the maximum, where score c - maximum c is off by half a step of a large score.
+    const uint64_t c22 = f32x2(c2, c2), lift2 = f32x2(kLift, kLift);
+    const float size = fabsf(c2);
     int32_t* const tile_max = reinterpret_cast<int32_t*>(smem + kOffMax) + r;
     const uint32_t prow = smem_u32(smem + kOffP + hh * kBox);
     uint32_t into = 0;                                // tile_max's next third
@@ -381,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = kUp ? -CUDART_INF_F : CUDART_INF_F;
         row_extreme<kUp>(s, e);
-        float mt = visible > 0 ? extreme4<kUp>(e) * c2 : -CUDART_INF_F;
+        float mt = visible <= 0 ? -CUDART_INF_F : kUp ? extreme4<kUp>(e) : -extreme4<kUp>(e);
         // the largest of the four warps' (the third that comes next was read by all before they came here)
         const uint32_t next = into == 2 ? 0 : into + 1;
         atomicMax(tile_max + 64 * into, ordered(mt));
@@ -391,17 +394,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
         mt = unordered(*reinterpret_cast<volatile int32_t*>(tile_max + 64 * into));
         into = next;
         float a = 1.f;
-        if (mt > m + kRescale || m == -CUDART_INF_F) {
-          a = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mt);
+        if ((mt - m) * size > kRescale || m == -CUDART_INF_F) {
+          a = m == -CUDART_INF_F ? 0.f : ex2_approx((m - mt) * size);
           m = mt;
         }
-        const float ref = m == -CUDART_INF_F ? 0.f : m;
-        const uint64_t nref = f32x2(kLift - ref, kLift - ref);
+        const float ref = m == -CUDART_INF_F ? 0.f : kUp ? -m : m;
+        const uint64_t ref2 = f32x2(ref, ref);
         uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {                 // packed into the first sixteen words
           float x0, x1;
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c22, nref), x0, x1);
+          f32x2_split(fma_f32x2(add_f32x2(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ref2), c22, lift2), x0, x1);
           x0 = ex2_approx(x0), x1 = ex2_approx(x1);
           sum[i & 1] = add_f32x2(sum[i & 1], f32x2(x0, x1));
           s[i] = pack_f16x2(x0, x1);
@@ -432,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       float* stat = p.part_stat + slot_row * 8;       // the maximum and the four sums
       if (row < it.g.rows && guard_span(p.err, G_PART_LSE, stat, 32, p.part_stat, p.part_stat_bytes)) {
         stat[1 + 2 * hh + cc] = l * 0x1p-7f;
-        if (hh == 0 && cc == 0) stat[0] = m;
+        if (hh == 0 && cc == 0) stat[0] = m * size;
       }
       tc_fence_before();
       first_cta_arrive<false>(&bars.ofree, cta);

@@ -84,6 +84,33 @@ def test_decode_a_nan_reaches_the_tokens_that_see_it_alone(s, H, scale, nan):
         assert torch.isnan(out[b, seen:]).all() and torch.isnan(lse[b, seen:]).all()
 
 
+@pytest.mark.parametrize("scale", [2e5, 1e6, 4e6, -4e6, 1.5e7])
+def test_decode_scores_whose_steps_are_large(scale):
+    """Scores of 2^24 to 2^30, where fp32 has steps of 2 to 128: a weight may be off by many powers of two, but it is a number, and the
+    output lies among the values; that of a key far above all others is the output."""
+    lens, H = [300, 129, 64, 1000], 64
+    cache, table, keys = cases._paged("fp4", lens, 64, 97)
+    q = cases._query(len(lens), 1, H, 97)
+    qn = to_np(q)
+    for splits in (0, 1, 3):
+        out, lse = mla_decode_fp4(q.to(dev()), cache, 1.0, table, cases._i32(lens), scale, num_splits=splits)
+        cases._done()
+        o, e, plain = to_np(out), to_np(lse), 0
+        assert np.isfinite(o).all() and np.isfinite(e).all()
+        for b, k in enumerate(keys):
+            raw = np.sign(scale) * (k @ qn[b, 0].T)                   # [keys, H]
+            error = cases.SCORE * (np.abs(k) @ np.abs(qn[b, 0]).T).max(0) + 2.0 ** -22 * np.abs(raw).max(0)
+            v = k[:, :512]
+            assert (o[b, 0] <= v.max(0) + cases.BF16 * np.abs(v).max(0)).all() and (o[b, 0] >= v.min(0) - cases.BF16 * np.abs(v).max(0)).all()
+            top, second = np.sort(raw, 0)[-1], np.sort(raw, 0)[-2]
+            clear = top - second > 2 * error + 1e2 / abs(scale)
+            plain += clear.sum()
+            best = v[raw.argmax(0)]
+            assert (np.abs(o[b, 0] - best) <= cases.BF16 * np.abs(best))[clear].all()
+            assert (np.abs(e[b, 0] - abs(scale) * top) <= abs(scale) * 2 * error + 10).all()
+        assert plain > 200
+
+
 # ---------------------------------------------------------------------------------------------
 # the keys' weights
 # ---------------------------------------------------------------------------------------------
