@@ -16,7 +16,7 @@
 //   10     the tiles' rows through the block table, up to three tiles ahead, and their lines asked for in L2
 //   11     the RoPE columns
 //   12-27  4-bit rows into f16, 16 keys and 256 columns each: of K and of V
-// 64 requests of 4096 to 32768 keys with 128 heads: 0.345 ms, 0.95 PFLOP/s.  No pipe is full: of 5000 cycles a tile the tensor
+// 64 requests of 4096 to 32768 keys with 128 heads: 0.344 ms, 0.96 PFLOP/s.  No pipe is full: of 5000 cycles a tile the tensor
 // pipe has 2200 (37 % with 32 requests), the issue slots 38 %, the first-level cache's data pipe 65 %, DRAM 19 %, and without any one
 // of the parts it takes some 5 % less; what is left is the chain rows, conversion, scores, exponentials, values of two tiles at a
 // time.  A second set of row registers a converting warp: 0.362.  One request of 4097 keys: 25 us, of which 5.5 join the partials and 18
